@@ -380,6 +380,136 @@ int ddp_shard_range(int64_t n, int32_t G, int32_t g, int64_t* chunk, int64_t* lo
  * Asynchronous on `stream`.  G <= 64.  Errors: INVALID_ARG, CUDA. */
 int ddp_shard_mean(int32_t G, ddp_dtype dtype, const void* const* chunks, float* out, int64_t n, void* stream);
 
+/* ---------------------------------------------------------------- optimizer step */
+
+/* AdamW over every parameter at once: the step that follows the reduction and
+ * reads its mean gradients where they lie (bucket views in the arena, or the
+ * copied-back gradients).  With g' = c g, c = min(1, max_norm / (norm + 1e-6)):
+ *   m' = beta1 m + (1 - beta1) g'
+ *   v' = beta2 v + (1 - beta2) g'^2
+ *   w' = w (1 - lr wd_v) - lr / (1 - beta1^t) m' / (sqrt(v') / sqrt(1 - beta2^t) + eps)
+ * in fp32, w the parameter or, for bf16 parameters, its fp32 master copy, of
+ * which the parameter is then the rounding (to nearest even).  The moments are
+ * held in 32 bits, or in 8: m as e4m3 and v as e5m2 numbers times one fp32
+ * scale for each block of DDP_ADAMW_BLOCK elements of a tensor.  An 8-bit
+ * moment's new scale is its block's largest magnitude over the format's
+ * largest finite value (448, 57344); blocks whose scale would be below
+ * 2^-126 become zeros, and blocks that hold a value that is not finite get
+ * a NaN scale.  Values between two codes round up with the probability of the
+ * rest (16 bits of a counter hash of the step's seed, the block and the place
+ * in it), so that averages stay unbiased where a step of (1 - beta2) is far
+ * below the codes' spacing; a v that is not zero is never stored as zero.
+ * The pages have no counterpart beyond the SGD step of the DDP notes' example. */
+#define DDP_ADAMW_BLOCK 256
+
+typedef struct ddp_adamw ddp_adamw;
+
+/* A step over P tensors of numel[v] elements (host array, >= 0; P >= 0).
+ *   param_dtype  DDP_F32, or DDP_BF16 (with fp32 master copies)
+ *   state_bits   32 or 8
+ * Host memory only.  Errors: INVALID_ARG, NO_MEMORY. */
+int ddp_adamw_create(const int64_t* numel, int32_t P, ddp_dtype param_dtype, int32_t state_bits, ddp_adamw** out);
+
+/* Bind the tensors: host arrays [P] of device addresses, each tensor
+ * contiguous (entries of empty tensors may be NULL).
+ *   grads             fp32 mean gradients
+ *   params            parameters (param_dtype); NULL binds the gradients alone,
+ *                     for ddp_adamw_grad_norm; the arrays below are then unused
+ *   master            fp32 master copies of bf16 parameters, else NULL
+ *   exp_avg, exp_avg_sq              m and v: fp32, or 8-bit codes
+ *   exp_avg_scale, exp_avg_sq_scale  fp32 scales of 8-bit moments,
+ *                     ceil(numel[v] / DDP_ADAMW_BLOCK) each, else NULL
+ *   weight_decay      host array [P] of wd_v >= 0, or NULL (none)
+ * Any element alignment is correct; tensors whose addresses are 16-byte
+ * aligned (4-byte for 8-bit codes) are read and written in vectors.
+ * Zero-filled moments and scales are the state before the first step.
+ * Synchronous; builds a device table (library-owned, freed by
+ * ddp_adamw_destroy or the next bind) on the current device, which later calls
+ * must have current.  Errors: INVALID_ARG, CUDA, NO_MEMORY. */
+int ddp_adamw_bind(ddp_adamw* opt, const float* const* grads, void* const* params, float* const* master,
+                   void* const* exp_avg, void* const* exp_avg_sq, float* const* exp_avg_scale,
+                   float* const* exp_avg_sq_scale, const float* weight_decay);
+
+typedef struct ddp_adamw_args {
+    int64_t t;               /* number of this step, from 1 */
+    double lr, beta1, beta2, eps;   /* finite; lr >= 0, 0 <= beta < 1, eps > 0 */
+    double max_norm;         /* > 0: clip by *norm; 0: no clipping */
+    const float* norm;       /* device fp32, read by the kernel (ddp_adamw_grad_norm writes one), or NULL */
+    const uint8_t* used;     /* device [P], or NULL = all: tensors with 0 keep parameter and moments */
+    uint64_t seed;           /* of the 8-bit rounding; another one each step */
+    int32_t skip_nonfinite;  /* != 0: a *norm that is not finite leaves everything as it is */
+} ddp_adamw_args;
+
+/* One step over the bound tensors, one launch, asynchronous on `stream`.
+ * Errors: INVALID_ARG, NOT_BOUND, CUDA. */
+int ddp_adamw_step(ddp_adamw* opt, const ddp_adamw_args* args, void* stream);
+
+/* *norm = sqrt of the sum of squares over the bound gradients (of the tensors
+ * with used[v] != 0; device array [P] or NULL = all), one launch,
+ * asynchronous on `stream`.  Squares are fp32 (gradients past 1.8e19 give an
+ * infinite norm), long sums are double; the order is fixed, so equal inputs
+ * give equal bits.  Calls of one `opt` share its partial sums: they run in
+ * one stream's order.  Errors: INVALID_ARG, NOT_BOUND, CUDA. */
+int ddp_adamw_grad_norm(ddp_adamw* opt, const uint8_t* used, float* norm, void* stream);
+
+/* Detail of the last failure on opt (or of the last failed ddp_adamw_create in
+ * this thread when opt is NULL). */
+const char* ddp_adamw_last_error(const ddp_adamw* opt);
+
+void ddp_adamw_destroy(ddp_adamw* opt);
+
+/* ---------------------------------------------------------------- expert routing */
+
+/* Tokens to experts.  What a router chose decides which experts' parameters
+ * get a gradient on a replica (ddp_set_local_used), and its counts say so.
+ * For every token, over its E logits x:
+ *   s_i = softmax(x)_i, or sigmoid(x_i)                              (fp32)
+ *   c_i = s_i + bias_i, what the choice goes by (without a bias and groups,
+ *         x_i itself, whose order is that of s)
+ *   groups > 1: the E experts are `groups` equal runs; a run is worth the sum
+ *         of its two largest c (of its one where it has one), and only the
+ *         top_groups best runs stay
+ *   the k experts of the largest c, in descending order; ties of experts and
+ *         of groups go to the lowest index
+ *   w_j = s_j of the chosen, over their sum with renorm (zero if that is), times scale
+ * A logit of -inf (or NaN) is never chosen, nor is a c of -inf; slots that no
+ * expert is left for, and all of a masked token's, get index -1 and weight 0.
+ * A token with a NaN logit, or under softmax with an infinite one, gets NaN
+ * weights in every slot.  The bias takes no gradient. */
+enum ddp_score { DDP_SCORE_SOFTMAX = 0, DDP_SCORE_SIGMOID = 1 };
+
+typedef struct ddp_route_args {
+    int64_t tokens;          /* >= 0 */
+    int64_t row_stride;      /* elements between two tokens' logits, >= experts */
+    int32_t experts;         /* 1 .. 512 */
+    int32_t k;               /* 1 .. 32, <= top_groups * (experts / groups) */
+    int32_t score;           /* enum ddp_score */
+    int32_t groups;          /* 1 .. 32, divides experts */
+    int32_t top_groups;      /* 1 .. groups */
+    int32_t renorm;          /* != 0: weights over their sum */
+    float scale;             /* finite, != 0 */
+    ddp_dtype dtype;         /* of the logits (and of their gradient) */
+} ddp_route_args;
+
+/*   logits   device [tokens] rows of `experts`, row_stride apart
+ *   bias     device fp32 [experts] or NULL
+ *   mask     device bytes [tokens] or NULL: 0 = the token is not routed (its logits are not read)
+ *   indices  device int32 [tokens * k]
+ *   weights  device fp32 [tokens * k]
+ *   counts   device int32 [experts] or NULL: the number of tokens each expert
+ *            got is ADDED to it (over micro-steps and replicas, as the caller wants)
+ * Asynchronous on `stream`; no workspace.  Errors: INVALID_ARG, CUDA. */
+int ddp_route(const ddp_route_args* args, const void* logits, const float* bias, const uint8_t* mask,
+              int32_t* indices, float* weights, int32_t* counts, void* stream);
+
+/* The logits' gradient from the weights': grad_logits (device, dtype,
+ * [tokens] rows of `experts`, grad_stride apart, every element written) from
+ * grad_weights (device fp32 [tokens * k]) and the call's own indices and
+ * weights.  Of args, bias and groups play no part.
+ * Errors: INVALID_ARG, CUDA. */
+int ddp_route_backward(const ddp_route_args* args, const void* logits, const int32_t* indices, const float* weights,
+                       const float* grad_weights, void* grad_logits, int64_t grad_stride, void* stream);
+
 /* ---------------------------------------------------------------- options, info */
 
 enum ddp_option {
@@ -449,7 +579,7 @@ int ddp_get_device_status(ddp_ctx* ctx, int32_t* status);
 /* Read and clear the bounds-check record of a bound context (synchronous:
  * waits for the device).
  * Only a library built with -DDDP_DEBUG (libddpreducer_debug.so) checks, in
- * every kernel, that each range it walks lies inside its segment, launch and
+ * every kernel of the gradient path, that each range it walks lies inside its segment, launch and
  * stage and that every bulk copy is 16-byte aligned and sized; the first
  * failed check stores its code (101 segment range, 102 staged chunk range,
  * 103 bulk-copy alignment, 104 accumulate pair range) and the element index

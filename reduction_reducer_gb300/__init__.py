@@ -8,3 +8,5 @@ C++ host core + hand-written sm_103a CUDA kernels behind the C ABI of
 from .reducer import (AlreadyReady, CudaError, DDPError, HookError, InvalidArg, NoMemory,  # noqa: F401
                       NotBound, OutOfOrder, PriorReductionUnfinished, Reducer, selftest_bounded_wait)
 from ._lib import LIB_PATH, load  # noqa: F401
+from .optim import AdamW  # noqa: F401
+from .routing import route, route_backward, routed  # noqa: F401

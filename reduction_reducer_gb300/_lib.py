@@ -46,6 +46,20 @@ class GradBucket(C.Structure):
                 ("lengths", C.POINTER(C.c_int64))]
 
 
+class AdamWArgs(C.Structure):
+    """struct ddp_adamw_args."""
+    _fields_ = [("t", C.c_int64), ("lr", C.c_double), ("beta1", C.c_double), ("beta2", C.c_double),
+                ("eps", C.c_double), ("max_norm", C.c_double), ("norm", C.c_void_p), ("used", C.c_void_p),
+                ("seed", C.c_uint64), ("skip_nonfinite", C.c_int32)]
+
+
+class RouteArgs(C.Structure):
+    """struct ddp_route_args."""
+    _fields_ = [("tokens", C.c_int64), ("row_stride", C.c_int64), ("experts", C.c_int32), ("k", C.c_int32),
+                ("score", C.c_int32), ("groups", C.c_int32), ("top_groups", C.c_int32), ("renorm", C.c_int32),
+                ("scale", C.c_float), ("dtype", C.c_int32)]
+
+
 # int (*ddp_comm_hook_fn)(void* state, const ddp_grad_bucket* bucket, void* stream)
 HOOKFN = C.CFUNCTYPE(C.c_int, C.c_void_p, C.POINTER(GradBucket), C.c_void_p)
 
@@ -83,6 +97,14 @@ SIGNATURES = {
     "ddp_shard_range": (C.c_int, [C.c_int64, C.c_int32, C.c_int32, C.POINTER(C.c_int64), C.POINTER(C.c_int64),
                                   C.POINTER(C.c_int64)]),
     "ddp_shard_mean": (C.c_int, [C.c_int32, C.c_int, C.POINTER(C.c_void_p), C.c_void_p, C.c_int64, C.c_void_p]),
+    "ddp_adamw_create": (C.c_int, [C.POINTER(C.c_int64), C.c_int32, C.c_int, C.c_int32, C.POINTER(C.c_void_p)]),
+    "ddp_adamw_bind": (C.c_int, [C.c_void_p] + [C.POINTER(C.c_void_p)] * 7 + [C.POINTER(C.c_float)]),
+    "ddp_adamw_step": (C.c_int, [C.c_void_p, C.POINTER(AdamWArgs), C.c_void_p]),
+    "ddp_adamw_grad_norm": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "ddp_adamw_last_error": (C.c_char_p, [C.c_void_p]),
+    "ddp_adamw_destroy": (None, [C.c_void_p]),
+    "ddp_route": (C.c_int, [C.POINTER(RouteArgs)] + [C.c_void_p] * 7),
+    "ddp_route_backward": (C.c_int, [C.POINTER(RouteArgs)] + [C.c_void_p] * 5 + [C.c_int64, C.c_void_p]),
     "ddp_read_launch_trace": (C.c_int, [C.POINTER(C.c_uint64), C.POINTER(C.c_int32), C.POINTER(C.c_int64)]),
     "ddp_status_string": (C.c_char_p, [C.c_int]),
     "ddp_last_error": (C.c_char_p, [C.c_void_p]),

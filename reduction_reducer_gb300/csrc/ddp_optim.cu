@@ -1,0 +1,641 @@
+// The optimizer step behind the gradient path: AdamW over every parameter in
+// one launch (moments in 32 or in 8 bits), and the global gradient norm it
+// clips by.
+//
+// Both kernels see the tensors as runs of blocks of 256 elements (a tensor's
+// last block may be short), numbered through all non-empty tensors in
+// registration order.  A CTA owns an equal run of blocks, its warps take them
+// in turn, and a warp finds its first block's tensor with the warp-ballot
+// search over the tensors' first blocks; so one launch serves any mix of
+// large matrices and small vectors.  Within a block lane l holds elements
+// 4 l .. 4 l + 3 and 128 + 4 l .. 128 + 4 l + 3: every 128-bit access of a
+// warp covers 512 consecutive bytes, and an 8-bit moment's block, whose scale
+// needs the largest magnitude of all 256 values, is one warp's registers.
+
+#include "ddp_reducer.h"
+
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <new>
+#include <string>
+#include <vector>
+
+#include "ddp_device.cuh"
+
+namespace {
+
+constexpr int kBlock = DDP_ADAMW_BLOCK;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+static_assert(kBlock == 256, "a warp holds a block as 8 values a lane");
+
+// One non-empty tensor, as the kernels read it.
+struct __align__(16) Tensor {
+    const float* g;
+    void* p;            // parameter: fp32, or bf16
+    float* master;      // fp32 master copy of a bf16 parameter
+    void* m;            // moments: fp32, or e4m3 / e5m2 codes
+    void* v;
+    float* ms;          // scales of 8-bit moments, one per block
+    float* vs;
+    long long n;
+    float wd;
+    int var;            // its index among all tensors
+    int vec_g;          // gradients: 16-byte aligned
+    int vec;            // all others: aligned for 4-element accesses
+};
+
+struct Scalars {
+    float beta1, beta1c, beta2, beta2c;   // betas and 1 - beta
+    float lr, step;                       // step = lr / (1 - beta1^t)
+    float rbc2;                           // 1 / sqrt(1 - beta2^t)
+    float eps, max_norm;
+    uint32_t seed_lo, seed_hi;
+    int clip, skip_nonfinite;
+};
+
+struct StepParams {
+    const Tensor* tensors;
+    const long long* first;    // [S + 1] first block of each tensor
+    const float* norm;
+    const uint8_t* used;
+    long long blocks, piece;   // all blocks; blocks per CTA
+    int S;
+    Scalars c;
+};
+
+// ------------------------------------------------------------------ four values
+
+__device__ __forceinline__ void load4(const float* p, int left, bool vec, float (&f)[4]) {
+    if (vec && left >= 4) {
+        const float4 x = __ldcs(reinterpret_cast<const float4*>(p));
+        f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = i < left ? p[i] : 0.0f;
+    }
+}
+
+__device__ __forceinline__ void store4(float* p, int left, bool vec, const float (&f)[4]) {
+    if (vec && left >= 4) {
+        __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < left) p[i] = f[i];
+    }
+}
+
+__device__ __forceinline__ uint32_t load4_code(const uint8_t* p, int left, bool vec) {
+    if (vec && left >= 4) return __ldcs(reinterpret_cast<const uint32_t*>(p));
+    uint32_t x = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < left) x |= static_cast<uint32_t>(p[i]) << (8 * i);
+    return x;
+}
+
+__device__ __forceinline__ void store4_code(uint8_t* p, int left, bool vec, uint32_t x) {
+    if (vec && left >= 4) {
+        __stcs(reinterpret_cast<uint32_t*>(p), x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < left) p[i] = static_cast<uint8_t>(x >> (8 * i));
+    }
+}
+
+// fp32 -> bf16 bits, round to nearest even, as the high half of a word.
+__device__ __forceinline__ uint32_t bf16_bits(float x) { return __float_as_uint(ddpk::dev::round_bf16(x)) >> 16; }
+
+__device__ __forceinline__ void store4_bf16(uint16_t* p, int left, bool vec, const float (&f)[4]) {
+    if (vec && left >= 4) {
+        __stcs(reinterpret_cast<uint2*>(p), make_uint2(bf16_bits(f[0]) | bf16_bits(f[1]) << 16,
+                                                       bf16_bits(f[2]) | bf16_bits(f[3]) << 16));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < left) p[i] = static_cast<uint16_t>(bf16_bits(f[i]));
+    }
+}
+
+// ------------------------------------------------------------------ 8-bit moments
+
+// Value of an e4m3 / e5m2 code (never an infinity or NaN code): its exponent
+// and mantissa bits, put in an fp32 pattern's place, are the value times
+// 2^(bias - 127), subnormals included.
+__device__ __forceinline__ float e4m3_value(uint32_t c) {
+    const float x = __fmul_rn(__uint_as_float((c & 0x7fu) << 20), 0x1p120f);
+    return __uint_as_float(__float_as_uint(x) | (c & 0x80u) << 24);
+}
+
+__device__ __forceinline__ float e5m2_value(uint32_t c) {
+    return __fmul_rn(__uint_as_float((c & 0x7fu) << 21), 0x1p112f);
+}
+
+// Codes of |x| / scale, given y = |x| / scale and 16 random bits r, rounded up
+// with the probability of the rest: for normal numbers the random bits are
+// added below the kept mantissa bits; below them the spacing is 2^-9 (2^-16),
+// where floor(y / spacing + r / 2^16) continues the same code sequence.
+__device__ __forceinline__ uint32_t e4m3_code(float y, uint32_t r) {
+    const uint32_t normal = ((__float_as_uint(y) + (r << 4)) >> 20) - 960u;
+    const uint32_t small = static_cast<uint32_t>(__fmaf_rn(y, 512.0f, __uint2float_rn(r) * 0x1p-16f));
+    return min(y < 0x1p-6f ? small : normal, 126u);
+}
+
+__device__ __forceinline__ uint32_t e5m2_code(float y, uint32_t r) {
+    const uint32_t normal = ((__float_as_uint(y) + (r << 5)) >> 21) - 448u;
+    const uint32_t small = static_cast<uint32_t>(__fmaf_rn(y, 65536.0f, __uint2float_rn(r) * 0x1p-16f));
+    const uint32_t c = min(y < 0x1p-14f ? small : normal, 123u);
+    return y > 0.0f ? max(c, 1u) : c;      // m / (sqrt(v) + eps) must not meet a v rounded to zero
+}
+
+// The scale of a block whose largest magnitude has the bits `peak`.
+__device__ __forceinline__ float block_scale(uint32_t peak, float over_top) {
+    const float s = __fmul_rn(__uint_as_float(peak), over_top);
+    if (!(s < __int_as_float(0x7f800000))) return __int_as_float(0x7fffffff);
+    return s >= 0x1p-126f ? s : 0.0f;
+}
+
+// 32 random bits of (seed, block, place): odd multipliers from the fractional
+// bits of sqrt(2) and sqrt(3), places spread by the golden ratio's.
+__device__ __forceinline__ uint32_t mix(uint32_t x) {
+    x ^= x >> 16;
+    x *= 0x6A09E667u;
+    x ^= x >> 15;
+    x *= 0xBB67AE85u;
+    return x ^ (x >> 16);
+}
+
+__device__ __forceinline__ uint32_t block_key(const Scalars& c, long long block) {
+    return mix(mix(static_cast<uint32_t>(block) ^ c.seed_lo) + c.seed_hi);
+}
+
+__device__ __forceinline__ uint32_t random_bits(uint32_t key, uint32_t place) { return mix(key + place * 0x9E3779B9u); }
+
+// ------------------------------------------------------------------ the step
+
+// Products and sums are rounded one by one (no contraction into fused
+// multiply-adds): the stored moments, and with them the 8-bit codes, are then
+// those of the formula's own order of fp32 operations.
+__device__ __forceinline__ void moments(const Scalars& c, float g, float& m, float& v) {
+    m = __fadd_rn(__fmul_rn(m, c.beta1), __fmul_rn(g, c.beta1c));
+    v = __fadd_rn(__fmul_rn(v, c.beta2), __fmul_rn(__fmul_rn(g, g), c.beta2c));
+}
+
+__device__ __forceinline__ float weight(const Scalars& c, float keep, float w, float m, float v) {
+    const float denom = __fadd_rn(__fmul_rn(__fsqrt_rn(v), c.rbc2), c.eps);
+    return __fsub_rn(__fmul_rn(w, keep), __fdiv_rn(__fmul_rn(c.step, m), denom));
+}
+
+template <bool BF16, bool Q8>
+__global__ void __launch_bounds__(kThreads)
+adamw_kernel(const __grid_constant__ StepParams a) {
+    const int lane = threadIdx.x & 31;
+    const long long begin = static_cast<long long>(blockIdx.x) * a.piece;
+    const long long end = min(begin + a.piece, a.blocks);
+    long long b = begin + (threadIdx.x >> 5);
+    int s = b < end ? ddpk::dev::find_segment(a.first, 0, a.S, b) : 0;   // the library's own table: before the wait
+    ddpk::dev::pdl_wait();
+    ddpk::dev::pdl_trigger();
+
+    float clip = 1.0f;
+    if (a.norm) {
+        const float norm = *a.norm;
+        if (a.c.skip_nonfinite && !(norm < __int_as_float(0x7f800000))) return;
+        if (a.c.clip) {
+            const float x = __fdiv_rn(a.c.max_norm, __fadd_rn(norm, 1e-6f));
+            clip = x > 1.0f ? 1.0f : x;        // a NaN stays one
+        }
+    }
+
+    for (; b < end; b += kWarps) {
+        while (b >= __ldg(a.first + s + 1)) ++s;
+        const Tensor& t = a.tensors[s];
+        if (a.used && !a.used[t.var]) continue;
+        const long long j = b - __ldg(a.first + s);          // block of the tensor
+        const long long rest = t.n - j * kBlock;
+        const int left = static_cast<int>(min(rest, static_cast<long long>(kBlock)));
+        const bool vec = t.vec, vec_g = t.vec_g;
+        const float keep = __fsub_rn(1.0f, __fmul_rn(a.c.lr, t.wd));
+        float* const w_ptr = BF16 ? t.master : static_cast<float*>(t.p);
+        float g[2][4], w[2][4], m[2][4], v[2][4];
+        uint32_t mc[2], vc[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int e = 128 * h + 4 * lane;
+            const long long i = j * kBlock + e;
+            load4(t.g + i, left - e, vec_g, g[h]);
+            load4(w_ptr + i, left - e, vec, w[h]);
+            if constexpr (Q8) {
+                mc[h] = load4_code(static_cast<const uint8_t*>(t.m) + i, left - e, vec);
+                vc[h] = load4_code(static_cast<const uint8_t*>(t.v) + i, left - e, vec);
+            } else {
+                load4(static_cast<const float*>(t.m) + i, left - e, vec, m[h]);
+                load4(static_cast<const float*>(t.v) + i, left - e, vec, v[h]);
+            }
+        }
+        if constexpr (Q8) {
+            const float ms = t.ms[j], vs = t.vs[j];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    m[h][q] = __fmul_rn(e4m3_value(mc[h] >> (8 * q)), ms);
+                    v[h][q] = __fmul_rn(e5m2_value(vc[h] >> (8 * q)), vs);
+                }
+        }
+        uint32_t peak_m = 0, peak_v = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                moments(a.c, __fmul_rn(g[h][q], clip), m[h][q], v[h][q]);
+                w[h][q] = weight(a.c, keep, w[h][q], m[h][q], v[h][q]);
+                if constexpr (Q8) {
+                    // magnitudes compare as their bits, NaN above infinity;
+                    // what lies past the tensor's end does not count
+                    const bool in = 128 * h + 4 * lane + q < left;
+                    peak_m = max(peak_m, in ? __float_as_uint(m[h][q]) & 0x7fffffffu : 0u);
+                    peak_v = max(peak_v, in ? __float_as_uint(v[h][q]) & 0x7fffffffu : 0u);
+                }
+            }
+        if constexpr (Q8) {
+            const float ms = block_scale(__reduce_max_sync(0xffffffffu, peak_m), 1.0f / 448.0f);
+            const float vs = block_scale(__reduce_max_sync(0xffffffffu, peak_v), 1.0f / 57344.0f);
+            const float mi = ms > 0.0f ? __fdiv_rn(1.0f, ms) : 0.0f;
+            const float vi = vs > 0.0f ? __fdiv_rn(1.0f, vs) : 0.0f;
+            const uint32_t key = block_key(a.c, b);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                mc[h] = vc[h] = 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t r = random_bits(key, 128 * h + 4 * lane + q);
+                    const uint32_t x = e4m3_code(__fmul_rn(fabsf(m[h][q]), mi), r >> 16) |
+                                       (__float_as_uint(m[h][q]) >> 24 & 0x80u);
+                    mc[h] |= x << (8 * q);
+                    vc[h] |= e5m2_code(__fmul_rn(v[h][q], vi), r & 0xffffu) << (8 * q);
+                }
+            }
+            if (lane == 0) {
+                t.ms[j] = ms;
+                t.vs[j] = vs;
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int e = 128 * h + 4 * lane;
+            const long long i = j * kBlock + e;
+            store4(w_ptr + i, left - e, vec, w[h]);
+            if constexpr (BF16) store4_bf16(static_cast<uint16_t*>(t.p) + i, left - e, vec, w[h]);
+            if constexpr (Q8) {
+                store4_code(static_cast<uint8_t*>(t.m) + i, left - e, vec, mc[h]);
+                store4_code(static_cast<uint8_t*>(t.v) + i, left - e, vec, vc[h]);
+            } else {
+                store4(static_cast<float*>(t.m) + i, left - e, vec, m[h]);
+                store4(static_cast<float*>(t.v) + i, left - e, vec, v[h]);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ the norm
+
+struct NormParams {
+    const Tensor* tensors;
+    const long long* first;
+    const uint8_t* used;
+    double* partial;           // [grid]
+    unsigned* done;            // CTAs finished; wraps to 0
+    float* norm;
+    long long blocks, piece;
+    int S;
+};
+
+__device__ __forceinline__ double cta_sum(double x, double* smem) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_down_sync(0xffffffffu, x, o);
+    if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = x;
+    __syncthreads();
+    double total = 0.0;
+    if (threadIdx.x == 0)
+        for (int i = 0; i < kWarps; ++i) total += smem[i];
+    return total;              // thread 0's is the sum
+}
+
+__global__ void __launch_bounds__(kThreads)
+norm_kernel(const __grid_constant__ NormParams a) {
+    __shared__ double smem[kWarps];
+    __shared__ bool last;
+    const int lane = threadIdx.x & 31;
+    const long long begin = static_cast<long long>(blockIdx.x) * a.piece;
+    const long long end = min(begin + a.piece, a.blocks);
+    long long b = begin + (threadIdx.x >> 5);
+    int s = b < end ? ddpk::dev::find_segment(a.first, 0, a.S, b) : 0;
+    ddpk::dev::pdl_wait();
+    ddpk::dev::pdl_trigger();
+
+    double sum = 0.0;
+    for (; b < end; b += kWarps) {
+        while (b >= __ldg(a.first + s + 1)) ++s;
+        const Tensor& t = a.tensors[s];
+        if (a.used && !a.used[t.var]) continue;
+        const long long j = b - __ldg(a.first + s);
+        const int left = static_cast<int>(min(t.n - j * kBlock, static_cast<long long>(kBlock)));
+        float part = 0.0f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float g[4];
+            const int e = 128 * h + 4 * lane;
+            load4(t.g + j * kBlock + e, left - e, t.vec_g, g);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) part = __fmaf_rn(g[q], g[q], part);
+        }
+        sum += part;
+    }
+    const double total = cta_sum(sum, smem);
+    if (threadIdx.x == 0) {
+        a.partial[blockIdx.x] = total;
+        __threadfence();
+        last = atomicInc(a.done, gridDim.x - 1) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    // the CTA that finishes last adds the partial sums, in an order of their own
+    __threadfence();
+    double x = 0.0;
+    for (unsigned i = threadIdx.x; i < gridDim.x; i += kThreads) x += __ldcg(a.partial + i);
+    __syncthreads();
+    const double all = cta_sum(x, smem);
+    if (threadIdx.x == 0) *a.norm = static_cast<float>(sqrt(all));
+}
+
+template <typename K, typename P>
+cudaError_t launch(K kernel, int grid, const P& params, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, params);
+}
+
+thread_local std::string g_create_error;
+
+}  // namespace
+
+struct ddp_adamw {
+    std::vector<int64_t> numel;
+    bool bf16 = false;
+    bool q8 = false;
+    // binding
+    int device = -1;
+    int sms = 0;
+    bool has_params = false;
+    bool bound = false;
+    int S = 0;
+    int64_t blocks = 0;
+    void* table = nullptr;       // device: Tensor[S], first[S + 1], partial[], done
+    const Tensor* tensors = nullptr;
+    const long long* first = nullptr;
+    double* partial = nullptr;
+    unsigned* done = nullptr;
+    std::string error;
+
+    int fail(int status, const char* what) {
+        try { error = what; } catch (...) {}
+        return status;
+    }
+    int cuda(cudaError_t e) { return fail(DDP_ERR_CUDA, cudaGetErrorString(e)); }
+};
+
+namespace {
+
+constexpr int kNormCtasPerSm = 8;
+constexpr int kStepCtasPerSm = 8;
+
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+// CTAs for `blocks`, at most `most`: as few blocks a warp as fills the grid.
+void split(int64_t blocks, int64_t most, int* grid, long long* piece) {
+    const int64_t ctas = (blocks + kWarps - 1) / kWarps;
+    const int64_t n = ctas < most ? ctas : most;
+    *piece = (blocks + n - 1) / n;
+    *grid = static_cast<int>((blocks + *piece - 1) / *piece);
+}
+
+int check_device(ddp_adamw* o) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return o->cuda(e);
+    if (dev != o->device) return o->fail(DDP_ERR_INVALID_ARG, "the current device is not the one of ddp_adamw_bind");
+    return DDP_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ddp_adamw_create(const int64_t* numel, int32_t P, ddp_dtype param_dtype, int32_t state_bits, ddp_adamw** out) {
+    const auto fail = [](const char* what) {
+        try { g_create_error = what; } catch (...) {}
+        return DDP_ERR_INVALID_ARG;
+    };
+    if (!out) return fail("out is NULL");
+    *out = nullptr;
+    if (P < 0 || (P > 0 && !numel)) return fail("P < 0, or numel is NULL");
+    if (param_dtype != DDP_F32 && param_dtype != DDP_BF16) return fail("param_dtype is neither DDP_F32 nor DDP_BF16");
+    if (state_bits != 32 && state_bits != 8) return fail("state_bits is neither 32 nor 8");
+    for (int32_t v = 0; v < P; ++v)
+        if (numel[v] < 0) return fail("negative numel");
+    ddp_adamw* o = new (std::nothrow) ddp_adamw;
+    if (!o) return DDP_ERR_NO_MEMORY;
+    try {
+        o->numel.assign(numel, numel + P);
+    } catch (...) {
+        delete o;
+        return DDP_ERR_NO_MEMORY;
+    }
+    o->bf16 = param_dtype == DDP_BF16;
+    o->q8 = state_bits == 8;
+    *out = o;
+    return DDP_OK;
+}
+
+int ddp_adamw_bind(ddp_adamw* o, const float* const* grads, void* const* params, float* const* master,
+                   void* const* exp_avg, void* const* exp_avg_sq, float* const* exp_avg_scale,
+                   float* const* exp_avg_sq_scale, const float* weight_decay) {
+    if (!o) return DDP_ERR_INVALID_ARG;
+    const int P = static_cast<int>(o->numel.size());
+    if (P > 0 && !grads) return o->fail(DDP_ERR_INVALID_ARG, "grads is NULL");
+    const bool step = params != nullptr;
+    if (step && P > 0) {
+        if (!exp_avg || !exp_avg_sq) return o->fail(DDP_ERR_INVALID_ARG, "exp_avg or exp_avg_sq is NULL");
+        if (o->bf16 != (master != nullptr))
+            return o->fail(DDP_ERR_INVALID_ARG, "master copies belong to bf16 parameters, and to them alone");
+        if (o->q8 != (exp_avg_scale != nullptr) || o->q8 != (exp_avg_sq_scale != nullptr))
+            return o->fail(DDP_ERR_INVALID_ARG, "scales belong to 8-bit moments, and to them alone");
+    }
+    try {
+        std::vector<Tensor> tensors;
+        std::vector<long long> first;
+        long long blocks = 0;
+        for (int v = 0; v < P; ++v) {
+            const int64_t n = o->numel[v];
+            if (n == 0) continue;
+            Tensor t = {};
+            t.g = grads[v];
+            t.n = n;
+            t.var = v;
+            if (!t.g || !aligned(t.g, 4)) return o->fail(DDP_ERR_INVALID_ARG, "a gradient is NULL or misaligned");
+            t.vec_g = aligned(t.g, 16);
+            if (step) {
+                const uintptr_t psize = o->bf16 ? 2 : 4, ssize = o->q8 ? 1 : 4;
+                t.p = params[v];
+                t.m = exp_avg[v];
+                t.v = exp_avg_sq[v];
+                t.master = o->bf16 ? master[v] : nullptr;
+                t.ms = o->q8 ? exp_avg_scale[v] : nullptr;
+                t.vs = o->q8 ? exp_avg_sq_scale[v] : nullptr;
+                t.wd = weight_decay ? weight_decay[v] : 0.0f;
+                if (!t.p || !t.m || !t.v || (o->bf16 && !t.master) || (o->q8 && (!t.ms || !t.vs)))
+                    return o->fail(DDP_ERR_INVALID_ARG, "a tensor that is not empty has a NULL address");
+                if (!aligned(t.p, psize) || !aligned(t.m, ssize) || !aligned(t.v, ssize) || !aligned(t.master, 4) ||
+                    !aligned(t.ms, 4) || !aligned(t.vs, 4))
+                    return o->fail(DDP_ERR_INVALID_ARG, "an address is not aligned to its element");
+                if (!(t.wd >= 0.0f) || std::isinf(t.wd))
+                    return o->fail(DDP_ERR_INVALID_ARG, "weight_decay is negative or not finite");
+                t.vec = aligned(t.p, 4 * psize) && aligned(t.m, 4 * ssize) && aligned(t.v, 4 * ssize) &&
+                        aligned(t.master, 16);
+            }
+            tensors.push_back(t);
+            first.push_back(blocks);
+            blocks += (n + kBlock - 1) / kBlock;
+        }
+        first.push_back(blocks);
+
+        int dev = 0, sms = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return o->cuda(e);
+        const size_t at_first = tensors.size() * sizeof(Tensor);
+        const size_t at_partial = at_first + (first.size() * sizeof(long long) + 15) / 16 * 16;
+        const size_t at_done = at_partial + static_cast<size_t>(sms) * kNormCtasPerSm * sizeof(double);
+        std::vector<unsigned char> image(at_done + 16, 0);
+        if (!tensors.empty()) std::memcpy(image.data(), tensors.data(), at_first);
+        std::memcpy(image.data() + at_first, first.data(), first.size() * sizeof(long long));
+        void* table = nullptr;
+        e = cudaMalloc(&table, image.size());
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return e == cudaErrorMemoryAllocation ? o->fail(DDP_ERR_NO_MEMORY, cudaGetErrorString(e)) : o->cuda(e);
+        }
+        e = cudaMemcpy(table, image.data(), image.size(), cudaMemcpyHostToDevice);
+        if (e != cudaSuccess) {
+            cudaFree(table);
+            return o->cuda(e);
+        }
+        if (o->table) cudaFree(o->table);      // waits for the kernels that read it
+        unsigned char* base = static_cast<unsigned char*>(table);
+        o->table = table;
+        o->tensors = reinterpret_cast<const Tensor*>(base);
+        o->first = reinterpret_cast<const long long*>(base + at_first);
+        o->partial = reinterpret_cast<double*>(base + at_partial);
+        o->done = reinterpret_cast<unsigned*>(base + at_done);
+        o->S = static_cast<int>(tensors.size());
+        o->blocks = blocks;
+        o->device = dev;
+        o->sms = sms;
+        o->has_params = step;
+        o->bound = true;
+    } catch (...) {
+        return o->fail(DDP_ERR_NO_MEMORY, "out of host memory");
+    }
+    return DDP_OK;
+}
+
+int ddp_adamw_step(ddp_adamw* o, const ddp_adamw_args* x, void* stream) {
+    if (!o) return DDP_ERR_INVALID_ARG;
+    if (!x) return o->fail(DDP_ERR_INVALID_ARG, "args is NULL");
+    if (x->t < 1) return o->fail(DDP_ERR_INVALID_ARG, "t < 1");
+    const auto number = [](double y) { return std::isfinite(static_cast<float>(y)); };   // as the kernel has it
+    if (!(x->lr >= 0.0) || !number(x->lr)) return o->fail(DDP_ERR_INVALID_ARG, "lr is negative or not finite");
+    if (!(x->beta1 >= 0.0 && x->beta1 < 1.0) || !(x->beta2 >= 0.0 && x->beta2 < 1.0))
+        return o->fail(DDP_ERR_INVALID_ARG, "a beta is not in [0, 1)");
+    if (!(static_cast<float>(x->eps) > 0.0f) || !number(x->eps))
+        return o->fail(DDP_ERR_INVALID_ARG, "eps is not a positive number");
+    if (!(x->max_norm >= 0.0) || !number(x->max_norm))
+        return o->fail(DDP_ERR_INVALID_ARG, "max_norm is negative or not finite");
+    if ((x->max_norm > 0.0 || x->skip_nonfinite) && !x->norm)
+        return o->fail(DDP_ERR_INVALID_ARG, "max_norm and skip_nonfinite need a norm");
+    if (!o->bound || !o->has_params) return o->fail(DDP_ERR_NOT_BOUND, "no parameters are bound");
+    if (const int st = check_device(o)) return st;
+    if (o->blocks == 0) return DDP_OK;
+
+    StepParams a = {};
+    a.tensors = o->tensors;
+    a.first = o->first;
+    a.norm = x->norm;
+    a.used = x->used;
+    a.blocks = o->blocks;
+    a.S = o->S;
+    a.c.beta1 = static_cast<float>(x->beta1);
+    a.c.beta1c = static_cast<float>(1.0 - x->beta1);
+    a.c.beta2 = static_cast<float>(x->beta2);
+    a.c.beta2c = static_cast<float>(1.0 - x->beta2);
+    a.c.lr = static_cast<float>(x->lr);
+    a.c.step = static_cast<float>(x->lr / (1.0 - std::pow(x->beta1, static_cast<double>(x->t))));
+    a.c.rbc2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(x->beta2, static_cast<double>(x->t))));
+    a.c.eps = static_cast<float>(x->eps);
+    a.c.max_norm = static_cast<float>(x->max_norm);
+    a.c.clip = x->max_norm > 0.0;
+    a.c.skip_nonfinite = x->skip_nonfinite != 0;
+    a.c.seed_lo = static_cast<uint32_t>(x->seed);
+    a.c.seed_hi = static_cast<uint32_t>(x->seed >> 32);
+    int grid = 0;
+    split(o->blocks, static_cast<int64_t>(o->sms) * kStepCtasPerSm, &grid, &a.piece);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = o->bf16 ? (o->q8 ? launch(adamw_kernel<true, true>, grid, a, st)
+                                           : launch(adamw_kernel<true, false>, grid, a, st))
+                                  : (o->q8 ? launch(adamw_kernel<false, true>, grid, a, st)
+                                           : launch(adamw_kernel<false, false>, grid, a, st));
+    return e == cudaSuccess ? DDP_OK : o->cuda(e);
+}
+
+int ddp_adamw_grad_norm(ddp_adamw* o, const uint8_t* used, float* norm, void* stream) {
+    if (!o) return DDP_ERR_INVALID_ARG;
+    if (!norm) return o->fail(DDP_ERR_INVALID_ARG, "norm is NULL");
+    if (!o->bound) return o->fail(DDP_ERR_NOT_BOUND, "no gradients are bound");
+    if (const int st = check_device(o)) return st;
+    NormParams a = {};
+    a.tensors = o->tensors;
+    a.first = o->first;
+    a.used = used;
+    a.partial = o->partial;
+    a.done = o->done;
+    a.norm = norm;
+    a.blocks = o->blocks;
+    a.S = o->S;
+    int grid = 1;                    // without elements one CTA writes the zero
+    if (o->blocks) split(o->blocks, static_cast<int64_t>(o->sms) * kNormCtasPerSm, &grid, &a.piece);
+    const cudaError_t e = launch(norm_kernel, grid, a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? DDP_OK : o->cuda(e);
+}
+
+const char* ddp_adamw_last_error(const ddp_adamw* o) { return o ? o->error.c_str() : g_create_error.c_str(); }
+
+void ddp_adamw_destroy(ddp_adamw* o) {
+    if (!o) return;
+    if (o->table) cudaFree(o->table);
+    delete o;
+}
+
+}  // extern "C"

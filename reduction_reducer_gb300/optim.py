@@ -1,0 +1,169 @@
+"""AdamW over every parameter in one launch, and the gradient norm it clips by
+(the ``ddp_adamw_*`` calls of include/ddp_reducer.h).
+
+The step takes the mean gradients where a reduction left them: bucket views in
+the arena or the copied-back gradients.  Only argument marshalling happens
+here; the arithmetic is the library's kernels'.
+"""
+
+from __future__ import annotations
+
+import ctypes as C
+
+from . import _lib
+from .reducer import _ERRORS, DTYPES, DDPError, _ptr, _ptr_array, _stream
+
+BLOCK = 256             # elements that share one scale of an 8-bit moment (DDP_ADAMW_BLOCK)
+
+
+def _expect(name, v, t, numel, dtypes):
+    if t is None and numel == 0:
+        return
+    if isinstance(t, int):
+        return
+    if t is None or t.numel() != numel or not t.is_contiguous() or str(t.dtype)[6:] not in dtypes or not t.is_cuda:
+        raise ValueError(f"{name}[{v}]: expected {numel} contiguous elements of {' or '.join(dtypes)} on a GPU")
+
+
+class AdamW:
+    """One optimizer over P tensors (``ddp_adamw``)."""
+
+    def __init__(self, numel, param_dtype: str = "f32", state_bits: int = 32, lib_path: str = _lib.LIB_PATH):
+        """numel: element counts in registration order; param_dtype: "f32", or
+        "bf16" with fp32 master copies; state_bits: 32 or 8."""
+        self._h = None
+        self.lib = _lib.load(lib_path)
+        self.numel = [int(n) for n in numel]
+        self.P = len(self.numel)
+        self.param_dtype, self.state_bits = param_dtype, state_bits
+        if param_dtype not in DTYPES:
+            raise ValueError("param_dtype: expected 'f32' or 'bf16'")
+        h = C.c_void_p()
+        st = self.lib.ddp_adamw_create((C.c_int64 * max(self.P, 1))(*self.numel), self.P, DTYPES[param_dtype],
+                                       int(state_bits), C.byref(h))
+        if st != 0:
+            raise _ERRORS.get(st, DDPError)(st, self.lib.ddp_adamw_last_error(None).decode())
+        self._h = h
+        self._args = _lib.AdamWArgs()
+        self._ref = C.byref(self._args)
+
+    def _check(self, st: int):
+        if st != 0:
+            raise _ERRORS.get(st, DDPError)(st, (self.lib.ddp_adamw_last_error(self._h) or b"").decode())
+
+    # ---------------------------------------------------------------- state
+    def zero_state(self, device="cuda"):
+        """The state before the first step: keyword arguments of ``bind``
+        (exp_avg, exp_avg_sq and, with 8 bits, their scales), views of one
+        flat buffer each in which every tensor starts on a block."""
+        import torch
+        rows = [-(-n // BLOCK) for n in self.numel]
+        start, total = [], 0
+        for r in rows:
+            start.append(total)
+            total += r
+        m_kind, v_kind = ((torch.float8_e4m3fn, torch.float8_e5m2) if self.state_bits == 8
+                          else (torch.float32, torch.float32))
+
+        def views(kind):
+            flat = torch.zeros(total * BLOCK, dtype=torch.uint8 if self.state_bits == 8 else kind, device=device)
+            flat = flat.view(kind)
+            return [flat[o * BLOCK:o * BLOCK + n] for o, n in zip(start, self.numel)]
+
+        state = dict(exp_avg=views(m_kind), exp_avg_sq=views(v_kind))
+        if self.state_bits == 8:
+            for name in ("exp_avg_scale", "exp_avg_sq_scale"):
+                flat = torch.zeros(total, device=device)
+                state[name] = [flat[o:o + r] for o, r in zip(start, rows)]
+        return state
+
+    # ---------------------------------------------------------------- bind
+    def bind(self, params, grads, exp_avg, exp_avg_sq, weight_decay=0.0, master=None, exp_avg_scale=None,
+             exp_avg_sq_scale=None):
+        """Lists of P tensors (or device addresses).  grads: fp32; params:
+        param_dtype; master: fp32, with bf16 parameters; exp_avg, exp_avg_sq:
+        fp32, or with 8 bits float8_e4m3fn and float8_e5m2 (or uint8) codes
+        with fp32 scales of ceil(numel / 256) elements; weight_decay: a number
+        for all or one per tensor."""
+        bf16, eight = self.param_dtype == "bf16", self.state_bits == 8
+        want = [("grads", grads, ("float32",), False), ("params", params, ("bfloat16" if bf16 else "float32",), False),
+                ("exp_avg", exp_avg, ("float8_e4m3fn", "uint8") if eight else ("float32",), False),
+                ("exp_avg_sq", exp_avg_sq, ("float8_e5m2", "uint8") if eight else ("float32",), False)]
+        if master is not None:
+            want.append(("master", master, ("float32",), False))
+        if exp_avg_scale is not None:
+            want.append(("exp_avg_scale", exp_avg_scale, ("float32",), True))
+        if exp_avg_sq_scale is not None:
+            want.append(("exp_avg_sq_scale", exp_avg_sq_scale, ("float32",), True))
+        for name, tensors, kinds, scale in want:
+            if len(tensors) != self.P:
+                raise ValueError(f"{name}: expected {self.P} tensors")
+            for v, t in enumerate(tensors):
+                _expect(name, v, t, -(-self.numel[v] // BLOCK) if scale else self.numel[v], kinds)
+        decay = [float(weight_decay)] * self.P if isinstance(weight_decay, (int, float)) else list(weight_decay)
+        if len(decay) != self.P:
+            raise ValueError(f"weight_decay: expected one number or {self.P}")
+
+        def pointers(tensors):
+            return None if tensors is None else _ptr_array([_ptr(t) for t in tensors])
+
+        self._check(self.lib.ddp_adamw_bind(self._h, pointers(grads), pointers(params), pointers(master),
+                                            pointers(exp_avg), pointers(exp_avg_sq), pointers(exp_avg_scale),
+                                            pointers(exp_avg_sq_scale), (C.c_float * max(self.P, 1))(*decay)))
+        self._keep = (params, grads, exp_avg, exp_avg_sq, master, exp_avg_scale, exp_avg_sq_scale)
+
+    def bind_grads(self, grads):
+        """Bind the gradients alone: for ``grad_norm`` without a step."""
+        if len(grads) != self.P:
+            raise ValueError(f"grads: expected {self.P} tensors")
+        for v, t in enumerate(grads):
+            _expect("grads", v, t, self.numel[v], ("float32",))
+        self._check(self.lib.ddp_adamw_bind(self._h, _ptr_array([_ptr(t) for t in grads]), None, None, None, None,
+                                            None, None, None))
+        self._keep = (grads,)
+
+    # ---------------------------------------------------------------- calls
+    def _used(self, used):
+        if used is None or isinstance(used, int):
+            return used
+        if used.numel() != self.P or used.element_size() != 1 or not used.is_contiguous() or not used.is_cuda:
+            raise ValueError(f"used: expected {self.P} contiguous bytes or truth values on a GPU")
+        return used.data_ptr()
+
+    @staticmethod
+    def _norm(norm):
+        if norm is None or isinstance(norm, int):
+            return norm
+        if norm.numel() != 1 or str(norm.dtype) != "torch.float32" or not norm.is_cuda:
+            raise ValueError("norm: expected one fp32 element on a GPU")
+        return norm.data_ptr()
+
+    def grad_norm(self, out, used=None, stream=None):
+        """out (one fp32 element on the device) = the 2-norm of the bound
+        gradients, of the tensors whose ``used`` byte is not 0; returns out."""
+        self._check(self.lib.ddp_adamw_grad_norm(self._h, self._used(used), self._norm(out), _stream(stream)))
+        return out
+
+    def step(self, t: int, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, norm=None, max_norm: float = 0.0,
+             used=None, seed: int = 0, skip_nonfinite: bool = False, stream=None):
+        """Step number t (from 1).  norm: device fp32 the kernel clips by with
+        max_norm > 0; used: device bytes [P], tensors with 0 stay as they are;
+        seed: of the 8-bit moments' rounding, another one each step;
+        skip_nonfinite: a norm that is not finite leaves everything as it is."""
+        a = self._args
+        a.t, a.lr, a.eps, a.max_norm = t, lr, eps, max_norm
+        a.beta1, a.beta2 = betas
+        a.norm, a.used = self._norm(norm), self._used(used)
+        a.seed, a.skip_nonfinite = seed, skip_nonfinite
+        self._check(self.lib.ddp_adamw_step(self._h, self._ref, _stream(stream)))
+
+    def destroy(self):
+        if getattr(self, "_h", None):
+            self.lib.ddp_adamw_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass

@@ -1,0 +1,124 @@
+"""Routing of tokens to experts and its gradient (``ddp_route`` and
+``ddp_route_backward`` of include/ddp_reducer.h).  Only argument marshalling
+happens here; the arithmetic is the library's kernels'."""
+
+from __future__ import annotations
+
+import ctypes as C
+
+from . import _lib
+from .reducer import DDPError, _ERRORS, _stream
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+_DTYPES = {"torch.float32": _lib.DDP_F32, "torch.bfloat16": _lib.DDP_BF16}
+
+
+def _args(logits, k, score, groups, top_groups, renorm, scale):
+    dtype = _DTYPES.get(str(logits.dtype))
+    if dtype is None or logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits: expected [tokens, experts] fp32 or bf16 on a GPU, experts next to one another")
+    if score not in SCORES:
+        raise ValueError("score: expected 'softmax' or 'sigmoid'")
+    tokens, experts = logits.shape
+    return _lib.RouteArgs(tokens, max(logits.stride(0), experts) if tokens <= 1 else logits.stride(0), experts, int(k),
+                          SCORES[score], int(groups), int(groups if top_groups is None else top_groups),
+                          1 if renorm else 0, float(scale), dtype)
+
+
+def _data(name, t, shape, dtype):
+    if t is None:
+        return None
+    if tuple(t.shape) != shape or str(t.dtype) not in dtype or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: expected {list(shape)} contiguous {' or '.join(dtype)} on a GPU")
+    return t.data_ptr()
+
+
+def _check(st: int, what: str):
+    if st != 0:
+        raise _ERRORS.get(st, DDPError)(st, what)
+
+
+def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups=None, renorm: bool = False,
+          scale: float = 1.0, mask=None, counts=None, out=None, stream=None, lib_path: str = _lib.LIB_PATH):
+    """The k experts of every token and their weights: (indices int32
+    [tokens, k], weights fp32 [tokens, k]).
+
+    logits: [tokens, experts] fp32 or bf16 (rows may be strided); score:
+    "softmax" or "sigmoid"; bias: fp32 [experts], added for the choice alone;
+    groups, top_groups: only the top_groups best of `groups` equal runs of
+    experts stay (worth: the sum of their two best); renorm: weights over
+    their sum; mask: bytes or truth values [tokens], 0 = not routed (index
+    -1, weight 0); counts: int32 [experts], the tokens each expert got are
+    added to it; out: (indices, weights) to write into."""
+    import torch
+    a = _args(logits, k, score, groups, top_groups, renorm, scale)
+    shape = (a.tokens, a.k)
+    indices, weights = out if out is not None else (
+        torch.empty(shape, dtype=torch.int32, device=logits.device),
+        torch.empty(shape, dtype=torch.float32, device=logits.device))
+    _check(_lib.load(lib_path).ddp_route(
+        C.byref(a), logits.data_ptr(), _data("bias", bias, (a.experts,), ("torch.float32",)),
+        _data("mask", mask, (a.tokens,), ("torch.bool", "torch.uint8")),
+        _data("indices", indices, shape, ("torch.int32",)), _data("weights", weights, shape, ("torch.float32",)),
+        _data("counts", counts, (a.experts,), ("torch.int32",)), _stream(stream)),
+        f"ddp_route: {a.tokens} tokens, {a.experts} experts, k {a.k}, groups {a.groups}, top_groups {a.top_groups}, "
+        f"scale {a.scale}")
+    return indices, weights
+
+
+def route_backward(grad_weights, logits, indices, weights, score: str = "softmax", renorm: bool = False,
+                   scale: float = 1.0, out=None, stream=None, lib_path: str = _lib.LIB_PATH):
+    """The gradient of the logits ([tokens, experts], their dtype) from that of
+    the weights, with the indices and weights that ``route`` returned for the
+    same score, renorm and scale."""
+    import torch
+    k = indices.shape[1] if indices.dim() == 2 else 0
+    a = _args(logits, k, score, 1, 1, renorm, scale)
+    shape = (a.tokens, a.k)
+    grad = out if out is not None else torch.empty((a.tokens, a.experts), dtype=logits.dtype, device=logits.device)
+    if tuple(grad.shape) != (a.tokens, a.experts) or grad.dtype != logits.dtype or not grad.is_cuda or (
+            a.experts > 1 and grad.stride(1) != 1):
+        raise ValueError("out: expected the logits' shape and dtype, experts next to one another")
+    _check(_lib.load(lib_path).ddp_route_backward(
+        C.byref(a), logits.data_ptr(), _data("indices", indices, shape, ("torch.int32",)),
+        _data("weights", weights, shape, ("torch.float32",)),
+        _data("grad_weights", grad_weights, shape, ("torch.float32",)), grad.data_ptr(),
+        max(grad.stride(0), a.experts) if a.tokens <= 1 else grad.stride(0), _stream(stream)),
+        f"ddp_route_backward: {a.tokens} tokens, {a.experts} experts, k {a.k}, scale {a.scale}")
+    return grad
+
+
+_Routed = None     # the autograd function, made on first use (torch is imported by the calls, not by the package)
+
+
+def _autograd():
+    global _Routed
+    if _Routed is None:
+        import torch
+
+        class Routed(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, logits, k, options):
+                indices, weights = route(logits, k, **options)
+                ctx.save_for_backward(logits, indices, weights)
+                ctx.options = {n: options[n] for n in ("score", "renorm", "scale", "lib_path") if n in options}
+                ctx.mark_non_differentiable(indices)
+                return indices, weights
+
+            @staticmethod
+            def backward(ctx, _indices, grad_weights):
+                logits, indices, weights = ctx.saved_tensors
+                grad = route_backward(grad_weights.contiguous(), logits, indices, weights, **ctx.options)
+                return grad, None, None
+
+        _Routed = Routed
+    return _Routed
+
+
+def routed(logits, k: int, **options):
+    """``route`` under autograd, on the current stream: (indices, weights),
+    where the weights pass their gradient on to the logits.  Options: those of
+    ``route`` but out and stream."""
+    if "out" in options or "stream" in options:
+        raise ValueError("routed: out and stream are not options here")
+    return _autograd().apply(logits, k, options)
