@@ -16,11 +16,13 @@
 
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <new>
 #include <string>
+#include <type_traits>
 #include <vector>
 
 #include "ddp_device.cuh"
@@ -69,8 +71,10 @@ struct StepParams {
 
 // ------------------------------------------------------------------ four values
 
-__device__ __forceinline__ void load4(const float* p, int left, bool vec, float (&f)[4]) {
-    if (vec && left >= 4) {
+// Whole: four values by one access.  Else value i where i < left (left may be
+// negative), past it nothing is read and zeros are given.
+__device__ __forceinline__ void load4(const float* p, bool whole, int left, float (&f)[4]) {
+    if (whole) {
         const float4 x = __ldcs(reinterpret_cast<const float4*>(p));
         f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
     } else {
@@ -79,8 +83,8 @@ __device__ __forceinline__ void load4(const float* p, int left, bool vec, float 
     }
 }
 
-__device__ __forceinline__ void store4(float* p, int left, bool vec, const float (&f)[4]) {
-    if (vec && left >= 4) {
+__device__ __forceinline__ void store4(float* p, bool whole, int left, const float (&f)[4]) {
+    if (whole) {
         __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
     } else {
 #pragma unroll
@@ -89,8 +93,8 @@ __device__ __forceinline__ void store4(float* p, int left, bool vec, const float
     }
 }
 
-__device__ __forceinline__ uint32_t load4_code(const uint8_t* p, int left, bool vec) {
-    if (vec && left >= 4) return __ldcs(reinterpret_cast<const uint32_t*>(p));
+__device__ __forceinline__ uint32_t load4(const uint8_t* p, bool whole, int left) {
+    if (whole) return __ldcs(reinterpret_cast<const uint32_t*>(p));
     uint32_t x = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -98,8 +102,8 @@ __device__ __forceinline__ uint32_t load4_code(const uint8_t* p, int left, bool 
     return x;
 }
 
-__device__ __forceinline__ void store4_code(uint8_t* p, int left, bool vec, uint32_t x) {
-    if (vec && left >= 4) {
+__device__ __forceinline__ void store4(uint8_t* p, bool whole, int left, uint32_t x) {
+    if (whole) {
         __stcs(reinterpret_cast<uint32_t*>(p), x);
     } else {
 #pragma unroll
@@ -108,49 +112,62 @@ __device__ __forceinline__ void store4_code(uint8_t* p, int left, bool vec, uint
     }
 }
 
-// fp32 -> bf16 bits, round to nearest even, as the high half of a word.
-__device__ __forceinline__ uint32_t bf16_bits(float x) { return __float_as_uint(ddpk::dev::round_bf16(x)) >> 16; }
+// Two fp32 -> two bf16, round to nearest even, the first in the low half.
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    uint32_t x;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(hi), "f"(lo));
+    return x;
+}
 
-__device__ __forceinline__ void store4_bf16(uint16_t* p, int left, bool vec, const float (&f)[4]) {
-    if (vec && left >= 4) {
-        __stcs(reinterpret_cast<uint2*>(p), make_uint2(bf16_bits(f[0]) | bf16_bits(f[1]) << 16,
-                                                       bf16_bits(f[2]) | bf16_bits(f[3]) << 16));
+__device__ __forceinline__ void store4(uint16_t* p, bool whole, int left, const float (&f)[4]) {
+    const uint32_t x[2] = {bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3])};
+    if (whole) {
+        __stcs(reinterpret_cast<uint2*>(p), make_uint2(x[0], x[1]));
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (i < left) p[i] = static_cast<uint16_t>(bf16_bits(f[i]));
+            if (i < left) p[i] = static_cast<uint16_t>(x[i / 2] >> (16 * (i % 2)));
     }
 }
 
 // ------------------------------------------------------------------ 8-bit moments
 
-// Value of an e4m3 / e5m2 code (never an infinity or NaN code): its exponent
-// and mantissa bits, put in an fp32 pattern's place, are the value times
-// 2^(bias - 127), subnormals included.
-__device__ __forceinline__ float e4m3_value(uint32_t c) {
-    const float x = __fmul_rn(__uint_as_float((c & 0x7fu) << 20), 0x1p120f);
-    return __uint_as_float(__float_as_uint(x) | (c & 0x80u) << 24);
+// Four e4m3 codes -> their values, by way of fp16, which holds them exactly.
+__device__ __forceinline__ void e4m3_values(uint32_t c, float (&f)[4]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        asm("{\n\t.reg .b16 c, a, b;\n\t.reg .b32 p;\n\t"
+            "cvt.u16.u32 c, %2;\n\tcvt.rn.f16x2.e4m3x2 p, c;\n\tmov.b32 {a, b}, p;\n\t"
+            "cvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+            : "=f"(f[2 * h]), "=f"(f[2 * h + 1]) : "r"(c >> (16 * h)));
+    }
 }
 
-__device__ __forceinline__ float e5m2_value(uint32_t c) {
-    return __fmul_rn(__uint_as_float((c & 0x7fu) << 21), 0x1p112f);
+// Four e5m2 codes -> their values: a code is the upper byte of an fp16.
+__device__ __forceinline__ void e5m2_values(uint32_t c, float (&f)[4]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+            : "=f"(f[2 * h]), "=f"(f[2 * h + 1]) : "r"(__byte_perm(c, 0, h ? 0x3424 : 0x1404)));
+    }
 }
 
-// Codes of |x| / scale, given y = |x| / scale and 16 random bits r, rounded up
-// with the probability of the rest: for normal numbers the random bits are
-// added below the kept mantissa bits; below them the spacing is 2^-9 (2^-16),
-// where floor(y / spacing + r / 2^16) continues the same code sequence.
+// Codes of y = |x| / scale with 16 random bits r, rounded up with the
+// probability of the rest: r is added where the dropped mantissa bits begin
+// and the rest cut off.  A number below the least normal one (2^-6, 2^-14) is
+// first moved up by it, rounding down: it then has the exponent whose spacing
+// the subnormal codes have, 8 (4) codes higher.
 __device__ __forceinline__ uint32_t e4m3_code(float y, uint32_t r) {
-    const uint32_t normal = ((__float_as_uint(y) + (r << 4)) >> 20) - 960u;
-    const uint32_t small = static_cast<uint32_t>(__fmaf_rn(y, 512.0f, __uint2float_rn(r) * 0x1p-16f));
-    return min(y < 0x1p-6f ? small : normal, 126u);
+    const bool small = y < 0x1p-6f;
+    const float z = small ? __fadd_rd(y, 0x1p-6f) : y;
+    return min(((__float_as_uint(z) + (r << 4)) >> 20) - (small ? 968u : 960u), 126u);
 }
 
 __device__ __forceinline__ uint32_t e5m2_code(float y, uint32_t r) {
-    const uint32_t normal = ((__float_as_uint(y) + (r << 5)) >> 21) - 448u;
-    const uint32_t small = static_cast<uint32_t>(__fmaf_rn(y, 65536.0f, __uint2float_rn(r) * 0x1p-16f));
-    const uint32_t c = min(y < 0x1p-14f ? small : normal, 123u);
-    return y > 0.0f ? max(c, 1u) : c;      // m / (sqrt(v) + eps) must not meet a v rounded to zero
+    const bool small = y < 0x1p-14f;
+    const float z = small ? __fadd_rd(y, 0x1p-14f) : y;
+    const uint32_t c = min(((__float_as_uint(z) + (r << 5)) >> 21) - (small ? 452u : 448u), 123u);
+    return max(c, min(__float_as_uint(y), 1u));   // m / (sqrt(v) + eps) must not meet a v rounded to zero
 }
 
 // The scale of a block whose largest magnitude has the bits `peak`.
@@ -186,9 +203,13 @@ __device__ __forceinline__ void moments(const Scalars& c, float g, float& m, flo
     v = __fadd_rn(__fmul_rn(v, c.beta2), __fmul_rn(__fmul_rn(g, g), c.beta2c));
 }
 
+// The hardware's root and reciprocal (1 ulp each): w' is rounded to far less
+// than the 2^-24 of w that an update of lr w can show.  Subnormal v count as 0.
 __device__ __forceinline__ float weight(const Scalars& c, float keep, float w, float m, float v) {
-    const float denom = __fadd_rn(__fmul_rn(__fsqrt_rn(v), c.rbc2), c.eps);
-    return __fsub_rn(__fmul_rn(w, keep), __fdiv_rn(__fmul_rn(c.step, m), denom));
+    float root, over;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(v));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(over) : "f"(__fmaf_rn(root, c.rbc2, c.eps)));
+    return __fmaf_rn(-__fmul_rn(c.step, m), over, __fmul_rn(w, keep));
 }
 
 template <bool BF16, bool Q8>
@@ -219,34 +240,43 @@ adamw_kernel(const __grid_constant__ StepParams a) {
         const long long j = b - __ldg(a.first + s);          // block of the tensor
         const long long rest = t.n - j * kBlock;
         const int left = static_cast<int>(min(rest, static_cast<long long>(kBlock)));
-        const bool vec = t.vec, vec_g = t.vec_g;
+        const bool whole = t.vec && left == kBlock, whole_g = t.vec_g && left == kBlock;
         const float keep = __fsub_rn(1.0f, __fmul_rn(a.c.lr, t.wd));
-        float* const w_ptr = BF16 ? t.master : static_cast<float*>(t.p);
+        const long long i = j * kBlock + 4 * lane;           // this lane's first element, and how many are left from it
+        const int more = left - 4 * lane;
+        const float* const g_ptr = t.g + i;
+        float* const w_ptr = (BF16 ? t.master : static_cast<float*>(t.p)) + i;
+        using State = typename std::conditional<Q8, uint8_t, float>::type;
+        State* const m_ptr = static_cast<State*>(t.m) + i;
+        State* const v_ptr = static_cast<State*>(t.v) + i;
         float g[2][4], w[2][4], m[2][4], v[2][4];
         uint32_t mc[2], vc[2];
+        float ms = 0.0f, vs = 0.0f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int e = 128 * h + 4 * lane;
-            const long long i = j * kBlock + e;
-            load4(t.g + i, left - e, vec_g, g[h]);
-            load4(w_ptr + i, left - e, vec, w[h]);
+            load4(g_ptr + 128 * h, whole_g, more - 128 * h, g[h]);
+            load4(w_ptr + 128 * h, whole, more - 128 * h, w[h]);
             if constexpr (Q8) {
-                mc[h] = load4_code(static_cast<const uint8_t*>(t.m) + i, left - e, vec);
-                vc[h] = load4_code(static_cast<const uint8_t*>(t.v) + i, left - e, vec);
+                mc[h] = load4(m_ptr + 128 * h, whole, more - 128 * h);
+                vc[h] = load4(v_ptr + 128 * h, whole, more - 128 * h);
             } else {
-                load4(static_cast<const float*>(t.m) + i, left - e, vec, m[h]);
-                load4(static_cast<const float*>(t.v) + i, left - e, vec, v[h]);
+                load4(m_ptr + 128 * h, whole, more - 128 * h, m[h]);
+                load4(v_ptr + 128 * h, whole, more - 128 * h, v[h]);
             }
         }
         if constexpr (Q8) {
-            const float ms = t.ms[j], vs = t.vs[j];
+            ms = t.ms[j];
+            vs = t.vs[j];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h) {
+                e4m3_values(mc[h], m[h]);
+                e5m2_values(vc[h], v[h]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    m[h][q] = __fmul_rn(e4m3_value(mc[h] >> (8 * q)), ms);
-                    v[h][q] = __fmul_rn(e5m2_value(vc[h] >> (8 * q)), vs);
+                    m[h][q] = __fmul_rn(m[h][q], ms);
+                    v[h][q] = __fmul_rn(v[h][q], vs);
                 }
+            }
         }
         uint32_t peak_m = 0, peak_v = 0;
 #pragma unroll
@@ -257,29 +287,29 @@ adamw_kernel(const __grid_constant__ StepParams a) {
                 w[h][q] = weight(a.c, keep, w[h][q], m[h][q], v[h][q]);
                 if constexpr (Q8) {
                     // magnitudes compare as their bits, NaN above infinity;
-                    // what lies past the tensor's end does not count
-                    const bool in = 128 * h + 4 * lane + q < left;
-                    peak_m = max(peak_m, in ? __float_as_uint(m[h][q]) & 0x7fffffffu : 0u);
-                    peak_v = max(peak_v, in ? __float_as_uint(v[h][q]) & 0x7fffffffu : 0u);
+                    // past the tensor's end both moments are zero
+                    peak_m = max(peak_m, __float_as_uint(m[h][q]) & 0x7fffffffu);
+                    peak_v = max(peak_v, __float_as_uint(v[h][q]) & 0x7fffffffu);
                 }
             }
         if constexpr (Q8) {
-            const float ms = block_scale(__reduce_max_sync(0xffffffffu, peak_m), 1.0f / 448.0f);
-            const float vs = block_scale(__reduce_max_sync(0xffffffffu, peak_v), 1.0f / 57344.0f);
+            ms = block_scale(__reduce_max_sync(0xffffffffu, peak_m), 1.0f / 448.0f);
+            vs = block_scale(__reduce_max_sync(0xffffffffu, peak_v), 1.0f / 57344.0f);
             const float mi = ms > 0.0f ? __fdiv_rn(1.0f, ms) : 0.0f;
             const float vi = vs > 0.0f ? __fdiv_rn(1.0f, vs) : 0.0f;
-            const uint32_t key = block_key(a.c, b);
+            const uint32_t key = block_key(a.c, b) + static_cast<uint32_t>(4 * lane) * 0x9E3779B9u;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                mc[h] = vc[h] = 0;
+                uint32_t x[4], y[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const uint32_t r = random_bits(key, 128 * h + 4 * lane + q);
-                    const uint32_t x = e4m3_code(__fmul_rn(fabsf(m[h][q]), mi), r >> 16) |
-                                       (__float_as_uint(m[h][q]) >> 24 & 0x80u);
-                    mc[h] |= x << (8 * q);
-                    vc[h] |= e5m2_code(__fmul_rn(v[h][q], vi), r & 0xffffu) << (8 * q);
+                    const uint32_t r = random_bits(key, 128 * h + q);
+                    x[q] = e4m3_code(__fmul_rn(fabsf(m[h][q]), mi), r >> 16) |
+                           (__float_as_uint(m[h][q]) >> 24 & 0x80u);
+                    y[q] = e5m2_code(__fmul_rn(v[h][q], vi), r & 0xffffu);
                 }
+                mc[h] = __byte_perm(__byte_perm(x[0], x[1], 0x0040), __byte_perm(x[2], x[3], 0x0040), 0x5410);
+                vc[h] = __byte_perm(__byte_perm(y[0], y[1], 0x0040), __byte_perm(y[2], y[3], 0x0040), 0x5410);
             }
             if (lane == 0) {
                 t.ms[j] = ms;
@@ -288,16 +318,14 @@ adamw_kernel(const __grid_constant__ StepParams a) {
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int e = 128 * h + 4 * lane;
-            const long long i = j * kBlock + e;
-            store4(w_ptr + i, left - e, vec, w[h]);
-            if constexpr (BF16) store4_bf16(static_cast<uint16_t*>(t.p) + i, left - e, vec, w[h]);
+            store4(w_ptr + 128 * h, whole, more - 128 * h, w[h]);
+            if constexpr (BF16) store4(static_cast<uint16_t*>(t.p) + i + 128 * h, whole, more - 128 * h, w[h]);
             if constexpr (Q8) {
-                store4_code(static_cast<uint8_t*>(t.m) + i, left - e, vec, mc[h]);
-                store4_code(static_cast<uint8_t*>(t.v) + i, left - e, vec, vc[h]);
+                store4(m_ptr + 128 * h, whole, more - 128 * h, mc[h]);
+                store4(v_ptr + 128 * h, whole, more - 128 * h, vc[h]);
             } else {
-                store4(static_cast<float*>(t.m) + i, left - e, vec, m[h]);
-                store4(static_cast<float*>(t.v) + i, left - e, vec, v[h]);
+                store4(m_ptr + 128 * h, whole, more - 128 * h, m[h]);
+                store4(v_ptr + 128 * h, whole, more - 128 * h, v[h]);
             }
         }
     }
@@ -351,7 +379,7 @@ norm_kernel(const __grid_constant__ NormParams a) {
         for (int h = 0; h < 2; ++h) {
             float g[4];
             const int e = 128 * h + 4 * lane;
-            load4(t.g + j * kBlock + e, left - e, t.vec_g, g);
+            load4(t.g + j * kBlock + e, t.vec_g && left == kBlock, left - e, g);
 #pragma unroll
             for (int q = 0; q < 4; ++q) part = __fmaf_rn(g[q], g[q], part);
         }
@@ -570,8 +598,8 @@ int ddp_adamw_step(ddp_adamw* o, const ddp_adamw_args* x, void* stream) {
     if (!(x->lr >= 0.0) || !number(x->lr)) return o->fail(DDP_ERR_INVALID_ARG, "lr is negative or not finite");
     if (!(x->beta1 >= 0.0 && x->beta1 < 1.0) || !(x->beta2 >= 0.0 && x->beta2 < 1.0))
         return o->fail(DDP_ERR_INVALID_ARG, "a beta is not in [0, 1)");
-    if (!(static_cast<float>(x->eps) > 0.0f) || !number(x->eps))
-        return o->fail(DDP_ERR_INVALID_ARG, "eps is not a positive number");
+    if (!(static_cast<float>(x->eps) >= FLT_MIN) || !number(x->eps))
+        return o->fail(DDP_ERR_INVALID_ARG, "eps is not a positive (normal fp32) number");
     if (!(x->max_norm >= 0.0) || !number(x->max_norm))
         return o->fail(DDP_ERR_INVALID_ARG, "max_norm is negative or not finite");
     if ((x->max_norm > 0.0 || x->skip_nonfinite) && !x->norm)
