@@ -421,7 +421,7 @@ int ddp_adamw_create(const int64_t* numel, int32_t P, ddp_dtype param_dtype, int
  *                     ceil(numel[v] / DDP_ADAMW_BLOCK) each, else NULL
  *   weight_decay      host array [P] of wd_v >= 0, or NULL (none)
  * Any element alignment is correct; tensors whose addresses are 16-byte
- * aligned (4-byte for 8-bit codes) are read and written in vectors.
+ * aligned are read and written in vectors.
  * Zero-filled moments and scales are the state before the first step.
  * Synchronous; builds a device table (library-owned, freed by
  * ddp_adamw_destroy or the next bind) on the current device, which later calls
