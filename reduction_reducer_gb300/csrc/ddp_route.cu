@@ -1,12 +1,19 @@
 // Routing of tokens to experts and its gradient.
 //
-// One warp serves a token.  Lane l holds EPL consecutive experts (EPL * 32 >=
-// E), so that the lowest lane of those that tie is also the lowest expert.
-// The choice goes by 32-bit keys that compare as the numbers do; 0 is "never":
-// the k best are found one after another by a warp-wide maximum of the lanes'
-// own best keys and a ballot.  Scores are computed where they are compared; of
-// the chosen experts each is computed again by a lane of its own, which then
-// also holds the slot's index and weight.
+// A token's experts lie EPL to a lane over LPT lanes, so a warp holds 32 / LPT
+// tokens; a group's experts start on a lane of their own (its last lanes may be
+// partly empty) and take a power of two of lanes.  The choice goes by 32-bit
+// keys: 23 bits of the compared value above 9 bits of 511 - expert, so no two
+// are equal, the larger key is the better expert, and ties of the value go to
+// the lowest expert.  Each lane sorts its keys once; the k best of a token are
+// then the largest of the lanes' first keys, k times over.
+//
+// 23 bits, and scores from the hardware's approximate exponential and
+// reciprocal, do not always tell which of two experts the fp32 definition puts
+// first: where two values that the choice told apart are nearer than the
+// errors of both, or a logit or bias is not an ordinary number, the
+// token is chosen again by the definition itself (choose_exact).  The scores
+// of the chosen experts are always computed by the definition.
 
 #include "ddp_reducer.h"
 
@@ -19,10 +26,19 @@
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxExperts = 512;
+constexpr int kMaxSlots = 256;           // slots of a warp's tokens at once
 constexpr unsigned kAll = 0xffffffffu;
+
+// Least distance, in units of 2^-21 (the keys' step), of two values whose
+// order is certain.  A sigmoid score plus bias is within 0.9e-6 of the fp32
+// definition's (approximate exponential 2^-22, reciprocal 2^-23, each weighed
+// by the sigmoid's slope; the definition's own roundings; the key's), so two
+// are certain 3.8 units apart, and sums of two 8.6.  A softmax score has the
+// relative errors of two sums of up to 512 terms as well: 12.6 and 26 units.
+constexpr uint32_t kMarginSoftmax = 24, kMarginSigmoid = 6;
 
 struct RouteParams {
     const void* logits;
@@ -37,6 +53,12 @@ struct RouteParams {
     int E, k, groups, top_groups;
     int softmax, renorm;
     float scale;
+    int group_slots;             // slots of a group: a multiple of EPL, over it a power of two
+    int reps;                    // forward: rounds of 32 / LPT tokens before their slots are weighed
+    int fits;                    // forward: the groups fit the lanes' slots (else every token is chosen exactly)
+    int vec;                     // rows start 16-byte aligned (chosen-only backward: the gradient's, next to one another)
+    int row_tokens;              // chosen-only backward: tokens of a warp at once
+    int slot_lanes;              // chosen-only backward: lanes of a token, a power of two >= k
 };
 
 __device__ __forceinline__ float widen(float x) { return x; }
@@ -48,154 +70,364 @@ template <> __device__ __forceinline__ uint16_t narrow<uint16_t>(float x) {
 }
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+__device__ __forceinline__ float nan_value() { return __int_as_float(0x7fffffff); }
 
 // A key that orders like the number (-0 equal to +0); 0 for -inf and NaN.
-__device__ __forceinline__ uint32_t key_of(float x) {
-    if (!(x > neg_inf())) return 0;
+__device__ __forceinline__ uint32_t order_bits(float x) {
     const uint32_t b = __float_as_uint(x + 0.0f);
-    return b ^ (static_cast<int>(b) < 0 ? 0xffffffffu : 0x80000000u);
+    return b ^ (static_cast<uint32_t>(static_cast<int>(b) >> 31) | 0x80000000u);
 }
+
+__device__ __forceinline__ uint32_t key_of(float x) { return x > neg_inf() ? order_bits(x) : 0u; }
 
 __device__ __forceinline__ float number_of(uint32_t key) {
     return key == 0 ? neg_inf() : __uint_as_float(key ^ (key & 0x80000000u ? 0x80000000u : 0xffffffffu));
 }
 
-__device__ __forceinline__ float warp_sum(float x) {
+// Over a token's LPT lanes.
+template <int LPT>
+__device__ __forceinline__ uint32_t token_max(uint32_t x) {
+    if constexpr (LPT == 32) {
+        return __reduce_max_sync(kAll, x);
+    } else {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
+        for (int o = LPT / 2; o; o >>= 1) x = max(x, __shfl_xor_sync(kAll, x, o));
+        return x;
+    }
+}
+
+template <int LPT>
+__device__ __forceinline__ float token_sum(float x) {
+#pragma unroll
+    for (int o = LPT / 2; o; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
     return x;
 }
 
 __device__ __forceinline__ float sigmoid(float x) { return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-x))); }
 
-// Largest number and sum of exponentials of a row (its NaN and -inf left out).
+__device__ __forceinline__ float fast_exp(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    return y;
+}
+
+__device__ __forceinline__ float fast_sigmoid(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + fast_exp(-x)));
+    return y;
+}
+
+// A lane's experts of a row: n consecutive ones from `from` (n <= EPL); the
+// rest are `fill`.
+template <int EPL, typename T>
+__device__ __forceinline__ void load_lane(const T* from, int n, bool vec, float fill, float (&x)[EPL]) {
+    if (vec && n == EPL) {
+        constexpr int V = 16 / sizeof(T);
+        using Raw = typename ddpk::dev::Vec<T>::Raw;
+#pragma unroll
+        for (int c = 0; c < EPL / V; ++c) {
+            float f[V];
+            ddpk::dev::Vec<T>::unpack(__ldg(reinterpret_cast<const Raw*>(from) + c), f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[c * V + i] = f[i];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) x[j] = j < n ? widen(from[j]) : fill;
+    }
+}
+
 template <int EPL>
-__device__ __forceinline__ void softmax_stats(const float (&x)[EPL], float& top, float& sum) {
-    uint32_t best = 0;
+__device__ __forceinline__ void store_lane(float* to, int n, bool vec, const float (&d)[EPL]) {
+    if (vec && n == EPL) {
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) best = max(best, key_of(x[j]));
-    top = number_of(__reduce_max_sync(kAll, best));
-    float part = 0.0f;
+        for (int c = 0; c < EPL; c += 4) ddpk::dev::st_stream(to + c, make_float4(d[c], d[c + 1], d[c + 2], d[c + 3]));
+    } else {
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) part += x[j] > neg_inf() ? expf(x[j] - top) : 0.0f;
-    sum = warp_sum(part);
+        for (int j = 0; j < EPL; ++j)
+            if (j < n) to[j] = d[j];
+    }
 }
 
-template <int EPL, typename T>
-__device__ __forceinline__ void load_row(const T* row, int E, float (&x)[EPL]) {
-    const int e0 = (threadIdx.x & 31) * EPL;
+template <int EPL>
+__device__ __forceinline__ void store_lane(uint16_t* to, int n, bool vec, const float (&d)[EPL]) {
+    uint32_t x[EPL / 2];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) x[j] = e0 + j < E ? widen(row[e0 + j]) : neg_inf();
+    for (int j = 0; j < EPL; j += 2)
+        x[j / 2] = narrow<uint16_t>(d[j]) | static_cast<uint32_t>(narrow<uint16_t>(d[j + 1])) << 16;
+    if (vec && n == EPL) {
+#pragma unroll
+        for (int c = 0; c < EPL / 2; c += 4)
+            __stcs(reinterpret_cast<uint4*>(to) + c / 4, make_uint4(x[c], x[c + 1], x[c + 2], x[c + 3]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            if (j < n) to[j] = static_cast<uint16_t>(x[j / 2] >> (16 * (j % 2)));
+    }
 }
 
-template <int EPL, typename T>
+// Descending order (Batcher's odd-even merge sort, unrolled).
+template <int N>
+__device__ __forceinline__ void sort_down(uint32_t (&x)[N]) {
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int d = p; d >= 1; d /= 2)
+#pragma unroll
+            for (int j = d % p; j + d < N; j += 2 * d)
+#pragma unroll
+                for (int i = 0; i < d; ++i)
+                    if (i + j + d < N && (i + j) / (2 * p) == (i + j + d) / (2 * p)) {
+                        const uint32_t a = x[i + j], b = x[i + j + d];
+                        x[i + j] = max(a, b);
+                        x[i + j + d] = min(a, b);
+                    }
+}
+
+// What the scores of a token's slots are computed from.
+struct Stat {
+    float top, sum;    // softmax
+    int bad;           // every weight is NaN
+};
+
+struct WarpRows {
+    float c[kMaxExperts];        // choose_exact: what the choice goes by
+    int32_t sel[kMaxSlots];
+    float score[kMaxSlots];
+    Stat stat[32];
+};
+
+// One token's choice by the fp32 definition, by a whole warp.
+template <typename T>
+__device__ __noinline__ void choose_exact(const RouteParams& a, const T* row, float* c, int32_t* sel, Stat* stat) {
+    const int lane = threadIdx.x & 31;
+    const int E = a.E;
+    const bool by_logit = !a.bias && a.groups == 1;
+    bool bad = false;
+    uint32_t most = 0;
+    for (int e = lane; e < E; e += 32) {
+        const float x = widen(row[e]);
+        bad |= !(x == x) || (a.softmax && x == -neg_inf());
+        most = max(most, key_of(x));
+    }
+    bad = __any_sync(kAll, bad);
+    float top = 0.0f, sum = 1.0f;
+    if (a.softmax) {
+        top = number_of(__reduce_max_sync(kAll, most));
+        float part = 0.0f;
+        for (int e = lane; e < E; e += 32) {
+            const float x = widen(row[e]);
+            if (x > neg_inf()) part += expf(x - top);
+        }
+        sum = token_sum<32>(part);
+    }
+    for (int e = lane; e < E; e += 32) {
+        const float x = widen(row[e]);
+        float y = x;
+        if (!by_logit) {
+            y = a.softmax ? __fdiv_rn(expf(x - top), sum) : sigmoid(x);
+            if (a.bias) y = __fadd_rn(y, a.bias[e]);
+        }
+        c[e] = x > neg_inf() && y > neg_inf() ? y + 0.0f : neg_inf();
+    }
+    __syncwarp();
+    if (a.groups > 1) {
+        const int size = E / a.groups;
+        uint32_t worth = 0;
+        if (lane < a.groups) {           // lane g: group g
+            float a1 = neg_inf(), a2 = neg_inf();
+            for (int i = 0; i < size; ++i) {
+                const float y = c[lane * size + i];
+                a2 = fmaxf(a2, fminf(a1, y));
+                a1 = fmaxf(a1, y);
+            }
+            worth = max(key_of(size > 1 ? __fadd_rn(a1, a2) : a1), 1u);
+        }
+        unsigned stay = 0;
+        for (int r = 0; r < a.top_groups; ++r) {
+            const uint32_t best = __reduce_max_sync(kAll, worth);
+            const int g = __ffs(__ballot_sync(kAll, worth == best)) - 1;
+            stay |= 1u << g;
+            if (lane == g) worth = 0;
+        }
+        __syncwarp();
+        for (int e = lane; e < E; e += 32)
+            if (!(stay >> (e / size) & 1)) c[e] = neg_inf();
+        __syncwarp();
+    }
+    for (int r = 0; r < a.k; ++r) {
+        uint32_t mine = 0;
+        int at = E;
+        for (int e = lane; e < E; e += 32) {
+            const uint32_t key = key_of(c[e]);
+            if (key > mine) { mine = key; at = e; }
+        }
+        const uint32_t best = __reduce_max_sync(kAll, mine);
+        const int chosen = __reduce_min_sync(kAll, best && mine == best ? at : E);
+        if (lane == 0) sel[r] = chosen < E ? chosen : -1;
+        if (lane == (chosen & 31) && chosen < E) c[chosen] = neg_inf();
+        __syncwarp();
+    }
+    if (lane == 0) *stat = Stat{top, sum, bad};
+    __syncwarp();
+}
+
+template <int LPT, int EPL, typename T>
 __global__ void __launch_bounds__(kThreads)
 route_kernel(const __grid_constant__ RouteParams a) {
+    constexpr int kTokens = 32 / LPT;     // of a warp
     __shared__ int hist[kMaxExperts];
-    __shared__ float rows[kWarps][EPL * 32];
+    __shared__ WarpRows rows[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int l = lane % LPT, tl = lane / LPT;
     const int E = a.E, k = a.k;
+    WarpRows& mem = rows[warp];
     if (a.counts)
         for (int i = threadIdx.x; i < E; i += kThreads) hist[i] = 0;
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
     __syncthreads();
 
-    float bias[EPL];
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) bias[j] = a.bias && lane * EPL + j < E ? a.bias[lane * EPL + j] : 0.0f;
+    // this lane's experts: n from e0 on, of group g
+    const int size = E / a.groups, group_lanes = a.group_slots / EPL;
+    const int g = l * EPL / a.group_slots, off = l * EPL % a.group_slots;
+    const int e0 = g * size + off;
+    const int n = g < a.groups ? max(0, min(size - off, EPL)) : 0;
     const bool by_logit = !a.bias && a.groups == 1;
+    const bool vec = a.vec && (e0 * sizeof(T)) % 16 == 0;
+    float bias[EPL];
+    bool plain = true;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+        bias[j] = a.bias && j < n ? a.bias[e0 + j] : 0.0f;
+        plain = plain && bias[j] >= -1.9f && bias[j] <= 0.9f;     // the keys' range is scores + bias in [-2, 2)
+    }
+    const bool fast = a.fits && __all_sync(kAll, plain);
+    const uint32_t by_score = a.softmax ? kMarginSoftmax : kMarginSigmoid;
+    const uint32_t margin = !by_logit ? by_score : sizeof(T) == 2 ? 0u : 1u;   // a key holds all of a bf16 logit
+    const bool need_sum = a.softmax && (!a.renorm || !by_logit);
 
-    for (long long t = static_cast<long long>(blockIdx.x) * kWarps + warp; t < a.tokens;
-         t += static_cast<long long>(gridDim.x) * kWarps) {
-        int index = -1;               // lane r: slot r
-        float score = 0.0f;
-        bool bad = false;
-        if (!a.mask || a.mask[t]) {
+    const int tile = kTokens * a.reps;
+    for (long long t0 = (static_cast<long long>(blockIdx.x) * kWarps + warp) * tile; t0 < a.tokens;
+         t0 += static_cast<long long>(gridDim.x) * kWarps * tile) {
+        for (int rep = 0; rep < a.reps; ++rep) {
+            const int slot = rep * kTokens + tl;                  // the token's place in the tile
+            const long long t = t0 + slot;
+            const bool on = t < a.tokens && (!a.mask || a.mask[t]);
             const T* row = static_cast<const T*>(a.logits) + t * a.stride;
-            float x[EPL];
-            uint32_t key[EPL];
-            load_row<EPL>(row, E, x);
-            float top = 0.0f, sum = 1.0f;
+            int32_t* sel = mem.sel + slot * k;
+            bool again = on;                                      // choose exactly
+            if (fast) {
+                float x[EPL];
+                uint32_t key[EPL];
+                load_lane<EPL>(row + e0, on ? n : 0, vec, 0.0f, x);
+                float zero = 0.0f;                                // NaN where a logit is not finite
 #pragma unroll
-            for (int j = 0; j < EPL; ++j)
-                bad |= !(x[j] == x[j]) || (a.softmax && x[j] == -neg_inf());
-            bad = __any_sync(kAll, bad);
-            if (a.softmax) softmax_stats<EPL>(x, top, sum);
+                for (int j = 0; j < EPL; ++j) zero = fmaf(x[j], 0.0f, zero);
+                again = !(zero == 0.0f);
+                float top = 0.0f, sum = 1.0f, over = 1.0f;
+                if (a.softmax) {
+                    uint32_t most = 0;
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) {
-                float c = x[j];
-                if (!by_logit) {
-                    const float s = a.softmax ? __fdiv_rn(expf(x[j] - top), sum) : sigmoid(x[j]);
-                    c = __fadd_rn(s, bias[j]);
+                    for (int j = 0; j < EPL; ++j) most = max(most, j < n ? order_bits(x[j]) : 0u);
+                    top = number_of(token_max<LPT>(most));
                 }
-                key[j] = x[j] > neg_inf() ? key_of(c) : 0u;
-            }
-
-            if (a.groups > 1) {
-                // lane g: the worth of group g, then whether it stays
-                const int size = E / a.groups;
-                float* c = rows[warp];
+                if (need_sum) {
+                    sum = 0.0f;
 #pragma unroll
-                for (int j = 0; j < EPL; ++j) c[lane * EPL + j] = number_of(key[j]);
-                __syncwarp();
-                uint32_t worth = 0;
-                if (lane < a.groups) {
-                    float a1 = neg_inf(), a2 = neg_inf();
-                    for (int i = 0; i < size; ++i) {
-                        const float y = c[lane * size + i];
-                        a2 = fmaxf(a2, fminf(a1, y));
-                        a1 = fmaxf(a1, y);
-                    }
-                    worth = max(key_of(size > 1 ? __fadd_rn(a1, a2) : a1), 1u);
-                }
-                __syncwarp();
-                unsigned stay = 0;
-                for (int r = 0; r < a.top_groups; ++r) {
-                    const uint32_t best = __reduce_max_sync(kAll, worth);
-                    const int g = __ffs(__ballot_sync(kAll, worth == best)) - 1;
-                    stay |= 1u << g;
-                    if (lane == g) worth = 0;
+                    for (int j = 0; j < EPL; ++j) sum += j < n ? fast_exp(x[j] - top) : 0.0f;
+                    sum = token_sum<LPT>(sum);
+                    over = __fdividef(1.0f, sum);
                 }
 #pragma unroll
                 for (int j = 0; j < EPL; ++j) {
-                    const int e = lane * EPL + j;
-                    if (e < E && !(stay >> (e / size) & 1)) key[j] = 0;
+                    const uint32_t place = kMaxExperts - 1 - (e0 + j);
+                    if (by_logit) {
+                        key[j] = (order_bits(x[j]) & ~0x1ffu) | place;
+                    } else {
+                        // 6 + c lies in [4, 8), where fp32 has steps of 2^-21; the exponent is shifted out
+                        const float c = (a.softmax ? fast_exp(x[j] - top) * over : fast_sigmoid(x[j])) + bias[j];
+                        key[j] = __float_as_uint(c + 6.0f) * 512u + place;
+                    }
+                    if (!on || j >= n) key[j] = 0;
                 }
-            }
+                sort_down(key);
 
-            for (int r = 0; r < k; ++r) {
-                uint32_t mine = 0;
-                int at = 0;
+                if (a.top_groups < a.groups) {
+                    uint32_t a1 = key[0] >> 9, a2 = EPL > 1 ? key[1] >> 9 : 0u;
+                    for (int o = 1; o < group_lanes; o *= 2) {
+                        const uint32_t b1 = __shfl_xor_sync(kAll, a1, o), b2 = __shfl_xor_sync(kAll, a2, o);
+                        a2 = max(min(a1, b1), max(a2, b2));
+                        a1 = max(a1, b1);
+                    }
+                    const uint32_t worth = g < a.groups ? (a1 + a2) << 5 | static_cast<uint32_t>(31 - g) : 0u;
+                    int better = 0;
+                    for (int h = 0; h < a.groups; ++h)
+                        better += __shfl_sync(kAll, worth, tl * LPT + h * group_lanes) > worth;
+                    const bool stays = better < a.top_groups && g < a.groups;
+                    // the least worth that stays against the largest that does not
+                    const uint32_t least = ~token_max<LPT>(stays ? ~worth : 0u) >> 5;
+                    const uint32_t most = token_max<LPT>(stays ? 0u : worth) >> 5;
+                    again |= least - most < 2 * by_score;
+                    if (!stays) key[0] = 0;
+                }
+
+                uint32_t last = 0xffffffffu;
+                for (int r = 0; r <= k; ++r) {
+                    const uint32_t best = token_max<LPT>(key[0]);
+                    again |= best && (last >> 9) - (best >> 9) < margin;
+                    last = best;
+                    if (r == k) break;
+                    if (l == 0) sel[r] = best ? kMaxExperts - 1 - static_cast<int>(best & 0x1ffu) : -1;
+                    const bool mine = key[0] == best;
 #pragma unroll
-                for (int j = EPL - 1; j >= 0; --j)
-                    if (key[j] >= mine) { mine = key[j]; at = j; }
-                const uint32_t best = __reduce_max_sync(kAll, mine);
-                if (best == 0) break;
-                const int from = __ffs(__ballot_sync(kAll, mine == best)) - 1;
-                const int chosen = __shfl_sync(kAll, lane * EPL + at, from);
-                if (lane == r) index = chosen;
-#pragma unroll
-                for (int j = 0; j < EPL; ++j)
-                    if (lane * EPL + j == chosen) key[j] = 0;
+                    for (int j = 0; j + 1 < EPL; ++j) key[j] = mine ? key[j + 1] : key[j];
+                    key[EPL - 1] = mine ? 0u : key[EPL - 1];
+                }
+                if (l == 0) mem.stat[slot] = Stat{top, sum, 0};
+                again = again && on;
+            } else if (!on) {
+                for (int r = l; r < k; r += LPT) sel[r] = -1;
+                if (l == 0) mem.stat[slot] = Stat{0.0f, 1.0f, 0};
             }
-            if (index >= 0) {
-                const float y = widen(row[index]);
-                score = a.softmax ? __fdiv_rn(expf(y - top), sum) : sigmoid(y);
+            unsigned left = __ballot_sync(kAll, again);
+            __syncwarp();
+            while (left) {
+                const int which = (__ffs(left) - 1) / LPT;
+                left &= ~static_cast<unsigned>(((1ull << LPT) - 1) << (which * LPT));
+                const int place = rep * kTokens + which;
+                choose_exact(a, static_cast<const T*>(a.logits) + (t0 + place) * a.stride, mem.c, mem.sel + place * k,
+                             mem.stat + place);
             }
         }
-        float w = score;
-        if (a.renorm) {
-            const float total = warp_sum(score);
-            w = total > 0.0f ? __fdiv_rn(score, total) : 0.0f;
+        __syncwarp();
+        // the slots' scores, and then the weights, a lane a slot
+        const long long tokens = min(a.tokens - t0, static_cast<long long>(tile));
+        const int slots = static_cast<int>(tokens) * k;
+        for (int i = lane; i < slots; i += 32) {
+            const int token = i / k, e = mem.sel[i];
+            float score = 0.0f;
+            if (e >= 0) {
+                const float x = widen(static_cast<const T*>(a.logits)[(t0 + token) * a.stride + e]);
+                const Stat st = mem.stat[token];
+                score = a.softmax ? __fdiv_rn(expf(x - st.top), st.sum) : sigmoid(x);
+                if (a.counts) atomicAdd(hist + e, 1);
+            }
+            mem.score[i] = score;
         }
-        w = __fmul_rn(w, a.scale);
-        if (bad) w = __int_as_float(0x7fffffff);
-        if (lane < k) {
-            a.indices[t * k + lane] = index;
-            a.weights[t * k + lane] = w;
-            if (a.counts && index >= 0) atomicAdd(hist + index, 1);
+        __syncwarp();
+        for (int i = lane; i < slots; i += 32) {
+            const int token = i / k;
+            float w = mem.score[i];
+            if (a.renorm) {
+                float total = 0.0f;
+                for (int r = 0; r < k; ++r) total += mem.score[token * k + r];
+                w = total > 0.0f ? __fdiv_rn(w, total) : 0.0f;
+            }
+            a.indices[t0 * k + i] = mem.sel[i];
+            a.weights[t0 * k + i] = mem.stat[token].bad ? nan_value() : __fmul_rn(w, a.scale);
         }
+        __syncwarp();
     }
     if (a.counts) {
         __syncthreads();
@@ -204,64 +436,141 @@ route_kernel(const __grid_constant__ RouteParams a) {
     }
 }
 
-// The gradient.  With D = sum over the slots of part_r, in the slots r
-//   part_r = g_r w_r                          (weights as they are)
+// The gradient.  In the slots r, and with D their sum,
+//   part_r = g_r w_r                            (weights as they are)
 //   part_r = w_r (g_r - sum_l g_l w_l / scale)  (renormalised)
 // sigmoid:  dx = part_r (1 - s_r) at the chosen, 0 elsewhere
 // softmax:  dx = [chosen] part_r - s_i D; renormalised D is zero, and only the
 //           chosen get a gradient
-template <int EPL, typename T>
+
+constexpr int kRowBytes = 4096;          // of a warp's rows under construction
+
+// Gradients that only the chosen get: the slots of row_tokens tokens at once,
+// slot_lanes lanes a token; their values go into rows of zeros in shared
+// memory, which leave in 16-byte stores and are cleared where they were set.
+template <typename T>
 __global__ void __launch_bounds__(kThreads)
-route_backward_kernel(const __grid_constant__ RouteParams a) {
-    __shared__ float rows[kWarps][EPL * 32];
+route_backward_chosen_kernel(const __grid_constant__ RouteParams a) {
+    __shared__ __align__(16) uint8_t buffer[kWarps][kRowBytes];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int E = a.E, k = a.k;
-    float* out = rows[warp];
+    const int E = a.E, k = a.k, lanes = a.slot_lanes;
+    const int tl = lane / lanes, r = lane % lanes;
+    T* const rows = reinterpret_cast<T*>(buffer[warp]);
+    for (int i = lane; i < kRowBytes / 16; i += 32) reinterpret_cast<uint4*>(buffer[warp])[i] = make_uint4(0, 0, 0, 0);
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
-    for (long long t = static_cast<long long>(blockIdx.x) * kWarps + warp; t < a.tokens;
-         t += static_cast<long long>(gridDim.x) * kWarps) {
-        const T* row = static_cast<const T*>(a.logits) + t * a.stride;
+    __syncwarp();
+    const int tile = a.row_tokens;
+    for (long long t0 = (static_cast<long long>(blockIdx.x) * kWarps + warp) * tile; t0 < a.tokens;
+         t0 += static_cast<long long>(gridDim.x) * kWarps * tile) {
+        const long long t = t0 + tl;
+        const int tokens = static_cast<int>(min(a.tokens - t0, static_cast<long long>(tile)));
         int index = -1;
-        float part = 0.0f;
-        if (lane < k) index = a.indices[t * k + lane];
-        if (index < 0 || index >= E) index = -1;      // never an address past the row
         float w = 0.0f, g = 0.0f;
+        if (tl < tokens && r < k) {
+            index = a.indices[t * k + r];
+            w = a.weights[t * k + r];
+            g = a.grad_weights[t * k + r];
+        }
+        if (index < 0 || index >= E) { index = -1; w = g = 0.0f; }    // never an address past the row
+        float part = g * w;
+        if (a.renorm) {
+            float total = part;
+            for (int o = lanes / 2; o; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+            part = w * (g - total / a.scale);
+        }
         if (index >= 0) {
-            w = a.weights[t * k + lane];
-            g = a.grad_weights[t * k + lane];
+            if (!a.softmax) part *= 1.0f - sigmoid(widen(static_cast<const T*>(a.logits)[t * a.stride + index]));
+            rows[tl * E + index] = narrow<T>(part);
         }
-        part = g * w;
-        const float total = warp_sum(part);
-        if (a.renorm) part = index >= 0 ? w * (g - total / a.scale) : 0.0f;
-        if (!a.softmax && index >= 0) part *= 1.0f - sigmoid(widen(row[index]));
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) out[j * 32 + lane] = 0.0f;
         __syncwarp();
-        if (index >= 0) out[index] = part;
+        T* const to = static_cast<T*>(a.grad_logits) + t0 * a.grad_stride;
+        if (a.vec) {
+            const int pieces = tokens * E * static_cast<int>(sizeof(T)) / 16;
+            for (int i = lane; i < pieces; i += 32)
+                __stcs(reinterpret_cast<uint4*>(to) + i, reinterpret_cast<const uint4*>(rows)[i]);
+        } else {
+            for (int token = 0; token < tokens; ++token)
+                for (int e = lane; e < E; e += 32) to[token * a.grad_stride + e] = rows[token * E + e];
+        }
         __syncwarp();
-        const bool whole = a.softmax && !a.renorm && __any_sync(kAll, index >= 0);
-        float x[EPL], top = 0.0f, sum = 1.0f;
-        if (whole) {
-            load_row<EPL>(row, E, x);
-            softmax_stats<EPL>(x, top, sum);
-        }
-        T* to = static_cast<T*>(a.grad_logits) + t * a.grad_stride;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            const int e = lane * EPL + j;
-            float d = out[e];
-            if (whole && x[j] != neg_inf()) d -= expf(x[j] - top) / sum * total;
-            if (e < E) to[e] = narrow<T>(d);
-        }
+        if (index >= 0) rows[tl * E + index] = narrow<T>(0.0f);
         __syncwarp();
     }
 }
 
-template <typename T, int EPL>
-cudaError_t launch_epl(bool backward, int grid, const RouteParams& a, cudaStream_t stream) {
+// Softmax weights as they are: every expert of a token gets a gradient.
+template <int LPT, int EPL, typename T>
+__global__ void __launch_bounds__(kThreads)
+route_backward_whole_kernel(const __grid_constant__ RouteParams a) {
+    constexpr int kTokens = 32 / LPT;
+    __shared__ float rows[kWarps][32 * EPL];          // the chosen experts' parts, zeros elsewhere
+    __shared__ float parts[kWarps][kMaxSlots];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int l = lane % LPT, tl = lane / LPT;
+    const int E = a.E, k = a.k;
+    float* const row_part = rows[warp];
+    float* const part = parts[warp];
+    const int e0 = l * EPL, n = max(0, min(E - e0, EPL));
+    const bool vec = a.vec && (e0 * sizeof(T)) % 16 == 0;
+    for (int j = 0; j < EPL; ++j) row_part[j * 32 + lane] = 0.0f;
+    ddpk::dev::pdl_wait();
+    ddpk::dev::pdl_trigger();
+    __syncwarp();
+    for (long long t0 = (static_cast<long long>(blockIdx.x) * kWarps + warp) * kTokens; t0 < a.tokens;
+         t0 += static_cast<long long>(gridDim.x) * kWarps * kTokens) {
+        const long long t = t0 + tl;
+        const bool on = t < a.tokens;
+        const int slots = static_cast<int>(min(a.tokens - t0, static_cast<long long>(kTokens))) * k;
+        float x[EPL];
+        load_lane<EPL>(static_cast<const T*>(a.logits) + t * a.stride + e0, on ? n : 0, vec, neg_inf(), x);
+        for (int i = lane; i < slots; i += 32) {
+            const int index = a.indices[t0 * k + i];
+            float p = 0.0f;
+            if (index >= 0 && index < E) {
+                p = a.grad_weights[t0 * k + i] * a.weights[t0 * k + i];
+                row_part[i / k * (LPT * EPL) + index] = p;
+            }
+            part[i] = p;
+        }
+        __syncwarp();
+        float total = 0.0f;
+        if (on)
+            for (int r = 0; r < k; ++r) total += part[tl * k + r];
+        uint32_t most = 0;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) most = max(most, key_of(x[j]));
+        const float top = number_of(token_max<LPT>(most));
+        float e[EPL], sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            e[j] = x[j] == neg_inf() ? 0.0f : expf(x[j] - top);
+            sum += e[j];
+        }
+        sum = token_sum<LPT>(sum);
+        const float f = total / sum;
+        T* const to = static_cast<T*>(a.grad_logits) + t * a.grad_stride + e0;
+        float d[EPL];
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            d[j] = row_part[lane * EPL + j];
+            if (total != 0.0f) d[j] -= e[j] * f;      // a masked token's logits may be anything
+        }
+        __syncwarp();
+        for (int i = lane; i < slots; i += 32) {
+            const int index = a.indices[t0 * k + i];
+            if (index >= 0 && index < E) row_part[i / k * (LPT * EPL) + index] = 0.0f;
+        }
+        if (on) store_lane<EPL>(to, n, vec, d);
+        __syncwarp();
+    }
+}
+
+template <typename K>
+cudaError_t launch(K kernel, long long warps, int sms, int ctas_per_sm, const RouteParams& a, cudaStream_t stream) {
+    const long long want = (warps + kWarps - 1) / kWarps, most = static_cast<long long>(ctas_per_sm) * sms;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.gridDim = dim3(static_cast<unsigned>(want < most ? want : most));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -269,23 +578,64 @@ cudaError_t launch_epl(bool backward, int grid, const RouteParams& a, cudaStream
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return backward ? cudaLaunchKernelEx(&cfg, route_backward_kernel<EPL, T>, a)
-                    : cudaLaunchKernelEx(&cfg, route_kernel<EPL, T>, a);
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+int power_of_two(int x) {
+    int p = 1;
+    while (p < x) p *= 2;
+    return p;
+}
+
+// Lanes of a token: 1, 2, 4, .. 32 with 8 experts each, or 32 with 16.
+constexpr int kForwardCtas = 8;          // CTAs per SM at most
+constexpr int kBackwardCtas = 16;
+
+template <int LPT, int EPL, typename T>
+cudaError_t launch_sized(bool backward, int sms, RouteParams& a, cudaStream_t stream) {
+    constexpr int kTokens = 32 / LPT;
+    const long long groups = (a.tokens + kTokens - 1) / kTokens;
+    if (backward)
+        return launch(route_backward_whole_kernel<LPT, EPL, T>, groups, sms, kBackwardCtas, a, stream);
+    // with tokens enough for every warp, those of four rounds are weighed
+    // together: their slots then fill the warp's lanes
+    a.reps = kTokens < 4 && groups >= 4LL * kForwardCtas * sms * kWarps ? 4 / kTokens : 1;
+    return launch(route_kernel<LPT, EPL, T>, (groups + a.reps - 1) / a.reps, sms, kForwardCtas, a, stream);
 }
 
 template <typename T>
-cudaError_t launch(bool backward, const RouteParams& a, cudaStream_t stream) {
+cudaError_t launch_any(bool backward, RouteParams& a, cudaStream_t stream) {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    const long long want = (a.tokens + kWarps - 1) / kWarps, most = 8LL * sms;
-    const int grid = static_cast<int>(want < most ? want : most);
-    if (a.E <= 32) return launch_epl<T, 1>(backward, grid, a, stream);
-    if (a.E <= 64) return launch_epl<T, 2>(backward, grid, a, stream);
-    if (a.E <= 128) return launch_epl<T, 4>(backward, grid, a, stream);
-    if (a.E <= 256) return launch_epl<T, 8>(backward, grid, a, stream);
-    return launch_epl<T, 16>(backward, grid, a, stream);
+    if (backward && !(a.softmax && !a.renorm)) {
+        a.slot_lanes = power_of_two(a.k);
+        const int room = kRowBytes / static_cast<int>(sizeof(T)) / a.E, tokens = 32 / a.slot_lanes;
+        a.row_tokens = room < tokens ? room : tokens;
+        return launch(route_backward_chosen_kernel<T>, (a.tokens + a.row_tokens - 1) / a.row_tokens, sms, kBackwardCtas,
+                      a, stream);
+    }
+    // slots of a group, each group from a lane of its own on
+    const int size = a.E / a.groups;
+    const auto slots_of = [&](int epl) { return power_of_two((size + epl - 1) / epl) * epl; };
+    const bool wide = backward ? a.E > 256 : a.groups * slots_of(8) > 256;
+    a.group_slots = slots_of(wide ? 16 : 8);
+    int slots = backward ? a.E : a.groups * a.group_slots;
+    a.fits = slots <= 512;
+    if (!a.fits) {                       // every token is chosen exactly: one a warp
+        slots = 512;
+        a.group_slots = 512;
+    }
+    if (wide) return launch_sized<32, 16, T>(backward, sms, a, stream);
+    switch (power_of_two((slots + 7) / 8)) {
+        case 1: return launch_sized<1, 8, T>(backward, sms, a, stream);
+        case 2: return launch_sized<2, 8, T>(backward, sms, a, stream);
+        case 4: return launch_sized<4, 8, T>(backward, sms, a, stream);
+        case 8: return launch_sized<8, 8, T>(backward, sms, a, stream);
+        case 16: return launch_sized<16, 8, T>(backward, sms, a, stream);
+        default: return launch_sized<32, 8, T>(backward, sms, a, stream);
+    }
 }
 
 bool valid(const ddp_route_args* x) {
@@ -331,8 +681,10 @@ int ddp_route(const ddp_route_args* x, const void* logits, const float* bias, co
     a.indices = indices;
     a.weights = weights;
     a.counts = counts;
+    const int64_t size = x->dtype == DDP_F32 ? 4 : 2;
+    a.vec = aligned(logits, 16) && x->row_stride * size % 16 == 0;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = x->dtype == DDP_F32 ? launch<float>(false, a, st) : launch<uint16_t>(false, a, st);
+    const cudaError_t e = x->dtype == DDP_F32 ? launch_any<float>(false, a, st) : launch_any<uint16_t>(false, a, st);
     return e == cudaSuccess ? DDP_OK : DDP_ERR_CUDA;
 }
 
@@ -352,8 +704,14 @@ int ddp_route_backward(const ddp_route_args* x, const void* logits, const int32_
     a.grad_weights = grad_weights;
     a.grad_logits = grad_logits;
     a.grad_stride = grad_stride;
+    const int64_t bytes = static_cast<int64_t>(size);
+    if (a.softmax && !a.renorm)
+        a.vec = aligned(logits, 16) && x->row_stride * bytes % 16 == 0 && aligned(grad_logits, 16) &&
+                grad_stride * bytes % 16 == 0;
+    else
+        a.vec = aligned(grad_logits, 16) && grad_stride == x->experts && x->experts * bytes % 16 == 0;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = x->dtype == DDP_F32 ? launch<float>(true, a, st) : launch<uint16_t>(true, a, st);
+    const cudaError_t e = x->dtype == DDP_F32 ? launch_any<float>(true, a, st) : launch_any<uint16_t>(true, a, st);
     return e == cudaSuccess ? DDP_OK : DDP_ERR_CUDA;
 }
 
