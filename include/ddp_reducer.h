@@ -493,7 +493,7 @@ typedef struct ddp_route_args {
 
 /*   logits   device [tokens] rows of `experts`, row_stride apart
  *   bias     device fp32 [experts] or NULL
- *   mask     device bytes [tokens] or NULL: 0 = the token is not routed (its logits are not read)
+ *   mask     device bytes [tokens] or NULL: 0 = the token is not routed (its logits may be anything)
  *   indices  device int32 [tokens * k]
  *   weights  device fp32 [tokens * k]
  *   counts   device int32 [experts] or NULL: the number of tokens each expert

@@ -5,14 +5,15 @@
 // partly empty) and take a power of two of lanes.  The choice goes by 32-bit
 // keys: 23 bits of the compared value above 9 bits of 511 - expert, so no two
 // are equal, the larger key is the better expert, and ties of the value go to
-// the lowest expert.  Each lane sorts its keys once; the k best of a token are
-// then the largest of the lanes' first keys, k times over.
+// the lowest expert.  Each lane sorts its eight largest; the k best of a token
+// are the largest of its lanes' first, k times over.
 //
 // 23 bits, and scores from the hardware's approximate exponential and
 // reciprocal, do not always tell which of two experts the fp32 definition puts
-// first: where two values that the choice told apart are nearer than the
-// errors of both, or a logit or bias is not an ordinary number, the
-// token is chosen again by the definition itself (choose_exact).  The scores
+// first.  Where values that the choice told apart are nearer than the errors
+// of both, the k chosen and the next best are put into order by the definition
+// (order_exact); where that may not be enough, or a logit or bias is not an
+// ordinary number, the token is chosen by it alone (choose_exact).  The scores
 // of the chosen experts are always computed by the definition.
 
 #include "ddp_reducer.h"
@@ -26,7 +27,7 @@
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxExperts = 512;
 constexpr int kMaxSlots = 256;           // slots of a warp's tokens at once
@@ -166,22 +167,44 @@ __device__ __forceinline__ void store_lane(uint16_t* to, int n, bool vec, const 
     }
 }
 
-// Descending order (Batcher's odd-even merge sort, unrolled).
+// Larger first.
+__device__ __forceinline__ void order(uint32_t& a, uint32_t& b) {
+    const uint32_t x = max(a, b), y = min(a, b);
+    a = x;
+    b = y;
+}
+
+// Eight in descending order (19 comparisons, Batcher's odd-even merge sort).
+__device__ __forceinline__ void sort8(uint32_t (&x)[8]) {
+    order(x[0], x[1]); order(x[2], x[3]); order(x[4], x[5]); order(x[6], x[7]);
+    order(x[0], x[2]); order(x[1], x[3]); order(x[4], x[6]); order(x[5], x[7]);
+    order(x[1], x[2]); order(x[5], x[6]);
+    order(x[0], x[4]); order(x[1], x[5]); order(x[2], x[6]); order(x[3], x[7]);
+    order(x[2], x[4]); order(x[3], x[5]);
+    order(x[1], x[2]); order(x[3], x[4]); order(x[5], x[6]);
+}
+
+// The eight largest of N, in descending order: sorted eights, of which two give
+// the larger of x[i] and y[7 - i], a bitonic sequence that three steps sort.
 template <int N>
-__device__ __forceinline__ void sort_down(uint32_t (&x)[N]) {
+__device__ __forceinline__ void top8(const uint32_t (&key)[N], uint32_t (&x)[8]) {
 #pragma unroll
-    for (int p = 1; p < N; p *= 2)
+    for (int i = 0; i < 8; ++i) x[i] = key[i];
+    sort8(x);
 #pragma unroll
-        for (int d = p; d >= 1; d /= 2)
+    for (int c = 8; c < N; c += 8) {
+        uint32_t y[8];
 #pragma unroll
-            for (int j = d % p; j + d < N; j += 2 * d)
+        for (int i = 0; i < 8; ++i) y[i] = key[c + i];
+        sort8(y);
 #pragma unroll
-                for (int i = 0; i < d; ++i)
-                    if (i + j + d < N && (i + j) / (2 * p) == (i + j + d) / (2 * p)) {
-                        const uint32_t a = x[i + j], b = x[i + j + d];
-                        x[i + j] = max(a, b);
-                        x[i + j + d] = min(a, b);
-                    }
+        for (int i = 0; i < 8; ++i) x[i] = max(x[i], y[7 - i]);
+#pragma unroll
+        for (int d = 4; d; d /= 2)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (!(i & d)) order(x[i], x[i + d]);
+    }
 }
 
 // What the scores of a token's slots are computed from.
@@ -193,11 +216,14 @@ struct Stat {
 struct WarpRows {
     float c[kMaxExperts];        // choose_exact: what the choice goes by
     int32_t sel[kMaxSlots];
+    int32_t next[32];            // a token's best that was not chosen
     float score[kMaxSlots];
     Stat stat[32];
 };
 
-// One token's choice by the fp32 definition, by a whole warp.
+// One token's choice by the fp32 definition, by a whole warp.  sel: as the
+// keys give it, 511 - expert in the low 9 bits below something not zero; 0 for
+// none.
 template <typename T>
 __device__ __noinline__ void choose_exact(const RouteParams& a, const T* row, float* c, int32_t* sel, Stat* stat) {
     const int lane = threadIdx.x & 31;
@@ -264,7 +290,7 @@ __device__ __noinline__ void choose_exact(const RouteParams& a, const T* row, fl
         }
         const uint32_t best = __reduce_max_sync(kAll, mine);
         const int chosen = __reduce_min_sync(kAll, best && mine == best ? at : E);
-        if (lane == 0) sel[r] = chosen < E ? chosen : -1;
+        if (lane == 0) sel[r] = chosen < E ? kMaxExperts | (kMaxExperts - 1 - chosen) : 0;
         if (lane == (chosen & 31) && chosen < E) c[chosen] = neg_inf();
         __syncwarp();
     }
@@ -272,8 +298,69 @@ __device__ __noinline__ void choose_exact(const RouteParams& a, const T* row, fl
     __syncwarp();
 }
 
+// The order of a token's k chosen and the next best, by the fp32 definition,
+// by a whole warp: for tokens where these are known to be the k + 1 best, but
+// not in which order.  sel, next: as the keys give them; k < 32.
+template <typename T>
+__device__ __forceinline__ void order_exact(const RouteParams& a, const T* row, int32_t* sel, int32_t next, const Stat& stat) {
+    const int lane = threadIdx.x & 31;
+    const int32_t word = lane < a.k ? sel[lane] : lane == a.k ? next : 0;
+    const int e = kMaxExperts - 1 - (word & (kMaxExperts - 1));
+    uint32_t key = 0;
+    if (word) {
+        const float x = widen(row[e]);
+        float y = x;
+        if (a.bias || a.groups > 1) {
+            y = a.softmax ? __fdiv_rn(expf(x - stat.top), stat.sum) : sigmoid(x);
+            if (a.bias) y = __fadd_rn(y, a.bias[e]);
+        }
+        key = key_of(y);
+    }
+    int rank = 0;
+    for (int r = 0; r <= a.k; ++r) {
+        const uint32_t other = __shfl_sync(kAll, key, r);
+        const int place = __shfl_sync(kAll, e, r);
+        rank += other > key || (other == key && place < e);
+    }
+    __syncwarp();
+    if (word && rank < a.k) sel[rank] = kMaxExperts | (kMaxExperts - 1 - e);
+    __syncwarp();
+}
+
+// Whether this lane's group stays, by the fp32 definition; for all tokens of a
+// warp.  The lane's experts are n from e0 on.
 template <int LPT, int EPL, typename T>
-__global__ void __launch_bounds__(kThreads)
+__device__ __noinline__ bool groups_exact(const RouteParams& a, const T* row, int e0, int n, float top, float sum, int g,
+                                          int group_lanes, int size) {
+    float a1 = neg_inf(), a2 = neg_inf();
+#pragma unroll 4
+    for (int j = 0; j < EPL; ++j) {
+        float c = neg_inf();
+        if (j < n) {
+            const float x = widen(row[e0 + j]);
+            c = a.softmax ? __fdiv_rn(expf(x - top), sum) : sigmoid(x);
+            if (a.bias) c = __fadd_rn(c, a.bias[e0 + j]);
+        }
+        a2 = fmaxf(a2, fminf(a1, c));
+        a1 = fmaxf(a1, c);
+    }
+    for (int o = 1; o < group_lanes; o *= 2) {
+        const float b1 = __shfl_xor_sync(kAll, a1, o), b2 = __shfl_xor_sync(kAll, a2, o);
+        a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
+        a1 = fmaxf(a1, b1);
+    }
+    uint32_t worth = g < a.groups ? max(key_of(size > 1 ? __fadd_rn(a1, a2) : a1), 1u) : 0u;
+    bool stays = false;
+    for (int r = 0; r < a.top_groups; ++r) {
+        const uint32_t best = token_max<LPT>(worth);
+        const uint32_t first = token_max<LPT>(worth == best ? static_cast<uint32_t>(32 - g) : 0u);   // the lowest of those that tie
+        if (worth == best && g == 32 - static_cast<int>(first)) { worth = 0; stays = true; }
+    }
+    return stays;
+}
+
+template <int LPT, int EPL, typename T>
+__global__ void __launch_bounds__(kThreads, EPL == 32 ? 2 : 3)
 route_kernel(const __grid_constant__ RouteParams a) {
     constexpr int kTokens = 32 / LPT;     // of a warp
     __shared__ int hist[kMaxExperts];
@@ -295,109 +382,159 @@ route_kernel(const __grid_constant__ RouteParams a) {
     const int n = g < a.groups ? max(0, min(size - off, EPL)) : 0;
     const bool by_logit = !a.bias && a.groups == 1;
     const bool vec = a.vec && (e0 * sizeof(T)) % 16 == 0;
-    float bias[EPL];
-    bool plain = true;
+    float bias[EPL], widest = 0.0f;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
         bias[j] = a.bias && j < n ? a.bias[e0 + j] : 0.0f;
-        plain = plain && bias[j] >= -1.9f && bias[j] <= 0.9f;     // the keys' range is scores + bias in [-2, 2)
+        widest = fmaxf(widest, bias[j] == bias[j] ? fabsf(bias[j]) : __int_as_float(0x7f800000));
     }
-    const bool fast = a.fits && __all_sync(kAll, plain);
+    // scores + bias lie in [-range, range), a power of two; keys hold them times 2 / range
+    widest = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(widest)));
+    const bool fast = a.fits && widest < 0x1p20f;
+    const float over_range = 2.0f / __uint_as_float((__float_as_uint(1.0f + widest) & 0x7f800000u) + 0x00800000u);
     const uint32_t by_score = a.softmax ? kMarginSoftmax : kMarginSigmoid;
-    const uint32_t margin = !by_logit ? by_score : sizeof(T) == 2 ? 0u : 1u;   // a key holds all of a bf16 logit
+    const uint32_t near = !by_logit ? (by_score + 1) << 9 : sizeof(T) == 2 ? 0u : 2u << 9;   // a key holds all of a bf16 logit
+    const uint32_t over_k = (65536u + k - 1) / k;                 // i / k for i < 256
     const bool need_sum = a.softmax && (!a.renorm || !by_logit);
 
     const int tile = kTokens * a.reps;
-    for (long long t0 = (static_cast<long long>(blockIdx.x) * kWarps + warp) * tile; t0 < a.tokens;
-         t0 += static_cast<long long>(gridDim.x) * kWarps * tile) {
+    const long long stride = static_cast<long long>(gridDim.x) * kWarps * tile;
+    long long t0 = (static_cast<long long>(blockIdx.x) * kWarps + warp) * tile;
+    // the logits of this lane's next token
+    float x[EPL];
+    const auto load = [&](long long t) {
+        const bool in = t < a.tokens;
+        if (fast) load_lane<EPL>(static_cast<const T*>(a.logits) + t * a.stride + e0, in ? n : 0, vec, 0.0f, x);
+        return in && (!a.mask || a.mask[t]);
+    };
+    bool next_on = load(t0 + tl);
+    for (; t0 < a.tokens; t0 += stride) {
         for (int rep = 0; rep < a.reps; ++rep) {
             const int slot = rep * kTokens + tl;                  // the token's place in the tile
-            const long long t = t0 + slot;
-            const bool on = t < a.tokens && (!a.mask || a.mask[t]);
-            const T* row = static_cast<const T*>(a.logits) + t * a.stride;
+            const long long next = rep + 1 < a.reps ? t0 + slot + kTokens : t0 + stride + tl;
+            const bool on = next_on;
             int32_t* sel = mem.sel + slot * k;
-            bool again = on;                                      // choose exactly
+            bool again = on, reorder = false;                     // choose exactly; put into order exactly
             if (fast) {
-                float x[EPL];
                 uint32_t key[EPL];
-                load_lane<EPL>(row + e0, on ? n : 0, vec, 0.0f, x);
                 float zero = 0.0f;                                // NaN where a logit is not finite
 #pragma unroll
                 for (int j = 0; j < EPL; ++j) zero = fmaf(x[j], 0.0f, zero);
                 again = !(zero == 0.0f);
-                float top = 0.0f, sum = 1.0f, over = 1.0f;
+                float top = 0.0f, sum = 1.0f;
                 if (a.softmax) {
                     uint32_t most = 0;
 #pragma unroll
                     for (int j = 0; j < EPL; ++j) most = max(most, j < n ? order_bits(x[j]) : 0u);
                     top = number_of(token_max<LPT>(most));
-                }
-                if (need_sum) {
-                    sum = 0.0f;
+                    if (need_sum) {
+                        sum = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < EPL; ++j) sum += j < n ? fast_exp(x[j] - top) : 0.0f;
-                    sum = token_sum<LPT>(sum);
-                    over = __fdividef(1.0f, sum);
-                }
-#pragma unroll
-                for (int j = 0; j < EPL; ++j) {
-                    const uint32_t place = kMaxExperts - 1 - (e0 + j);
-                    if (by_logit) {
-                        key[j] = (order_bits(x[j]) & ~0x1ffu) | place;
-                    } else {
-                        // 6 + c lies in [4, 8), where fp32 has steps of 2^-21; the exponent is shifted out
-                        const float c = (a.softmax ? fast_exp(x[j] - top) * over : fast_sigmoid(x[j])) + bias[j];
-                        key[j] = __float_as_uint(c + 6.0f) * 512u + place;
+                        for (int j = 0; j < EPL; ++j) sum += j < n ? fast_exp(x[j] - top) : 0.0f;
+                        sum = token_sum<LPT>(sum);
                     }
-                    if (!on || j >= n) key[j] = 0;
                 }
-                sort_down(key);
+                const uint32_t place = kMaxExperts - 1 - e0;
+                if (by_logit) {
+#pragma unroll
+                    for (int j = 0; j < EPL; ++j) key[j] = (order_bits(x[j]) & ~0x1ffu) | (place - j);
+                } else {
+                    if (a.softmax) {
+                        const float over = __fdividef(1.0f, sum);
+#pragma unroll
+                        for (int j = 0; j < EPL; ++j) x[j] = fast_exp(x[j] - top) * over;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < EPL; ++j) x[j] = fast_sigmoid(x[j]);
+                    }
+                    // [4, 8) is where fp32 has steps of 2^-21; the exponent is shifted out
+#pragma unroll
+                    for (int j = 0; j < EPL; ++j)
+                        key[j] = __float_as_uint(fmaf(x[j] + bias[j], over_range, 6.0f)) * 512u + (place - j);
+                }
+                if (n < EPL || !on) {
+#pragma unroll
+                    for (int j = 0; j < EPL; ++j)
+                        if (!on || j >= n) key[j] = 0;
+                }
+                next_on = load(next);                             // on its way while this one is chosen
+                uint32_t head[8];                                 // this lane's best
+                top8(key, head);
 
                 if (a.top_groups < a.groups) {
-                    uint32_t a1 = key[0] >> 9, a2 = EPL > 1 ? key[1] >> 9 : 0u;
+                    uint32_t a1 = head[0] >> 9, a2 = head[1] >> 9;
                     for (int o = 1; o < group_lanes; o *= 2) {
                         const uint32_t b1 = __shfl_xor_sync(kAll, a1, o), b2 = __shfl_xor_sync(kAll, a2, o);
                         a2 = max(min(a1, b1), max(a2, b2));
                         a1 = max(a1, b1);
                     }
-                    const uint32_t worth = g < a.groups ? (a1 + a2) << 5 | static_cast<uint32_t>(31 - g) : 0u;
-                    int better = 0;
-                    for (int h = 0; h < a.groups; ++h)
-                        better += __shfl_sync(kAll, worth, tl * LPT + h * group_lanes) > worth;
-                    const bool stays = better < a.top_groups && g < a.groups;
-                    // the least worth that stays against the largest that does not
-                    const uint32_t least = ~token_max<LPT>(stays ? ~worth : 0u) >> 5;
-                    const uint32_t most = token_max<LPT>(stays ? 0u : worth) >> 5;
-                    again |= least - most < 2 * by_score;
-                    if (!stays) key[0] = 0;
+                    // no two groups' worth is equal; lanes past the last group have none
+                    uint32_t worth = g < a.groups ? (a1 + a2) << 5 | static_cast<uint32_t>(31 - g) : 0u;
+                    uint32_t worst = 0;
+                    bool stays = false;
+                    for (int r = 0; r < a.top_groups; ++r) {
+                        worst = token_max<LPT>(worth);
+                        if (worth == worst) { worth = 0; stays = true; }
+                    }
+                    const uint32_t out = token_max<LPT>(worth);
+                    if (__any_sync(kAll, on && (worst >> 5) - (out >> 5) < 2 * by_score))
+                        stays = groups_exact<LPT, EPL>(a, static_cast<const T*>(a.logits) + (t0 + slot) * a.stride, e0, on ? n : 0,
+                                                       top, sum, g, group_lanes, size);
+                    if (!stays) head[0] = 0;
                 }
 
-                uint32_t last = 0xffffffffu;
-                for (int r = 0; r <= k; ++r) {
-                    const uint32_t best = token_max<LPT>(key[0]);
-                    again |= best && (last >> 9) - (best >> 9) < margin;
+                // keys less than `near` apart may be of values less than the margin apart
+                uint32_t last = 0xffffffffu, least = 0xffffffffu;
+                const bool had = head[0] != 0;
+                const auto pop = [&](uint32_t best) {
+                    least = min(least, last - best);
                     last = best;
-                    if (r == k) break;
-                    if (l == 0) sel[r] = best ? kMaxExperts - 1 - static_cast<int>(best & 0x1ffu) : -1;
-                    const bool mine = key[0] == best;
+                    if (head[0] == best) {
 #pragma unroll
-                    for (int j = 0; j + 1 < EPL; ++j) key[j] = mine ? key[j + 1] : key[j];
-                    key[EPL - 1] = mine ? 0u : key[EPL - 1];
+                        for (int i = 0; i < 7; ++i) head[i] = head[i + 1];
+                        head[7] = 0;
+                    }
+                };
+#pragma unroll 2
+                for (int r = 0; r < k; ++r) {
+                    const uint32_t best = token_max<LPT>(head[0]);
+                    if (l == 0) sel[r] = static_cast<int32_t>(best);
+                    pop(best);
                 }
+                const uint32_t after = token_max<LPT>(head[0]);
+                if (l == 0) mem.next[slot] = static_cast<int32_t>(after);
+                least = min(least, last - after);
+                if (on && !again && least < near) {
+                    // which of the k + 1 best comes where is not certain; that they are it, mostly is
+                    pop(after);
+                    reorder = true;
+                }
+                if (__any_sync(kAll, reorder)) {
+                    const uint32_t beyond = token_max<LPT>(head[0]);
+                    if (reorder && (k == 32 || after - beyond < near)) again = true;
+                }
+                // a lane of more than eight experts may have had a ninth among the best
+                if (EPL > 8) again |= on && had && head[0] == 0;
                 if (l == 0) mem.stat[slot] = Stat{top, sum, 0};
                 again = again && on;
-            } else if (!on) {
-                for (int r = l; r < k; r += LPT) sel[r] = -1;
-                if (l == 0) mem.stat[slot] = Stat{0.0f, 1.0f, 0};
+            } else {
+                if (!on) {
+                    for (int r = l; r < k; r += LPT) sel[r] = 0;
+                    if (l == 0) mem.stat[slot] = Stat{0.0f, 1.0f, 0};
+                }
+                next_on = load(next);
             }
-            unsigned left = __ballot_sync(kAll, again);
+            const unsigned exactly = __ballot_sync(kAll, again);
+            unsigned left = exactly | __ballot_sync(kAll, reorder);
             __syncwarp();
             while (left) {
                 const int which = (__ffs(left) - 1) / LPT;
-                left &= ~static_cast<unsigned>(((1ull << LPT) - 1) << (which * LPT));
+                const unsigned lanes = static_cast<unsigned>(((1ull << LPT) - 1) << (which * LPT));
                 const int place = rep * kTokens + which;
-                choose_exact(a, static_cast<const T*>(a.logits) + (t0 + place) * a.stride, mem.c, mem.sel + place * k,
-                             mem.stat + place);
+                const T* row = static_cast<const T*>(a.logits) + (t0 + place) * a.stride;
+                if (exactly & lanes) choose_exact(a, row, mem.c, mem.sel + place * k, mem.stat + place);
+                else order_exact(a, row, mem.sel + place * k, mem.next[place], mem.stat[place]);
+                left &= ~lanes;
             }
         }
         __syncwarp();
@@ -405,26 +542,29 @@ route_kernel(const __grid_constant__ RouteParams a) {
         const long long tokens = min(a.tokens - t0, static_cast<long long>(tile));
         const int slots = static_cast<int>(tokens) * k;
         for (int i = lane; i < slots; i += 32) {
-            const int token = i / k, e = mem.sel[i];
+            const int token = static_cast<int>(i * over_k >> 16), chosen = mem.sel[i];
             float score = 0.0f;
-            if (e >= 0) {
+            int e = -1;
+            if (chosen) {
+                e = kMaxExperts - 1 - (chosen & (kMaxExperts - 1));
                 const float x = widen(static_cast<const T*>(a.logits)[(t0 + token) * a.stride + e]);
                 const Stat st = mem.stat[token];
                 score = a.softmax ? __fdiv_rn(expf(x - st.top), st.sum) : sigmoid(x);
                 if (a.counts) atomicAdd(hist + e, 1);
             }
             mem.score[i] = score;
+            a.indices[t0 * k + i] = e;
         }
         __syncwarp();
         for (int i = lane; i < slots; i += 32) {
-            const int token = i / k;
+            const int token = static_cast<int>(i * over_k >> 16);
             float w = mem.score[i];
             if (a.renorm) {
                 float total = 0.0f;
+#pragma unroll 4
                 for (int r = 0; r < k; ++r) total += mem.score[token * k + r];
                 w = total > 0.0f ? __fdiv_rn(w, total) : 0.0f;
             }
-            a.indices[t0 * k + i] = mem.sel[i];
             a.weights[t0 * k + i] = mem.stat[token].bad ? nan_value() : __fmul_rn(w, a.scale);
         }
         __syncwarp();
@@ -587,16 +727,18 @@ int power_of_two(int x) {
     return p;
 }
 
-// Lanes of a token: 1, 2, 4, .. 32 with 8 experts each, or 32 with 16.
-constexpr int kForwardCtas = 8;          // CTAs per SM at most
-constexpr int kBackwardCtas = 16;
+#ifndef WIDE_FROM
+#define WIDE_FROM 64
+#endif
+constexpr int kBackwardCtas = 8;
 
 template <int LPT, int EPL, typename T>
 cudaError_t launch_sized(bool backward, int sms, RouteParams& a, cudaStream_t stream) {
     constexpr int kTokens = 32 / LPT;
     const long long groups = (a.tokens + kTokens - 1) / kTokens;
-    if (backward)
-        return launch(route_backward_whole_kernel<LPT, EPL, T>, groups, sms, kBackwardCtas, a, stream);
+    if constexpr (EPL < 32)
+        if (backward) return launch(route_backward_whole_kernel<LPT, EPL, T>, groups, sms, kBackwardCtas, a, stream);
+    constexpr int kForwardCtas = EPL == 32 ? 2 : 3;      // what fits an SM
     // with tokens enough for every warp, those of four rounds are weighed
     // together: their slots then fill the warp's lanes
     a.reps = kTokens < 4 && groups >= 4LL * kForwardCtas * sms * kWarps ? 4 / kTokens : 1;
@@ -616,26 +758,48 @@ cudaError_t launch_any(bool backward, RouteParams& a, cudaStream_t stream) {
         return launch(route_backward_chosen_kernel<T>, (a.tokens + a.row_tokens - 1) / a.row_tokens, sms, kBackwardCtas,
                       a, stream);
     }
+    if (backward) {
+        a.group_slots = 512;
+        if (a.E > 256) return launch_sized<32, 16, T>(true, sms, a, stream);
+        switch (power_of_two((a.E + 7) / 8)) {
+            case 1: return launch_sized<1, 8, T>(true, sms, a, stream);
+            case 2: return launch_sized<2, 8, T>(true, sms, a, stream);
+            case 4: return launch_sized<4, 8, T>(true, sms, a, stream);
+            case 8: return launch_sized<8, 8, T>(true, sms, a, stream);
+            case 16: return launch_sized<16, 8, T>(true, sms, a, stream);
+            default: return launch_sized<32, 8, T>(true, sms, a, stream);
+        }
+    }
     // slots of a group, each group from a lane of its own on
     const int size = a.E / a.groups;
     const auto slots_of = [&](int epl) { return power_of_two((size + epl - 1) / epl) * epl; };
-    const bool wide = backward ? a.E > 256 : a.groups * slots_of(8) > 256;
-    a.group_slots = slots_of(wide ? 16 : 8);
-    int slots = backward ? a.E : a.groups * a.group_slots;
-    a.fits = slots <= 512;
-    if (!a.fits) {                       // every token is chosen exactly: one a warp
-        slots = 512;
+    a.fits = 1;
+    const int lanes = power_of_two(a.groups * slots_of(32) / 32), staying = a.top_groups * slots_of(32) / 32;
+    if (a.E >= WIDE_FROM && lanes <= 16 && a.groups * slots_of(32) <= 2 * a.E && (a.k < 8 || a.k <= 2 * staying)) {
+        a.group_slots = slots_of(32);
+        switch (lanes) {
+            case 1: case 2: return launch_sized<2, 32, T>(false, sms, a, stream);
+            case 4: return launch_sized<4, 32, T>(false, sms, a, stream);
+            case 8: return launch_sized<8, 32, T>(false, sms, a, stream);
+            default: return launch_sized<16, 32, T>(false, sms, a, stream);
+        }
+    }
+    a.group_slots = slots_of(8);
+    switch (power_of_two(a.groups * a.group_slots / 8)) {
+        case 1: return launch_sized<1, 8, T>(false, sms, a, stream);
+        case 2: return launch_sized<2, 8, T>(false, sms, a, stream);
+        case 4: return launch_sized<4, 8, T>(false, sms, a, stream);
+        case 8: return launch_sized<8, 8, T>(false, sms, a, stream);
+        case 16: return launch_sized<16, 8, T>(false, sms, a, stream);
+        case 32: return launch_sized<32, 8, T>(false, sms, a, stream);
+        default: break;
+    }
+    a.group_slots = slots_of(16);
+    if (a.groups * a.group_slots > 512) {    // every token is chosen exactly: one a warp
+        a.fits = 0;
         a.group_slots = 512;
     }
-    if (wide) return launch_sized<32, 16, T>(backward, sms, a, stream);
-    switch (power_of_two((slots + 7) / 8)) {
-        case 1: return launch_sized<1, 8, T>(backward, sms, a, stream);
-        case 2: return launch_sized<2, 8, T>(backward, sms, a, stream);
-        case 4: return launch_sized<4, 8, T>(backward, sms, a, stream);
-        case 8: return launch_sized<8, 8, T>(backward, sms, a, stream);
-        case 16: return launch_sized<16, 8, T>(backward, sms, a, stream);
-        default: return launch_sized<32, 8, T>(backward, sms, a, stream);
-    }
+    return launch_sized<32, 16, T>(false, sms, a, stream);
 }
 
 bool valid(const ddp_route_args* x) {

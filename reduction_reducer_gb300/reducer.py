@@ -51,18 +51,32 @@ def _ptr(x) -> int:
     return int(x.data_ptr())
 
 
-_torch = None   # resolved on first use: torch.cuda when a GPU is present, else False
+_current = None   # resolved on first use: () -> handle of the current stream
+
+
+def _resolve_current():
+    """torch's current stream on the current device as a handle; 0 without a
+    GPU.  torch.cuda.current_stream() makes a Stream object around the same
+    handle (3 to 5 us a call, more than a launch takes), so the handle is asked
+    for directly where torch offers it."""
+    import torch
+    if not torch.cuda.is_available():
+        return lambda: 0
+    torch.cuda.current_stream()                       # CUDA initialised
+    raw, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+    if raw is None or device is None:
+        return lambda: int(torch.cuda.current_stream().cuda_stream)
+    return lambda: raw(device())
 
 
 def _stream(stream) -> int:
     """cudaStream_t of a torch stream, an int handle, or (None) torch's
     current stream; 0 without a GPU (dry runs)."""
-    global _torch
+    global _current
     if stream is None:
-        if _torch is None:
-            import torch
-            _torch = torch.cuda if torch.cuda.is_available() else False
-        return int(_torch.current_stream().cuda_stream) if _torch else 0
+        if _current is None:
+            _current = _resolve_current()
+        return _current()
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)

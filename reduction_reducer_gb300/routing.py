@@ -10,32 +10,45 @@ from . import _lib
 from .reducer import DDPError, _ERRORS, _stream
 
 SCORES = {"softmax": 0, "sigmoid": 1}
-_DTYPES = {"torch.float32": _lib.DDP_F32, "torch.bfloat16": _lib.DDP_BF16}
+torch = None       # imported by the first call, not by the package; the dtypes below then too
+_DTYPES = _INT = _FLOAT = _MASK = None
+
+
+def _torch():
+    global torch, _DTYPES, _INT, _FLOAT, _MASK
+    if torch is None:
+        import torch as module
+        _DTYPES = {module.float32: _lib.DDP_F32, module.bfloat16: _lib.DDP_BF16}
+        _INT, _FLOAT, _MASK = (module.int32,), (module.float32,), (module.bool, module.uint8)
+        torch = module
+    return torch
 
 
 def _args(logits, k, score, groups, top_groups, renorm, scale):
-    dtype = _DTYPES.get(str(logits.dtype))
+    _torch()
+    dtype = _DTYPES.get(logits.dtype)
     if dtype is None or logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError("logits: expected [tokens, experts] fp32 or bf16 on a GPU, experts next to one another")
     if score not in SCORES:
         raise ValueError("score: expected 'softmax' or 'sigmoid'")
     tokens, experts = logits.shape
-    return _lib.RouteArgs(tokens, max(logits.stride(0), experts) if tokens <= 1 else logits.stride(0), experts, int(k),
-                          SCORES[score], int(groups), int(groups if top_groups is None else top_groups),
-                          1 if renorm else 0, float(scale), dtype)
+    stride = logits.stride(0)
+    return _lib.RouteArgs(tokens, max(stride, experts) if tokens <= 1 else stride, experts, k, SCORES[score], groups,
+                          groups if top_groups is None else top_groups, 1 if renorm else 0, scale, dtype)
 
 
-def _data(name, t, shape, dtype):
+def _data(name, t, shape, dtypes):
     if t is None:
         return None
-    if tuple(t.shape) != shape or str(t.dtype) not in dtype or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name}: expected {list(shape)} contiguous {' or '.join(dtype)} on a GPU")
+    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: expected {list(shape)} contiguous {' or '.join(map(str, dtypes))} on a GPU")
     return t.data_ptr()
 
 
-def _check(st: int, what: str):
+def _check(st: int, what: str, a):
     if st != 0:
-        raise _ERRORS.get(st, DDPError)(st, what)
+        raise _ERRORS.get(st, DDPError)(st, f"{what}: {a.tokens} tokens, {a.experts} experts, k {a.k}, groups {a.groups}, "
+                                            f"top_groups {a.top_groups}, scale {a.scale}")
 
 
 def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups=None, renorm: bool = False,
@@ -50,19 +63,17 @@ def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, to
     their sum; mask: bytes or truth values [tokens], 0 = not routed (index
     -1, weight 0); counts: int32 [experts], the tokens each expert got are
     added to it; out: (indices, weights) to write into."""
-    import torch
     a = _args(logits, k, score, groups, top_groups, renorm, scale)
     shape = (a.tokens, a.k)
     indices, weights = out if out is not None else (
         torch.empty(shape, dtype=torch.int32, device=logits.device),
         torch.empty(shape, dtype=torch.float32, device=logits.device))
     _check(_lib.load(lib_path).ddp_route(
-        C.byref(a), logits.data_ptr(), _data("bias", bias, (a.experts,), ("torch.float32",)),
-        _data("mask", mask, (a.tokens,), ("torch.bool", "torch.uint8")),
-        _data("indices", indices, shape, ("torch.int32",)), _data("weights", weights, shape, ("torch.float32",)),
-        _data("counts", counts, (a.experts,), ("torch.int32",)), _stream(stream)),
-        f"ddp_route: {a.tokens} tokens, {a.experts} experts, k {a.k}, groups {a.groups}, top_groups {a.top_groups}, "
-        f"scale {a.scale}")
+        C.byref(a), logits.data_ptr(), _data("bias", bias, (a.experts,), _FLOAT),
+        _data("mask", mask, (a.tokens,), _MASK),
+        _data("indices", indices, shape, _INT), _data("weights", weights, shape, _FLOAT),
+        _data("counts", counts, (a.experts,), _INT), _stream(stream)),
+        "ddp_route", a)
     return indices, weights
 
 
@@ -71,7 +82,6 @@ def route_backward(grad_weights, logits, indices, weights, score: str = "softmax
     """The gradient of the logits ([tokens, experts], their dtype) from that of
     the weights, with the indices and weights that ``route`` returned for the
     same score, renorm and scale."""
-    import torch
     k = indices.shape[1] if indices.dim() == 2 else 0
     a = _args(logits, k, score, 1, 1, renorm, scale)
     shape = (a.tokens, a.k)
@@ -80,11 +90,11 @@ def route_backward(grad_weights, logits, indices, weights, score: str = "softmax
             a.experts > 1 and grad.stride(1) != 1):
         raise ValueError("out: expected the logits' shape and dtype, experts next to one another")
     _check(_lib.load(lib_path).ddp_route_backward(
-        C.byref(a), logits.data_ptr(), _data("indices", indices, shape, ("torch.int32",)),
-        _data("weights", weights, shape, ("torch.float32",)),
-        _data("grad_weights", grad_weights, shape, ("torch.float32",)), grad.data_ptr(),
+        C.byref(a), logits.data_ptr(), _data("indices", indices, shape, _INT),
+        _data("weights", weights, shape, _FLOAT),
+        _data("grad_weights", grad_weights, shape, _FLOAT), grad.data_ptr(),
         max(grad.stride(0), a.experts) if a.tokens <= 1 else grad.stride(0), _stream(stream)),
-        f"ddp_route_backward: {a.tokens} tokens, {a.experts} experts, k {a.k}, scale {a.scale}")
+        "ddp_route_backward", a)
     return grad
 
 
@@ -94,7 +104,7 @@ _Routed = None     # the autograd function, made on first use (torch is imported
 def _autograd():
     global _Routed
     if _Routed is None:
-        import torch
+        _torch()
 
         class Routed(torch.autograd.Function):
             @staticmethod
