@@ -727,9 +727,6 @@ int power_of_two(int x) {
     return p;
 }
 
-#ifndef WIDE_FROM
-#define WIDE_FROM 64
-#endif
 constexpr int kBackwardCtas = 8;
 
 template <int LPT, int EPL, typename T>
@@ -774,15 +771,17 @@ cudaError_t launch_any(bool backward, RouteParams& a, cudaStream_t stream) {
     const int size = a.E / a.groups;
     const auto slots_of = [&](int epl) { return power_of_two((size + epl - 1) / epl) * epl; };
     a.fits = 1;
-    const int lanes = power_of_two(a.groups * slots_of(32) / 32), staying = a.top_groups * slots_of(32) / 32;
-    if (a.E >= WIDE_FROM && lanes <= 16 && a.groups * slots_of(32) <= 2 * a.E && (a.k < 8 || a.k <= 2 * staying)) {
+    // 32 experts a lane put four to sixteen tokens into a warp, whose k rounds
+    // they share; more registers and a longer chain for each.  65,536 tokens,
+    // against 8 (16) a lane: 64 experts 13.3 / 15.3 us, 128 21.9 / 27.9, 256
+    // 33.8 / 39.2, 512 61.7 / 57.9; in 8 groups of 32, 8,192 tokens 17.2 / 12.3
+    // and 65,536 44.2 / 42.7.  More than eight of a token's best in one lane
+    // must stay rare.
+    if (a.groups == 1 && a.E >= 64 && a.E <= 256 && (a.k < 8 || a.k <= 2 * ((a.E + 31) / 32))) {
         a.group_slots = slots_of(32);
-        switch (lanes) {
-            case 1: case 2: return launch_sized<2, 32, T>(false, sms, a, stream);
-            case 4: return launch_sized<4, 32, T>(false, sms, a, stream);
-            case 8: return launch_sized<8, 32, T>(false, sms, a, stream);
-            default: return launch_sized<16, 32, T>(false, sms, a, stream);
-        }
+        if (a.E <= 64) return launch_sized<2, 32, T>(false, sms, a, stream);
+        if (a.E <= 128) return launch_sized<4, 32, T>(false, sms, a, stream);
+        return launch_sized<8, 32, T>(false, sms, a, stream);
     }
     a.group_slots = slots_of(8);
     switch (power_of_two(a.groups * a.group_slots / 8)) {

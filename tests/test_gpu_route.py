@@ -262,3 +262,67 @@ def test_refusals_of_tensors():
         route(x, 9)
     with pytest.raises(InvalidArg):
         route(x, 2, groups=3)
+
+
+def fp32_choice(x, k, score, bias, groups=1, top_groups=1):
+    """The choice by the definition in fp32, step by step: exponentials, products and sums as torch rounds them."""
+    x = x.float()
+    s = 1 / (1 + torch.exp(-x)) if score == "sigmoid" else x
+    c = s + bias
+    if groups > 1:
+        T, E = x.shape
+        worth = c.view(T, groups, E // groups).topk(min(2, E // groups)).values.sum(2)
+        first = worth.argsort(dim=1, descending=True, stable=True)[:, :top_groups]
+        stay = torch.zeros(T, groups, dtype=torch.bool, device="cuda").scatter_(1, first, True)
+        c = torch.where(stay.repeat_interleave(E // groups, dim=1), c, float("-inf"))
+    return c.argsort(dim=1, descending=True, stable=True)[:, :k]
+
+
+@pytest.mark.parametrize("E", [8, 24, 64, 128, 256, 320, 512])
+@pytest.mark.parametrize("spread", [0.0, 6e-8, 1e-6, 1e-4])
+def test_near_ties_are_decided_by_the_fp32_definition(E, spread):
+    """A bias that brings all experts of the first row within `spread` of one another: no two keys, or all, tell them
+    apart; the fp32 sums do, and equal sums go to the lowest expert."""
+    gen = torch.Generator("cuda").manual_seed(E)
+    x = torch.randn(1, E, generator=gen, device="cuda") + torch.randn(50, 1, generator=gen, device="cuda") * 1e-3
+    bias = 0.7 - torch.sigmoid(x[0]) + torch.rand(E, generator=gen, device="cuda") * spread
+    for k in (1, 4, 8):
+        index, _ = route(x, k, score="sigmoid", bias=bias)
+        assert torch.equal(index.long(), fp32_choice(x, k, "sigmoid", bias)), k
+    for groups, top in ((4, 2), (8, 3)):
+        index, _ = route(x, 2, score="sigmoid", bias=bias, groups=groups, top_groups=top)
+        assert torch.equal(index.long(), fp32_choice(x, 2, "sigmoid", bias, groups, top))
+    # logits themselves a few ulps apart
+    y = 1.0 + torch.randint(0, 5, (50, E), generator=gen, device="cuda") * 2.0 ** -23
+    for k in (1, 4, 8):
+        assert torch.equal(route(y, k)[0].long(), y.argsort(dim=1, descending=True, stable=True)[:, :k])
+
+
+@pytest.mark.parametrize("scale", [0.5, 3.0, 100.0, 1e5, 1e8])
+def test_biases_of_any_range(scale):
+    gen = torch.Generator("cuda").manual_seed(2)
+    x = torch.randn(60, 96, generator=gen, device="cuda")
+    bias = torch.randn(96, generator=gen, device="cuda") * scale
+    for groups, top in ((1, 1), (8, 3)):
+        index, _ = route(x, 6, score="sigmoid", bias=bias, groups=groups, top_groups=top)
+        assert torch.equal(index.long(), fp32_choice(x, 6, "sigmoid", bias, groups, top))
+
+
+@pytest.mark.parametrize("E,k", [(64, 7), (128, 8), (256, 16), (512, 12), (512, 32)])
+def test_all_the_best_next_to_one_another(E, k):
+    """Sorted logits: one lane holds every expert that is chosen."""
+    x = torch.linspace(3, -3, E, device="cuda").repeat(20, 1)
+    x[1::2] = x[1::2].flip(1)
+    want = x.argsort(dim=1, descending=True, stable=True)[:, :k]
+    assert torch.equal(route(x, k)[0].long(), want)
+    zero = torch.zeros(E, device="cuda")
+    assert torch.equal(route(x, k, score="sigmoid", bias=zero)[0].long(), fp32_choice(x, k, "sigmoid", zero))
+
+
+@pytest.mark.parametrize("E,groups,top,k", [(510, 3, 2, 5), (510, 30, 7, 8), (96, 32, 9, 12), (512, 32, 3, 20)])
+def test_groups_of_odd_sizes(E, groups, top, k):
+    gen = torch.Generator("cuda").manual_seed(E + groups)
+    x = torch.randn(90, E, generator=gen, device="cuda")
+    bias = torch.randn(E, generator=gen, device="cuda") * 0.1
+    index, _ = route(x, k, score="sigmoid", bias=bias, groups=groups, top_groups=top)
+    assert torch.equal(index.long(), fp32_choice(x, k, "sigmoid", bias, groups, top))
