@@ -288,6 +288,11 @@ __device__ __forceinline__ void copy16(void* to, const void* from) {
                  :: "r"(static_cast<uint32_t>(__cvta_generic_to_shared(to))), "l"(from) : "memory");
 }
 
+__device__ __forceinline__ void copy4(void* to, const void* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;"
+                 :: "r"(static_cast<uint32_t>(__cvta_generic_to_shared(to))), "l"(from) : "memory");
+}
+
 // A block's inputs on their way to a warp.
 struct __align__(16) Stage {
     float g[kBlock], w[kBlock];
@@ -335,6 +340,9 @@ adamw_kernel(const __grid_constant__ StepParams a) {
             if (t.vec_g) {
                 copy16(to.g + 4 * lane, t.g + at + 4 * lane);
                 copy16(to.g + 4 * lane + 128, t.g + at + 4 * lane + 128);
+            } else {        // bucket views start anywhere
+#pragma unroll
+                for (int i = 0; i < kBlock; i += 32) copy4(to.g + i + lane, t.g + at + i + lane);
             }
             const int c = 16 * (lane & 15);
             if (lane < 16) copy16(to.m + c, static_cast<const uint8_t*>(t.m) + at + c);
@@ -414,7 +422,7 @@ adamw_kernel(const __grid_constant__ StepParams a) {
                         mc[h] = load4(m_ptr + 128 * h, false, more - 128 * h);
                         vc[h] = load4(v_ptr + 128 * h, false, more - 128 * h);
                     }
-                    if (whole && whole_g) {
+                    if (whole) {
                         const float4 x = *reinterpret_cast<const float4*>(in.g + e);
                         g[h][0] = x.x; g[h][1] = x.y; g[h][2] = x.z; g[h][3] = x.w;
                     } else {
@@ -540,26 +548,33 @@ norm_kernel(const __grid_constant__ NormParams a) {
         const Tensor& t = a.tensors[s];
         if (a.used && !a.used[t.var]) continue;
         const long long at = (u - __ldg(a.first + s)) * a.run * kBlock;
-        const int left = static_cast<int>(min(t.n - at, static_cast<long long>(a.run) * kBlock)) - 4 * lane;
-        const float* const g_ptr = t.g + at + 4 * lane;
-        const bool vec = t.vec_g;
-        // a lane's squares of a run: at most 64, in four fp32 sums
+        const int n = static_cast<int>(min(t.n - at, static_cast<long long>(a.run) * kBlock));
+        const float* const g = t.g + at;
+        // up to three elements on either side of the 16-byte aligned ones
+        const int head = min(n, static_cast<int>(-(reinterpret_cast<uintptr_t>(g) >> 2) & 3));
+        const int vectors = (n - head) / 4, tail = n - head - 4 * vectors;
+        const float4* const v = reinterpret_cast<const float4*>(g + head);
+        // a lane's squares of a run: at most 68, in four fp32 sums
         float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        int e = 0;
-        for (; vec && e + 1024 <= left + 4 * lane; e += 1024) {
-            float g[8][4];
+        const auto add = [&](const float4& x) {
+            part[0] = __fmaf_rn(x.x, x.x, part[0]);
+            part[1] = __fmaf_rn(x.y, x.y, part[1]);
+            part[2] = __fmaf_rn(x.z, x.z, part[2]);
+            part[3] = __fmaf_rn(x.w, x.w, part[3]);
+        };
+        int i = lane;
+        for (; i + 7 * 32 < vectors; i += 8 * 32) {
+            float4 x[8];
 #pragma unroll
-            for (int h = 0; h < 8; ++h) load4(g_ptr + e + 128 * h, true, 4, g[h]);
+            for (int h = 0; h < 8; ++h) x[h] = ddpk::dev::ld_stream(v + i + 32 * h);
 #pragma unroll
-            for (int h = 0; h < 8; ++h)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) part[q] = __fmaf_rn(g[h][q], g[h][q], part[q]);
+            for (int h = 0; h < 8; ++h) add(x[h]);
         }
-        for (; e < left; e += 128) {
-            float g[4];
-            load4(g_ptr + e, vec && e + 4 <= left, left - e, g);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) part[q] = __fmaf_rn(g[q], g[q], part[q]);
+#pragma unroll 4
+        for (; i < vectors; i += 32) add(ddpk::dev::ld_stream(v + i));
+        if (lane < head + tail) {
+            const float x = lane < head ? g[lane] : g[n - tail + lane - head];
+            part[0] = __fmaf_rn(x, x, part[0]);
         }
         sum += static_cast<double>(part[0] + part[1]) + static_cast<double>(part[2] + part[3]);
     }
