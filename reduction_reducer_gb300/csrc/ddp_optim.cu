@@ -646,8 +646,13 @@ struct ddp_adamw {
 
 namespace {
 
-constexpr int kNormCtasPerSm = 8;
-constexpr int kStepCtasPerSm = 128;
+// CTAs per SM at most.  The step takes many short shares, which keep the SMs'
+// streams near one another and end together (BERT-large, 32 / 64 / 128 a SM:
+// 1,397 / 1,373 / 1,355 us, 256: 1,345; GPT-2-medium with 8-bit moments, 128 /
+// 256: 959 / 981); the norm takes one resident wave, of which the last adds all
+// partial sums (BERT-large, 8 / 12 / 14: 205.7 / 200.4 / 241 us).
+constexpr int kNormCtasPerSm = 12;
+constexpr int kStepCtasPerSm[2] = {256, 128};    // 32-bit and 8-bit moments
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
@@ -846,7 +851,7 @@ int ddp_adamw_step(ddp_adamw* o, const ddp_adamw_args* x, void* stream) {
     a.c.seed_lo = static_cast<uint32_t>(x->seed);
     a.c.seed_hi = static_cast<uint32_t>(x->seed >> 32);
     int grid = 0;
-    split(o->step.count, static_cast<int64_t>(o->sms) * kStepCtasPerSm, &grid, &a.piece);
+    split(o->step.count, static_cast<int64_t>(o->sms) * kStepCtasPerSm[o->q8], &grid, &a.piece);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = o->bf16 ? (o->q8 ? launch(adamw_kernel<true, true>, grid, a, st)
                                            : launch(adamw_kernel<true, false>, grid, a, st))

@@ -20,6 +20,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -360,10 +361,14 @@ __device__ __noinline__ bool groups_exact(const RouteParams& a, const T* row, in
 }
 
 template <int LPT, int EPL, typename T>
-__global__ void __launch_bounds__(kThreads, EPL == 32 ? 2 : 3)
+__global__ void __launch_bounds__(kThreads, 3)
 route_kernel(const __grid_constant__ RouteParams a) {
     constexpr int kTokens = 32 / LPT;     // of a warp
+    // 32 experts a lane leave no registers for the next token's logits and for
+    // the biases: those come when their turn is, these lie in shared memory
+    constexpr bool kWide = EPL == 32;
     __shared__ int hist[kMaxExperts];
+    __shared__ float4 wide_bias[kWide ? EPL / 4 : 1][kWide ? LPT : 1];
     __shared__ WarpRows rows[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int l = lane % LPT, tl = lane / LPT;
@@ -373,7 +378,6 @@ route_kernel(const __grid_constant__ RouteParams a) {
         for (int i = threadIdx.x; i < E; i += kThreads) hist[i] = 0;
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
-    __syncthreads();
 
     // this lane's experts: n from e0 on, of group g
     const int size = E / a.groups, group_lanes = a.group_slots / EPL;
@@ -382,12 +386,15 @@ route_kernel(const __grid_constant__ RouteParams a) {
     const int n = g < a.groups ? max(0, min(size - off, EPL)) : 0;
     const bool by_logit = !a.bias && a.groups == 1;
     const bool vec = a.vec && (e0 * sizeof(T)) % 16 == 0;
-    float bias[EPL], widest = 0.0f;
+    float bias[kWide ? 1 : EPL], widest = 0.0f;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-        bias[j] = a.bias && j < n ? a.bias[e0 + j] : 0.0f;
-        widest = fmaxf(widest, bias[j] == bias[j] ? fabsf(bias[j]) : __int_as_float(0x7f800000));
+        const float b = a.bias && j < n ? a.bias[e0 + j] : 0.0f;
+        widest = fmaxf(widest, b == b ? fabsf(b) : __int_as_float(0x7f800000));
+        if constexpr (!kWide) bias[j] = b;
+        else if (warp == 0 && lane < LPT) reinterpret_cast<float*>(&wide_bias[j / 4][lane])[j % 4] = b;
     }
+    __syncthreads();
     // scores + bias lie in [-range, range), a power of two; keys hold them times 2 / range
     widest = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(widest)));
     const bool fast = a.fits && widest < 0x1p20f;
@@ -402,12 +409,12 @@ route_kernel(const __grid_constant__ RouteParams a) {
     long long t0 = (static_cast<long long>(blockIdx.x) * kWarps + warp) * tile;
     // the logits of this lane's next token
     float x[EPL];
-    const auto load = [&](long long t) {
+    const auto load = [&](long long t, bool logits) {
         const bool in = t < a.tokens;
-        if (fast) load_lane<EPL>(static_cast<const T*>(a.logits) + t * a.stride + e0, in ? n : 0, vec, 0.0f, x);
+        if (fast && logits) load_lane<EPL>(static_cast<const T*>(a.logits) + t * a.stride + e0, in ? n : 0, vec, 0.0f, x);
         return in && (!a.mask || a.mask[t]);
     };
-    bool next_on = load(t0 + tl);
+    bool next_on = load(t0 + tl, !kWide);
     for (; t0 < a.tokens; t0 += stride) {
         for (int rep = 0; rep < a.reps; ++rep) {
             const int slot = rep * kTokens + tl;                  // the token's place in the tile
@@ -416,6 +423,7 @@ route_kernel(const __grid_constant__ RouteParams a) {
             int32_t* sel = mem.sel + slot * k;
             bool again = on, reorder = false;                     // choose exactly; put into order exactly
             if (fast) {
+                if (kWide) load(t0 + slot, true);
                 uint32_t key[EPL];
                 float zero = 0.0f;                                // NaN where a logit is not finite
 #pragma unroll
@@ -449,15 +457,19 @@ route_kernel(const __grid_constant__ RouteParams a) {
                     }
                     // [4, 8) is where fp32 has steps of 2^-21; the exponent is shifted out
 #pragma unroll
-                    for (int j = 0; j < EPL; ++j)
-                        key[j] = __float_as_uint(fmaf(x[j] + bias[j], over_range, 6.0f)) * 512u + (place - j);
+                    for (int j = 0; j < EPL; ++j) {
+                        float b;
+                        if constexpr (kWide) b = reinterpret_cast<const float*>(&wide_bias[j / 4][l])[j % 4];
+                        else b = bias[j];
+                        key[j] = __float_as_uint(fmaf(x[j] + b, over_range, 6.0f)) * 512u + (place - j);
+                    }
                 }
                 if (n < EPL || !on) {
 #pragma unroll
                     for (int j = 0; j < EPL; ++j)
                         if (!on || j >= n) key[j] = 0;
                 }
-                next_on = load(next);                             // on its way while this one is chosen
+                next_on = load(next, !kWide);                     // on its way while this one is chosen
                 uint32_t head[8];                                 // this lane's best
                 top8(key, head);
 
@@ -522,7 +534,7 @@ route_kernel(const __grid_constant__ RouteParams a) {
                     for (int r = l; r < k; r += LPT) sel[r] = 0;
                     if (l == 0) mem.stat[slot] = Stat{0.0f, 1.0f, 0};
                 }
-                next_on = load(next);
+                next_on = load(next, false);
             }
             const unsigned exactly = __ballot_sync(kAll, again);
             unsigned left = exactly | __ballot_sync(kAll, reorder);
@@ -721,6 +733,19 @@ cudaError_t launch(K kernel, long long warps, int sms, int ctas_per_sm, const Ro
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+// Of the current device, asked for once.
+cudaError_t multiprocessors(int* sms) {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    *sms = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (*sms) return cudaSuccess;
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
+    return e;
+}
+
 int power_of_two(int x) {
     int p = 1;
     while (p < x) p *= 2;
@@ -735,7 +760,7 @@ cudaError_t launch_sized(bool backward, int sms, RouteParams& a, cudaStream_t st
     const long long groups = (a.tokens + kTokens - 1) / kTokens;
     if constexpr (EPL < 32)
         if (backward) return launch(route_backward_whole_kernel<LPT, EPL, T>, groups, sms, kBackwardCtas, a, stream);
-    constexpr int kForwardCtas = EPL == 32 ? 2 : 3;      // what fits an SM
+    constexpr int kForwardCtas = 3;                      // what fits an SM
     // with tokens enough for every warp, those of four rounds are weighed
     // together: their slots then fill the warp's lanes
     a.reps = kTokens < 4 && groups >= 4LL * kForwardCtas * sms * kWarps ? 4 / kTokens : 1;
@@ -744,9 +769,8 @@ cudaError_t launch_sized(bool backward, int sms, RouteParams& a, cudaStream_t st
 
 template <typename T>
 cudaError_t launch_any(bool backward, RouteParams& a, cudaStream_t stream) {
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    int sms = 0;
+    const cudaError_t e = multiprocessors(&sms);
     if (e != cudaSuccess) return e;
     if (backward && !(a.softmax && !a.renorm)) {
         a.slot_lanes = power_of_two(a.k);
@@ -772,12 +796,14 @@ cudaError_t launch_any(bool backward, RouteParams& a, cudaStream_t stream) {
     const auto slots_of = [&](int epl) { return power_of_two((size + epl - 1) / epl) * epl; };
     a.fits = 1;
     // 32 experts a lane put four to sixteen tokens into a warp, whose k rounds
-    // they share; more registers and a longer chain for each.  65,536 tokens,
-    // against 8 (16) a lane: 64 experts 13.3 / 15.3 us, 128 21.9 / 27.9, 256
-    // 33.8 / 39.2, 512 61.7 / 57.9; in 8 groups of 32, 8,192 tokens 17.2 / 12.3
-    // and 65,536 44.2 / 42.7.  More than eight of a token's best in one lane
-    // must stay rare.
-    if (a.groups == 1 && a.E >= 64 && a.E <= 256 && (a.k < 8 || a.k <= 2 * ((a.E + 31) / 32))) {
+    // they share, for a longer chain of instructions: from about 2^20 logits on.
+    // Against 8 (16) a lane, 65,536 tokens over 64 experts 11.6 / 14.6 us, 256
+    // 31.2 / 39.2, 512 61.7 / 57.9; 8,192 over 64 6.0 / 5.3, over 128 5.8 / 6.8;
+    // 256 over 256 5.4 / 3.6; in 8 groups of 32, 8,192 tokens 17.4 / 13.1 and
+    // 65,536 43.5 / 43.0.  More than eight of a token's best in one lane must
+    // stay rare.
+    if (a.groups == 1 && a.E >= 64 && a.E <= 256 && a.tokens * a.E >= 1 << 20 &&
+        (a.k < 8 || a.k <= 2 * ((a.E + 31) / 32))) {
         a.group_slots = slots_of(32);
         if (a.E <= 64) return launch_sized<2, 32, T>(false, sms, a, stream);
         if (a.E <= 128) return launch_sized<4, 32, T>(false, sms, a, stream);
