@@ -326,3 +326,69 @@ def test_groups_of_odd_sizes(E, groups, top, k):
     bias = torch.randn(E, generator=gen, device="cuda") * 0.1
     index, _ = route(x, k, score="sigmoid", bias=bias, groups=groups, top_groups=top)
     assert torch.equal(index.long(), fp32_choice(x, k, "sigmoid", bias, groups, top))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("E,k", [(64, 7), (64, 12), (100, 4), (128, 8), (130, 3), (200, 14), (256, 8), (256, 16)])
+def test_more_than_a_million_logits(E, k, dtype):
+    """Batches large enough for every layout, against the fp32 definition: ordinary rows, rows of near ties, sorted
+    ones, masked ones and ones that are not numbers, mixed within warps."""
+    T = (1 << 20) // E + 37
+    gen = torch.Generator("cuda").manual_seed(E * k)
+    x = torch.randn(T, E, generator=gen, device="cuda") * 1.5
+    x[1::7] = 1.0 + torch.randint(0, 4, x[1::7].shape, generator=gen, device="cuda") * 2.0 ** -23
+    x[2::7] = torch.linspace(3, -3, E, device="cuda")
+    x[3::11] = x[3::11].round()                                      # exact ties
+    x = x.to(KINDS[dtype])
+    mask = torch.rand(T, generator=gen, device="cuda") < 0.9
+    x[~mask] = float("nan")
+    x[5::301] = float("-inf")
+    x[6::301, : E - 2] = float("-inf")
+    x[7::301, 3] = float("nan")
+    bias = torch.randn(E, generator=gen, device="cuda") * 0.2
+    live = mask.clone()
+    live[7::301] = False                                             # NaN weights: checked by themselves
+    y = torch.where(torch.isnan(x), float("-inf"), x.float())
+    for score, b in (("softmax", None), ("sigmoid", bias), ("sigmoid", None)):
+        counts = torch.zeros(E, dtype=torch.int32, device="cuda")
+        index, w = route(x, k, score=score, bias=b, renorm=True, mask=mask, counts=counts)
+        c = y if b is None else torch.where(y > float("-inf"), 1 / (1 + torch.exp(-y)) + b, float("-inf"))
+        order = c.argsort(dim=1, descending=True, stable=True)[:, :k]
+        want = torch.where(c.gather(1, order) > float("-inf"), order, -1)
+        assert torch.equal(index.long()[live], want[live])
+        assert bool((index[~mask] == -1).all()) and bool((w[~mask] == 0).all())
+        assert bool(torch.isnan(w[7::301][mask[7::301]]).all())
+        chosen = index[index >= 0].long()
+        assert torch.equal(counts.long(), torch.bincount(chosen, minlength=E))
+        d = y.double()
+        s = torch.sigmoid(d) if score == "sigmoid" else torch.exp(d - d.amax(1, keepdim=True).clamp(min=-1e30))
+        s = torch.where(index >= 0, s.gather(1, index.clamp(min=0).long()), 0.0)
+        total = s.sum(1, keepdim=True)
+        ref = torch.where(total > 0, s / total, 0.0)
+        assert bool(((w.double() - ref).abs()[live] <= 64 * U * ref[live]).all())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_softmax_with_a_bias_and_many_tokens(score):
+    """Against the 64-bit scores where these tell the experts apart by more than the bound of a score, 27u, twice."""
+    T, E, k = 9000, 256, 8
+    gen = torch.Generator("cuda").manual_seed(8)
+    x = torch.randn(T, E, generator=gen, device="cuda")
+    bias = torch.randn(E, generator=gen, device="cuda") * 0.01
+    for groups, top in ((1, 1), (8, 4)):
+        index, w = route(x, k, score=score, bias=bias, groups=groups, top_groups=top)
+        s = torch.softmax(x.double(), 1) if score == "softmax" else torch.sigmoid(x.double())
+        c = s + bias.double()
+        clear = torch.ones(T, dtype=torch.bool, device="cuda")
+        if groups > 1:
+            worth = c.view(T, groups, -1).topk(2).values.sum(2)
+            ranked = worth.sort(dim=1, descending=True)
+            clear &= ranked.values[:, top - 1] - ranked.values[:, top] > 1e-5
+            stay = torch.zeros(T, groups, dtype=torch.bool, device="cuda").scatter_(1, ranked.indices[:, :top], True)
+            c = torch.where(stay.repeat_interleave(E // groups, dim=1), c, -9.0)
+        ranked = c.sort(dim=1, descending=True)
+        clear &= (ranked.values[:, :k] - ranked.values[:, 1:k + 1]).amin(1) > 1e-5
+        assert float(clear.float().mean()) > 0.5
+        assert torch.equal(index.long()[clear], ranked.indices[:, :k][clear])
+        ref = s.gather(1, index.long())
+        assert bool(((w.double() - ref).abs() <= 64 * U * ref).all())
