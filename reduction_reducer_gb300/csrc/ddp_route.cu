@@ -1,12 +1,13 @@
 // Routing of tokens to experts and its gradient.
 //
-// A token's experts lie EPL to a lane over LPT lanes, so a warp holds 32 / LPT
-// tokens; a group's experts start on a lane of their own (its last lanes may be
-// partly empty) and take a power of two of lanes.  The choice goes by 32-bit
-// keys: 23 bits of the compared value above 9 bits of 511 - expert, so no two
-// are equal, the larger key is the better expert, and ties of the value go to
-// the lowest expert.  Each lane sorts its eight largest; the k best of a token
-// are the largest of its lanes' first, k times over.
+// A token's experts lie in runs of 8 `chunks` to a lane over LPT lanes, so a
+// warp holds 32 / LPT tokens; a group's experts start on a lane of their own
+// (its last lanes may be partly empty) and take a power of two of lanes.  The
+// choice goes by 32-bit keys: 23 bits of the compared value above 9 bits of 511
+// - expert, so no two are equal, the larger key is the better expert, and ties
+// of the value go to the lowest expert.  Each lane keeps the eight largest of
+// its chunks sorted; the k best of a token are the largest of its lanes' first,
+// k times over.
 //
 // 23 bits, and scores from the hardware's approximate exponential and
 // reciprocal, do not always tell which of two experts the fp32 definition puts
@@ -33,6 +34,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxExperts = 512;
 constexpr int kMaxSlots = 256;           // slots of a warp's tokens at once
 constexpr unsigned kAll = 0xffffffffu;
+constexpr int kForwardCtas = 3;          // route_kernel's on an SM: 80 registers; at 64 it spills (65,536 tokens 37.7 -> 49.5 us)
+constexpr int kBackwardCtas = 8;         // CTAs per SM at most
 
 // Least distance, in units of 2^-21 (the keys' step), of two values whose
 // order is certain.  A sigmoid score plus bias is within 0.9e-6 of the fp32
@@ -55,7 +58,8 @@ struct RouteParams {
     int E, k, groups, top_groups;
     int softmax, renorm;
     float scale;
-    int group_slots;             // slots of a group: a multiple of EPL, over it a power of two
+    int chunks;                  // forward: of 8 experts, of a lane
+    int group_slots;             // forward: slots of a group: a multiple of a lane's, over it a power of two
     int reps;                    // forward: rounds of 32 / LPT tokens before their slots are weighed
     int fits;                    // forward: the groups fit the lanes' slots (else every token is chosen exactly)
     int vec;                     // rows start 16-byte aligned (chosen-only backward: the gradient's, next to one another)
@@ -185,27 +189,16 @@ __device__ __forceinline__ void sort8(uint32_t (&x)[8]) {
     order(x[1], x[2]); order(x[3], x[4]); order(x[5], x[6]);
 }
 
-// The eight largest of N, in descending order: sorted eights, of which two give
-// the larger of x[i] and y[7 - i], a bitonic sequence that three steps sort.
-template <int N>
-__device__ __forceinline__ void top8(const uint32_t (&key)[N], uint32_t (&x)[8]) {
+// The eight largest of two sorted eights, in descending order: the larger of
+// x[i] and y[7 - i] are a bitonic sequence, which three steps sort.
+__device__ __forceinline__ void merge8(uint32_t (&x)[8], const uint32_t (&y)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = key[i];
-    sort8(x);
+    for (int i = 0; i < 8; ++i) x[i] = max(x[i], y[7 - i]);
 #pragma unroll
-    for (int c = 8; c < N; c += 8) {
-        uint32_t y[8];
+    for (int d = 4; d; d /= 2)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = key[c + i];
-        sort8(y);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = max(x[i], y[7 - i]);
-#pragma unroll
-        for (int d = 4; d; d /= 2)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (!(i & d)) order(x[i], x[i + d]);
-    }
+        for (int i = 0; i < 8; ++i)
+            if (!(i & d)) order(x[i], x[i + d]);
 }
 
 // What the scores of a token's slots are computed from.
@@ -330,18 +323,15 @@ __device__ __forceinline__ void order_exact(const RouteParams& a, const T* row, 
 
 // Whether this lane's group stays, by the fp32 definition; for all tokens of a
 // warp.  The lane's experts are n from e0 on.
-template <int LPT, int EPL, typename T>
+template <int LPT, typename T>
 __device__ __noinline__ bool groups_exact(const RouteParams& a, const T* row, int e0, int n, float top, float sum, int g,
                                           int group_lanes, int size) {
     float a1 = neg_inf(), a2 = neg_inf();
 #pragma unroll 4
-    for (int j = 0; j < EPL; ++j) {
-        float c = neg_inf();
-        if (j < n) {
-            const float x = widen(row[e0 + j]);
-            c = a.softmax ? __fdiv_rn(expf(x - top), sum) : sigmoid(x);
-            if (a.bias) c = __fadd_rn(c, a.bias[e0 + j]);
-        }
+    for (int j = 0; j < n; ++j) {
+        const float x = widen(row[e0 + j]);
+        float c = a.softmax ? __fdiv_rn(expf(x - top), sum) : sigmoid(x);
+        if (a.bias) c = __fadd_rn(c, a.bias[e0 + j]);
         a2 = fmaxf(a2, fminf(a1, c));
         a1 = fmaxf(a1, c);
     }
@@ -360,118 +350,140 @@ __device__ __noinline__ bool groups_exact(const RouteParams& a, const T* row, in
     return stays;
 }
 
-template <int LPT, int EPL, typename T>
-__global__ void __launch_bounds__(kThreads, 3)
+template <int LPT, typename T>
+__global__ void __launch_bounds__(kThreads, kForwardCtas)
 route_kernel(const __grid_constant__ RouteParams a) {
     constexpr int kTokens = 32 / LPT;     // of a warp
-    // 32 experts a lane leave no registers for the next token's logits and for
-    // the biases: those come when their turn is, these lie in shared memory
-    constexpr bool kWide = EPL == 32;
     __shared__ int hist[kMaxExperts];
-    __shared__ float4 wide_bias[kWide ? EPL / 4 : 1][kWide ? LPT : 1];
+    __shared__ float4 biases[kMaxExperts / 4];     // piece h of chunk c of lane l at (2 c + h) LPT + l
+    __shared__ uint32_t widest_bits;               // largest magnitude of a bias
     __shared__ WarpRows rows[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int l = lane % LPT, tl = lane / LPT;
-    const int E = a.E, k = a.k;
+    const int E = a.E, k = a.k, chunks = a.chunks, lane_slots = 8 * chunks;
     WarpRows& mem = rows[warp];
     if (a.counts)
         for (int i = threadIdx.x; i < E; i += kThreads) hist[i] = 0;
+    if (threadIdx.x == 0) widest_bits = 0;
+    __syncthreads();
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
 
     // this lane's experts: n from e0 on, of group g
-    const int size = E / a.groups, group_lanes = a.group_slots / EPL;
-    const int g = l * EPL / a.group_slots, off = l * EPL % a.group_slots;
+    const int size = E / a.groups, group_lanes = a.group_slots / lane_slots;
+    const int g = l * lane_slots / a.group_slots, off = l * lane_slots % a.group_slots;
     const int e0 = g * size + off;
-    const int n = g < a.groups ? max(0, min(size - off, EPL)) : 0;
+    const int n = g < a.groups ? max(0, min(size - off, lane_slots)) : 0;
     const bool by_logit = !a.bias && a.groups == 1;
     const bool vec = a.vec && (e0 * sizeof(T)) % 16 == 0;
-    float bias[kWide ? 1 : EPL], widest = 0.0f;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        const float b = a.bias && j < n ? a.bias[e0 + j] : 0.0f;
-        widest = fmaxf(widest, b == b ? fabsf(b) : __int_as_float(0x7f800000));
-        if constexpr (!kWide) bias[j] = b;
-        else if (warp == 0 && lane < LPT) reinterpret_cast<float*>(&wide_bias[j / 4][lane])[j % 4] = b;
-    }
+    if (a.bias)
+        for (int e = threadIdx.x; e < E; e += kThreads) {
+            const float b = a.bias[e];
+            const int at = e / size * a.group_slots + e % size, j = at % lane_slots;
+            reinterpret_cast<float*>(&biases[j / 4 * LPT + at / lane_slots])[j % 4] = b;
+            atomicMax(&widest_bits, __float_as_uint(b) & 0x7fffffffu);    // of a NaN above infinity's
+        }
     __syncthreads();
     // scores + bias lie in [-range, range), a power of two; keys hold them times 2 / range
-    widest = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(widest)));
+    const float widest = __uint_as_float(widest_bits);
     const bool fast = a.fits && widest < 0x1p20f;
     const float over_range = 2.0f / __uint_as_float((__float_as_uint(1.0f + widest) & 0x7f800000u) + 0x00800000u);
     const uint32_t by_score = a.softmax ? kMarginSoftmax : kMarginSigmoid;
     const uint32_t near = !by_logit ? (by_score + 1) << 9 : sizeof(T) == 2 ? 0u : 2u << 9;   // a key holds all of a bf16 logit
     const uint32_t over_k = (65536u + k - 1) / k;                 // i / k for i < 256
+    // renormalised softmax weights of a choice by logits need no sum over the
+    // row, and their largest logit is that of the first chosen
     const bool need_sum = a.softmax && (!a.renorm || !by_logit);
 
     const int tile = kTokens * a.reps;
     const long long stride = static_cast<long long>(gridDim.x) * kWarps * tile;
     long long t0 = (static_cast<long long>(blockIdx.x) * kWarps + warp) * tile;
-    // the logits of this lane's next token
-    float x[EPL];
-    const auto load = [&](long long t, bool logits) {
-        const bool in = t < a.tokens;
-        if (fast && logits) load_lane<EPL>(static_cast<const T*>(a.logits) + t * a.stride + e0, in ? n : 0, vec, 0.0f, x);
-        return in && (!a.mask || a.mask[t]);
+    // this lane's next eight logits
+    float x[8];
+    const auto load = [&](long long t, int c) {
+        const int left = t < a.tokens ? n - 8 * c : 0;
+        if (fast) load_lane<8>(static_cast<const T*>(a.logits) + t * a.stride + e0 + 8 * c, min(left, 8), vec, 0.0f, x);
     };
-    bool next_on = load(t0 + tl, !kWide);
+    const auto routed = [&](long long t) { return t < a.tokens && (!a.mask || a.mask[t]); };
+    bool next_on = routed(t0 + tl);
+    load(t0 + tl, 0);
     for (; t0 < a.tokens; t0 += stride) {
         for (int rep = 0; rep < a.reps; ++rep) {
             const int slot = rep * kTokens + tl;                  // the token's place in the tile
             const long long next = rep + 1 < a.reps ? t0 + slot + kTokens : t0 + stride + tl;
             const bool on = next_on;
+            next_on = routed(next);
             int32_t* sel = mem.sel + slot * k;
             bool again = on, reorder = false;                     // choose exactly; put into order exactly
             if (fast) {
-                if (kWide) load(t0 + slot, true);
-                uint32_t key[EPL];
-                float zero = 0.0f;                                // NaN where a logit is not finite
-#pragma unroll
-                for (int j = 0; j < EPL; ++j) zero = fmaf(x[j], 0.0f, zero);
-                again = !(zero == 0.0f);
-                float top = 0.0f, sum = 1.0f;
-                if (a.softmax) {
+                float top = 0.0f, sum = 1.0f, over = 1.0f;
+                if (need_sum) {
+                    const T* from = static_cast<const T*>(a.logits) + (t0 + slot) * a.stride + e0;
                     uint32_t most = 0;
+                    for (int c = 0; c < chunks; ++c) {
+                        float y[8];
+                        load_lane<8>(from + 8 * c, on ? min(n - 8 * c, 8) : 0, vec, neg_inf(), y);
 #pragma unroll
-                    for (int j = 0; j < EPL; ++j) most = max(most, j < n ? order_bits(x[j]) : 0u);
+                        for (int j = 0; j < 8; ++j) most = max(most, key_of(y[j]));
+                    }
                     top = number_of(token_max<LPT>(most));
-                    if (need_sum) {
-                        sum = 0.0f;
+                    sum = 0.0f;
+                    for (int c = 0; c < chunks; ++c) {
+                        float y[8];
+                        load_lane<8>(from + 8 * c, on ? min(n - 8 * c, 8) : 0, vec, neg_inf(), y);
 #pragma unroll
-                        for (int j = 0; j < EPL; ++j) sum += j < n ? fast_exp(x[j] - top) : 0.0f;
-                        sum = token_sum<LPT>(sum);
+                        for (int j = 0; j < 8; ++j) sum += fast_exp(y[j] - top);
                     }
+                    sum = token_sum<LPT>(sum);
+                    over = __fdividef(1.0f, sum);
                 }
-                const uint32_t place = kMaxExperts - 1 - e0;
-                if (by_logit) {
-#pragma unroll
-                    for (int j = 0; j < EPL; ++j) key[j] = (order_bits(x[j]) & ~0x1ffu) | (place - j);
-                } else {
-                    if (a.softmax) {
-                        const float over = __fdividef(1.0f, sum);
-#pragma unroll
-                        for (int j = 0; j < EPL; ++j) x[j] = fast_exp(x[j] - top) * over;
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < EPL; ++j) x[j] = fast_sigmoid(x[j]);
-                    }
-                    // [4, 8) is where fp32 has steps of 2^-21; the exponent is shifted out
-#pragma unroll
-                    for (int j = 0; j < EPL; ++j) {
-                        float b;
-                        if constexpr (kWide) b = reinterpret_cast<const float*>(&wide_bias[j / 4][l])[j % 4];
-                        else b = bias[j];
-                        key[j] = __float_as_uint(fmaf(x[j] + b, over_range, 6.0f)) * 512u + (place - j);
-                    }
-                }
-                if (n < EPL || !on) {
-#pragma unroll
-                    for (int j = 0; j < EPL; ++j)
-                        if (!on || j >= n) key[j] = 0;
-                }
-                next_on = load(next, !kWide);                     // on its way while this one is chosen
                 uint32_t head[8];                                 // this lane's best
-                top8(key, head);
+                float zero = 0.0f;                                // NaN where a logit is not finite
+#pragma unroll 1
+                for (int c = 0; c < chunks; ++c) {
+                    uint32_t key[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) zero = fmaf(x[j], 0.0f, zero);
+                    const uint32_t place = kMaxExperts - 1 - e0 - 8 * c;
+                    if (by_logit) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) key[j] = (order_bits(x[j]) & ~0x1ffu) | (place - j);
+                    } else {
+                        if (a.softmax) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) x[j] = fast_exp(x[j] - top) * over;
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) x[j] = fast_sigmoid(x[j]);
+                        }
+                        if (a.bias) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const float4 b = biases[(2 * c + h) * LPT + l];
+                                x[4 * h] += b.x; x[4 * h + 1] += b.y; x[4 * h + 2] += b.z; x[4 * h + 3] += b.w;
+                            }
+                        }
+                        // [4, 8) is where fp32 has steps of 2^-21; the exponent is shifted out
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) key[j] = __float_as_uint(fmaf(x[j], over_range, 6.0f)) * 512u + (place - j);
+                    }
+                    const int left = on ? n - 8 * c : 0;
+                    if (left < 8) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (j >= left) key[j] = 0;
+                    }
+                    // the next eight are on their way while these are sorted
+                    load(c + 1 < chunks ? t0 + slot : next, c + 1 < chunks ? c + 1 : 0);
+                    sort8(key);
+                    if (c == 0) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) head[j] = key[j];
+                    } else {
+                        merge8(head, key);
+                    }
+                }
+                again = !(zero == 0.0f);
 
                 if (a.top_groups < a.groups) {
                     uint32_t a1 = head[0] >> 9, a2 = head[1] >> 9;
@@ -490,8 +502,8 @@ route_kernel(const __grid_constant__ RouteParams a) {
                     }
                     const uint32_t out = token_max<LPT>(worth);
                     if (__any_sync(kAll, on && (worst >> 5) - (out >> 5) < 2 * by_score))
-                        stays = groups_exact<LPT, EPL>(a, static_cast<const T*>(a.logits) + (t0 + slot) * a.stride, e0, on ? n : 0,
-                                                       top, sum, g, group_lanes, size);
+                        stays = groups_exact<LPT>(a, static_cast<const T*>(a.logits) + (t0 + slot) * a.stride, e0, on ? n : 0,
+                                                  top, sum, g, group_lanes, size);
                     if (!stays) head[0] = 0;
                 }
 
@@ -526,15 +538,12 @@ route_kernel(const __grid_constant__ RouteParams a) {
                     if (reorder && (k == 32 || after - beyond < near)) again = true;
                 }
                 // a lane of more than eight experts may have had a ninth among the best
-                if (EPL > 8) again |= on && had && head[0] == 0;
+                again |= on && n > 8 && had && head[0] == 0;
                 if (l == 0) mem.stat[slot] = Stat{top, sum, 0};
                 again = again && on;
-            } else {
-                if (!on) {
-                    for (int r = l; r < k; r += LPT) sel[r] = 0;
-                    if (l == 0) mem.stat[slot] = Stat{0.0f, 1.0f, 0};
-                }
-                next_on = load(next, false);
+            } else if (!on) {
+                for (int r = l; r < k; r += LPT) sel[r] = 0;
+                if (l == 0) mem.stat[slot] = Stat{0.0f, 1.0f, 0};
             }
             const unsigned exactly = __ballot_sync(kAll, again);
             unsigned left = exactly | __ballot_sync(kAll, reorder);
@@ -559,8 +568,13 @@ route_kernel(const __grid_constant__ RouteParams a) {
             int e = -1;
             if (chosen) {
                 e = kMaxExperts - 1 - (chosen & (kMaxExperts - 1));
-                const float x = widen(static_cast<const T*>(a.logits)[(t0 + token) * a.stride + e]);
-                const Stat st = mem.stat[token];
+                const T* row = static_cast<const T*>(a.logits) + (t0 + token) * a.stride;
+                const float x = widen(row[e]);
+                Stat st = mem.stat[token];
+                if (a.softmax && !need_sum) {
+                    st.top = widen(row[kMaxExperts - 1 - (mem.sel[token * k] & (kMaxExperts - 1))]);
+                    st.sum = 1.0f;
+                }
                 score = a.softmax ? __fdiv_rn(expf(x - st.top), st.sum) : sigmoid(x);
                 if (a.counts) atomicAdd(hist + e, 1);
             }
@@ -752,19 +766,20 @@ int power_of_two(int x) {
     return p;
 }
 
-constexpr int kBackwardCtas = 8;
-
-template <int LPT, int EPL, typename T>
-cudaError_t launch_sized(bool backward, int sms, RouteParams& a, cudaStream_t stream) {
+template <int LPT, typename T>
+cudaError_t launch_forward(int sms, RouteParams& a, cudaStream_t stream) {
     constexpr int kTokens = 32 / LPT;
     const long long groups = (a.tokens + kTokens - 1) / kTokens;
-    if constexpr (EPL < 32)
-        if (backward) return launch(route_backward_whole_kernel<LPT, EPL, T>, groups, sms, kBackwardCtas, a, stream);
-    constexpr int kForwardCtas = 3;                      // what fits an SM
     // with tokens enough for every warp, those of four rounds are weighed
     // together: their slots then fill the warp's lanes
     a.reps = kTokens < 4 && groups >= 4LL * kForwardCtas * sms * kWarps ? 4 / kTokens : 1;
-    return launch(route_kernel<LPT, EPL, T>, (groups + a.reps - 1) / a.reps, sms, kForwardCtas, a, stream);
+    return launch(route_kernel<LPT, T>, (groups + a.reps - 1) / a.reps, sms, kForwardCtas, a, stream);
+}
+
+template <int LPT, int EPL, typename T>
+cudaError_t launch_whole(int sms, const RouteParams& a, cudaStream_t stream) {
+    constexpr int kTokens = 32 / LPT;
+    return launch(route_backward_whole_kernel<LPT, EPL, T>, (a.tokens + kTokens - 1) / kTokens, sms, kBackwardCtas, a, stream);
 }
 
 template <typename T>
@@ -780,51 +795,53 @@ cudaError_t launch_any(bool backward, RouteParams& a, cudaStream_t stream) {
                       a, stream);
     }
     if (backward) {
-        a.group_slots = 512;
-        if (a.E > 256) return launch_sized<32, 16, T>(true, sms, a, stream);
+        if (a.E > 256) return launch_whole<32, 16, T>(sms, a, stream);
         switch (power_of_two((a.E + 7) / 8)) {
-            case 1: return launch_sized<1, 8, T>(true, sms, a, stream);
-            case 2: return launch_sized<2, 8, T>(true, sms, a, stream);
-            case 4: return launch_sized<4, 8, T>(true, sms, a, stream);
-            case 8: return launch_sized<8, 8, T>(true, sms, a, stream);
-            case 16: return launch_sized<16, 8, T>(true, sms, a, stream);
-            default: return launch_sized<32, 8, T>(true, sms, a, stream);
+            case 1: return launch_whole<1, 8, T>(sms, a, stream);
+            case 2: return launch_whole<2, 8, T>(sms, a, stream);
+            case 4: return launch_whole<4, 8, T>(sms, a, stream);
+            case 8: return launch_whole<8, 8, T>(sms, a, stream);
+            case 16: return launch_whole<16, 8, T>(sms, a, stream);
+            default: return launch_whole<32, 8, T>(sms, a, stream);
         }
     }
     // slots of a group, each group from a lane of its own on
     const int size = a.E / a.groups;
-    const auto slots_of = [&](int epl) { return power_of_two((size + epl - 1) / epl) * epl; };
-    a.fits = 1;
-    // 32 experts a lane put four to sixteen tokens into a warp, whose k rounds
-    // they share, for a longer chain of instructions: from about 2^20 logits on.
-    // Against 8 (16) a lane, 65,536 tokens over 64 experts 11.6 / 14.6 us, 256
-    // 31.2 / 39.2, 512 61.7 / 57.9; 8,192 over 64 6.0 / 5.3, over 128 5.8 / 6.8;
-    // 256 over 256 5.4 / 3.6; in 8 groups of 32, 8,192 tokens 17.4 / 13.1 and
-    // 65,536 43.5 / 43.0.  More than eight of a token's best in one lane must
-    // stay rare.
-    if (a.groups == 1 && a.E >= 64 && a.E <= 256 && a.tokens * a.E >= 1 << 20 &&
-        (a.k < 8 || a.k <= 2 * ((a.E + 31) / 32))) {
-        a.group_slots = slots_of(32);
-        if (a.E <= 64) return launch_sized<2, 32, T>(false, sms, a, stream);
-        if (a.E <= 128) return launch_sized<4, 32, T>(false, sms, a, stream);
-        return launch_sized<8, 32, T>(false, sms, a, stream);
+    int lanes = 0;
+    a.fits = 0;
+    // Four chunks a lane put several tokens into a warp, which share its rounds
+    // and its bookkeeping, for a longer chain of instructions: from about 2^20
+    // logits on.  Against one, 65,536 tokens over 64 experts 10.3 / 15.6 us, 128
+    // 17.2 / 27.8, 256 27.4 / 39.2, 512 49.3 / 54.0, over 256 in 8 groups 37.7 /
+    // 47.1; 2,048 tokens over 128 5.3 / 4.2, 256 over 256 in groups 6.4 / 4.5.
+    for (a.chunks = a.tokens * a.E >= 1 << 20 ? 4 : 1; a.chunks; a.chunks /= 2) {
+        const int mine = 8 * a.chunks;
+        a.group_slots = power_of_two((size + mine - 1) / mine) * mine;
+        lanes = power_of_two(a.groups * a.group_slots / mine);
+        const int staying = a.top_groups * a.group_slots / mine;
+        a.fits = lanes <= 32 && lanes * mine <= kMaxExperts;
+        // more chunks while they waste no lanes, the slots fit, and more than
+        // eight of a token's best in one lane stay rare
+        if (a.chunks == 1 || (a.fits && a.groups * a.group_slots <= a.E + a.E / 2 && 32 / lanes * a.k <= kMaxSlots &&
+                              (a.k < 8 || a.k <= 2 * staying)))
+            break;
     }
-    a.group_slots = slots_of(8);
-    switch (power_of_two(a.groups * a.group_slots / 8)) {
-        case 1: return launch_sized<1, 8, T>(false, sms, a, stream);
-        case 2: return launch_sized<2, 8, T>(false, sms, a, stream);
-        case 4: return launch_sized<4, 8, T>(false, sms, a, stream);
-        case 8: return launch_sized<8, 8, T>(false, sms, a, stream);
-        case 16: return launch_sized<16, 8, T>(false, sms, a, stream);
-        case 32: return launch_sized<32, 8, T>(false, sms, a, stream);
-        default: break;
+    if (!a.fits) {
+        // 256 slots are not enough for one chunk a lane: two
+        a.chunks = 2;
+        a.group_slots = power_of_two((size + 15) / 16) * 16;
+        lanes = 32;
+        a.fits = a.groups * a.group_slots <= kMaxExperts;
+        if (!a.fits) a.group_slots = kMaxExperts;    // every token is chosen exactly: one a warp
     }
-    a.group_slots = slots_of(16);
-    if (a.groups * a.group_slots > 512) {    // every token is chosen exactly: one a warp
-        a.fits = 0;
-        a.group_slots = 512;
+    switch (lanes) {
+        case 1: return launch_forward<1, T>(sms, a, stream);
+        case 2: return launch_forward<2, T>(sms, a, stream);
+        case 4: return launch_forward<4, T>(sms, a, stream);
+        case 8: return launch_forward<8, T>(sms, a, stream);
+        case 16: return launch_forward<16, T>(sms, a, stream);
+        default: return launch_forward<32, T>(sms, a, stream);
     }
-    return launch_sized<32, 16, T>(false, sms, a, stream);
 }
 
 bool valid(const ddp_route_args* x) {
