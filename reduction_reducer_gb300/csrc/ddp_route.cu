@@ -35,7 +35,7 @@ constexpr int kMaxExperts = 512;
 constexpr int kMaxSlots = 256;           // slots of a warp's tokens at once
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kForwardCtas = 3;          // route_kernel's on an SM: 80 registers; at 64 it spills (65,536 tokens 37.7 -> 49.5 us)
-constexpr int kBackwardCtas = 8;         // CTAs per SM at most
+constexpr int kChosenCtas = 8, kWholeCtas = 16;      // the backward kernels' on an SM at most
 
 // Least distance, in units of 2^-21 (the keys' step), of two values whose
 // order is certain.  A sigmoid score plus bias is within 0.9e-6 of the fp32
@@ -679,6 +679,7 @@ route_backward_whole_kernel(const __grid_constant__ RouteParams a) {
     float* const part = parts[warp];
     const int e0 = l * EPL, n = max(0, min(E - e0, EPL));
     const bool vec = a.vec && (e0 * sizeof(T)) % 16 == 0;
+    const uint32_t over_k = (65536u + k - 1) / k;                 // i / k for i < 256
     for (int j = 0; j < EPL; ++j) row_part[j * 32 + lane] = 0.0f;
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
@@ -695,38 +696,37 @@ route_backward_whole_kernel(const __grid_constant__ RouteParams a) {
             float p = 0.0f;
             if (index >= 0 && index < E) {
                 p = a.grad_weights[t0 * k + i] * a.weights[t0 * k + i];
-                row_part[i / k * (LPT * EPL) + index] = p;
+                row_part[static_cast<int>(i * over_k >> 16) * (LPT * EPL) + index] = p;
             }
             part[i] = p;
         }
+        float top = x[0], sum = 0.0f;
+#pragma unroll
+        for (int j = 1; j < EPL; ++j) top = fmaxf(top, x[j]);
+#pragma unroll
+        for (int o = LPT / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+        // the approximate exponential errs by 2^-22 and 2^-24 |x - top| of a score
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            x[j] = fast_exp(x[j] - top);
+            sum += x[j];
+        }
+        sum = token_sum<LPT>(sum);
         __syncwarp();
         float total = 0.0f;
         if (on)
+#pragma unroll 4
             for (int r = 0; r < k; ++r) total += part[tl * k + r];
-        uint32_t most = 0;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) most = max(most, key_of(x[j]));
-        const float top = number_of(token_max<LPT>(most));
-        float e[EPL], sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            e[j] = x[j] == neg_inf() ? 0.0f : expf(x[j] - top);
-            sum += e[j];
-        }
-        sum = token_sum<LPT>(sum);
-        const float f = total / sum;
+        const float f = __fdividef(total, sum);
         T* const to = static_cast<T*>(a.grad_logits) + t * a.grad_stride + e0;
         float d[EPL];
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
             d[j] = row_part[lane * EPL + j];
-            if (total != 0.0f) d[j] -= e[j] * f;      // a masked token's logits may be anything
+            if (total != 0.0f) d[j] = fmaf(-x[j], f, d[j]);       // a masked token's logits may be anything
         }
         __syncwarp();
-        for (int i = lane; i < slots; i += 32) {
-            const int index = a.indices[t0 * k + i];
-            if (index >= 0 && index < E) row_part[i / k * (LPT * EPL) + index] = 0.0f;
-        }
+        for (int j = 0; j < EPL; ++j) row_part[j * 32 + lane] = 0.0f;
         if (on) store_lane<EPL>(to, n, vec, d);
         __syncwarp();
     }
@@ -779,7 +779,7 @@ cudaError_t launch_forward(int sms, RouteParams& a, cudaStream_t stream) {
 template <int LPT, int EPL, typename T>
 cudaError_t launch_whole(int sms, const RouteParams& a, cudaStream_t stream) {
     constexpr int kTokens = 32 / LPT;
-    return launch(route_backward_whole_kernel<LPT, EPL, T>, (a.tokens + kTokens - 1) / kTokens, sms, kBackwardCtas, a, stream);
+    return launch(route_backward_whole_kernel<LPT, EPL, T>, (a.tokens + kTokens - 1) / kTokens, sms, kWholeCtas, a, stream);
 }
 
 template <typename T>
@@ -791,7 +791,7 @@ cudaError_t launch_any(bool backward, RouteParams& a, cudaStream_t stream) {
         a.slot_lanes = power_of_two(a.k);
         const int room = kRowBytes / static_cast<int>(sizeof(T)) / a.E, tokens = 32 / a.slot_lanes;
         a.row_tokens = room < tokens ? room : tokens;
-        return launch(route_backward_chosen_kernel<T>, (a.tokens + a.row_tokens - 1) / a.row_tokens, sms, kBackwardCtas,
+        return launch(route_backward_chosen_kernel<T>, (a.tokens + a.row_tokens - 1) / a.row_tokens, sms, kChosenCtas,
                       a, stream);
     }
     if (backward) {
