@@ -14,6 +14,8 @@ Modules:
   readiness  -- per-iteration readiness state machine (in-order launch, parking)
   reduce     -- gather into buckets, W-way fp32 mean, copy-back
   nosync     -- local accumulation under no_sync
+  adamw      -- AdamW step, 8-bit moments and the gradient norm, in 64 bits
+  route      -- routing of tokens to experts and its gradient, in 64 bits
 
 Only ``tests/``, ``__graft_entry__.smoke()`` and the CPU-baseline leg of
 ``bench.py`` may import this package.  The product (the C-ABI library and

@@ -299,11 +299,22 @@ struct __align__(16) Stage {
     uint8_t m[kBlock], v[kBlock];
 };
 
+// Bound by HBM: an element moves 28 bytes with 32-bit moments (weight and both
+// moments read and written, gradient read), 30 with bf16 weights beside their
+// master copies, 16 and 18 with 8-bit ones.  GB300, copy peak 6,780 GB/s:
+// BERT-large (335 M elements) 1,345 us, 6,980 GB/s; GPT-2-medium with bf16
+// weights 1,541 us, 6,910 GB/s, and with 8-bit moments 959 us, 6,680 GB/s;
+// ResNet-50 104 us, 6,890 GB/s.
+//
+// 32-bit moments: eight 128-bit loads a lane in flight on 28 warps an SM carry
+// it; single blocks to a warp, its neighbours on the next ones.  8-bit moments
+// take about 75 instructions an element, so a warp's loads must run while it
+// computes: its next whole block is copied to shared memory meanwhile (without
+// the copy, and with a scale a block read and written by itself, GPT-2-medium
+// took 1,217 us; the scales as whole sectors were most of the difference).
 template <bool BF16, bool Q8>
 __global__ void __launch_bounds__(kThreads)
 adamw_kernel(const __grid_constant__ StepParams a) {
-    // 8-bit moments take enough arithmetic a byte that a warp's loads must run
-    // while it computes: its next whole block is copied to shared memory meanwhile
     __shared__ Stage stages[Q8 ? kWarps : 1][2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long begin = static_cast<long long>(blockIdx.x) * a.piece;
@@ -530,6 +541,12 @@ __device__ __forceinline__ double cta_sum(double x, double* smem) {
     return total;              // thread 0's is the sum
 }
 
+// Reads 4 bytes an element and nothing else of size.  Eight 128-bit loads a
+// lane in flight; a lane's squares of a run (at most 68) are fp32 sums, runs
+// and CTAs are added in double, partial sums in an order that does not depend
+// on which CTA comes last.  GB300: BERT-large 201 us, 6,670 GB/s (a read-only
+// torch sum streams at 6,435 to 6,570); ResNet-50 17 us from a graph, of which
+// 2 us launch, search and the last CTA.
 __global__ void __launch_bounds__(kThreads)
 norm_kernel(const __grid_constant__ NormParams a) {
     __shared__ double smem[kWarps];

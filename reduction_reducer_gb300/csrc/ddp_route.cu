@@ -16,6 +16,14 @@
 // (order_exact); where that may not be enough, or a logit or bias is not an
 // ordinary number, the token is chosen by it alone (choose_exact).  The scores
 // of the chosen experts are always computed by the definition.
+//
+// The forward kernel is bound by instructions, not by HBM: over 256 experts it
+// reads 1 KiB a token and executes about 390 warp instructions (scores, keys
+// and sorting of 256 values; k rounds; the k slots' exact scores), half of them
+// on the integer and compare pipe, which takes one every other cycle.  GB300,
+// 65,536 tokens: 256 experts in 8 groups with a bias 37.5 us (1.9 TB/s; the
+// logits alone at the copy peak 10 us), ungrouped softmax over 64 / 128 / 256
+// experts in bf16 10.3 / 17.2 / 27.4 us.  A few tokens take 3.3 us.
 
 #include "ddp_reducer.h"
 
@@ -608,6 +616,11 @@ route_kernel(const __grid_constant__ RouteParams a) {
 // sigmoid:  dx = part_r (1 - s_r) at the chosen, 0 elsewhere
 // softmax:  dx = [chosen] part_r - s_i D; renormalised D is zero, and only the
 //           chosen get a gradient
+// GB300, 65,536 tokens over 256 experts, buffers in HBM: sigmoid in bf16 13.6
+// us, where 34 MB of gradient are written, 6 read, and each chosen logit costs a
+// sector (17 MB); softmax renormalised 8.2 us without these.  Softmax not
+// renormalised, 131,072 tokens over 128 experts in fp32, 36 us (4.0 TB/s): bound
+// by the instructions of its exponentials and sums.
 
 constexpr int kRowBytes = 4096;          // of a warp's rows under construction
 

@@ -426,3 +426,28 @@ def test_gradient_step_against_differences():
             for g in (g0 - dg, g0 + dg)]
     # each side is within 24u of a value of about 0.1 / sqrt(200)
     np.testing.assert_allclose(moved[1] - moved[0], want[1] - want[0], rtol=0, atol=48 * U * 0.1)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_twenty_thousand_tensors(bits):
+    """Tensors of 1 to 60 elements, one block each: every fp32 moment and weight of the first step from zero state, where
+    m' = (1 - b1) g, v' = (1 - b2) g^2 and the update is lr g / (|g| + eps sqrt-corrected) to 12u."""
+    sizes = [1 + (i * 7919) % 60 for i in range(20_000)]
+    flat = torch.randn(sum(sizes), generator=torch.Generator("cuda").manual_seed(0), device="cuda")
+    weight = torch.zeros(sum(sizes), device="cuda")
+    opt = AdamW(sizes, state_bits=bits)
+    state = opt.zero_state()
+    opt.bind(list(weight.split(sizes)), list(flat.split(sizes)), **state)
+    norm = opt.grad_norm(torch.empty(1, device="cuda"))
+    opt.step(1, lr=0.5, eps=1e-30)
+    torch.cuda.synchronize()
+    exact = float(flat.double().square().sum().sqrt())
+    assert abs(float(norm) - exact) <= 8 * U * exact
+    assert torch.allclose(weight, -0.5 * torch.sign(flat), rtol=24 * U, atol=0)
+    if bits == 32:
+        m = torch.cat(state["exp_avg"])
+        assert torch.allclose(m, flat * np.float32(1 - 0.9), rtol=2 * U, atol=0)
+    else:
+        peak = torch.stack([x.abs().amax() for x in flat.split(sizes)[:200]])
+        got = torch.stack([x[0] for x in state["exp_avg_scale"][:200]])
+        assert torch.allclose(got, peak * np.float32(1 - 0.9) / 448, rtol=4 * U, atol=0)

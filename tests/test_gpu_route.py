@@ -392,3 +392,26 @@ def test_softmax_with_a_bias_and_many_tokens(score):
         assert torch.equal(index.long()[clear], ranked.indices[:, :k][clear])
         ref = s.gather(1, index.long())
         assert bool(((w.double() - ref).abs() <= 64 * U * ref).all())
+
+
+def test_offsets_past_32_bits():
+    """8,388,613 tokens over 256 experts: logits, and their gradient, of more than 2^31 elements."""
+    T, E, k = (1 << 23) + 5, 256, 2
+    x = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
+    x[-3:, 200] = 2.0
+    x[-3:, 17] = 1.0
+    counts = torch.zeros(E, dtype=torch.int32, device="cuda")
+    index, w = route(x, k, renorm=True, counts=counts)
+    assert index[-3:].tolist() == [[200, 17]] * 3 and index[:-3].unique().tolist() == [0, 1]
+    assert int(counts.sum()) == 2 * T and counts[[0, 1, 17, 200]].tolist() == [T - 3, T - 3, 3, 3]
+    s = torch.softmax(torch.tensor([2.0, 1.0]), 0)
+    assert torch.allclose(w[-3:].cpu(), s.repeat(3, 1), rtol=64 * U) and torch.equal(w[:-3], torch.full((T - 3, 2), 0.5, device="cuda"))
+    g = torch.zeros(T, k, device="cuda")
+    g[-1, 0] = 1.0
+    for renorm in (True, False):
+        if not renorm:
+            index, w = route(x, k)
+        d = route_backward(g, x, index, w, renorm=renorm)
+        assert int((d[:-1] != 0).sum()) == 0
+        want = R.backward_token(x[-1].double().cpu().numpy(), [200, 17], [1.0, 0.0], "softmax", renorm, 1.0)
+        assert np.all(np.abs(d[-1].double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + 160 * U)
