@@ -11,18 +11,29 @@ from __future__ import annotations
 import ctypes as C
 
 from . import _lib
-from .reducer import _ERRORS, DTYPES, DDPError, _ptr, _ptr_array, _stream
+from .reducer import _ERRORS, DTYPES, DDPError, _stream
 
 BLOCK = 256             # elements that share one scale of an 8-bit moment (DDP_ADAMW_BLOCK)
 
 
-def _expect(name, v, t, numel, dtypes):
-    if t is None and numel == 0:
-        return
-    if isinstance(t, int):
-        return
-    if t is None or t.numel() != numel or not t.is_contiguous() or str(t.dtype)[6:] not in dtypes or not t.is_cuda:
-        raise ValueError(f"{name}[{v}]: expected {numel} contiguous elements of {' or '.join(dtypes)} on a GPU")
+def _addresses(name, tensors, numel, dtypes):
+    """Checked device addresses of a list of tensors (or addresses), as the C
+    ABI takes them; None for None."""
+    if tensors is None:
+        return None
+    if len(tensors) != len(numel):
+        raise ValueError(f"{name}: expected {len(numel)} tensors")
+    out = (C.c_void_p * max(len(numel), 1))()
+    for v, (t, n) in enumerate(zip(tensors, numel)):
+        if isinstance(t, int):
+            out[v] = t or None
+        elif t is None or t.numel() != n or t.dtype not in dtypes or not t.is_contiguous() or not t.is_cuda:
+            if t is not None or n:
+                raise ValueError(f"{name}[{v}]: expected {n} contiguous elements of "
+                                 f"{' or '.join(str(d) for d in dtypes)} on a GPU")
+        else:
+            out[v] = t.data_ptr() or None
+    return out
 
 
 class AdamW:
@@ -85,41 +96,28 @@ class AdamW:
         fp32, or with 8 bits float8_e4m3fn and float8_e5m2 (or uint8) codes
         with fp32 scales of ceil(numel / 256) elements; weight_decay: a number
         for all or one per tensor."""
+        import torch
         bf16, eight = self.param_dtype == "bf16", self.state_bits == 8
-        want = [("grads", grads, ("float32",), False), ("params", params, ("bfloat16" if bf16 else "float32",), False),
-                ("exp_avg", exp_avg, ("float8_e4m3fn", "uint8") if eight else ("float32",), False),
-                ("exp_avg_sq", exp_avg_sq, ("float8_e5m2", "uint8") if eight else ("float32",), False)]
-        if master is not None:
-            want.append(("master", master, ("float32",), False))
-        if exp_avg_scale is not None:
-            want.append(("exp_avg_scale", exp_avg_scale, ("float32",), True))
-        if exp_avg_sq_scale is not None:
-            want.append(("exp_avg_sq_scale", exp_avg_sq_scale, ("float32",), True))
-        for name, tensors, kinds, scale in want:
-            if len(tensors) != self.P:
-                raise ValueError(f"{name}: expected {self.P} tensors")
-            for v, t in enumerate(tensors):
-                _expect(name, v, t, -(-self.numel[v] // BLOCK) if scale else self.numel[v], kinds)
+        f32 = (torch.float32,)
         decay = [float(weight_decay)] * self.P if isinstance(weight_decay, (int, float)) else list(weight_decay)
         if len(decay) != self.P:
             raise ValueError(f"weight_decay: expected one number or {self.P}")
-
-        def pointers(tensors):
-            return None if tensors is None else _ptr_array([_ptr(t) for t in tensors])
-
-        self._check(self.lib.ddp_adamw_bind(self._h, pointers(grads), pointers(params), pointers(master),
-                                            pointers(exp_avg), pointers(exp_avg_sq), pointers(exp_avg_scale),
-                                            pointers(exp_avg_sq_scale), (C.c_float * max(self.P, 1))(*decay)))
+        n, blocks = self.numel, [-(-n // BLOCK) for n in self.numel]
+        self._check(self.lib.ddp_adamw_bind(
+            self._h, _addresses("grads", grads, n, f32),
+            _addresses("params", params, n, (torch.bfloat16,) if bf16 else f32),
+            _addresses("master", master, n, f32),
+            _addresses("exp_avg", exp_avg, n, (torch.float8_e4m3fn, torch.uint8) if eight else f32),
+            _addresses("exp_avg_sq", exp_avg_sq, n, (torch.float8_e5m2, torch.uint8) if eight else f32),
+            _addresses("exp_avg_scale", exp_avg_scale, blocks, f32),
+            _addresses("exp_avg_sq_scale", exp_avg_sq_scale, blocks, f32), (C.c_float * max(self.P, 1))(*decay)))
         self._keep = (params, grads, exp_avg, exp_avg_sq, master, exp_avg_scale, exp_avg_sq_scale)
 
     def bind_grads(self, grads):
         """Bind the gradients alone: for ``grad_norm`` without a step."""
-        if len(grads) != self.P:
-            raise ValueError(f"grads: expected {self.P} tensors")
-        for v, t in enumerate(grads):
-            _expect("grads", v, t, self.numel[v], ("float32",))
-        self._check(self.lib.ddp_adamw_bind(self._h, _ptr_array([_ptr(t) for t in grads]), None, None, None, None,
-                                            None, None, None))
+        import torch
+        self._check(self.lib.ddp_adamw_bind(self._h, _addresses("grads", grads, self.numel, (torch.float32,)), None, None,
+                                            None, None, None, None, None))
         self._keep = (grads,)
 
     # ---------------------------------------------------------------- calls
