@@ -324,16 +324,6 @@ adamw_kernel(const __grid_constant__ StepParams a) {
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
 
-    float clip = 1.0f;
-    if (a.norm) {
-        const float norm = *a.norm;
-        if (a.c.skip_nonfinite && !(norm < __int_as_float(0x7f800000))) return;
-        if (a.c.clip) {
-            const float x = __fdiv_rn(a.c.max_norm, __fadd_rn(norm, 1e-6f));
-            clip = x > 1.0f ? 1.0f : x;        // a NaN stays one
-        }
-    }
-
     // the next run from u on of a tensor that has a gradient
     const auto settle = [&](long long& u, int& s) {
         for (; u < end; u += kWarps) {
@@ -379,6 +369,21 @@ adamw_kernel(const __grid_constant__ StepParams a) {
         if (const float* x = scale_at(t, j0, blocks_of(t, j0))) next_scale = *x;
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
+
+    // (after the first inputs are on their way, which do not wait for it)
+    float clip = 1.0f;
+    if (a.norm) {
+        const float norm = *a.norm;
+        if (a.c.skip_nonfinite && !(norm < __int_as_float(0x7f800000))) {
+            if constexpr (Q8) asm volatile("cp.async.wait_all;" ::: "memory");
+            return;
+        }
+        if (a.c.clip) {
+            const float x = __fdiv_rn(a.c.max_norm, __fadd_rn(norm, 1e-6f));
+            clip = x > 1.0f ? 1.0f : x;        // a NaN stays one
+        }
+    }
+
     while (u < end) {
         const Tensor& t = a.tensors[s];
         const long long j0 = (u - __ldg(a.first + s)) * a.run;
@@ -605,8 +610,16 @@ norm_kernel(const __grid_constant__ NormParams a) {
     if (!last) return;
     // the CTA that finishes last adds the partial sums, in an order of their own
     __threadfence();
+    // (all of a thread's loads at once: one after another they are most of this CTA's time)
     double x = 0.0;
-    for (unsigned i = threadIdx.x; i < gridDim.x; i += kThreads) x += __ldcg(a.partial + i);
+    constexpr int kAtOnce = 16;
+    for (unsigned i = threadIdx.x; i < gridDim.x; i += kAtOnce * kThreads) {
+        double y[kAtOnce];
+#pragma unroll
+        for (int h = 0; h < kAtOnce; ++h) y[h] = i + h * kThreads < gridDim.x ? __ldcg(a.partial + i + h * kThreads) : 0.0;
+#pragma unroll
+        for (int h = 0; h < kAtOnce; ++h) x += y[h];
+    }
     __syncthreads();
     const double all = cta_sum(x, smem);
     if (threadIdx.x == 0) *a.norm = static_cast<float>(sqrt(all));

@@ -132,7 +132,7 @@ class AdamW:
     def _norm(norm):
         if norm is None or isinstance(norm, int):
             return norm
-        if norm.numel() != 1 or str(norm.dtype) != "torch.float32" or not norm.is_cuda:
+        if norm.numel() != 1 or not norm.is_cuda or str(norm.dtype) != "torch.float32":
             raise ValueError("norm: expected one fp32 element on a GPU")
         return norm.data_ptr()
 
