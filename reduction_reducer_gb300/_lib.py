@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libddpreducer.so")
@@ -63,6 +64,10 @@ class RouteArgs(C.Structure):
 # int (*ddp_comm_hook_fn)(void* state, const ddp_grad_bucket* bucket, void* stream)
 HOOKFN = C.CFUNCTYPE(C.c_int, C.c_void_p, C.POINTER(GradBucket), C.c_void_p)
 
+# The same structs packed into bytes, which costs a call half a microsecond less than filling one in.
+pack_adamw = struct.Struct("@q5dPPQi4x").pack
+pack_route = struct.Struct("@2q6ifi").pack
+
 # name -> (restype, argtypes); every symbol of include/ddp_reducer.h
 SIGNATURES = {
     "ddp_build_buckets": (C.c_int, [C.POINTER(C.c_int64), C.c_int32, C.c_int, C.c_int64, C.POINTER(C.c_void_p)]),
@@ -99,12 +104,13 @@ SIGNATURES = {
     "ddp_shard_mean": (C.c_int, [C.c_int32, C.c_int, C.POINTER(C.c_void_p), C.c_void_p, C.c_int64, C.c_void_p]),
     "ddp_adamw_create": (C.c_int, [C.POINTER(C.c_int64), C.c_int32, C.c_int, C.c_int32, C.POINTER(C.c_void_p)]),
     "ddp_adamw_bind": (C.c_int, [C.c_void_p] + [C.POINTER(C.c_void_p)] * 7 + [C.POINTER(C.c_float)]),
-    "ddp_adamw_step": (C.c_int, [C.c_void_p, C.POINTER(AdamWArgs), C.c_void_p]),
+    # the argument structs of the calls below as void*: the binding passes packed bytes (their layouts above)
+    "ddp_adamw_step": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p]),
     "ddp_adamw_grad_norm": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
     "ddp_adamw_last_error": (C.c_char_p, [C.c_void_p]),
     "ddp_adamw_destroy": (None, [C.c_void_p]),
-    "ddp_route": (C.c_int, [C.POINTER(RouteArgs)] + [C.c_void_p] * 7),
-    "ddp_route_backward": (C.c_int, [C.POINTER(RouteArgs)] + [C.c_void_p] * 5 + [C.c_int64, C.c_void_p]),
+    "ddp_route": (C.c_int, [C.c_void_p] * 8),
+    "ddp_route_backward": (C.c_int, [C.c_void_p] * 6 + [C.c_int64, C.c_void_p]),
     "ddp_read_launch_trace": (C.c_int, [C.POINTER(C.c_uint64), C.POINTER(C.c_int32), C.POINTER(C.c_int64)]),
     "ddp_status_string": (C.c_char_p, [C.c_int]),
     "ddp_last_error": (C.c_char_p, [C.c_void_p]),

@@ -385,7 +385,10 @@ adamw_kernel(const __grid_constant__ StepParams a) {
     }
 
     while (u < end) {
-        const Tensor& t = a.tensors[s];
+        // an entry in registers is not read again after every store; with 8-bit
+        // moments there are none left for it (GPT-2-medium, by value / by
+        // reference: 1,529 / 1,543 us, 8-bit 973 / 958)
+        typename std::conditional<Q8, const Tensor&, const Tensor>::type t = a.tensors[s];
         const long long j0 = (u - __ldg(a.first + s)) * a.run;
         const int blocks = blocks_of(t, j0);
         long long next_u = u + kWarps;
@@ -601,6 +604,10 @@ norm_kernel(const __grid_constant__ NormParams a) {
         sum += static_cast<double>(part[0] + part[1]) + static_cast<double>(part[2] + part[3]);
     }
     const double total = cta_sum(sum, smem);
+    if (gridDim.x == 1) {
+        if (threadIdx.x == 0) *a.norm = static_cast<float>(sqrt(total));
+        return;
+    }
     if (threadIdx.x == 0) {
         a.partial[blockIdx.x] = total;
         __threadfence();

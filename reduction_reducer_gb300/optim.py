@@ -9,6 +9,7 @@ here; the arithmetic is the library's kernels'.
 from __future__ import annotations
 
 import ctypes as C
+import struct
 
 from . import _lib
 from .reducer import _ERRORS, DTYPES, DDPError, _stream
@@ -55,8 +56,7 @@ class AdamW:
         if st != 0:
             raise _ERRORS.get(st, DDPError)(st, self.lib.ddp_adamw_last_error(None).decode())
         self._h = h
-        self._args = _lib.AdamWArgs()
-        self._ref = C.byref(self._args)
+        self._f32 = None
 
     def _check(self, st: int):
         if st != 0:
@@ -123,17 +123,18 @@ class AdamW:
     # ---------------------------------------------------------------- calls
     def _used(self, used):
         if used is None or isinstance(used, int):
-            return used
+            return used or 0
         if used.numel() != self.P or used.element_size() != 1 or not used.is_contiguous() or not used.is_cuda:
             raise ValueError(f"used: expected {self.P} contiguous bytes or truth values on a GPU")
         return used.data_ptr()
 
-    @staticmethod
-    def _norm(norm):
+    def _norm(self, norm):
         if norm is None or isinstance(norm, int):
-            return norm
-        if norm.numel() != 1 or not norm.is_cuda or str(norm.dtype) != "torch.float32":
+            return norm or 0
+        # a 0-d or one-element fp32 tensor; its dtype is asked for by name once
+        if norm.numel() != 1 or not norm.is_cuda or (norm.dtype is not self._f32 and str(norm.dtype) != "torch.float32"):
             raise ValueError("norm: expected one fp32 element on a GPU")
+        self._f32 = norm.dtype
         return norm.data_ptr()
 
     def grad_norm(self, out, used=None, stream=None):
@@ -148,12 +149,12 @@ class AdamW:
         max_norm > 0; used: device bytes [P], tensors with 0 stay as they are;
         seed: of the 8-bit moments' rounding, another one each step;
         skip_nonfinite: a norm that is not finite leaves everything as it is."""
-        a = self._args
-        a.t, a.lr, a.eps, a.max_norm = t, lr, eps, max_norm
-        a.beta1, a.beta2 = betas
-        a.norm, a.used = self._norm(norm), self._used(used)
-        a.seed, a.skip_nonfinite = seed, skip_nonfinite
-        self._check(self.lib.ddp_adamw_step(self._h, self._ref, _stream(stream)))
+        norm, used = self._norm(norm), self._used(used)
+        try:
+            args = _lib.pack_adamw(t, lr, betas[0], betas[1], eps, max_norm, norm, used, seed, 1 if skip_nonfinite else 0)
+        except struct.error as e:
+            raise ValueError(f"t, a hyperparameter or seed: {e}") from None
+        self._check(self.lib.ddp_adamw_step(self._h, args, _stream(stream)))
 
     def destroy(self):
         if getattr(self, "_h", None):

@@ -4,12 +4,11 @@ happens here; the arithmetic is the library's kernels'."""
 
 from __future__ import annotations
 
-import ctypes as C
+import struct
 
 from . import _lib
 from .reducer import DDPError, _ERRORS, _stream
 
-SCORES = {"softmax": 0, "sigmoid": 1}
 torch = None       # imported by the first call, not by the package; the dtypes below then too
 _DTYPES = _INT = _FLOAT = _MASK = None
 
@@ -25,16 +24,27 @@ def _torch():
 
 
 def _args(logits, k, score, groups, top_groups, renorm, scale):
-    _torch()
+    """(packed ddp_route_args, tokens, experts) of a call."""
+    if torch is None:
+        _torch()
     dtype = _DTYPES.get(logits.dtype)
-    if dtype is None or logits.dim() != 2 or not logits.is_cuda or (logits.shape[1] > 1 and logits.stride(1) != 1):
-        raise ValueError("logits: expected [tokens, experts] fp32 or bf16 on a GPU, experts next to one another")
-    if score not in SCORES:
-        raise ValueError("score: expected 'softmax' or 'sigmoid'")
+    if dtype is None or logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError("logits: expected [tokens, experts] fp32 or bf16 on a GPU")
     tokens, experts = logits.shape
-    stride = logits.stride(0)
-    return _lib.RouteArgs(tokens, max(stride, experts) if tokens <= 1 else stride, experts, k, SCORES[score], groups,
-                          groups if top_groups is None else top_groups, 1 if renorm else 0, scale, dtype)
+    stride = _row_stride("logits", logits, tokens, experts)
+    try:
+        a = _lib.pack_route(tokens, stride, experts, k, _SCORES[score], groups,
+                            groups if top_groups is None else top_groups, 1 if renorm else 0, scale, dtype)
+    except (struct.error, OverflowError) as e:
+        raise ValueError(f"k, groups, top_groups or scale: {e}") from None
+    return a, tokens, experts
+
+
+def _row_stride(name, t, tokens, experts):
+    row, column = t.stride()
+    if column != 1 and experts > 1:
+        raise ValueError(f"{name}: expected a token's experts next to one another")
+    return row if tokens > 1 else max(row, experts)
 
 
 def _data(name, t, shape, dtypes):
@@ -45,10 +55,17 @@ def _data(name, t, shape, dtypes):
     return t.data_ptr()
 
 
-def _check(st: int, what: str, a):
-    if st != 0:
-        raise _ERRORS.get(st, DDPError)(st, f"{what}: {a.tokens} tokens, {a.experts} experts, k {a.k}, groups {a.groups}, "
-                                            f"top_groups {a.top_groups}, scale {a.scale}")
+class _Scores(dict):
+    def __missing__(self, score):
+        raise ValueError("score: expected 'softmax' or 'sigmoid'")
+
+
+_SCORES = _Scores(softmax=0, sigmoid=1)
+
+
+def _refused(st: int, what: str, tokens, experts, k, **more):
+    detail = ", ".join(f"{n} {v}" for n, v in dict(tokens=tokens, experts=experts, k=k, **more).items())
+    raise _ERRORS.get(st, DDPError)(st, f"{what}: {detail}")
 
 
 def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, top_groups=None, renorm: bool = False,
@@ -63,17 +80,17 @@ def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, to
     their sum; mask: bytes or truth values [tokens], 0 = not routed (index
     -1, weight 0); counts: int32 [experts], the tokens each expert got are
     added to it; out: (indices, weights) to write into."""
-    a = _args(logits, k, score, groups, top_groups, renorm, scale)
-    shape = (a.tokens, a.k)
+    a, tokens, experts = _args(logits, k, score, groups, top_groups, renorm, scale)
+    shape, each = (tokens, k), (experts,)
     indices, weights = out if out is not None else (
         torch.empty(shape, dtype=torch.int32, device=logits.device),
         torch.empty(shape, dtype=torch.float32, device=logits.device))
-    _check(_lib.load(lib_path).ddp_route(
-        C.byref(a), logits.data_ptr(), _data("bias", bias, (a.experts,), _FLOAT),
-        _data("mask", mask, (a.tokens,), _MASK),
+    st = _lib.load(lib_path).ddp_route(
+        a, logits.data_ptr(), _data("bias", bias, each, _FLOAT), _data("mask", mask, (tokens,), _MASK),
         _data("indices", indices, shape, _INT), _data("weights", weights, shape, _FLOAT),
-        _data("counts", counts, (a.experts,), _INT), _stream(stream)),
-        "ddp_route", a)
+        _data("counts", counts, each, _INT), _stream(stream))
+    if st:
+        _refused(st, "ddp_route", tokens, experts, k, groups=groups, top_groups=top_groups, scale=scale)
     return indices, weights
 
 
@@ -83,18 +100,17 @@ def route_backward(grad_weights, logits, indices, weights, score: str = "softmax
     the weights, with the indices and weights that ``route`` returned for the
     same score, renorm and scale."""
     k = indices.shape[1] if indices.dim() == 2 else 0
-    a = _args(logits, k, score, 1, 1, renorm, scale)
-    shape = (a.tokens, a.k)
-    grad = out if out is not None else torch.empty((a.tokens, a.experts), dtype=logits.dtype, device=logits.device)
-    if tuple(grad.shape) != (a.tokens, a.experts) or grad.dtype != logits.dtype or not grad.is_cuda or (
-            a.experts > 1 and grad.stride(1) != 1):
-        raise ValueError("out: expected the logits' shape and dtype, experts next to one another")
-    _check(_lib.load(lib_path).ddp_route_backward(
-        C.byref(a), logits.data_ptr(), _data("indices", indices, shape, _INT),
-        _data("weights", weights, shape, _FLOAT),
-        _data("grad_weights", grad_weights, shape, _FLOAT), grad.data_ptr(),
-        max(grad.stride(0), a.experts) if a.tokens <= 1 else grad.stride(0), _stream(stream)),
-        "ddp_route_backward", a)
+    a, tokens, experts = _args(logits, k, score, 1, 1, renorm, scale)
+    shape = (tokens, k)
+    grad = out if out is not None else torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
+    if grad.shape != logits.shape or grad.dtype is not logits.dtype or not grad.is_cuda:
+        raise ValueError("out: expected the logits' shape and dtype on a GPU")
+    st = _lib.load(lib_path).ddp_route_backward(
+        a, logits.data_ptr(), _data("indices", indices, shape, _INT), _data("weights", weights, shape, _FLOAT),
+        _data("grad_weights", grad_weights, shape, _FLOAT), grad.data_ptr(), _row_stride("out", grad, tokens, experts),
+        _stream(stream))
+    if st:
+        _refused(st, "ddp_route_backward", tokens, experts, k, scale=scale)
     return grad
 
 

@@ -116,3 +116,14 @@ def test_route_pointer_refusals(lib):
         route(torch.zeros(3, 8), 2)                                # not on a GPU
     with pytest.raises(ValueError):
         route_backward(torch.zeros(3, 2), torch.zeros(3, 8), torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, 2))
+
+
+def test_packed_arguments_have_the_structs_layout():
+    a = _lib.AdamWArgs.from_buffer_copy(_lib.pack_adamw(7, 1.5, 0.25, 0.5, 2.0, 3.0, 16, 32, 2 ** 63 + 5, 1))
+    assert [getattr(a, n) for n, _ in _lib.AdamWArgs._fields_] == [7, 1.5, 0.25, 0.5, 2.0, 3.0, 16, 32, 2 ** 63 + 5, 1]
+    assert C.sizeof(_lib.AdamWArgs) == len(_lib.pack_adamw(7, 1, 1, 1, 1, 1, 0, 0, 0, 0))
+    r = _lib.RouteArgs.from_buffer_copy(_lib.pack_route(3, 70, 64, 8, 1, 4, 2, 1, 2.5, 1))
+    assert [getattr(r, n) for n, _ in _lib.RouteArgs._fields_] == [3, 70, 64, 8, 1, 4, 2, 1, 2.5, 1]
+    assert C.sizeof(_lib.RouteArgs) == len(_lib.pack_route(3, 70, 64, 8, 1, 4, 2, 1, 2.5, 1))
+    with pytest.raises(ValueError):
+        AdamW([5]).step(1, seed=-1, stream=0)
