@@ -447,7 +447,7 @@ int ddp_adamw_step(ddp_adamw* opt, const ddp_adamw_args* args, void* stream);
 /* *norm = sqrt of the sum of squares over the bound gradients (of the tensors
  * with used[v] != 0; device array [P] or NULL = all), one launch,
  * asynchronous on `stream`.  Squares are fp32 (gradients past 1.8e19 give an
- * infinite norm), long sums are double; the order is fixed, so equal inputs
+ * infinite norm), long sums have twice fp32's digits; the order is fixed, so equal inputs
  * give equal bits.  Calls of one `opt` share its partial sums: they run in
  * one stream's order.  Errors: INVALID_ARG, NOT_BOUND, CUDA. */
 int ddp_adamw_grad_norm(ddp_adamw* opt, const uint8_t* used, float* norm, void* stream);

@@ -34,6 +34,7 @@ namespace {
 constexpr int kBlock = DDP_ADAMW_BLOCK;
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
+constexpr int kNormThreads = 512;
 constexpr int kMaxRun = 8;                // blocks
 static_assert(kBlock == 256, "a warp holds a block as 8 values a lane");
 
@@ -526,11 +527,18 @@ adamw_kernel(const __grid_constant__ StepParams a) {
 
 // ------------------------------------------------------------------ the norm
 
+// A sum in two fp32 numbers: hi the rounded sum, lo what the roundings left out
+// (exactly, per addition), about 46 bits together.  GB300 has two double lanes
+// an SM: with doubles the warps' and CTAs' sums alone took 2 us of a norm.
+struct Sum {
+    float hi, lo;
+};
+
 struct NormParams {
     const Tensor* tensors;
     const long long* first;
     const uint8_t* used;
-    double* partial;           // [grid]
+    Sum* partial;              // [grid]
     unsigned* done;            // CTAs finished; wraps to 0
     float* norm;
     long long runs, piece;
@@ -538,26 +546,42 @@ struct NormParams {
     int run;
 };
 
-__device__ __forceinline__ double cta_sum(double x, double* smem) {
+__device__ __forceinline__ Sum plus(const Sum& a, const Sum& b) {
+    const float s = __fadd_rn(a.hi, b.hi), t = __fsub_rn(s, a.hi);
+    const float rest = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, t)), __fsub_rn(b.hi, t));
+    return Sum{s, __fadd_rn(__fadd_rn(a.lo, b.lo), rest)};
+}
+
+__device__ __forceinline__ Sum warp_sum(Sum x) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_down_sync(0xffffffffu, x, o);
-    if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = x;
+    for (int o = 16; o; o >>= 1)
+        x = plus(x, Sum{__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)});
+    return x;
+}
+
+// All threads' sum, in every thread of the first warp.
+__device__ __forceinline__ Sum cta_sum(Sum x, Sum* smem) {
+    x = warp_sum(x);
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) smem[threadIdx.x >> 5] = x;
     __syncthreads();
-    double total = 0.0;
-    if (threadIdx.x == 0)
-        for (int i = 0; i < kWarps; ++i) total += smem[i];
-    return total;              // thread 0's is the sum
+    return threadIdx.x < 32 ? warp_sum(lane < kNormThreads / 32 ? smem[lane] : Sum{0.0f, 0.0f}) : Sum{0.0f, 0.0f};
+}
+
+// An infinite hi has a lo that is no number.
+__device__ __forceinline__ float root(const Sum& x) {
+    return isfinite(x.hi) ? static_cast<float>(sqrt(static_cast<double>(x.hi) + static_cast<double>(x.lo))) : sqrtf(x.hi);
 }
 
 // Reads 4 bytes an element and nothing else of size.  Eight 128-bit loads a
 // lane in flight; a lane's squares of a run (at most 68) are fp32 sums, runs
-// and CTAs are added in double, partial sums in an order that does not depend
-// on which CTA comes last.  GB300: BERT-large 201 us, 6,670 GB/s (a read-only
+// and CTAs are added in two fp32 numbers, partial sums in an order that does not
+// depend on which CTA comes last.  GB300: BERT-large 201 us, 6,670 GB/s (a read-only
 // torch sum streams at 6,435 to 6,570); ResNet-50 17 us from a graph, of which
 // 2 us launch, search and the last CTA.
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kNormThreads)
 norm_kernel(const __grid_constant__ NormParams a) {
-    __shared__ double smem[kWarps];
+    __shared__ Sum smem[kNormThreads / 32];
     __shared__ bool last;
     const int lane = threadIdx.x & 31;
     const long long begin = static_cast<long long>(blockIdx.x) * a.piece;
@@ -567,8 +591,8 @@ norm_kernel(const __grid_constant__ NormParams a) {
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
 
-    double sum = 0.0;
-    for (; u < end; u += kWarps) {
+    Sum sum{0.0f, 0.0f};
+    for (; u < end; u += kNormThreads / 32) {
         while (u >= __ldg(a.first + s + 1)) ++s;
         const Tensor& t = a.tensors[s];
         if (a.used && !a.used[t.var]) continue;
@@ -601,42 +625,37 @@ norm_kernel(const __grid_constant__ NormParams a) {
             const float x = lane < head ? g[lane] : g[n - tail + lane - head];
             part[0] = __fmaf_rn(x, x, part[0]);
         }
-        sum += static_cast<double>(part[0] + part[1]) + static_cast<double>(part[2] + part[3]);
+        sum = plus(sum, Sum{(part[0] + part[1]) + (part[2] + part[3]), 0.0f});
     }
-    const double total = cta_sum(sum, smem);
+    const Sum total = cta_sum(sum, smem);
     if (gridDim.x == 1) {
-        if (threadIdx.x == 0) *a.norm = static_cast<float>(sqrt(total));
+        if (threadIdx.x == 0) *a.norm = root(total);
         return;
     }
     if (threadIdx.x == 0) {
         a.partial[blockIdx.x] = total;
         __threadfence();
         last = atomicInc(a.done, gridDim.x - 1) == gridDim.x - 1;
+        __threadfence();
     }
     __syncthreads();
     if (!last) return;
     // the CTA that finishes last adds the partial sums, in an order of their own
-    __threadfence();
-    // (all of a thread's loads at once: one after another they are most of this CTA's time)
-    double x = 0.0;
-    constexpr int kAtOnce = 16;
-    for (unsigned i = threadIdx.x; i < gridDim.x; i += kAtOnce * kThreads) {
-        double y[kAtOnce];
-#pragma unroll
-        for (int h = 0; h < kAtOnce; ++h) y[h] = i + h * kThreads < gridDim.x ? __ldcg(a.partial + i + h * kThreads) : 0.0;
-#pragma unroll
-        for (int h = 0; h < kAtOnce; ++h) x += y[h];
+    Sum x{0.0f, 0.0f};
+    for (unsigned i = threadIdx.x; i < gridDim.x; i += kNormThreads) {
+        const float2 y = __ldcg(reinterpret_cast<const float2*>(a.partial + i));
+        x = plus(x, Sum{y.x, y.y});
     }
     __syncthreads();
-    const double all = cta_sum(x, smem);
-    if (threadIdx.x == 0) *a.norm = static_cast<float>(sqrt(all));
+    const Sum all = cta_sum(x, smem);
+    if (threadIdx.x == 0) *a.norm = root(all);
 }
 
 template <typename K, typename P>
-cudaError_t launch(K kernel, int grid, const P& params, cudaStream_t stream) {
+cudaError_t launch(K kernel, int threads, int grid, const P& params, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -670,7 +689,7 @@ struct ddp_adamw {
     Runs step, norm;
     void* table = nullptr;       // device: Tensor[S], first[S + 1], partial[], done
     const Tensor* tensors = nullptr;
-    double* partial = nullptr;
+    Sum* partial = nullptr;
     unsigned* done = nullptr;
     std::string error;
 
@@ -688,14 +707,14 @@ namespace {
 // 1,397 / 1,373 / 1,355 us, 256: 1,345; GPT-2-medium with 8-bit moments, 128 /
 // 256: 959 / 981); the norm takes one resident wave, of which the last adds all
 // partial sums (BERT-large, 8 / 12 / 14: 205.7 / 200.4 / 241 us).
-constexpr int kNormCtasPerSm = 12;
+constexpr int kNormCtasPerSm = 3;
 constexpr int kStepCtasPerSm[2] = {256, 128};    // 32-bit and 8-bit moments
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
 // CTAs for `runs`, at most `most`: as few runs a warp as fills the grid.
-void split(int64_t runs, int64_t most, int* grid, long long* piece) {
-    const int64_t ctas = (runs + kWarps - 1) / kWarps;
+void split(int64_t runs, int warps, int64_t most, int* grid, long long* piece) {
+    const int64_t ctas = (runs + warps - 1) / warps;
     const int64_t n = ctas < most ? ctas : most;
     *piece = (runs + n - 1) / n;
     *grid = static_cast<int>((runs + *piece - 1) / *piece);
@@ -811,7 +830,7 @@ int ddp_adamw_bind(ddp_adamw* o, const float* const* grads, void* const* params,
         }
         const size_t at_first = S * sizeof(Tensor);
         const size_t at_partial = at_first + (first.size() * sizeof(long long) + 15) / 16 * 16;
-        const size_t at_done = at_partial + static_cast<size_t>(sms) * kNormCtasPerSm * sizeof(double);
+        const size_t at_done = at_partial + static_cast<size_t>(sms) * kNormCtasPerSm * sizeof(Sum);
         std::vector<unsigned char> image(at_done + 16, 0);
         if (S) std::memcpy(image.data(), tensors.data(), at_first);
         std::memcpy(image.data() + at_first, first.data(), first.size() * sizeof(long long));
@@ -834,7 +853,7 @@ int ddp_adamw_bind(ddp_adamw* o, const float* const* grads, void* const* params,
         runs[1].first = runs[0].first + S + 1;
         o->norm = runs[0];
         o->step = runs[1];
-        o->partial = reinterpret_cast<double*>(base + at_partial);
+        o->partial = reinterpret_cast<Sum*>(base + at_partial);
         o->done = reinterpret_cast<unsigned*>(base + at_done);
         o->S = static_cast<int>(S);
         o->device = dev;
@@ -888,12 +907,12 @@ int ddp_adamw_step(ddp_adamw* o, const ddp_adamw_args* x, void* stream) {
     a.c.seed_lo = static_cast<uint32_t>(x->seed);
     a.c.seed_hi = static_cast<uint32_t>(x->seed >> 32);
     int grid = 0;
-    split(o->step.count, static_cast<int64_t>(o->sms) * kStepCtasPerSm[o->q8], &grid, &a.piece);
+    split(o->step.count, kWarps, static_cast<int64_t>(o->sms) * kStepCtasPerSm[o->q8], &grid, &a.piece);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = o->bf16 ? (o->q8 ? launch(adamw_kernel<true, true>, grid, a, st)
-                                           : launch(adamw_kernel<true, false>, grid, a, st))
-                                  : (o->q8 ? launch(adamw_kernel<false, true>, grid, a, st)
-                                           : launch(adamw_kernel<false, false>, grid, a, st));
+    const cudaError_t e = o->bf16 ? (o->q8 ? launch(adamw_kernel<true, true>, kThreads, grid, a, st)
+                                           : launch(adamw_kernel<true, false>, kThreads, grid, a, st))
+                                  : (o->q8 ? launch(adamw_kernel<false, true>, kThreads, grid, a, st)
+                                           : launch(adamw_kernel<false, false>, kThreads, grid, a, st));
     return e == cudaSuccess ? DDP_OK : o->cuda(e);
 }
 
@@ -913,8 +932,8 @@ int ddp_adamw_grad_norm(ddp_adamw* o, const uint8_t* used, float* norm, void* st
     a.run = o->norm.run;
     a.S = o->S;
     int grid = 1;                    // without elements one CTA writes the zero
-    if (o->norm.count) split(o->norm.count, static_cast<int64_t>(o->sms) * kNormCtasPerSm, &grid, &a.piece);
-    const cudaError_t e = launch(norm_kernel, grid, a, static_cast<cudaStream_t>(stream));
+    if (o->norm.count) split(o->norm.count, kNormThreads / 32, static_cast<int64_t>(o->sms) * kNormCtasPerSm, &grid, &a.piece);
+    const cudaError_t e = launch(norm_kernel, kNormThreads, grid, a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? DDP_OK : o->cuda(e);
 }
 

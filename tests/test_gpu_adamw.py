@@ -310,7 +310,8 @@ def test_norm(sizes, shift):
     a = case.opt.grad_norm(norm).clone()
     b = case.opt.grad_norm(norm).clone()
     exact = A.grad_norm(case.g)
-    # squares and sums of eight in fp32, all else in double: 9u on the square, half of it on the root, and its rounding
+    # a lane's squares are summed in fp32, all else in twice its digits: errors of either sign, of which 16u of the square
+    # (8u of its root) are far out
     assert abs(float(a) - exact) <= 8 * U * exact
     assert torch.equal(a, b)
     alone = AdamW(case.sizes)
