@@ -812,16 +812,16 @@ int ddp_adamw_bind(ddp_adamw* o, const float* const* grads, void* const* params,
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
         if (e != cudaSuccess) return o->cuda(e);
         // first runs for the norm, then for the step.  Runs of eight blocks
-        // where they still give every warp of the grid some.  32-bit moments
-        // have no scales and take single blocks: a warp's neighbours then work
-        // on the same pages (GPT-2-medium, bf16 weights: 1,579 us against 1,595)
+        // where they still give an SM 32 (the norm; 10 M elements, eight / four:
+        // 11.4 / 12.8 us) or 64 warps theirs.  32-bit moments have no scales and
+        // take single blocks: a warp's neighbours then work on the same pages
+        // (GPT-2-medium, bf16 weights: 1,579 us against 1,595)
         const size_t S = tensors.size();
         std::vector<long long> first;
-        int longest = kMaxRun;
-        while (longest > 1 && blocks < static_cast<int64_t>(longest) * sms * 64) longest /= 2;
         Runs runs[2];
         for (int k = 0; k < 2; ++k) {
-            runs[k].run = k == 0 || o->q8 ? longest : 1;
+            runs[k].run = k == 0 || o->q8 ? kMaxRun : 1;
+            while (runs[k].run > 1 && blocks < static_cast<int64_t>(runs[k].run) * sms * (k == 0 ? 32 : 64)) runs[k].run /= 2;
             for (const Tensor& t : tensors) {
                 first.push_back(runs[k].count);
                 runs[k].count += ((t.n + kBlock - 1) / kBlock + runs[k].run - 1) / runs[k].run;
