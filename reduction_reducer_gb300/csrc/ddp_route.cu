@@ -330,16 +330,22 @@ __device__ __forceinline__ void order_exact(const RouteParams& a, const T* row, 
 }
 
 // Whether this lane's group stays, by the fp32 definition; for all tokens of a
-// warp.  The lane's experts are n from e0 on.
+// warp.  The lane's experts are n from e0 on; k1, k2, k3: its largest keys.
+// Its two largest values are those of k1 and k2, unless k3 is less than `near`
+// below.
 template <int LPT, typename T>
-__device__ __noinline__ bool groups_exact(const RouteParams& a, const T* row, int e0, int n, float top, float sum, int g,
-                                          int group_lanes, int size) {
+__device__ __noinline__ bool groups_exact(const RouteParams& a, const T* row, int e0, int n, uint32_t k1, uint32_t k2,
+                                          uint32_t k3, uint32_t near, float top, float sum, int g, int group_lanes,
+                                          int size) {
+    const auto value = [&](int e) {
+        const float x = widen(row[e]);
+        const float s = a.softmax ? __fdiv_rn(expf(x - top), sum) : sigmoid(x);
+        return a.bias ? __fadd_rn(s, a.bias[e]) : s;
+    };
     float a1 = neg_inf(), a2 = neg_inf();
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-        const float x = widen(row[e0 + j]);
-        float c = a.softmax ? __fdiv_rn(expf(x - top), sum) : sigmoid(x);
-        if (a.bias) c = __fadd_rn(c, a.bias[e0 + j]);
+    const bool two = k2 - k3 >= near;
+    for (int j = 0; j < (two ? min(n, 2) : n); ++j) {
+        const float c = value(two ? kMaxExperts - 1 - static_cast<int>((j ? k2 : k1) & (kMaxExperts - 1)) : e0 + j);
         a2 = fmaxf(a2, fminf(a1, c));
         a1 = fmaxf(a1, c);
     }
@@ -511,7 +517,7 @@ route_kernel(const __grid_constant__ RouteParams a) {
                     const uint32_t out = token_max<LPT>(worth);
                     if (__any_sync(kAll, on && (worst >> 5) - (out >> 5) < 2 * by_score))
                         stays = groups_exact<LPT>(a, static_cast<const T*>(a.logits) + (t0 + slot) * a.stride, e0, on ? n : 0,
-                                                  top, sum, g, group_lanes, size);
+                                                  head[0], head[1], head[2], near, top, sum, g, group_lanes, size);
                     if (!stays) head[0] = 0;
                 }
 
