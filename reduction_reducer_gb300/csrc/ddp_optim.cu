@@ -303,11 +303,11 @@ struct __align__(16) Stage {
 // Bound by HBM: an element moves 28 bytes with 32-bit moments (weight and both
 // moments read and written, gradient read), 30 with bf16 weights beside their
 // master copies, 16 and 18 with 8-bit ones.  GB300, copy peak 6,780 GB/s:
-// BERT-large (335 M elements) 1,345 us, 6,980 GB/s; GPT-2-medium with bf16
-// weights 1,541 us, 6,910 GB/s, and with 8-bit moments 959 us, 6,680 GB/s;
-// ResNet-50 104 us, 6,890 GB/s.
+// BERT-large (335 M elements) 1,339 us, 7,010 GB/s; GPT-2-medium with bf16
+// weights 1,528 us, 6,970 GB/s, and with 8-bit moments 959 us, 6,680 GB/s;
+// ResNet-50 103 us, 6,930 GB/s.
 //
-// 32-bit moments: eight 128-bit loads a lane in flight on 28 warps an SM carry
+// 32-bit moments: eight 128-bit loads a lane in flight on 24 warps an SM carry
 // it; single blocks to a warp, its neighbours on the next ones.  8-bit moments
 // take about 75 instructions an element, so a warp's loads must run while it
 // computes: its next whole block is copied to shared memory meanwhile (without
@@ -576,9 +576,11 @@ __device__ __forceinline__ float root(const Sum& x) {
 // Reads 4 bytes an element and nothing else of size.  Eight 128-bit loads a
 // lane in flight; a lane's squares of a run (at most 68) are fp32 sums, runs
 // and CTAs are added in two fp32 numbers, partial sums in an order that does not
-// depend on which CTA comes last.  GB300: BERT-large 201 us, 6,670 GB/s (a read-only
-// torch sum streams at 6,435 to 6,570); ResNet-50 17 us from a graph, of which
-// 2 us launch, search and the last CTA.
+// depend on which CTA comes last.  GB300: BERT-large 192 us, 6,970 GB/s (a
+// read-only torch sum streams at 6,435 to 6,570); ResNet-50 20 us and 1 M
+// elements 5.4 us, of which 2 are an empty launch's.  CTAs of 512 threads: as
+// many as fit finish together and count at one address (BERT-large, 128 / 256 /
+// 512 threads 202 / 195 / 192 us).
 __global__ void __launch_bounds__(kNormThreads)
 norm_kernel(const __grid_constant__ NormParams a) {
     __shared__ Sum smem[kNormThreads / 32];
@@ -706,7 +708,7 @@ namespace {
 // streams near one another and end together (BERT-large, 32 / 64 / 128 a SM:
 // 1,397 / 1,373 / 1,355 us, 256: 1,345; GPT-2-medium with 8-bit moments, 128 /
 // 256: 959 / 981); the norm takes one resident wave, of which the last adds all
-// partial sums (BERT-large, 8 / 12 / 14: 205.7 / 200.4 / 241 us).
+// partial sums (BERT-large, 2 / 3 / 4: 201 / 192 / 216 us).
 constexpr int kNormCtasPerSm = 3;
 constexpr int kStepCtasPerSm[2] = {256, 128};    // 32-bit and 8-bit moments
 

@@ -21,7 +21,7 @@
 // reads 1 KiB a token and executes about 390 warp instructions (scores, keys
 // and sorting of 256 values; k rounds; the k slots' exact scores), half of them
 // on the integer and compare pipe, which takes one every other cycle.  GB300,
-// 65,536 tokens: 256 experts in 8 groups with a bias 37.5 us (1.9 TB/s; the
+// 65,536 tokens: 256 experts in 8 groups with a bias 34.7 us (2.1 TB/s; the
 // logits alone at the copy peak 10 us), ungrouped softmax over 64 / 128 / 256
 // experts in bf16 10.3 / 17.2 / 27.4 us.  A few tokens take 3.3 us.
 
