@@ -390,7 +390,7 @@ route_kernel(const __grid_constant__ RouteParams a) {
     const int n = g < a.groups ? max(0, min(size - off, lane_slots)) : 0;
     const bool by_logit = !a.bias && a.groups == 1;
     const bool vec = a.vec && (e0 * sizeof(T)) % 16 == 0;
-    if (a.bias)
+    if (a.bias && a.fits)                          // else a group's slots may lie past the biases'
         for (int e = threadIdx.x; e < E; e += kThreads) {
             const float b = a.bias[e];
             const int at = e / size * a.group_slots + e % size, j = at % lane_slots;

@@ -264,6 +264,18 @@ def test_refusals_of_tensors():
         route(x, 2, groups=3)
 
 
+@pytest.mark.parametrize("E,groups,top,k", [(500, 10, 4, 8), (480, 12, 3, 6), (510, 30, 7, 8)])
+def test_counts_where_the_groups_do_not_fit_the_lanes(E, groups, top, k):
+    """Groups that waste so many slots that every token is chosen by the definition: with a bias, the counts and the
+    choice stay whole."""
+    x = draw(700, E, "f32", seed=E)
+    bias = torch.randn(E, generator=torch.Generator("cuda").manual_seed(1), device="cuda") * 0.1
+    counts = torch.zeros(E, dtype=torch.int32, device="cuda")
+    index, _ = route(x, k, score="sigmoid", bias=bias, groups=groups, top_groups=top, counts=counts)
+    assert torch.equal(index.long(), fp32_choice(x, k, "sigmoid", bias, groups, top))
+    assert torch.equal(counts.long(), torch.bincount(index.flatten().long(), minlength=E))
+
+
 def fp32_choice(x, k, score, bias, groups=1, top_groups=1):
     """The choice by the definition in fp32, step by step: exponentials, products and sums as torch rounds them."""
     x = x.float()
