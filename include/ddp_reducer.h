@@ -424,8 +424,9 @@ int ddp_adamw_create(const int64_t* numel, int32_t P, ddp_dtype param_dtype, int
  * aligned are read and written in vectors.
  * Zero-filled moments and scales are the state before the first step.
  * Synchronous; builds a device table (library-owned, freed by
- * ddp_adamw_destroy or the next bind) on the current device, which later calls
- * must have current.  Errors: INVALID_ARG, CUDA, NO_MEMORY. */
+ * ddp_adamw_destroy or the next bind: a CUDA graph captured before holds the
+ * freed one and is captured anew) on the current device, which later calls
+ * must have current.  Not during a capture.  Errors: INVALID_ARG, CUDA, NO_MEMORY. */
 int ddp_adamw_bind(ddp_adamw* opt, const float* const* grads, void* const* params, float* const* master,
                    void* const* exp_avg, void* const* exp_avg_sq, float* const* exp_avg_scale,
                    float* const* exp_avg_sq_scale, const float* weight_decay);

@@ -842,7 +842,10 @@ int ddp_adamw_bind(ddp_adamw* o, const float* const* grads, void* const* params,
             cudaGetLastError();
             return e == cudaErrorMemoryAllocation ? o->fail(DDP_ERR_NO_MEMORY, cudaGetErrorString(e)) : o->cuda(e);
         }
+        // a copy from pageable memory returns before it has landed, and streams
+        // that do not block on the legacy one would not wait for it
         e = cudaMemcpy(table, image.data(), image.size(), cudaMemcpyHostToDevice);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);
         if (e != cudaSuccess) {
             cudaFree(table);
             return o->cuda(e);

@@ -95,7 +95,8 @@ class AdamW:
         param_dtype; master: fp32, with bf16 parameters; exp_avg, exp_avg_sq:
         fp32, or with 8 bits float8_e4m3fn and float8_e5m2 (or uint8) codes
         with fp32 scales of ceil(numel / 256) elements; weight_decay: a number
-        for all or one per tensor."""
+        for all or one per tensor.  A CUDA graph captured before this bind is
+        captured anew: it holds the earlier one's table."""
         import torch
         bf16, eight = self.param_dtype == "bf16", self.state_bits == 8
         f32 = (torch.float32,)

@@ -360,6 +360,25 @@ def test_other_stream_and_graph():
     case.check(1, A.clip_factor(float(norm), 0.1))
 
 
+def test_a_step_on_another_stream_straight_after_bind():
+    """bind has put its table in place when it returns, for streams that wait for no other too."""
+    sizes = [1 + v % 5 for v in range(900)]
+    g = [torch.full((n,), 2.0, device="cuda") for n in sizes]
+    w = [torch.zeros(n, device="cuda") for n in sizes]
+    opt = AdamW(sizes, "f32", 32)
+    state = opt.zero_state()
+    side = torch.cuda.Stream()
+    norm = torch.zeros(1, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(20):
+        opt.bind(w, g, **state)
+        opt.grad_norm(norm, stream=side)
+        side.synchronize()
+        assert float(norm) == pytest.approx(2.0 * sum(sizes) ** 0.5, rel=1e-6)
+        norm.zero_()
+        torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_offsets_past_32_bits(bits):
     """One tensor of 2^31 + 301 elements: zeros but for its ends."""
