@@ -63,6 +63,15 @@ class _Scores(dict):
 _SCORES = _Scores(softmax=0, sigmoid=1)
 
 
+def _empty(shape, dtype, like, stream):
+    """Memory of the stream that the kernel runs on: memory that was freed on
+    torch's current stream may still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
 def _refused(st: int, what: str, tokens, experts, k, **more):
     detail = ", ".join(f"{n} {v}" for n, v in dict(tokens=tokens, experts=experts, k=k, **more).items())
     raise _ERRORS.get(st, DDPError)(st, f"{what}: {detail}")
@@ -79,12 +88,12 @@ def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, to
     experts stay (worth: the sum of their two best); renorm: weights over
     their sum; mask: bytes or truth values [tokens], 0 = not routed (index
     -1, weight 0); counts: int32 [experts], the tokens each expert got are
-    added to it; out: (indices, weights) to write into."""
+    added to it; out: (indices, weights) to write into (without it they are
+    allocated on `stream`)."""
     a, tokens, experts = _args(logits, k, score, groups, top_groups, renorm, scale)
     shape, each = (tokens, k), (experts,)
     indices, weights = out if out is not None else (
-        torch.empty(shape, dtype=torch.int32, device=logits.device),
-        torch.empty(shape, dtype=torch.float32, device=logits.device))
+        _empty(shape, torch.int32, logits, stream), _empty(shape, torch.float32, logits, stream))
     st = _lib.load(lib_path).ddp_route(
         a, logits.data_ptr(), _data("bias", bias, each, _FLOAT), _data("mask", mask, (tokens,), _MASK),
         _data("indices", indices, shape, _INT), _data("weights", weights, shape, _FLOAT),
@@ -102,7 +111,7 @@ def route_backward(grad_weights, logits, indices, weights, score: str = "softmax
     k = indices.shape[1] if indices.dim() == 2 else 0
     a, tokens, experts = _args(logits, k, score, 1, 1, renorm, scale)
     shape = (tokens, k)
-    grad = out if out is not None else torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
+    grad = out if out is not None else _empty((tokens, experts), logits.dtype, logits, stream)
     if grad.shape != logits.shape or grad.dtype is not logits.dtype or not grad.is_cuda:
         raise ValueError("out: expected the logits' shape and dtype on a GPU")
     st = _lib.load(lib_path).ddp_route_backward(

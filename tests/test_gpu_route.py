@@ -241,6 +241,26 @@ def test_other_stream():
     assert torch.equal(out[0], route(x, 4)[0]) and torch.equal(out[1], route(x, 4)[1])
 
 
+def test_outputs_are_memory_of_their_stream():
+    """The allocator may hand out, on the current stream, memory that kernels queued there still use: what a call on
+    another stream writes into comes from that stream's."""
+    x, g = draw(500, 64, "f32"), torch.ones(500, 4, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def owner(t):
+        p = t.data_ptr()
+        return [s["stream"] for s in torch.cuda.memory_snapshot()
+                if s["address"] <= p < s["address"] + s["total_size"]][0]
+
+    for stream in (side, side.cuda_stream):
+        index, w = route(x, 4, stream=stream)
+        d = route_backward(g, x, index, w, stream=stream)
+        assert [owner(t) for t in (index, w, d)] == [side.cuda_stream] * 3
+        torch.cuda.synchronize()
+        assert torch.equal(index, route(x, 4)[0])
+
+
 def test_refusals_of_tensors():
     x = draw(4, 8, "f32")
     with pytest.raises(ValueError):
