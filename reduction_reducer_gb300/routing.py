@@ -141,6 +141,7 @@ def _autograd():
                 return indices, weights
 
             @staticmethod
+            @torch.autograd.function.once_differentiable      # a second derivative raises
             def backward(ctx, _indices, grad_weights):
                 logits, indices, weights = ctx.saved_tensors
                 grad = route_backward(grad_weights.contiguous(), logits, indices, weights, **ctx.options)

@@ -231,6 +231,14 @@ def test_autograd():
     assert not index.requires_grad
 
 
+def test_no_second_derivative():
+    x = draw(9, 16, "f32").requires_grad_(True)
+    _, w = routed(x, 4)
+    d, = torch.autograd.grad((w ** 2).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(d.sum(), x)
+
+
 def test_other_stream():
     x = draw(500, 64, "f32")
     side = torch.cuda.Stream()
