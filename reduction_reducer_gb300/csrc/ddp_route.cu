@@ -398,10 +398,11 @@ route_kernel(const __grid_constant__ RouteParams a) {
             atomicMax(&widest_bits, __float_as_uint(b) & 0x7fffffffu);    // of a NaN above infinity's
         }
     __syncthreads();
-    // scores + bias lie in [-range, range), a power of two; keys hold them times 2 / range
+    // scores + bias lie in [-range, range), a power of two and not within a
+    // part in 2^20 of its upper end: keys hold them times 2 / range, rounded
     const float widest = __uint_as_float(widest_bits);
     const bool fast = a.fits && widest < 0x1p20f;
-    const float over_range = 2.0f / __uint_as_float((__float_as_uint(1.0f + widest) & 0x7f800000u) + 0x00800000u);
+    const float over_range = 2.0f / __uint_as_float((__float_as_uint((1.0f + widest) * 1.000001f) & 0x7f800000u) + 0x00800000u);
     const uint32_t by_score = a.softmax ? kMarginSoftmax : kMarginSigmoid;
     const uint32_t near = !by_logit ? (by_score + 1) << 9 : sizeof(T) == 2 ? 0u : 2u << 9;   // a key holds all of a bf16 logit
     const uint32_t over_k = (65536u + k - 1) / k;                 // i / k for i < 256

@@ -292,6 +292,20 @@ def test_refusals_of_tensors():
         route(x, 2, groups=3)
 
 
+def test_a_bias_that_ends_at_a_power_of_two():
+    """score + bias just below 2, where a rounded key would be that of 2: still the best."""
+    for bias in (1 - 2.0 ** -23, 1 - 2.0 ** -24, 1.0, 3 - 2.0 ** -22, 2.0 ** 19 - 1):
+        x = draw(6, 16, "f32", seed=3)
+        x[:, 5] = 40.0
+        b = torch.zeros(16, device="cuda")
+        b[5] = bias
+        index, _ = route(x, 3, score="sigmoid", bias=b)
+        assert bool((index[:, 0] == 5).all()), bias
+        assert torch.equal(index.long(), fp32_choice(x, 3, "sigmoid", b))
+        b[5] = -bias
+        assert torch.equal(route(x, 3, score="sigmoid", bias=b)[0].long(), fp32_choice(x, 3, "sigmoid", b))
+
+
 @pytest.mark.parametrize("E,groups,top,k", [(500, 10, 4, 8), (480, 12, 3, 6), (510, 30, 7, 8)])
 def test_counts_where_the_groups_do_not_fit_the_lanes(E, groups, top, k):
     """Groups that waste so many slots that every token is chosen by the definition: with a bias, the counts and the
