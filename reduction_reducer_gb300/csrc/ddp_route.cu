@@ -21,7 +21,7 @@
 // reads 1 KiB a token and executes about 390 warp instructions (scores, keys
 // and sorting of 256 values; k rounds; the k slots' exact scores), half of them
 // on the integer and compare pipe, which takes one every other cycle.  GB300,
-// 65,536 tokens: 256 experts in 8 groups with a bias 34.7 us (2.1 TB/s; the
+// 65,536 tokens: 256 experts in 8 groups with a bias 33.7 us (2.1 TB/s; the
 // logits alone at the copy peak 10 us), ungrouped softmax over 64 / 128 / 256
 // experts in bf16 10.3 / 17.2 / 27.4 us.  A few tokens take 3.3 us.
 
@@ -507,16 +507,35 @@ route_kernel(const __grid_constant__ RouteParams a) {
                         a2 = max(min(a1, b1), max(a2, b2));
                         a1 = max(a1, b1);
                     }
-                    // no two groups' worth is equal; lanes past the last group have none
+                    // lanes past the last group have none
                     uint32_t worth = g < a.groups ? (a1 + a2) << 5 | static_cast<uint32_t>(31 - g) : 0u;
-                    uint32_t worst = 0;
-                    bool stays = false;
-                    for (int r = 0; r < a.top_groups; ++r) {
-                        worst = token_max<LPT>(worth);
-                        if (worth == worst) { worth = 0; stays = true; }
+                    // no two groups' worth is equal.  Over at most eight lanes each counts
+                    // the better ones, whose shuffles need not wait for one another; over
+                    // more the best are taken out in turn (65,536 tokens, 256 experts in
+                    // 8 groups 33.6 / 34.9 us, 64 in 8 17.3 / 18.3)
+                    bool stays = false, tie;
+                    if constexpr (LPT <= 8) {
+                        // a lane's rank: lanes of better groups; the last group that stays knows the next
+                        int rank = 0;
+                        uint32_t below = 0;
+#pragma unroll
+                        for (int o = 1; o < LPT; ++o) {
+                            const uint32_t other = __shfl_xor_sync(kAll, worth, o);
+                            if (other > worth) ++rank;
+                            else if (other != worth) below = max(below, other);
+                        }
+                        const int staying = a.top_groups * group_lanes;
+                        stays = rank < staying;
+                        tie = rank + group_lanes == staying && (worth >> 5) - (below >> 5) < 2 * by_score;
+                    } else {
+                        uint32_t worst = 0;
+                        for (int r = 0; r < a.top_groups; ++r) {
+                            worst = token_max<LPT>(worth);
+                            if (worth == worst) { worth = 0; stays = true; }
+                        }
+                        tie = (worst >> 5) - (token_max<LPT>(worth) >> 5) < 2 * by_score;
                     }
-                    const uint32_t out = token_max<LPT>(worth);
-                    if (__any_sync(kAll, on && (worst >> 5) - (out >> 5) < 2 * by_score))
+                    if (__any_sync(kAll, on && tie))
                         stays = groups_exact<LPT>(a, static_cast<const T*>(a.logits) + (t0 + slot) * a.stride, e0, on ? n : 0,
                                                   head[0], head[1], head[2], near, top, sum, g, group_lanes, size);
                     if (!stays) head[0] = 0;
@@ -833,7 +852,7 @@ cudaError_t launch_any(bool backward, RouteParams& a, cudaStream_t stream) {
     // and its bookkeeping, for a longer chain of instructions: from about 2^20
     // logits on.  Against one, 65,536 tokens over 64 experts 10.3 / 15.6 us, 128
     // 17.2 / 27.8, 256 27.4 / 39.2, 512 49.3 / 54.0, over 256 in 8 groups 37.7 /
-    // 47.1; 2,048 tokens over 128 5.3 / 4.2, 256 over 256 in groups 6.4 / 4.5.
+    // 47.1 (before the near ties of groups and their ranks took less); 2,048 tokens over 128 5.3 / 4.2, 256 over 256 in groups 6.4 / 4.5.
     for (a.chunks = a.tokens * a.E >= 1 << 20 ? 4 : 1; a.chunks; a.chunks /= 2) {
         const int mine = 8 * a.chunks;
         a.group_slots = power_of_two((size + mine - 1) / mine) * mine;
