@@ -645,8 +645,8 @@ route_kernel(const __grid_constant__ RouteParams a) {
 // GB300, 65,536 tokens over 256 experts, buffers in HBM: sigmoid in bf16 13.6
 // us, where 34 MB of gradient are written, 6 read, and each chosen logit costs a
 // sector (17 MB); softmax renormalised 8.2 us without these.  Softmax not
-// renormalised, 131,072 tokens over 128 experts in fp32, 36 us (4.0 TB/s): bound
-// by the instructions of its exponentials and sums.
+// renormalised, 131,072 tokens over 128 experts in fp32, 28.4 us (5.2 TB/s): HBM,
+// and the latency of a round's loads, sums and shared memory in turn.
 
 constexpr int kRowBytes = 4096;          // of a warp's rows under construction
 
@@ -704,22 +704,25 @@ route_backward_chosen_kernel(const __grid_constant__ RouteParams a) {
     }
 }
 
-// Softmax weights as they are: every expert of a token gets a gradient.
+// Softmax weights as they are: every expert of a token gets a gradient.  The
+// chosen experts' parts meet the lanes' experts in shared memory, laid out so
+// that a lane's 16-byte accesses meet no other's banks (131,072 tokens over 128
+// experts 28.4 us; a lane's experts next to one another 36.2).
 template <int LPT, int EPL, typename T>
 __global__ void __launch_bounds__(kThreads)
 route_backward_whole_kernel(const __grid_constant__ RouteParams a) {
     constexpr int kTokens = 32 / LPT;
-    __shared__ float rows[kWarps][32 * EPL];          // the chosen experts' parts, zeros elsewhere
+    __shared__ float4 rows[kWarps][8 * EPL];          // the chosen experts' parts, zeros elsewhere: a lane's c-th four at 32 c + lane
     __shared__ float parts[kWarps][kMaxSlots];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int l = lane % LPT, tl = lane / LPT;
     const int E = a.E, k = a.k;
-    float* const row_part = rows[warp];
+    float4* const row_part = rows[warp];
     float* const part = parts[warp];
     const int e0 = l * EPL, n = max(0, min(E - e0, EPL));
     const bool vec = a.vec && (e0 * sizeof(T)) % 16 == 0;
     const uint32_t over_k = (65536u + k - 1) / k;                 // i / k for i < 256
-    for (int j = 0; j < EPL; ++j) row_part[j * 32 + lane] = 0.0f;
+    for (int c = 0; c < EPL / 4; ++c) row_part[c * 32 + lane] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
     __syncwarp();
@@ -735,7 +738,8 @@ route_backward_whole_kernel(const __grid_constant__ RouteParams a) {
             float p = 0.0f;
             if (index >= 0 && index < E) {
                 p = a.grad_weights[t0 * k + i] * a.weights[t0 * k + i];
-                row_part[static_cast<int>(i * over_k >> 16) * (LPT * EPL) + index] = p;
+                const int at = static_cast<int>(i * over_k >> 16) * (LPT * EPL) + index;
+                reinterpret_cast<float*>(row_part)[(at % EPL / 4 * 32 + at / EPL) * 4 + at % 4] = p;
             }
             part[i] = p;
         }
@@ -760,12 +764,15 @@ route_backward_whole_kernel(const __grid_constant__ RouteParams a) {
         T* const to = static_cast<T*>(a.grad_logits) + t * a.grad_stride + e0;
         float d[EPL];
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            d[j] = row_part[lane * EPL + j];
-            if (total != 0.0f) d[j] = fmaf(-x[j], f, d[j]);       // a masked token's logits may be anything
+        for (int c = 0; c < EPL / 4; ++c) {
+            const float4 q = row_part[c * 32 + lane];
+            row_part[c * 32 + lane] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            d[4 * c] = q.x; d[4 * c + 1] = q.y; d[4 * c + 2] = q.z; d[4 * c + 3] = q.w;
         }
-        __syncwarp();
-        for (int j = 0; j < EPL; ++j) row_part[j * 32 + lane] = 0.0f;
+        if (total != 0.0f) {                                      // a masked token's logits may be anything
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) d[j] = fmaf(-x[j], f, d[j]);
+        }
         if (on) store_lane<EPL>(to, n, vec, d);
         __syncwarp();
     }
