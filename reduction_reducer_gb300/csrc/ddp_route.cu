@@ -125,11 +125,13 @@ __device__ __forceinline__ float fast_exp(float x) {
     return y;
 }
 
-__device__ __forceinline__ float fast_sigmoid(float x) {
+__device__ __forceinline__ float fast_reciprocal(float x) {
     float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + fast_exp(-x)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+__device__ __forceinline__ float fast_sigmoid(float x) { return fast_reciprocal(1.0f + fast_exp(-x)); }
 
 // A lane's experts of a row: n consecutive ones from `from` (n <= EPL); the
 // rest are `fill`.
@@ -642,9 +644,11 @@ route_kernel(const __grid_constant__ RouteParams a) {
 // sigmoid:  dx = part_r (1 - s_r) at the chosen, 0 elsewhere
 // softmax:  dx = [chosen] part_r - s_i D; renormalised D is zero, and only the
 //           chosen get a gradient
-// GB300, 65,536 tokens over 256 experts, buffers in HBM: sigmoid in bf16 13.6
-// us, where 34 MB of gradient are written, 6 read, and each chosen logit costs a
-// sector (17 MB); softmax renormalised 8.2 us without these.  Softmax not
+// A token's weights are to one another as its scores: one logit, that of the
+// first slot, gives them all.  GB300, 65,536 tokens over 256 experts, buffers in
+// HBM: sigmoid in bf16 11.3 us, where 34 MB of gradient are written, 6 read, and
+// a sector for each token's logit (13.4 with one for each slot's); softmax
+// renormalised, which needs none, 8.3 us.  Softmax not
 // renormalised, 131,072 tokens over 128 experts in fp32, 28.4 us (5.2 TB/s): HBM,
 // and the latency of a round's loads, sums and shared memory in turn.
 
@@ -666,6 +670,7 @@ route_backward_chosen_kernel(const __grid_constant__ RouteParams a) {
     ddpk::dev::pdl_trigger();
     __syncwarp();
     const int tile = a.row_tokens;
+    const float over_scale = 1.0f / a.scale;
     for (long long t0 = (static_cast<long long>(blockIdx.x) * kWarps + warp) * tile; t0 < a.tokens;
          t0 += static_cast<long long>(gridDim.x) * kWarps * tile) {
         const long long t = t0 + tl;
@@ -682,12 +687,20 @@ route_backward_chosen_kernel(const __grid_constant__ RouteParams a) {
         if (a.renorm) {
             float total = part;
             for (int o = lanes / 2; o; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
-            part = w * (g - total / a.scale);
+            part = w * (g - total * over_scale);
         }
-        if (index >= 0) {
-            if (!a.softmax) part *= 1.0f - sigmoid(widen(static_cast<const T*>(a.logits)[t * a.stride + index]));
-            rows[tl * E + index] = narrow<T>(part);
+        if (!a.softmax) {
+            const float w0 = __shfl_sync(kAll, w, tl * lanes);
+            const int index0 = __shfl_sync(kAll, index, tl * lanes);
+            if (index >= 0) {
+                const T* const row = static_cast<const T*>(a.logits) + t * a.stride;
+                const bool ratio = fabsf(w0) >= 0x1p-100f && fabsf(w0) <= 0x1p100f;    // precise, and within what __fdividef takes
+                float s = fast_reciprocal(1.0f + expf(-widen(row[ratio ? index0 : index])));
+                if (ratio) s *= __fdividef(w, w0);
+                part *= 1.0f - s;
+            }
         }
+        if (index >= 0) rows[tl * E + index] = narrow<T>(part);
         __syncwarp();
         T* const to = static_cast<T*>(a.grad_logits) + t0 * a.grad_stride;
         if (a.vec) {

@@ -194,6 +194,34 @@ def test_backward(T, E, k, score, renorm, dtype):
         assert np.all(np.abs(got[t] - want) <= bound), t
 
 
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("scale", [1.0, -2.0, 1e-30, 1e38])
+def test_backward_where_the_first_weight_says_little(scale, renorm):
+    """Sigmoid scores of a token over the whole range, the first slot's zero or the smallest (the bias puts it first),
+    and weights near the ends of fp32's range."""
+    T, E, k = 64, 24, 6
+    x = draw(T, E, "f32", seed=11) * 6.0
+    bias = torch.zeros(E, device="cuda")
+    bias[2:5] = 3.0
+    x[:16, 2] = -200.0
+    x[16:32, 2] = -60.0
+    x[8:24, 3:5] = -150.0
+    x[32:40] = -120.0
+    x[40:48, 7] = 90.0
+    index, w = route(x, k, score="sigmoid", bias=bias, renorm=renorm, scale=scale)
+    g = torch.randn(T, k, generator=torch.Generator("cuda").manual_seed(1), device="cuda") * 0.1
+    d = route_backward(g, x, index, w, score="sigmoid", renorm=renorm, scale=scale).double().cpu().numpy()
+    rows = x.double().cpu().numpy()
+    for t in range(T):
+        gt = g[t].double().cpu().numpy()
+        if not bool((w[t] != 0).any()):                              # scores below fp32's least number
+            assert np.all(d[t] == 0), t
+            continue
+        want = R.backward_token(rows[t], index[t].tolist(), gt, "sigmoid", renorm, scale)
+        size = np.abs(gt * w[t].double().cpu().numpy()).sum()
+        assert np.all(np.abs(d[t] - want) <= 160 * U * size + 2.0 ** -140), t
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_backward_against_differences(score, renorm):
