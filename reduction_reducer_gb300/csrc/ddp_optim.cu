@@ -711,6 +711,7 @@ namespace {
 // partial sums (BERT-large, 2 / 3 / 4: 201 / 192 / 216 us).
 constexpr int kNormCtasPerSm = 3;
 constexpr int kStepCtasPerSm[2] = {256, 128};    // 32-bit and 8-bit moments
+constexpr int kStep8WarpsPerSm = 28;             // resident: seven CTAs of 68 or 72 registers
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
@@ -813,17 +814,31 @@ int ddp_adamw_bind(ddp_adamw* o, const float* const* grads, void* const* params,
         cudaError_t e = cudaGetDevice(&dev);
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
         if (e != cudaSuccess) return o->cuda(e);
-        // first runs for the norm, then for the step.  Runs of eight blocks
-        // where they still give an SM 32 (the norm; 10 M elements, eight / four:
-        // 11.4 / 12.8 us) or 64 warps theirs.  32-bit moments have no scales and
-        // take single blocks: a warp's neighbours then work on the same pages
-        // (GPT-2-medium, bf16 weights: 1,579 us against 1,595)
+        // first runs for the norm, then for the step.  The norm's are of eight
+        // blocks where they still give an SM 32 warps theirs (10 M elements,
+        // eight / four: 11.4 / 12.8 us).  32-bit moments have no scales and take
+        // single blocks: a warp's neighbours then work on the same pages
+        // (GPT-2-medium, bf16 weights: 1,579 us against 1,595).  With 8-bit
+        // moments the runs fill whole waves of the warps that fit an SM: one of
+        // runs of at most two blocks, else two or more of up to eight (runs halved
+        // from eight on until an SM has 64 / this: 3 M elements 13.1 / 11.4 us, 4 M
+        // 16.2 / 14.2, 3 M of which a third is unused 11.1 / 9.5, 10 M 28.5 / 27.7;
+        // one wave of longer runs loses where tensors are unused: 11.3)
         const size_t S = tensors.size();
         std::vector<long long> first;
         Runs runs[2];
         for (int k = 0; k < 2; ++k) {
-            runs[k].run = k == 0 || o->q8 ? kMaxRun : 1;
-            while (runs[k].run > 1 && blocks < static_cast<int64_t>(runs[k].run) * sms * (k == 0 ? 32 : 64)) runs[k].run /= 2;
+            if (k == 0) {
+                runs[k].run = kMaxRun;
+                while (runs[k].run > 1 && blocks < static_cast<int64_t>(runs[k].run) * sms * 32) runs[k].run /= 2;
+            } else if (o->q8) {
+                int64_t run = 0, warps = 0;
+                do {
+                    warps += static_cast<int64_t>(sms) * kStep8WarpsPerSm;
+                    run = (blocks + warps - 1) / warps;
+                } while (run > (warps == static_cast<int64_t>(sms) * kStep8WarpsPerSm ? 2 : kMaxRun));
+                if (run > 1) runs[k].run = static_cast<int>(run);
+            }
             for (const Tensor& t : tensors) {
                 first.push_back(runs[k].count);
                 runs[k].count += ((t.n + kBlock - 1) / kBlock + runs[k].run - 1) / runs[k].run;
