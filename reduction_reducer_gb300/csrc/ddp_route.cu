@@ -694,7 +694,8 @@ route_backward_chosen_kernel(const __grid_constant__ RouteParams a) {
             const int index0 = __shfl_sync(kAll, index, tl * lanes);
             if (index >= 0) {
                 const T* const row = static_cast<const T*>(a.logits) + t * a.stride;
-                const bool ratio = fabsf(w0) >= 0x1p-100f && fabsf(w0) <= 0x1p100f;    // precise, and within what __fdividef takes
+                // a weight that has all its bits, and is within what __fdividef takes
+                const bool ratio = fabsf(w0) >= 0x1p-100f && fabsf(w0) <= 0x1p100f;
                 float s = fast_reciprocal(1.0f + expf(-widen(row[ratio ? index0 : index])));
                 if (ratio) s *= __fdividef(w, w0);
                 part *= 1.0f - s;
@@ -725,7 +726,8 @@ template <int LPT, int EPL, typename T>
 __global__ void __launch_bounds__(kThreads)
 route_backward_whole_kernel(const __grid_constant__ RouteParams a) {
     constexpr int kTokens = 32 / LPT;
-    __shared__ float4 rows[kWarps][8 * EPL];          // the chosen experts' parts, zeros elsewhere: a lane's c-th four at 32 c + lane
+    // the chosen experts' parts, zeros elsewhere: a lane's c-th four at 32 c + lane
+    __shared__ float4 rows[kWarps][8 * EPL];
     __shared__ float parts[kWarps][kMaxSlots];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int l = lane % LPT, tl = lane / LPT;
@@ -872,7 +874,8 @@ cudaError_t launch_any(bool backward, RouteParams& a, cudaStream_t stream) {
     // and its bookkeeping, for a longer chain of instructions: from about 2^20
     // logits on.  Against one, 65,536 tokens over 64 experts 10.3 / 15.6 us, 128
     // 17.2 / 27.8, 256 27.4 / 39.2, 512 49.3 / 54.0, over 256 in 8 groups 37.7 /
-    // 47.1 (before the near ties of groups and their ranks took less); 2,048 tokens over 128 5.3 / 4.2, 256 over 256 in groups 6.4 / 4.5.
+    // 47.1 (before the near ties of groups and their ranks took less); 2,048
+    // tokens over 128 5.3 / 4.2, 256 over 256 in groups 6.4 / 4.5.
     for (a.chunks = a.tokens * a.E >= 1 << 20 ? 4 : 1; a.chunks; a.chunks /= 2) {
         const int mine = 8 * a.chunks;
         a.group_slots = power_of_two((size + mine - 1) / mine) * mine;
