@@ -506,8 +506,7 @@ int ddp_route(const ddp_route_args* args, const void* logits, const float* bias,
 /* The logits' gradient from the weights': grad_logits (device, dtype,
  * [tokens] rows of `experts`, grad_stride apart, every element written) from
  * grad_weights (device fp32 [tokens * k]) and the indices and weights as
- * ddp_route wrote them (sigmoid scores are taken from the weights' ratios and
- * one logit).  Of args, bias and groups play no part.
+ * ddp_route wrote them.  Of args, bias and groups play no part.
  * Errors: INVALID_ARG, CUDA. */
 int ddp_route_backward(const ddp_route_args* args, const void* logits, const int32_t* indices, const float* weights,
                        const float* grad_weights, void* grad_logits, int64_t grad_stride, void* stream);

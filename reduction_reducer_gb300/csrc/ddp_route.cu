@@ -644,11 +644,12 @@ route_kernel(const __grid_constant__ RouteParams a) {
 // sigmoid:  dx = part_r (1 - s_r) at the chosen, 0 elsewhere
 // softmax:  dx = [chosen] part_r - s_i D; renormalised D is zero, and only the
 //           chosen get a gradient
-// A token's weights are to one another as its scores: one logit, that of the
-// first slot, gives them all.  GB300, 65,536 tokens over 256 experts, buffers in
-// HBM: sigmoid in bf16 11.3 us, where 34 MB of gradient are written, 6 read, and
-// a sector for each token's logit (13.4 with one for each slot's); softmax
-// renormalised, which needs none, 8.3 us.  Softmax not
+// GB300, 65,536 tokens over 256 experts, buffers in HBM: sigmoid in bf16 13.5 us,
+// where 34 MB of gradient are written, 6 read, and up to 17 more as a sector for
+// each slot's logit; softmax renormalised, which needs none, 8.3 us.  (Scores
+// taken from the weights' ratios and one logit a token gave 11.3 us and gradients
+// of confident experts that were off by percents at logits of 10 and could have
+// the wrong sign at 15.)  Softmax not
 // renormalised, 131,072 tokens over 128 experts in fp32, 28.4 us (5.2 TB/s): HBM,
 // and the latency of a round's loads, sums and shared memory in turn.
 
@@ -689,18 +690,8 @@ route_backward_chosen_kernel(const __grid_constant__ RouteParams a) {
             for (int o = lanes / 2; o; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
             part = w * (g - total * over_scale);
         }
-        if (!a.softmax) {
-            const float w0 = __shfl_sync(kAll, w, tl * lanes);
-            const int index0 = __shfl_sync(kAll, index, tl * lanes);
-            if (index >= 0) {
-                const T* const row = static_cast<const T*>(a.logits) + t * a.stride;
-                // a weight that has all its bits, and is within what __fdividef takes
-                const bool ratio = fabsf(w0) >= 0x1p-100f && fabsf(w0) <= 0x1p100f;
-                float s = fast_reciprocal(1.0f + expf(-widen(row[ratio ? index0 : index])));
-                if (ratio) s *= __fdividef(w, w0);
-                part *= 1.0f - s;
-            }
-        }
+        // 1 - s = sigmoid(-x) from the slot's own logit: a difference would leave nothing of it where s is near 1
+        if (!a.softmax && index >= 0) part *= sigmoid(-widen(static_cast<const T*>(a.logits)[t * a.stride + index]));
         if (index >= 0) rows[tl * E + index] = narrow<T>(part);
         __syncwarp();
         T* const to = static_cast<T*>(a.grad_logits) + t0 * a.grad_stride;
