@@ -671,7 +671,6 @@ route_backward_chosen_kernel(const __grid_constant__ RouteParams a) {
     ddpk::dev::pdl_trigger();
     __syncwarp();
     const int tile = a.row_tokens;
-    const float over_scale = 1.0f / a.scale;
     for (long long t0 = (static_cast<long long>(blockIdx.x) * kWarps + warp) * tile; t0 < a.tokens;
          t0 += static_cast<long long>(gridDim.x) * kWarps * tile) {
         const long long t = t0 + tl;
@@ -688,7 +687,7 @@ route_backward_chosen_kernel(const __grid_constant__ RouteParams a) {
         if (a.renorm) {
             float total = part;
             for (int o = lanes / 2; o; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
-            part = w * (g - total * over_scale);
+            part = w * (g - __fdiv_rn(total, a.scale));      // (1 / scale may be infinite)
         }
         // 1 - s = sigmoid(-x) from the slot's own logit: a difference would leave nothing of it where s is near 1
         if (!a.softmax && index >= 0) part *= sigmoid(-widen(static_cast<const T*>(a.logits)[t * a.stride + index]));

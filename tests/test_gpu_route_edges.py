@@ -48,3 +48,21 @@ def test_sigmoid_gradient_of_confident_experts(renorm, dtype):
     got = d.gather(1, at)
     assert bool(((got - want).abs() <= bound).all())
     assert int((d != 0).sum()) <= T * k
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("scale", [1e-39, -3e-40])
+def test_gradient_at_scales_below_the_least_normal_number(scale, score):
+    """1 / scale is infinite in fp32.  Weights and products are subnormal, each within 2^-150 of itself: k + 4 of these
+    beside the bound of ordinary scales."""
+    T, E, k = 50, 24, 6
+    x = torch.randn(T, E, generator=generator(3), device="cuda")
+    g = torch.randn(T, k, generator=generator(4), device="cuda")
+    index, w = route(x, k, score=score, renorm=True, scale=scale)
+    assert bool((w != 0).all())
+    d = route_backward(g, x, index, w, score=score, renorm=True, scale=scale).double().cpu().numpy()
+    fp32_scale = float(np.float32(scale))
+    for t in range(T):
+        gt = g[t].double().cpu().numpy()
+        want = R.backward_token(x[t].double().cpu().numpy(), index[t].tolist(), gt, score, True, fp32_scale)
+        size = np.abs(gt * w[t].double().cpu().numpy()).sum()
+        assert np.all(np.abs(d[t] - want) <= 160 * U * size + (k + 4) * 2.0 ** -149 * (1 + np.abs(gt).max())), t
