@@ -66,3 +66,84 @@ def test_gradient_at_scales_below_the_least_normal_number(scale, score):
         want = R.backward_token(x[t].double().cpu().numpy(), index[t].tolist(), gt, score, True, fp32_scale)
         size = np.abs(gt * w[t].double().cpu().numpy()).sum()
         assert np.all(np.abs(d[t] - want) <= 160 * U * size + (k + 4) * 2.0 ** -149 * (1 + np.abs(gt).max())), t
+
+def softmax_definition(x, groups):
+    """Softmax scores in fp32, step by step: e = exp(x - largest); the sum of a group's experts eight by eight, one
+    after another, the eights' sums and then the groups' in pairs; e over the sum."""
+    T, E = x.shape
+    x = x.float()
+    e = torch.exp(x - x.amax(1, keepdim=True))
+    size = E // groups
+    eights = 1
+    while 8 * eights < size:
+        eights *= 2
+    count = 1
+    while count < groups:
+        count *= 2
+    wide = torch.zeros(T, count, 8 * eights, device="cuda")
+    wide[:, :groups, :size] = e.view(T, groups, size)
+    wide = wide.view(T, count * eights, 8)
+    total = wide[:, :, 0]
+    for j in range(1, 8):
+        total = total + wide[:, :, j]
+    while total.shape[1] > 1:
+        total = total[:, 0::2] + total[:, 1::2]
+    return e / total
+
+
+def softmax_choice(x, k, bias, groups, top):
+    """(indices, weights) of route(score="softmax", bias=bias) by the definition in fp32."""
+    T, E = x.shape
+    s = softmax_definition(x, groups)
+    c = s + bias
+    if groups > 1:
+        worth = c.view(T, groups, E // groups).topk(min(2, E // groups)).values.sum(2)
+        first = worth.argsort(dim=1, descending=True, stable=True)[:, :top]
+        stay = torch.zeros(T, groups, dtype=torch.bool, device="cuda").scatter_(1, first, True)
+        c = torch.where(stay.repeat_interleave(E // groups, dim=1), c, float("-inf"))
+    index = c.argsort(dim=1, descending=True, stable=True)[:, :k]
+    return index, s.gather(1, index)
+
+
+# every layout: one to four eights a lane, groups that fill lanes and groups that do not, ones that fit no layout
+SOFTMAX = [(8, 1, 1, 3), (24, 1, 1, 4), (60, 1, 1, 5), (128, 1, 1, 8), (200, 1, 1, 12), (256, 1, 1, 8), (512, 1, 1, 10),
+           (64, 8, 3, 6), (72, 8, 3, 8), (60, 4, 2, 5), (256, 8, 4, 8), (320, 10, 3, 6), (500, 10, 4, 8), (510, 3, 2, 5),
+           (510, 30, 7, 8), (512, 16, 4, 8)]
+
+
+@pytest.mark.parametrize("E,groups,top,k", SOFTMAX)
+@pytest.mark.parametrize("spread", [0.0, 6e-8, 1e-6, 1e-2])
+def test_softmax_scores_and_near_ties_follow_the_definition(E, groups, top, k, spread):
+    """A bias that brings the experts of a row within `spread` of one another, rows that differ by a shift (the same
+    scores but for roundings) and rows of their own: choices and weights are the fp32 definition's bit for bit."""
+    x = torch.randn(1, E, generator=generator(E), device="cuda") + torch.randn(60, 1, generator=generator(7), device="cuda")
+    x[40:] = torch.randn(20, E, generator=generator(8), device="cuda") * 1.5
+    bias = 0.7 - softmax_definition(x[:1], groups)[0] + torch.rand(E, generator=generator(9), device="cuda") * spread
+    index, w = route(x, k, bias=bias, groups=groups, top_groups=top)
+    want, weight = softmax_choice(x, k, bias, groups, top)
+    assert torch.equal(index.long(), want)
+    assert torch.equal(w, weight)
+
+
+@pytest.mark.parametrize("E,groups,top,k", SOFTMAX)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_token_routes_alike_in_every_batch(E, groups, top, k, dtype):
+    """Softmax weights and choices of the same rows alone, among more than 2^20 logits (another layout of lanes), and
+    where one bias is too large for the fast keys: equal bit for bit."""
+    n = 50
+    x = (torch.randn(n, E, generator=generator(E + 1), device="cuda") * 1.5).to(KINDS[dtype])
+    many = x.repeat((1 << 20) // E // n + 2, 1)
+    near = 0.7 - softmax_definition(x[:1], groups)[0]
+    for bias in (None, near, near * 0.01) if groups == 1 else (near, near * 0.01):
+        how = dict(bias=bias, groups=groups, top_groups=top)
+        index, w = route(x, k, **how)
+        big_index, big_w = route(many, k, **how)
+        assert torch.equal(big_index, index.repeat(many.shape[0] // n, 1))
+        assert torch.equal(big_w, w.repeat(many.shape[0] // n, 1))
+    close = near.clone()
+    close[E - 1] = -2.0 ** 19                                        # never chosen
+    far = close.clone()
+    far[E - 1] = -2.0 ** 21
+    index, w = route(x, k, bias=close, groups=groups, top_groups=top)
+    exact_index, exact_w = route(x, k, bias=far, groups=groups, top_groups=top)
+    assert torch.equal(exact_index, index) and torch.equal(exact_w, w)
