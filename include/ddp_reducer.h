@@ -437,7 +437,8 @@ typedef struct ddp_adamw_args {
     double max_norm;         /* > 0: clip by *norm; 0: no clipping */
     const float* norm;       /* device fp32, read by the kernel (ddp_adamw_grad_norm writes one), or NULL */
     const uint8_t* used;     /* device [P], or NULL = all: tensors with 0 keep parameter and moments */
-    uint64_t seed;           /* of the 8-bit rounding; another one each step */
+    uint64_t seed;           /* of the 8-bit rounding; another one each step, t for instance: with one and the
+                              * same each element would keep its rounding threshold, and averages their bias */
     int32_t skip_nonfinite;  /* != 0: a *norm that is not finite leaves everything as it is */
 } ddp_adamw_args;
 

@@ -145,15 +145,17 @@ class AdamW:
         return out
 
     def step(self, t: int, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, norm=None, max_norm: float = 0.0,
-             used=None, seed: int = 0, skip_nonfinite: bool = False, stream=None):
+             used=None, seed=None, skip_nonfinite: bool = False, stream=None):
         """Step number t (from 1).  norm: device fp32 the kernel clips by with
         max_norm > 0; used: device bytes [P], tensors with 0 stay as they are;
-        seed: of the 8-bit moments' rounding, another one each step;
+        seed: of the 8-bit moments' rounding, another one each step (None: t; one
+        and the same would hold every element at a threshold of its own for ever);
         skip_nonfinite: a norm that is not finite leaves everything as it is."""
         norm, used = self._norm(norm), self._used(used)
         try:
-            args = _lib.pack_adamw(t, lr, betas[0], betas[1], eps, max_norm, norm, used, seed, 1 if skip_nonfinite else 0)
-        except struct.error as e:
+            args = _lib.pack_adamw(t, lr, betas[0], betas[1], eps, max_norm, norm, used,
+                                   max(t, 0) if seed is None else seed, 1 if skip_nonfinite else 0)
+        except (struct.error, TypeError) as e:
             raise ValueError(f"t, a hyperparameter or seed: {e}") from None
         self._check(self.lib.ddp_adamw_step(self._h, args, _stream(stream)))
 
