@@ -433,7 +433,7 @@ int ddp_adamw_bind(ddp_adamw* opt, const float* const* grads, void* const* param
 
 typedef struct ddp_adamw_args {
     int64_t t;               /* number of this step, from 1 */
-    double lr, beta1, beta2, eps;   /* finite; lr >= 0, 0 <= beta < 1, eps > 0 */
+    double lr, beta1, beta2, eps;   /* finite; lr >= 0, 0 <= beta < 1, eps >= 2^-126 */
     double max_norm;         /* > 0: clip by *norm; 0: no clipping */
     const float* norm;       /* device fp32, read by the kernel (ddp_adamw_grad_norm writes one), or NULL */
     const uint8_t* used;     /* device [P], or NULL = all: tensors with 0 keep parameter and moments */

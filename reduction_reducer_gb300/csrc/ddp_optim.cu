@@ -272,12 +272,26 @@ __device__ __forceinline__ void moments(const Scalars& c, float2 g, float2& m, f
 }
 
 // The hardware's root and reciprocal (1 ulp each): w' is rounded to far less
-// than the 2^-24 of w that an update of lr w can show.  Subnormal v count as 0.
+// than the 2^-24 of w that an update of lr w can show.  A v below 2^-126, which
+// gradients below 3e-18 give, is taken for what it is: with SMALL, where no v is
+// above 2^100, the flushing root of 2^24 v (rbc2 is then over 2^12), else the
+// root that does not flush, of three more instructions (8-bit moments, 100 M
+// elements 236.5 / 239.2 us; 32-bit ones wait for HBM: 399 with either).  A
+// denominator is at least eps, a normal number, and past 2^126, where the
+// reciprocal would be subnormal, only with such an eps: no update then.
+template <bool SMALL>
 __device__ __forceinline__ float2 weight(const Scalars& c, float keep, float2 w, float2 m, float2 v) {
-    float2 root, over;
-    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root.x) : "f"(v.x));
-    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root.y) : "f"(v.y));
-    const float2 denom = fma2(root, both(c.rbc2), both(c.eps));
+    float2 root, over, denom;
+    if constexpr (SMALL) {
+        v = mul2(v, both(0x1p24f));
+        asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root.x) : "f"(v.x));
+        asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root.y) : "f"(v.y));
+        denom = fma2(root, both(c.rbc2 * 0x1p-12f), both(c.eps));
+    } else {
+        asm("sqrt.approx.f32 %0, %1;" : "=f"(root.x) : "f"(v.x));
+        asm("sqrt.approx.f32 %0, %1;" : "=f"(root.y) : "f"(v.y));
+        denom = fma2(root, both(c.rbc2), both(c.eps));
+    }
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(over.x) : "f"(denom.x));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(over.y) : "f"(denom.y));
     return fma2(mul2(m, both(-c.step)), over, mul2(w, both(keep)));
@@ -472,8 +486,6 @@ adamw_kernel(const __grid_constant__ StepParams a) {
                         vv = mul2(vv, both(vs));
                     }
                     moments(a.c, mul2(make_float2(g[h][q], g[h][q + 1]), both(clip)), mm, vv);
-                    const float2 ww = weight(a.c, keep, make_float2(w[h][q], w[h][q + 1]), mm, vv);
-                    w[h][q] = ww.x; w[h][q + 1] = ww.y;
                     m[h][q] = mm.x; m[h][q + 1] = mm.y;
                     v[h][q] = vv.x; v[h][q + 1] = vv.y;
                     if constexpr (Q8) {     // past the tensor's end both moments are zero
@@ -481,6 +493,19 @@ adamw_kernel(const __grid_constant__ StepParams a) {
                         peak_v = peak(peak(peak_v, vv.x), vv.y);
                     }
                 }
+            const auto weights = [&](auto small) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int q = 0; q < 4; q += 2) {
+                        const float2 x = weight<decltype(small)::value>(
+                            a.c, keep, make_float2(w[h][q], w[h][q + 1]), make_float2(m[h][q], m[h][q + 1]),
+                            make_float2(v[h][q], v[h][q + 1]));
+                        w[h][q] = x.x; w[h][q + 1] = x.y;
+                    }
+            };
+            if (Q8 && peak_v <= 0x1p100f) weights(std::true_type());
+            else weights(std::false_type());
             if constexpr (Q8) {
                 ms = block_scale(peak_m, 1.0f / 448.0f);
                 vs = block_scale(peak_v, 1.0f / 57344.0f);

@@ -55,3 +55,34 @@ def test_the_default_seed_is_the_step():
         made.append(state["exp_avg"][0].view(torch.uint8).clone())
     assert torch.equal(made[0], made[1])
     assert not torch.equal(made[0], made[2]) and not torch.equal(made[0], made[3])
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_second_moments_below_the_least_normal_number(dtype, bits):
+    """The first step from zero state moves a weight by lr, however small the gradient: g of 3e-19 to 3e-18 gives v of
+    9e-41 to 9e-39, below 2^-126, whose rounding (2^-150 of it, half of that of its root) is at most 4e-6."""
+    n = 1000
+    gen = torch.Generator("cuda").manual_seed(0)
+    sign = torch.where(torch.rand(n, generator=gen, device="cuda") < 0.5, -1.0, 1.0)
+    g = sign * 3e-19 * 10 ** torch.rand(n, generator=gen, device="cuda")
+    opt = AdamW([n], dtype, bits)
+    w = torch.zeros(n, device="cuda")
+    bf16 = dict(master=[w]) if dtype == "bf16" else {}
+    opt.bind([w.bfloat16() if bf16 else w], [g], **bf16, **opt.zero_state())
+    opt.step(1, lr=0.5, eps=1e-30)
+    v = 1e-3 * g.double() ** 2
+    assert float(v.max()) < 2.0 ** -126
+    assert bool(((w.double() + 0.5 * sign).abs() <= 0.5 * (24 * U + 2.0 ** -151 / v)).all())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_second_moments_near_the_largest_number(bits):
+    """g of 1e13 to 1e19, v of 1e23 to 1e35, beside small ones in the same blocks: each first step moves its weight by lr."""
+    n = 1000
+    g = torch.logspace(13, 19, n, device="cuda")
+    g[1::2] = 10.0 ** -torch.linspace(0, 5, n // 2, device="cuda")
+    opt = AdamW([n], "f32", bits)
+    w = torch.zeros(n, device="cuda")
+    opt.bind([w], [g], **opt.zero_state())
+    opt.step(1, lr=0.5, eps=1e-30)
+    assert bool(((w + 0.5).abs() <= 0.5 * 24 * U).all())
