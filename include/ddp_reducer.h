@@ -393,12 +393,12 @@ int ddp_shard_mean(int32_t G, ddp_dtype dtype, const void* const* chunks, float*
  * held in 32 bits, or in 8: m as e4m3 and v as e5m2 numbers times one fp32
  * scale for each block of DDP_ADAMW_BLOCK elements of a tensor.  An 8-bit
  * moment's new scale is its block's largest magnitude over the format's
- * largest finite value (448, 57344); blocks whose scale would be below
- * 2^-126 become zeros, and blocks that hold a value that is not finite get
- * a NaN scale.  Values between two codes round up with the probability of the
- * rest (16 bits of a counter hash of the step's seed, the block and the place
- * in it), so that averages stay unbiased where a step of (1 - beta2) is far
- * below the codes' spacing; a v that is not zero is never stored as zero.
+ * largest finite value (448, 57344), but 2^-126 where that is less (0 for a
+ * block of zeros); blocks that hold a value that is not finite get a NaN scale.
+ * Values between two codes round up with the probability of the rest (16 bits
+ * of a counter hash of the step's seed, the block and the place in it), so that
+ * averages stay unbiased where a step of (1 - beta2) is far below the codes'
+ * spacing; a v that is not zero is never stored as zero.
  * The pages have no counterpart beyond the SGD step of the DDP notes' example. */
 #define DDP_ADAMW_BLOCK 256
 

@@ -236,11 +236,13 @@ __device__ __forceinline__ float peak(float a, float b) {
 }
 
 // The scale of a block from a lane's largest magnitude: magnitudes compare as
-// their bits, NaN above infinity.
+// their bits, NaN above infinity.  A normal number, so that its reciprocal is
+// one: blocks of less than 2^-126 times the format's top lie on the codes below it.
 __device__ __forceinline__ float block_scale(float mine, float over_top) {
-    const float s = __fmul_rn(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mine))), over_top);
+    const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(mine));
+    const float s = __fmul_rn(__uint_as_float(most), over_top);
     if (!(s < __int_as_float(0x7f800000))) return __int_as_float(0x7fffffff);
-    return s >= 0x1p-126f ? s : 0.0f;
+    return most ? fmaxf(s, 0x1p-126f) : 0.0f;
 }
 
 // 32 random bits of (seed, block, place): odd multipliers from the fractional

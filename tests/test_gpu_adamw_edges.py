@@ -86,3 +86,26 @@ def test_second_moments_near_the_largest_number(bits):
     opt.bind([w], [g], **opt.zero_state())
     opt.step(1, lr=0.5, eps=1e-30)
     assert bool(((w + 0.5).abs() <= 0.5 * 24 * U).all())
+
+@pytest.mark.parametrize("size", [1e-16, 1e-17, 1e-18])
+def test_eight_bit_moments_of_tiny_gradients(size):
+    """Blocks whose largest second moment over 57344 is no normal number keep their moments too.  m is within an eighth
+    of itself and v within a quarter, or half a spacing, of the unrounded ones; a step of equal gradients moves a weight
+    by lr to within the errors of both, and one without a gradient by less."""
+    n, steps = 600, 8
+    opt = AdamW([n], "f32", 8)
+    w, g = torch.zeros(n, device="cuda"), torch.full((n,), size, device="cuda")
+    state = opt.zero_state()
+    opt.bind([w], [g], **state)
+    for t in range(1, steps + 1):
+        opt.step(t, lr=0.5, eps=1e-30, seed=t)
+    assert bool((state["exp_avg_sq"][0].float() > 0).all())
+    m = state["exp_avg"][0].float() * state["exp_avg_scale"][0].repeat_interleave(256)[:n]
+    v = state["exp_avg_sq"][0].double() * state["exp_avg_sq_scale"][0].double().repeat_interleave(256)[:n]
+    assert float(m.mean()) == pytest.approx(size * (1 - 0.9 ** steps), rel=0.02)
+    assert float(v.mean()) == pytest.approx(size ** 2 * (1 - 0.999 ** steps), rel=0.05)
+    assert float((w / (-0.5 * steps)).mean()) == pytest.approx(1.0, rel=0.05)
+    before = w.clone()
+    g.zero_()
+    opt.step(steps + 1, lr=0.5, eps=1e-30, seed=steps + 1)
+    assert float((w - before).abs().max()) <= 0.5 * 1.5
