@@ -523,8 +523,8 @@ adamw_kernel(const __grid_constant__ StepParams a) {
                         const float2 vy = mul2(make_float2(v[h][q], v[h][q + 1]), both(vi));
                         e4m3_round(mul2(make_float2(m[h][q], m[h][q + 1]), both(mi)), r0, r1, x[q], x[q + 1]);
                         e5m2_round(vy, r0, r1, y[q], y[q + 1]);
-                        any[q] = __float_as_uint(vy.x);
-                        any[q + 1] = __float_as_uint(vy.y);
+                        any[q] = __float_as_uint(v[h][q]);            // vy can be zero beside a huge v
+                        any[q + 1] = __float_as_uint(v[h][q + 1]);
                     }
                     mc[h] = ms >= 0.0f ? e4m3_pack(x) : 0u;      // a block of NaN holds zeros and a NaN scale
                     vc[h] = vs >= 0.0f ? e5m2_pack(y, any) : 0u;

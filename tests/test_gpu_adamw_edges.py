@@ -109,3 +109,16 @@ def test_eight_bit_moments_of_tiny_gradients(size):
     g.zero_()
     opt.step(steps + 1, lr=0.5, eps=1e-30, seed=steps + 1)
     assert float((w - before).abs().max()) <= 0.5 * 1.5
+
+def test_a_second_moment_beside_a_huge_one_is_not_stored_as_zero():
+    """v of 1e-15 in a block whose largest is 2e35: their quotient by the scale is below fp32's least number."""
+    n = 256
+    opt = AdamW([n], "f32", 8)
+    w, g = torch.zeros(n, device="cuda"), torch.full((n,), 1e-6, device="cuda")
+    g[0] = 1.5e19
+    state = opt.zero_state()
+    opt.bind([w], [g], **state)
+    opt.step(1, seed=1)
+    scale = float(state["exp_avg_sq_scale"][0][0])
+    assert np.isfinite(scale) and np.float32(1e-15) / np.float32(scale) == 0
+    assert bool((state["exp_avg_sq"][0].float() > 0).all())
