@@ -12,29 +12,34 @@ import ctypes as C
 import struct
 
 from . import _lib
-from .reducer import _ERRORS, DTYPES, DDPError, _stream
+from .reducer import _ERRORS, DTYPES, DDPError, _device, _stream
 
 BLOCK = 256             # elements that share one scale of an 8-bit moment (DDP_ADAMW_BLOCK)
 
 
 def _addresses(name, tensors, numel, dtypes):
-    """Checked device addresses of a list of tensors (or addresses), as the C
-    ABI takes them; None for None."""
+    """Checked addresses, on the current device, of a list of tensors (or
+    addresses), as the C ABI takes them; None for None."""
     if tensors is None:
         return None
+    device = _device()
     if len(tensors) != len(numel):
         raise ValueError(f"{name}: expected {len(numel)} tensors")
     out = (C.c_void_p * max(len(numel), 1))()
     for v, (t, n) in enumerate(zip(tensors, numel)):
         if isinstance(t, int):
             out[v] = t or None
-        elif t is None or t.numel() != n or t.dtype not in dtypes or not t.is_contiguous() or not t.is_cuda:
+        elif t is None or t.numel() != n or t.dtype not in dtypes or not t.is_contiguous() or t.get_device() != device:
             if t is not None or n:
                 raise ValueError(f"{name}[{v}]: expected {n} contiguous elements of "
-                                 f"{' or '.join(str(d) for d in dtypes)} on a GPU")
+                                 f"{' or '.join(str(d) for d in dtypes)} on the current device cuda:{device}{_found(t)}")
         else:
             out[v] = t.data_ptr() or None
     return out
+
+
+def _found(t):
+    return "" if t is None else f"; found {t.numel()} of {t.dtype} on {t.device}"
 
 
 class AdamW:
@@ -91,7 +96,8 @@ class AdamW:
     # ---------------------------------------------------------------- bind
     def bind(self, params, grads, exp_avg, exp_avg_sq, weight_decay=0.0, master=None, exp_avg_scale=None,
              exp_avg_sq_scale=None):
-        """Lists of P tensors (or device addresses).  grads: fp32; params:
+        """Lists of P tensors on the current device (or device addresses), on
+        which later calls run too.  grads: fp32; params:
         param_dtype; master: fp32, with bf16 parameters; exp_avg, exp_avg_sq:
         fp32, or with 8 bits float8_e4m3fn and float8_e5m2 (or uint8) codes
         with fp32 scales of ceil(numel / 256) elements; weight_decay: a number
@@ -125,16 +131,18 @@ class AdamW:
     def _used(self, used):
         if used is None or isinstance(used, int):
             return used or 0
-        if used.numel() != self.P or used.element_size() != 1 or not used.is_contiguous() or not used.is_cuda:
-            raise ValueError(f"used: expected {self.P} contiguous bytes or truth values on a GPU")
+        if used.numel() != self.P or used.element_size() != 1 or not used.is_contiguous() or used.get_device() != _device():
+            raise ValueError(f"used: expected {self.P} contiguous bytes or truth values on the current device "
+                             f"cuda:{_device()}{_found(used)}")
         return used.data_ptr()
 
     def _norm(self, norm):
         if norm is None or isinstance(norm, int):
             return norm or 0
         # a 0-d or one-element fp32 tensor; its dtype is asked for by name once
-        if norm.numel() != 1 or not norm.is_cuda or (norm.dtype is not self._f32 and str(norm.dtype) != "torch.float32"):
-            raise ValueError("norm: expected one fp32 element on a GPU")
+        if norm.numel() != 1 or norm.get_device() != _device() or (
+                norm.dtype is not self._f32 and str(norm.dtype) != "torch.float32"):
+            raise ValueError(f"norm: expected one fp32 element on the current device cuda:{_device()}{_found(norm)}")
         self._f32 = norm.dtype
         return norm.data_ptr()
 

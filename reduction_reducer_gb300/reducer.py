@@ -52,34 +52,44 @@ def _ptr(x) -> int:
 
 
 _current = None   # resolved on first use: () -> handle of the current stream
+_current_device = None   # and () -> index of the current device
 
 
 def _resolve_current():
-    """torch's current stream on the current device as a handle; 0 without a
-    GPU.  torch.cuda.current_stream() makes a Stream object around the same
-    handle (3 to 5 us a call, more than a launch takes), so the handle is asked
-    for directly where torch offers it."""
+    """torch's current stream on the current device as a handle, and that
+    device's index; 0 and 0 without a GPU.  torch.cuda.current_stream() makes a
+    Stream object around the same handle (3 to 5 us a call, more than a launch
+    takes), so the handle is asked for directly where torch offers it."""
+    global _current, _current_device
     import torch
     if not torch.cuda.is_available():
-        return lambda: 0
+        _current = _current_device = lambda: 0
+        return
     torch.cuda.current_stream()                       # CUDA initialised
     raw, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
     if raw is None or device is None:
-        return lambda: int(torch.cuda.current_stream().cuda_stream)
-    return lambda: raw(device())
+        _current, _current_device = lambda: int(torch.cuda.current_stream().cuda_stream), torch.cuda.current_device
+    else:
+        _current, _current_device = lambda: raw(device()), device
 
 
 def _stream(stream) -> int:
     """cudaStream_t of a torch stream, an int handle, or (None) torch's
     current stream; 0 without a GPU (dry runs)."""
-    global _current
     if stream is None:
         if _current is None:
-            _current = _resolve_current()
+            _resolve_current()
         return _current()
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
+
+
+def _device() -> int:
+    """Index of the current device, on which every call runs."""
+    if _current_device is None:
+        _resolve_current()
+    return _current_device()
 
 
 def _ptr_array(ptrs):

@@ -7,7 +7,7 @@ from __future__ import annotations
 import struct
 
 from . import _lib
-from .reducer import DDPError, _ERRORS, _stream
+from .reducer import DDPError, _ERRORS, _device, _stream
 
 torch = None       # imported by the first call, not by the package; the dtypes below then too
 _DTYPES = _INT = _FLOAT = _MASK = None
@@ -24,12 +24,12 @@ def _torch():
 
 
 def _args(logits, k, score, groups, top_groups, renorm, scale):
-    """(packed ddp_route_args, tokens, experts) of a call."""
+    """(packed ddp_route_args, tokens, experts, the current device) of a call."""
     if torch is None:
         _torch()
-    dtype = _DTYPES.get(logits.dtype)
-    if dtype is None or logits.dim() != 2 or not logits.is_cuda:
-        raise ValueError("logits: expected [tokens, experts] fp32 or bf16 on a GPU")
+    dtype, device = _DTYPES.get(logits.dtype), _device()
+    if dtype is None or logits.dim() != 2 or logits.get_device() != device:
+        raise ValueError(f"logits: expected [tokens, experts] fp32 or bf16 on {_found(device, logits)}")
     tokens, experts = logits.shape
     stride = _row_stride("logits", logits, tokens, experts)
     try:
@@ -37,7 +37,7 @@ def _args(logits, k, score, groups, top_groups, renorm, scale):
                             groups if top_groups is None else top_groups, 1 if renorm else 0, scale, dtype)
     except (struct.error, OverflowError) as e:
         raise ValueError(f"k, groups, top_groups or scale: {e}") from None
-    return a, tokens, experts
+    return a, tokens, experts, device
 
 
 def _row_stride(name, t, tokens, experts):
@@ -47,11 +47,15 @@ def _row_stride(name, t, tokens, experts):
     return row if tokens > 1 else max(row, experts)
 
 
-def _data(name, t, shape, dtypes):
+def _found(device, t):
+    return f"the current device cuda:{device}; found {list(t.shape)} of {t.dtype} on {t.device}"
+
+
+def _data(name, t, shape, dtypes, device):
     if t is None:
         return None
-    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name}: expected {list(shape)} contiguous {' or '.join(map(str, dtypes))} on a GPU")
+    if t.dtype not in dtypes or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name}: expected {list(shape)} contiguous {' or '.join(map(str, dtypes))} on {_found(device, t)}")
     return t.data_ptr()
 
 
@@ -89,15 +93,15 @@ def route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, to
     their sum; mask: bytes or truth values [tokens], 0 = not routed (index
     -1, weight 0); counts: int32 [experts], the tokens each expert got are
     added to it; out: (indices, weights) to write into (without it they are
-    allocated on `stream`)."""
-    a, tokens, experts = _args(logits, k, score, groups, top_groups, renorm, scale)
+    allocated on `stream`).  All tensors lie on the current device."""
+    a, tokens, experts, device = _args(logits, k, score, groups, top_groups, renorm, scale)
     shape, each = (tokens, k), (experts,)
     indices, weights = out if out is not None else (
         _empty(shape, torch.int32, logits, stream), _empty(shape, torch.float32, logits, stream))
     st = _lib.load(lib_path).ddp_route(
-        a, logits.data_ptr(), _data("bias", bias, each, _FLOAT), _data("mask", mask, (tokens,), _MASK),
-        _data("indices", indices, shape, _INT), _data("weights", weights, shape, _FLOAT),
-        _data("counts", counts, each, _INT), _stream(stream))
+        a, logits.data_ptr(), _data("bias", bias, each, _FLOAT, device), _data("mask", mask, (tokens,), _MASK, device),
+        _data("indices", indices, shape, _INT, device), _data("weights", weights, shape, _FLOAT, device),
+        _data("counts", counts, each, _INT, device), _stream(stream))
     if st:
         _refused(st, "ddp_route", tokens, experts, k, groups=groups, top_groups=top_groups, scale=scale)
     return indices, weights
@@ -109,14 +113,14 @@ def route_backward(grad_weights, logits, indices, weights, score: str = "softmax
     the weights, with the indices and weights that ``route`` returned for the
     same score, renorm and scale."""
     k = indices.shape[1] if indices.dim() == 2 else 0
-    a, tokens, experts = _args(logits, k, score, 1, 1, renorm, scale)
+    a, tokens, experts, device = _args(logits, k, score, 1, 1, renorm, scale)
     shape = (tokens, k)
     grad = out if out is not None else _empty((tokens, experts), logits.dtype, logits, stream)
-    if grad.shape != logits.shape or grad.dtype is not logits.dtype or not grad.is_cuda:
-        raise ValueError("out: expected the logits' shape and dtype on a GPU")
+    if grad.shape != logits.shape or grad.dtype is not logits.dtype or grad.get_device() != device:
+        raise ValueError(f"out: expected the logits' shape and dtype on {_found(device, grad)}")
     st = _lib.load(lib_path).ddp_route_backward(
-        a, logits.data_ptr(), _data("indices", indices, shape, _INT), _data("weights", weights, shape, _FLOAT),
-        _data("grad_weights", grad_weights, shape, _FLOAT), grad.data_ptr(), _row_stride("out", grad, tokens, experts),
+        a, logits.data_ptr(), _data("indices", indices, shape, _INT, device), _data("weights", weights, shape, _FLOAT, device),
+        _data("grad_weights", grad_weights, shape, _FLOAT, device), grad.data_ptr(), _row_stride("out", grad, tokens, experts),
         _stream(stream))
     if st:
         _refused(st, "ddp_route_backward", tokens, experts, k, scale=scale)
