@@ -927,6 +927,7 @@ int ddp_adamw_step(ddp_adamw* o, const ddp_adamw_args* x, void* stream) {
         return o->fail(DDP_ERR_INVALID_ARG, "max_norm is negative or not finite");
     if ((x->max_norm > 0.0 || x->skip_nonfinite) && !x->norm)
         return o->fail(DDP_ERR_INVALID_ARG, "max_norm and skip_nonfinite need a norm");
+    if (!aligned(x->norm, 4)) return o->fail(DDP_ERR_INVALID_ARG, "norm is not aligned to its element");
     if (!o->bound || !o->has_params) return o->fail(DDP_ERR_NOT_BOUND, "no parameters are bound");
     if (const int st = check_device(o)) return st;
     if (o->step.count == 0) return DDP_OK;
@@ -965,7 +966,7 @@ int ddp_adamw_step(ddp_adamw* o, const ddp_adamw_args* x, void* stream) {
 
 int ddp_adamw_grad_norm(ddp_adamw* o, const uint8_t* used, float* norm, void* stream) {
     if (!o) return DDP_ERR_INVALID_ARG;
-    if (!norm) return o->fail(DDP_ERR_INVALID_ARG, "norm is NULL");
+    if (!norm || !aligned(norm, 4)) return o->fail(DDP_ERR_INVALID_ARG, "norm is NULL or not aligned to its element");
     if (!o->bound) return o->fail(DDP_ERR_NOT_BOUND, "no gradients are bound");
     if (const int st = check_device(o)) return st;
     NormParams a = {};

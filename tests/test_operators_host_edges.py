@@ -117,3 +117,14 @@ def test_tensors_on_the_host_are_refused():
                  lambda: AdamW([5]).bind_grads([torch.zeros(5)]), lambda: AdamW([5]).grad_norm(torch.zeros(1), stream=0)):
         with pytest.raises(ValueError, match="cpu"):
             call()
+
+
+def test_a_misaligned_norm_is_refused():
+    opt = AdamW([5])
+    for address in (2, 4097, 4098):
+        with pytest.raises(InvalidArg, match="aligned"):
+            opt.grad_norm(address, stream=0)
+        with pytest.raises(InvalidArg, match="aligned"):
+            opt.step(1, norm=address, max_norm=1.0, stream=0)
+    with pytest.raises(NotBound):
+        opt.step(1, norm=4100, max_norm=1.0, stream=0)
