@@ -443,13 +443,18 @@ typedef struct ddp_adamw_args {
 } ddp_adamw_args;
 
 /* One step over the bound tensors, one launch, asynchronous on `stream`.
+ * t, lr, the corrections by t and the seed are arguments of the launch: a CUDA
+ * graph that captured a step replays that very step number, rate and rounding
+ * (only *norm, used and the tensors are read anew), so each step of a training
+ * run is launched, or captured, by itself.
  * Errors: INVALID_ARG, NOT_BOUND, CUDA. */
 int ddp_adamw_step(ddp_adamw* opt, const ddp_adamw_args* args, void* stream);
 
 /* *norm = sqrt of the sum of squares over the bound gradients (of the tensors
  * with used[v] != 0; device array [P] or NULL = all), one launch,
- * asynchronous on `stream`.  Squares are fp32 (gradients past 1.8e19 give an
- * infinite norm), long sums have twice fp32's digits; the order is fixed, so equal inputs
+ * asynchronous on `stream`.  Squares are fp32 (a sum past 3.4e38, as of one
+ * gradient of 1.8e19, gives an infinite norm; gradients below 2.6e-23 count as
+ * zeros), long sums have twice fp32's digits; the order is fixed, so equal inputs
  * give equal bits.  Calls of one `opt` share its partial sums: they run in
  * one stream's order.  Errors: INVALID_ARG, NOT_BOUND, CUDA. */
 int ddp_adamw_grad_norm(ddp_adamw* opt, const uint8_t* used, float* norm, void* stream);
@@ -465,7 +470,8 @@ void ddp_adamw_destroy(ddp_adamw* opt);
 /* Tokens to experts.  What a router chose decides which experts' parameters
  * get a gradient on a replica (ddp_set_local_used), and its counts say so.
  * For every token, over its E logits x:
- *   s_i = softmax(x)_i, or sigmoid(x_i)                              (fp32)
+ *   s_i = softmax(x)_i, or sigmoid(x_i)    (fp32; a softmax's sum has one order,
+ *         whatever the batch)
  *   c_i = s_i + bias_i, what the choice goes by (without a bias and groups,
  *         x_i itself, whose order is that of s)
  *   groups > 1: the E experts are `groups` equal runs; a run is worth the sum

@@ -158,7 +158,9 @@ class AdamW:
         max_norm > 0; used: device bytes [P], tensors with 0 stay as they are;
         seed: of the 8-bit moments' rounding, another one each step (None: t; one
         and the same would hold every element at a threshold of its own for ever);
-        skip_nonfinite: a norm that is not finite leaves everything as it is."""
+        skip_nonfinite: a norm that is not finite leaves everything as it is.
+        t, lr and the seed travel with the launch: a CUDA graph replays the very
+        step that it captured."""
         norm, used = self._norm(norm), self._used(used)
         try:
             args = _lib.pack_adamw(t, lr, betas[0], betas[1], eps, max_norm, norm, used,
