@@ -122,3 +122,54 @@ def test_a_second_moment_beside_a_huge_one_is_not_stored_as_zero():
     scale = float(state["exp_avg_sq_scale"][0][0])
     assert np.isfinite(scale) and np.float32(1e-15) / np.float32(scale) == 0
     assert bool((state["exp_avg_sq"][0].float() > 0).all())
+
+def test_steps_on_another_stream_follow_each_bind():
+    """Each bind's table is the one that calls on a stream of their own then read: gradients and weights alternate, so a
+    table of the bind before would show in the norm and in the weights."""
+    sizes = [1 + v % 5 for v in range(900)]
+    total = sum(sizes)
+    opt = AdamW(sizes)
+    state = opt.zero_state()
+    side = torch.cuda.Stream()
+    norm = torch.zeros(1, device="cuda")
+    sets = []
+    for x in (2.0, -3.0):
+        sets.append((x, [torch.full((n,), x, device="cuda") for n in sizes], [torch.zeros(n, device="cuda") for n in sizes]))
+    torch.cuda.synchronize()
+    for i in range(12):
+        x, g, w = sets[i % 2]
+        for views in state.values():
+            for s in views:
+                s.zero_()
+        for t in w:
+            t.zero_()
+        norm.zero_()
+        torch.cuda.synchronize()
+        opt.bind(w, g, **state)
+        opt.grad_norm(norm, stream=side)
+        opt.step(1, lr=0.25, stream=side)
+        side.synchronize()
+        assert float(norm) == pytest.approx(abs(x) * total ** 0.5, rel=1e-6)
+        assert torch.allclose(torch.cat(w), torch.full((total,), -0.25 if x > 0 else 0.25, device="cuda"), rtol=24 * U, atol=0)
+        other = torch.cat(sets[1 - i % 2][2])
+        assert i == 0 or bool((other.abs() > 0).all())               # the set before stays as its own step left it
+        torch.cuda.synchronize()
+
+
+def test_one_optimizer_bound_again_and_again():
+    """Norms before and after binds of one optimizer to other tensors, with and without parameters; of grids that change
+    with the tensors that are left out."""
+    sizes = [700_000, 5, 1_500_000]
+    total = sum(sizes)
+    opt = AdamW(sizes)
+    norm = torch.zeros(1, device="cuda")
+    used = torch.tensor([1, 1, 0], dtype=torch.uint8, device="cuda")
+    for x in (0.5, 2.0, 0.25, 3.0):
+        g = [torch.full((n,), x, device="cuda") for n in sizes]
+        if x > 1:
+            opt.bind_grads(g)
+        else:
+            opt.bind([torch.zeros_like(t) for t in g], g, **opt.zero_state())
+        for _ in range(3):
+            assert float(opt.grad_norm(norm)) == pytest.approx(x * total ** 0.5, rel=1e-6)
+            assert float(opt.grad_norm(norm, used=used)) == pytest.approx(x * 700_005 ** 0.5, rel=1e-6)

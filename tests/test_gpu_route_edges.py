@@ -147,3 +147,55 @@ def test_a_token_routes_alike_in_every_batch(E, groups, top, k, dtype):
     index, w = route(x, k, bias=close, groups=groups, top_groups=top)
     exact_index, exact_w = route(x, k, bias=far, groups=groups, top_groups=top)
     assert torch.equal(exact_index, index) and torch.equal(exact_w, w)
+
+SHAPES = [(1, 1, 1), (5, 8, 2), (33, 32, 8), (7, 33, 4), (300, 60, 4), (40, 64, 6), (65, 128, 8), (20, 200, 12),
+          (257, 256, 8), (19, 300, 32), (9, 512, 10), (1201, 16, 3)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k", SHAPES)
+def test_gradient_into_contiguous_rows(T, E, k, score, renorm, dtype):
+    """Contiguous outputs leave in 16-byte stores where their rows allow it.  Bounds as for strided ones: weights 64u,
+    g w summed over k, a score times their sum; rows past the tokens stay as they were."""
+    x = (torch.randn(T, E, generator=generator(T), device="cuda") * 1.5).to(KINDS[dtype])
+    how = dict(score=score, renorm=renorm, scale=2.5)
+    index, w = route(x, k, **how)
+    g = torch.randn(T, k, generator=generator(1), device="cuda")
+    more = torch.full((T + 2, E), 7.0, dtype=x.dtype, device="cuda")
+    d = route_backward(g, x, index, w, out=more[:T], **how)
+    assert bool((more[T:] == 7.0).all())
+    assert torch.equal(route_backward(g, x, index, w, **how), d)
+    wide = torch.full((T, E + 3), 7.0, dtype=x.dtype, device="cuda")
+    assert torch.equal(route_backward(g, x, index, w, out=wide[:, :E], **how), d)      # the other path: the same numbers
+    got, rows = d.double().cpu().numpy(), x.double().cpu().numpy()
+    for t in [*range(min(T, 30)), T - 1]:
+        want = R.backward_token(rows[t], index[t].tolist(), g[t].cpu().numpy(), score, renorm, 2.5)
+        size = np.abs(g[t].cpu().numpy() * w[t].cpu().numpy()).sum()
+        bound = 160 * U * size + (2.0 ** -8 * np.abs(want) if dtype == "bf16" else 0)
+        assert np.all(np.abs(got[t] - want) <= bound), t
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("E", [16, 64, 256])
+@pytest.mark.parametrize("shift", [1, 2, 3, 5])
+def test_logits_that_start_anywhere(E, dtype, shift):
+    """Logits, and their gradient, from an address that is no multiple of 16 bytes: what aligned ones give."""
+    T, k = 70, 5
+    x = (torch.randn(T, E, generator=generator(E), device="cuda") * 1.5).to(KINDS[dtype])
+    flat = torch.empty(T * E + 8, dtype=x.dtype, device="cuda")
+    odd = flat[shift:shift + T * E].view(T, E)
+    odd.copy_(x)
+    g = torch.randn(T, k, generator=generator(2), device="cuda")
+    out = torch.full((T * E + 8,), 7.0, dtype=x.dtype, device="cuda")
+    for score in ("softmax", "sigmoid"):
+        for renorm in (False, True):
+            how = dict(score=score, renorm=renorm)
+            index, w = route(x, k, **how)
+            odd_index, odd_w = route(odd, k, **how)
+            assert torch.equal(index, odd_index) and torch.equal(w, odd_w)
+            d = route_backward(g, x, index, w, **how)
+            got = route_backward(g, odd, index, w, out=out[shift:shift + T * E].view(T, E), **how)
+            assert torch.equal(got, d)
+            assert bool((out[:shift] == 7.0).all()) and bool((out[shift + T * E:] == 7.0).all())
