@@ -319,13 +319,13 @@ struct __align__(16) Stage {
 // Bound by HBM: an element moves 28 bytes with 32-bit moments (weight and both
 // moments read and written, gradient read), 30 with bf16 weights beside their
 // master copies, 16 and 18 with 8-bit ones.  GB300, copy peak 6,780 GB/s:
-// BERT-large (335 M elements) 1,339 us, 7,010 GB/s; GPT-2-medium with bf16
-// weights 1,528 us, 6,970 GB/s, and with 8-bit moments 959 us, 6,680 GB/s;
+// BERT-large (335 M elements) 1,342 us, 6,990 GB/s; GPT-2-medium with bf16
+// weights 1,528 us, 6,970 GB/s, and with 8-bit moments 962 us, 6,660 GB/s;
 // ResNet-50 103 us, 6,930 GB/s.
 //
-// 32-bit moments: eight 128-bit loads a lane in flight on 24 warps an SM carry
-// it; single blocks to a warp, its neighbours on the next ones.  8-bit moments
-// take about 75 instructions an element, so a warp's loads must run while it
+// 32-bit moments: eight 128-bit loads a lane in flight on 24 or 28 warps an SM
+// carry it; single blocks to a warp, its neighbours on the next ones.  8-bit moments
+// take about 77 instructions an element, so a warp's loads must run while it
 // computes: its next whole block is copied to shared memory meanwhile (without
 // the copy, and with a scale a block read and written by itself, GPT-2-medium
 // took 1,217 us; the scales as whole sectors were most of the difference).
@@ -738,7 +738,7 @@ namespace {
 // partial sums (BERT-large, 2 / 3 / 4: 201 / 192 / 216 us).
 constexpr int kNormCtasPerSm = 3;
 constexpr int kStepCtasPerSm[2] = {256, 128};    // 32-bit and 8-bit moments
-constexpr int kStep8WarpsPerSm = 28;             // resident: seven CTAs of 68 or 72 registers
+constexpr int kStep8WarpsPerSm = 28;             // resident: seven CTAs of 69 registers
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 

@@ -27,9 +27,10 @@
 // reads 1 KiB a token and executes about 390 warp instructions (scores, keys
 // and sorting of 256 values; k rounds; the k slots' exact scores), half of them
 // on the integer and compare pipe, which takes one every other cycle.  GB300,
-// 65,536 tokens: 256 experts in 8 groups with a bias 33.7 us (2.1 TB/s; the
-// logits alone at the copy peak 10 us), ungrouped softmax over 64 / 128 / 256
-// experts in bf16 10.3 / 17.2 / 27.4 us.  A few tokens take 3.3 us.
+// 65,536 tokens, logits in HBM: 256 experts in 8 groups with a bias 32.8 us (2.1
+// TB/s; the logits alone at the copy peak 10 us), ungrouped softmax over 64 / 128
+// / 256 experts in bf16 13.2 / 18.3 / 27.9 us renormalised, and 16.6 / 24.6 / 40.0
+// as it is, for the sum over the row.  A few tokens take 3.3 us.
 
 #include "ddp_reducer.h"
 
@@ -680,9 +681,9 @@ route_kernel(const __grid_constant__ RouteParams a) {
 // sigmoid:  dx = part_r (1 - s_r) at the chosen, 0 elsewhere
 // softmax:  dx = [chosen] part_r - s_i D; renormalised D is zero, and only the
 //           chosen get a gradient
-// GB300, 65,536 tokens over 256 experts, buffers in HBM: sigmoid in bf16 13.5 us,
-// where 34 MB of gradient are written, 6 read, and up to 17 more as a sector for
-// each slot's logit; softmax renormalised, which needs none, 8.3 us.  (Scores
+// GB300, 65,536 tokens over 256 experts, buffers in HBM: sigmoid in bf16 13.4 us,
+// where 34 MB of gradient are written, 6 of slots read, and 26 as a sector or two
+// for each slot's logit; softmax renormalised, which needs none, 7.6 us.  (Scores
 // taken from the weights' ratios and one logit a token gave 11.3 us and gradients
 // of confident experts that were off by percents at logits of 10 and could have
 // the wrong sign at 15.)  Softmax not
