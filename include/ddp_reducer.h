@@ -518,6 +518,136 @@ int ddp_route(const ddp_route_args* args, const void* logits, const float* bias,
 int ddp_route_backward(const ddp_route_args* args, const void* logits, const int32_t* indices, const float* weights,
                        const float* grad_weights, void* grad_logits, int64_t grad_stride, void* stream);
 
+/* ---------------------------------------------------------------- between the matrix products */
+
+/* What a language model does with its tokens between the matrix products, in
+ * the forward pass and back: the embedding, layer norm, dropout on a residual
+ * branch, and the log probabilities that a loss is made of.  The gradients of
+ * the embedding's table and of a norm's weight and bias are sums over all
+ * tokens, in an order that depends on the sizes alone (equal inputs give equal
+ * bits), and are written, or with accumulate added, straight into the gradient
+ * fields that ddp_bind and ddp_adamw_bind take.
+ * Rows are elements next to one another; strides count elements between two
+ * rows.  Any element alignment is correct; rows that start on 16 bytes and
+ * whose length is a multiple of eight are read and written in vectors.
+ * Arithmetic is fp32; bf16 results are rounded once, to nearest even.
+ * Every call is asynchronous on `stream`, runs on the current device and keeps
+ * nothing; a workspace is the caller's, device memory aligned to 16 bytes, one
+ * for each call that may run at the same time, and of no value afterwards.
+ * Outputs overlap no inputs but where it is said. */
+
+typedef struct ddp_embed_args {
+    int64_t tokens;          /* >= 0, < 2^31 */
+    int64_t vocab;           /* rows of the table, >= 1, < 2^31 - 1 */
+    int64_t dim;             /* elements of a row, 1 .. 2^24 */
+    int64_t table_stride;    /* of the table, or of its gradient, >= dim */
+    int64_t row_stride;      /* of the tokens' rows, or of their gradient, >= dim */
+    float scale;             /* finite */
+    ddp_dtype table_dtype;   /* of the table, or of its gradient */
+    ddp_dtype dtype;         /* of the tokens' rows, or of their gradient */
+    int32_t index_bits;      /* of a token: 32 or 64 (signed) */
+} ddp_embed_args;
+
+/* out[i] = scale * table[tokens[i]], a row of zeros for a token outside
+ * [0, vocab) (as padding is).  Errors: INVALID_ARG, CUDA. */
+int ddp_embed(const ddp_embed_args* args, const void* table, const void* tokens, void* out, void* stream);
+
+/* Bytes of the workspace of ddp_embed_backward (>= 0), or INVALID_ARG. */
+int64_t ddp_embed_workspace(const ddp_embed_args* args);
+
+/* grad_table[v] = scale * sum of grad[i] over the tokens i that are v, in fp32
+ * and in ascending order (rows of more than 64 tokens in parts, and these in
+ * order); rows without a token get zeros.  With accumulate (fp32 tables only)
+ * the sums are added to grad_table, and rows without a token stay as they are.
+ * Errors: INVALID_ARG, CUDA. */
+int ddp_embed_backward(const ddp_embed_args* args, const void* grad, const void* tokens, void* grad_table,
+                       int32_t accumulate, void* workspace, void* stream);
+
+typedef struct ddp_layer_norm_args {
+    int64_t rows;            /* >= 0 */
+    int64_t dim;             /* elements of a row, 1 .. 2^24 */
+    int64_t x_stride;        /* >= dim */
+    int64_t out_stride;      /* of y, or of the gradient of x, >= dim */
+    float eps;               /* finite, >= 0 */
+    ddp_dtype dtype;         /* of x, y and their gradients */
+    ddp_dtype param_dtype;   /* of weight, bias and their gradients */
+} ddp_layer_norm_args;
+
+/* y = (x - mean) / sqrt(variance + eps) * weight + bias over each row, the
+ * variance about the mean, over dim (not dim - 1); weight and bias [dim] or
+ * NULL.  stats (fp32 [rows * 2]) gets each row's mean and 1 / sqrt(variance +
+ * eps).  Squares are fp32.  Errors: INVALID_ARG, CUDA. */
+int ddp_layer_norm(const ddp_layer_norm_args* args, const void* x, const void* weight, const void* bias, void* y,
+                   float* stats, void* stream);
+
+/* Bytes of the workspace of ddp_layer_norm_backward (>= 0), or INVALID_ARG. */
+int64_t ddp_layer_norm_workspace(const ddp_layer_norm_args* args);
+
+/* From grad_y (rows grad_stride apart) and the stats that ddp_layer_norm wrote:
+ * grad_x, and over all rows grad_weight and grad_bias [dim].  Each of the three
+ * may be NULL, not all.  With accumulate (fp32 parameters only) the latter two
+ * are added to.  workspace may be NULL where both of them are.
+ * Errors: INVALID_ARG, CUDA. */
+int ddp_layer_norm_backward(const ddp_layer_norm_args* args, const void* grad_y, int64_t grad_stride, const void* x,
+                            const float* stats, const void* weight, void* grad_x, void* grad_weight, void* grad_bias,
+                            int32_t accumulate, void* workspace, void* stream);
+
+typedef struct ddp_drop_args {
+    int64_t rows, cols;      /* >= 0 */
+    int64_t x_stride, residual_stride, out_stride;   /* >= cols */
+    double p;                /* 0 .. 1, counted in steps of 2^-32 */
+    uint64_t seed;
+    uint64_t offset;         /* < 2^63: tells the calls of one seed apart */
+    const uint64_t* device_seed;   /* device memory that the kernel takes the seed from, or NULL: a captured
+                                    * call draws anew at each replay only with this one */
+    ddp_dtype dtype;
+} ddp_drop_args;
+
+/* out = x / (1 - p) where an element stays and 0 where it is dropped (whatever
+ * it was), plus residual where that is given.  Element e (in the order of rows
+ * and columns, whatever the strides) is dropped where its 32 bits lie below
+ * p 2^32: halves of the words of Philox4x32-10 with the key `seed` and the
+ * counter (e / 8 as 64 bits, offset): word (e % 8) / 2 of it has in its low or,
+ * for odd e, high half the upper 16 bits, and with bit 63 of the offset set the
+ * lower 16.  The gradient of x is the same call on the gradient of out, without
+ * a residual.  out may be x or residual.  Errors: INVALID_ARG, CUDA. */
+int ddp_drop(const ddp_drop_args* args, const void* x, const void* residual, void* out, void* stream);
+
+typedef struct ddp_logprobs_args {
+    int64_t rows;            /* >= 0 */
+    int64_t vocab;           /* logits of a row, 1 .. 2^24 */
+    int64_t row_stride;      /* of the logits, >= vocab */
+    int32_t top;             /* alternatives, 0 .. 32, <= vocab */
+    int32_t index_bits;      /* of a target: 32 or 64 (signed) */
+    float scale;             /* finite, > 0: of the logits (1 / temperature) */
+    ddp_dtype dtype;         /* of the logits and of their gradient */
+} ddp_logprobs_args;
+
+/* For every row, z = scale * logits and m its largest:
+ *   stats      fp32 [rows * 2]: m, and log S of S = sum of e^(z - m)
+ *   logp       fp32 [rows]: z_target - m - log S
+ *   entropy    fp32 [rows] or NULL: log S - (sum of e^(z - m) (z - m)) / S
+ *   top_index, top_logp  int32 and fp32 [rows * top]: the largest logits, in
+ *              descending order, ties by the lowest index
+ * targets: [rows], or NULL (then logp is too).  A row whose target lies outside
+ * [0, vocab) is left out: its logits may be anything, and its results are zeros
+ * with indices -1.  Logits of -inf are probabilities of zero, and no
+ * alternatives: where these run out, index -1 and log probability -inf.  Of a
+ * row of nothing but -inf logp is -inf, the entropy 0 and the gradient 0; of one
+ * with a NaN or +inf they are NaN.  Errors: INVALID_ARG, CUDA. */
+int ddp_logprobs(const ddp_logprobs_args* args, const void* logits, const void* targets, float* logp, float* entropy,
+                 float* stats, int32_t* top_index, float* top_logp, void* stream);
+
+/* The logits' gradient from grad_logp and grad_entropy (fp32 [rows], either may
+ * be NULL, not both; the latter with the entropy as ddp_logprobs wrote it):
+ *   scale * (grad_logp ([i = target] - p_i) - grad_entropy p_i (log p_i + entropy))
+ * into rows grad_stride apart, every element written, zeros in rows left out.
+ * grad_logits may be logits itself.  Of args, top plays no part.
+ * Errors: INVALID_ARG, CUDA. */
+int ddp_logprobs_backward(const ddp_logprobs_args* args, const void* logits, const void* targets, const float* stats,
+                          const float* entropy, const float* grad_logp, const float* grad_entropy, void* grad_logits,
+                          int64_t grad_stride, void* stream);
+
 /* ---------------------------------------------------------------- options, info */
 
 enum ddp_option {

@@ -10,3 +10,7 @@ from .reducer import (AlreadyReady, CudaError, DDPError, HookError, InvalidArg, 
 from ._lib import LIB_PATH, load  # noqa: F401
 from .optim import AdamW  # noqa: F401
 from .routing import route, route_backward, routed  # noqa: F401
+from .embedding import embed, embed_backward, embedded  # noqa: F401
+from .layernorm import layer_norm, layer_norm_backward, layer_normed  # noqa: F401
+from .dropout import drop, dropped  # noqa: F401
+from .logprobs import LogProbs, logprobs, logprobs_backward, scored  # noqa: F401

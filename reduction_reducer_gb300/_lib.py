@@ -61,12 +61,42 @@ class RouteArgs(C.Structure):
                 ("scale", C.c_float), ("dtype", C.c_int32)]
 
 
+class EmbedArgs(C.Structure):
+    """struct ddp_embed_args."""
+    _fields_ = [("tokens", C.c_int64), ("vocab", C.c_int64), ("dim", C.c_int64), ("table_stride", C.c_int64),
+                ("row_stride", C.c_int64), ("scale", C.c_float), ("table_dtype", C.c_int32), ("dtype", C.c_int32),
+                ("index_bits", C.c_int32)]
+
+
+class LayerNormArgs(C.Structure):
+    """struct ddp_layer_norm_args."""
+    _fields_ = [("rows", C.c_int64), ("dim", C.c_int64), ("x_stride", C.c_int64), ("out_stride", C.c_int64),
+                ("eps", C.c_float), ("dtype", C.c_int32), ("param_dtype", C.c_int32)]
+
+
+class DropArgs(C.Structure):
+    """struct ddp_drop_args."""
+    _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("x_stride", C.c_int64), ("residual_stride", C.c_int64),
+                ("out_stride", C.c_int64), ("p", C.c_double), ("seed", C.c_uint64), ("offset", C.c_uint64),
+                ("device_seed", C.c_void_p), ("dtype", C.c_int32)]
+
+
+class LogprobsArgs(C.Structure):
+    """struct ddp_logprobs_args."""
+    _fields_ = [("rows", C.c_int64), ("vocab", C.c_int64), ("row_stride", C.c_int64), ("top", C.c_int32),
+                ("index_bits", C.c_int32), ("scale", C.c_float), ("dtype", C.c_int32)]
+
+
 # int (*ddp_comm_hook_fn)(void* state, const ddp_grad_bucket* bucket, void* stream)
 HOOKFN = C.CFUNCTYPE(C.c_int, C.c_void_p, C.POINTER(GradBucket), C.c_void_p)
 
 # The same structs packed into bytes, which costs a call half a microsecond less than filling one in.
 pack_adamw = struct.Struct("@q5dPPQi4x").pack
 pack_route = struct.Struct("@2q6ifi").pack
+pack_embed = struct.Struct("@5qf3i").pack
+pack_layer_norm = struct.Struct("@4qf2i4x").pack
+pack_drop = struct.Struct("@5qd2QPi4x").pack
+pack_logprobs = struct.Struct("@3q2ifi").pack
 
 # name -> (restype, argtypes); every symbol of include/ddp_reducer.h
 SIGNATURES = {
@@ -111,6 +141,15 @@ SIGNATURES = {
     "ddp_adamw_destroy": (None, [C.c_void_p]),
     "ddp_route": (C.c_int, [C.c_void_p] * 8),
     "ddp_route_backward": (C.c_int, [C.c_void_p] * 6 + [C.c_int64, C.c_void_p]),
+    "ddp_embed": (C.c_int, [C.c_void_p] * 5),
+    "ddp_embed_workspace": (C.c_int64, [C.c_void_p]),
+    "ddp_embed_backward": (C.c_int, [C.c_void_p] * 4 + [C.c_int32] + [C.c_void_p] * 2),
+    "ddp_layer_norm": (C.c_int, [C.c_void_p] * 7),
+    "ddp_layer_norm_workspace": (C.c_int64, [C.c_void_p]),
+    "ddp_layer_norm_backward": (C.c_int, [C.c_void_p] * 2 + [C.c_int64] + [C.c_void_p] * 6 + [C.c_int32] + [C.c_void_p] * 2),
+    "ddp_drop": (C.c_int, [C.c_void_p] * 5),
+    "ddp_logprobs": (C.c_int, [C.c_void_p] * 9),
+    "ddp_logprobs_backward": (C.c_int, [C.c_void_p] * 8 + [C.c_int64, C.c_void_p]),
     "ddp_read_launch_trace": (C.c_int, [C.POINTER(C.c_uint64), C.POINTER(C.c_int32), C.POINTER(C.c_int64)]),
     "ddp_status_string": (C.c_char_p, [C.c_int]),
     "ddp_last_error": (C.c_char_p, [C.c_void_p]),

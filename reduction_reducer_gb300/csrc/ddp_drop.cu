@@ -1,0 +1,209 @@
+// Dropout from a counter: which elements stay follows from the seed and each
+// element's place, and is never stored; the backward pass is the same call.
+//
+// The random bits are Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel
+// random numbers: as easy as 1, 2, 3", 2011): the counter is (place / 8, offset),
+// the key the seed.  An element is dropped where its 32 bits lie below p 2^32.
+// One block of four words gives eight elements the upper 16 bits of theirs; where
+// these alone do not tell (one in 65,536), a second block gives the lower 16.  A
+// probability thus counts in 32 bits, for about half the instructions of a word
+// an element.
+
+#include "ddp_reducer.h"
+
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "ddp_rows.cuh"
+
+namespace {
+
+using namespace ddpk::rows;
+
+constexpr int kThreads = 256;
+constexpr int kGroups = 2;        // of eight elements, of a thread
+
+struct DropParams {
+    const void* x;
+    const void* residual;
+    void* out;
+    long long n, cols, x_stride, residual_stride, out_stride;
+    const uint64_t* device_seed;
+    uint64_t seed;
+    uint32_t offset_lo, offset_hi;
+    uint32_t least;          // an element stays where its bits are no less
+    int none;                // nothing stays
+    float scale;
+};
+
+struct Words { uint32_t w[4]; };
+
+__device__ __forceinline__ Words philox(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t k0, uint32_t k1) {
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const uint64_t a = static_cast<uint64_t>(c0) * 0xD2511F53u, b = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
+        c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ (k0 + r * 0x9E3779B9u);
+        c1 = static_cast<uint32_t>(b);
+        c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ (k1 + r * 0xBB67AE85u);
+        c3 = static_cast<uint32_t>(a);
+    }
+    return Words{{c0, c1, c2, c3}};
+}
+
+// Which of the eight elements of a group stay: bit j for element j.
+__device__ __forceinline__ uint32_t staying(const DropParams& p, long long group, uint32_t k0, uint32_t k1) {
+    const uint32_t lo = static_cast<uint32_t>(group), hi = static_cast<uint32_t>(group >> 32);
+    const Words u = philox(lo, hi, p.offset_lo, p.offset_hi, k0, k1);
+    const uint32_t border = p.least & 0xffff0000u;
+    uint32_t mask = 0, closest = 0xffffffffu;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        // the 16 bits at the top, and something below them that does not matter
+        const uint32_t bits = j & 1 ? u.w[j / 2] : u.w[j / 2] << 16;
+        mask |= bits >= border ? 1u << j : 0u;
+        closest = min(closest, bits - border);
+    }
+    if (closest < 0x10000u && (p.least & 0xffffu)) {      // some have the border's upper half: the lower decides
+        const Words v = philox(lo, hi, p.offset_lo, p.offset_hi | 0x80000000u, k0, k1);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t upper = j & 1 ? u.w[j / 2] & 0xffff0000u : u.w[j / 2] << 16;
+            const uint32_t lower = j & 1 ? v.w[j / 2] >> 16 : v.w[j / 2] & 0xffffu;
+            if (upper == border && lower < (p.least & 0xffffu)) mask &= ~(1u << j);
+        }
+    }
+    return p.none ? 0u : mask;
+}
+
+// Whole: one run of n elements from 16-byte boundaries.  Rows: rows of a multiple
+// of eight elements, each from one.  Single: anything else, element by element.
+enum Layout { kWhole, kRows, kSingle };
+
+template <typename T, bool RESIDUAL, Layout LAYOUT>
+__global__ void __launch_bounds__(kThreads) drop_kernel(const __grid_constant__ DropParams p) {
+    ddpk::dev::pdl_wait();
+    ddpk::dev::pdl_trigger();
+    const uint64_t seed = p.device_seed ? *p.device_seed : p.seed;
+    const uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
+    const T* const x = static_cast<const T*>(p.x);
+    const T* const residual = static_cast<const T*>(p.residual);
+    T* const out = static_cast<T*>(p.out);
+    const long long first = static_cast<long long>(blockIdx.x) * (kThreads * kGroups) + threadIdx.x;
+    if constexpr (LAYOUT == kSingle) {
+        for (int i = 0; i < kGroups; ++i) {
+            const long long group = first + i * kThreads, from = group * 8;
+            if (from >= p.n) return;
+            const uint32_t mask = staying(p, group, k0, k1);
+            long long row = from / p.cols, col = from % p.cols;
+            for (int j = 0; j < 8 && from + j < p.n; ++j) {
+                float y = mask >> j & 1 ? widen(x[row * p.x_stride + col]) * p.scale : 0.0f;
+                if constexpr (RESIDUAL) y += widen(residual[row * p.residual_stride + col]);
+                out[row * p.out_stride + col] = narrow<T>(y);
+                if (++col == p.cols) { col = 0; ++row; }
+            }
+        }
+    } else {
+        Eight<T> a[kGroups], r[kGroups];
+        long long at[kGroups];
+        int count[kGroups];
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            const long long from = (first + i * kThreads) * 8;
+            const long long left = p.n - from;
+            count[i] = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;
+            long long rx = from, rr = from;
+            at[i] = from;
+            if constexpr (LAYOUT == kRows) {
+                const long long row = from / p.cols, col = from % p.cols;
+                rx = row * p.x_stride + col;
+                rr = row * p.residual_stride + col;
+                at[i] = row * p.out_stride + col;
+            }
+            if (count[i] == 8) {
+                a[i].load_once(x + rx);
+                if constexpr (RESIDUAL) r[i].load_once(residual + rr);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            const uint32_t mask = staying(p, first + i * kThreads, k0, k1);
+            if (count[i] == 8) {
+                float y[8], z[8];
+                a[i].get(y);
+                if constexpr (RESIDUAL) r[i].get(z);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    y[j] = mask >> j & 1 ? y[j] * p.scale : 0.0f;
+                    if constexpr (RESIDUAL) y[j] += z[j];
+                }
+                a[i].put(y);
+                a[i].store_once(out + at[i]);
+            } else {
+                for (int j = 0; j < count[i]; ++j) {          // the last few of a whole run
+                    float y = mask >> j & 1 ? widen(x[at[i] + j]) * p.scale : 0.0f;
+                    if constexpr (RESIDUAL) y += widen(residual[at[i] + j]);
+                    out[at[i] + j] = narrow<T>(y);
+                }
+            }
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch_drop(Layout layout, long long ctas, const DropParams& p, cudaStream_t stream) {
+    void (*kernel)(DropParams);
+    if (p.residual)
+        kernel = layout == kWhole ? drop_kernel<T, true, kWhole>
+                                  : layout == kRows ? drop_kernel<T, true, kRows> : drop_kernel<T, true, kSingle>;
+    else
+        kernel = layout == kWhole ? drop_kernel<T, false, kWhole>
+                                  : layout == kRows ? drop_kernel<T, false, kRows> : drop_kernel<T, false, kSingle>;
+    return launch(kernel, ctas, kThreads, 0, stream, p);
+}
+
+}  // namespace
+
+extern "C" int ddp_drop(const ddp_drop_args* a, const void* x, const void* residual, void* out, void* stream) {
+    if (!a || a->rows < 0 || a->cols < 0 || a->x_stride < a->cols || a->out_stride < a->cols ||
+        (residual && a->residual_stride < a->cols) || !(a->p >= 0.0 && a->p <= 1.0) || a->offset >> 63 ||
+        (a->dtype != DDP_F32 && a->dtype != DDP_BF16))
+        return DDP_ERR_INVALID_ARG;
+    if (a->rows == 0 || a->cols == 0) return DDP_OK;
+    const int size = a->dtype == DDP_F32 ? 4 : 2;
+    if (a->rows > INT64_MAX / 8 / a->cols || !x || !out || !aligned(x, size) || !aligned(residual, size) ||
+        !aligned(out, size) || !aligned(a->device_seed, 8))
+        return DDP_ERR_INVALID_ARG;
+    DropParams p = {};
+    p.x = x;
+    p.residual = residual;
+    p.out = out;
+    p.n = a->rows * a->cols;
+    p.cols = a->cols;
+    p.x_stride = a->x_stride;
+    p.residual_stride = residual ? a->residual_stride : a->x_stride;
+    p.out_stride = a->out_stride;
+    p.device_seed = a->device_seed;
+    p.seed = a->seed;
+    p.offset_lo = static_cast<uint32_t>(a->offset);
+    p.offset_hi = static_cast<uint32_t>(a->offset >> 32);
+    const long long least = std::llrint(a->p * 4294967296.0);
+    p.none = least >> 32 != 0;
+    p.least = static_cast<uint32_t>(least);
+    p.scale = p.none ? 0.0f : static_cast<float>(1.0 / (1.0 - a->p));
+    const bool vectors = aligned(x, 16) && aligned(residual, 16) && aligned(out, 16);
+    const auto strided = [&](int64_t stride) { return stride * size % 16 != 0; };
+    Layout layout = kSingle;
+    if (a->rows == 1 || (p.x_stride == p.cols && p.residual_stride == p.cols && p.out_stride == p.cols)) {
+        p.cols = p.n;                                       // one run
+        if (vectors) layout = kWhole;
+    } else if (vectors && p.cols % 8 == 0 && !strided(p.x_stride) && !strided(p.residual_stride) && !strided(p.out_stride)) {
+        layout = kRows;
+    }
+    const long long groups = (p.n + 7) / 8, ctas = (groups + kThreads * kGroups - 1) / (kThreads * kGroups);
+    if (ctas > INT32_MAX) return DDP_ERR_INVALID_ARG;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = a->dtype == DDP_F32 ? launch_drop<float>(layout, ctas, p, st) : launch_drop<uint16_t>(layout, ctas, p, st);
+    return e == cudaSuccess ? DDP_OK : DDP_ERR_CUDA;
+}

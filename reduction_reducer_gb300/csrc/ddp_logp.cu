@@ -1,0 +1,591 @@
+// Log probabilities of given tokens, with the entropy and the best alternatives
+// of each place, and the gradient of its logits.
+//
+// The forward pass reads a row once: every thread keeps its elements' largest m,
+// the sum S of e^(x - m) and the sum A of e^(x - m) (x - m), and rescales the sums
+// when m grows; log p_t = x_t - m - log S and the entropy is log S - A / S, two
+// terms of one sign.  A row is a warp's, a CTA's, or, where rows are too few to
+// fill the GPU, a cluster's, whose first CTA joins the parts.
+//
+// The alternatives: the k-th largest of the threads' own best is a bound that at
+// least k elements reach, and only the k threads whose best reaches it can hold
+// any.  These threads' elements are read again (from L2), and the few that reach
+// the bound sorted.  Keys are the value's order above the lowest index, so no two
+// are equal and ties go to the lowest index.
+
+#include "ddp_reducer.h"
+
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "ddp_rows.cuh"
+
+namespace {
+
+using namespace ddpk::rows;
+namespace cg = cooperative_groups;
+
+constexpr int kWarps = 16;             // of a CTA with a row to itself
+constexpr int kRowWarps = 8;           // of a CTA with a row a warp
+constexpr int kWarpVocab = 2048;       // up to which a row is a warp's
+constexpr int kBatch = 4;              // eights of a thread at once
+constexpr int kMaxTop = 32;
+constexpr int kMaxSplit = 8;           // CTAs of a row
+constexpr int kBackThreads = 256;
+constexpr int kBackEights = 4;         // of a thread
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kFloor = -1000.0f;     // 2^-1000 is zero; stands in for -inf where it meets a zero
+
+struct LogpParams {
+    const void* logits;
+    const void* targets;
+    float* logp;
+    float* entropy;
+    float* stats;
+    int* top_index;
+    float* top_logp;
+    const float* grad_logp;        // backward
+    const float* grad_entropy;
+    void* out;
+    long long rows, stride, out_stride;
+    long long segment;             // elements of a CTA of a row
+    int vocab, top, wide, split;
+    float scale, scale2;           // scale2: scale log2(e)
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The target of a row; -1: none (the row is left out), -2: no targets at all.
+__device__ __forceinline__ int target_of(const LogpParams& p, long long row) {
+    if (!p.targets) return -2;
+    const long long t = p.wide ? static_cast<const long long*>(p.targets)[row] : static_cast<const int*>(p.targets)[row];
+    return t >= 0 && t < p.vocab ? static_cast<int>(t) : -1;
+}
+
+// m: largest; s: sum of 2^((x - m) c); a: sum of 2^((x - m) c) (x - m) c.
+struct Sums {
+    float m, s, a;
+};
+
+__device__ __forceinline__ Sums join(const Sums& x, const Sums& y, float c) {
+    const float m = fmaxf(x.m, y.m);
+    // (-inf) - (-inf) is NaN, which the maximum takes for the floor
+    const float dx = fmaxf((x.m - m) * c, kFloor), dy = fmaxf((y.m - m) * c, kFloor);
+    const float fx = exp2_fast(dx), fy = exp2_fast(dy);
+    return Sums{m, x.s * fx + y.s * fy, fx * fmaf(dx, x.s, x.a) + fy * fmaf(dy, y.s, y.a)};
+}
+
+template <int LANES>
+__device__ __forceinline__ Sums join_lanes(Sums x, float c) {
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) {
+        const Sums y = {__shfl_xor_sync(kAll, x.m, o), __shfl_xor_sync(kAll, x.s, o), __shfl_xor_sync(kAll, x.a, o)};
+        x = join(x, y, c);
+    }
+    return x;
+}
+
+// N more elements.  Whether the largest grew.
+template <int N, bool ENTROPY>
+__device__ __forceinline__ bool take(const float (&x)[N], float c, Sums& t) {
+    float top = x[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) top = fmaxf(top, x[i]);
+    const bool grew = top > t.m;
+    if (grew) {
+        const float d = fmaxf((t.m - top) * c, kFloor), f = exp2_fast(d);
+        if constexpr (ENTROPY) t.a = f * fmaf(d, t.s, t.a);
+        t.s *= f;
+        t.m = top;
+    }
+    const float m = t.m == neg_inf() ? 0.0f : t.m;
+    float s = 0.0f, a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float d = (x[i] - m) * c, e = exp2_fast(d);
+        s += e;
+        if constexpr (ENTROPY) a = fmaf(e, fmaxf(d, kFloor), a);
+    }
+    t.s += s;
+    if constexpr (ENTROPY) t.a += a;
+    return grew;
+}
+
+// A run of n elements of a row: `head` elements, `eights` eights from a 16-byte
+// boundary on, and a rest.
+template <typename T>
+struct Run {
+    const T* from;
+    int n, head, eights;
+
+    __device__ __forceinline__ Run(const T* row, long long lo, long long hi) {
+        from = row + lo;
+        n = hi > lo ? static_cast<int>(hi - lo) : 0;
+        head = min(n, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(from) & 15)) % 16 / sizeof(T)));
+        eights = (n - head) / 8;
+    }
+    __device__ __forceinline__ const T* eight(int i) const { return from + head + 8 * i; }
+    __device__ __forceinline__ int rest() const { return head + 8 * eights; }
+};
+
+// ---------------------------------------------------------------- the best alternatives
+
+using Key = unsigned long long;
+
+// 0 for what is never chosen (-inf, NaN); the larger value, then the lower index first.
+__device__ __forceinline__ Key key_of(float x, int index) {
+    if (!(x > neg_inf())) return 0;
+    const uint32_t b = __float_as_uint(x + 0.0f);                       // -0 as +0
+    const uint32_t order = b ^ (static_cast<uint32_t>(static_cast<int>(b) >> 31) | 0x80000000u);
+    return static_cast<Key>(order) << 32 | (0xffffffffu - static_cast<uint32_t>(index));
+}
+
+__device__ __forceinline__ int index_of(Key k) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(k)); }
+
+__device__ __forceinline__ float value_of(Key k) {
+    const uint32_t order = static_cast<uint32_t>(k >> 32);
+    return __uint_as_float(order ^ (order & 0x80000000u ? 0x80000000u : 0xffffffffu));
+}
+
+__device__ __forceinline__ Key exchange(Key k, int o, bool larger) {
+    const Key other = __shfl_xor_sync(kAll, k, o);
+    return (other > k) == larger ? other : k;
+}
+
+// A warp's 32 keys in descending order (bitonic).
+__device__ __forceinline__ Key sort_keys(Key k) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+        for (int o = size / 2; o; o /= 2) k = exchange(k, o, ((lane & o) == 0) == ((lane & size) == 0));
+    return k;
+}
+
+// The 32 largest of two lists in descending order.
+__device__ __forceinline__ Key merge_keys(Key x, Key y) {
+    const int lane = threadIdx.x & 31;
+    y = __shfl_sync(kAll, y, 31 - lane);
+    Key k = x > y ? x : y;
+#pragma unroll
+    for (int o = 16; o; o /= 2) k = exchange(k, o, (lane & o) == 0);
+    return k;
+}
+
+// The largest keys that a warp was given, up to 32: in order in its lanes, and
+// up to 31 more that wait in `buffer` [64].
+struct Best {
+    Key list, least;       // least: what a key has to reach
+    int waiting, k;
+    Key* buffer;
+
+    __device__ __forceinline__ void flush() {
+        const int lane = threadIdx.x & 31;
+        list = merge_keys(list, sort_keys(lane < waiting ? buffer[lane] : 0));
+        const Key kth = __shfl_sync(kAll, list, k - 1);
+        if (kth > least) least = kth;
+        __syncwarp();
+        if (waiting > 32 && lane < waiting - 32) {
+            const Key x = buffer[32 + lane];
+            buffer[lane] = x;                       // (other places than those read)
+        }
+        waiting = max(waiting - 32, 0);
+        __syncwarp();
+    }
+    // by the whole warp
+    __device__ __forceinline__ void push(Key x) {
+        const bool on = x >= least && x != 0;
+        const unsigned b = __ballot_sync(kAll, on);
+        if (!b) return;
+        if (on) buffer[waiting + __popc(b & ((1u << (threadIdx.x & 31)) - 1))] = x;
+        waiting += __popc(b);
+        __syncwarp();
+        if (waiting >= 32) flush();
+    }
+};
+
+// ---------------------------------------------------------------- forward
+
+template <int WARPS>
+struct Shared {
+    Sums sums[WARPS];
+    Sums whole;                    // of this CTA's part of the row
+    Key lists[WARPS][32];
+    Key buffers[WARPS][64];
+};
+
+// The lists of all warps of a CTA as one, in the first warp's lanes.
+__device__ __forceinline__ Key join_lists(Key mine, Key (*lists)[32]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    lists[warp][lane] = mine;
+#pragma unroll
+    for (int n = kWarps / 2; n; n /= 2) {
+        __syncthreads();
+        if (warp < n) {
+            mine = merge_keys(mine, lists[warp + n][lane]);
+            lists[warp][lane] = mine;
+        }
+    }
+    return mine;
+}
+
+template <typename T, int WARPS, bool ENTROPY, bool TOP>
+__global__ void __launch_bounds__(32 * (WARPS == 1 ? kRowWarps : WARPS), WARPS == 1 ? 1 : 2)
+logp_kernel(const __grid_constant__ LogpParams p) {
+    constexpr int kThreads = 32 * WARPS;                    // of a row, in this CTA
+    __shared__ Shared<WARPS == 1 ? kRowWarps : WARPS> shared;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int t = WARPS == 1 ? lane : threadIdx.x;
+    ddpk::dev::pdl_wait();
+    ddpk::dev::pdl_trigger();
+    const long long row = WARPS == 1 ? static_cast<long long>(blockIdx.x) * kRowWarps + warp : blockIdx.x / p.split;
+    const int part = WARPS == 1 ? 0 : blockIdx.x % p.split;
+    if (WARPS == 1 && row >= p.rows) return;
+    const bool writer = part == 0 && (WARPS == 1 || warp == 0);     // this warp writes what the row gives
+    const int target = target_of(p, row);
+    if (target == -1) {                                     // the same in all CTAs of a cluster
+        if (writer) {
+            if (lane == 0) {
+                if (p.logp) p.logp[row] = 0.0f;
+                if (p.entropy) p.entropy[row] = 0.0f;
+                *reinterpret_cast<float2*>(p.stats + 2 * row) = make_float2(0.0f, 0.0f);
+            }
+            if (lane < p.top) {
+                p.top_index[row * p.top + lane] = -1;
+                p.top_logp[row * p.top + lane] = 0.0f;
+            }
+        }
+        return;
+    }
+    const T* const logits = static_cast<const T*>(p.logits) + row * p.stride;
+    const long long lo = part * p.segment, hi = min(static_cast<long long>(p.vocab), lo + p.segment);
+    const Run<T> run(logits, lo, hi);
+    const float c = p.scale2;
+    Sums sums = {neg_inf(), 0.0f, 0.0f};
+    int best = -1;                                          // where this thread's largest lies: its batch's first eight; -2: head, -3: rest
+    if (t < run.head) {
+        const float x[1] = {widen(run.from[t])};
+        if (take<1, ENTROPY>(x, c, sums)) best = -2;
+    }
+    int i = t;
+    for (; i + (kBatch - 1) * kThreads < run.eights; i += kBatch * kThreads) {
+        Eight<T> raw[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) raw[u].load(run.eight(i + u * kThreads));
+        float x[8 * kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            float f[8];
+            raw[u].get(f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[8 * u + j] = f[j];
+        }
+        if (take<8 * kBatch, ENTROPY>(x, c, sums)) best = i;
+    }
+    for (; i < run.eights; i += kThreads) {
+        Eight<T> raw;
+        raw.load(run.eight(i));
+        float x[8];
+        raw.get(x);
+        if (take<8, ENTROPY>(x, c, sums)) best = i;
+    }
+    if (t < run.n - run.rest()) {
+        const float x[1] = {widen(run.from[run.rest() + t])};
+        if (take<1, ENTROPY>(x, c, sums)) best = -3;
+    }
+
+    Key list = 0;
+    if constexpr (TOP) {
+        const int base = static_cast<int>(lo);
+        // this thread's best: the first of its batch that is as large
+        Key mine = 0;
+        if (best == -2) mine = key_of(sums.m, base + t);
+        if (best == -3) mine = key_of(sums.m, base + run.rest() + t);
+        if (best >= 0) {
+            for (int u = 0; u < kBatch && !mine; ++u) {
+                const int at = best + u * kThreads;
+                if (at >= run.eights) break;
+                Eight<T> raw;
+                raw.load(run.eight(at));
+                float x[8];
+                raw.get(x);
+#pragma unroll
+                for (int j = 7; j >= 0; --j)
+                    if (x[j] == sums.m) mine = key_of(x[j], base + run.head + 8 * at + j);
+            }
+        }
+        list = sort_keys(mine);
+        if constexpr (WARPS > 1) {
+            list = join_lists(list, shared.lists);
+            __syncthreads();
+            list = shared.lists[0][lane];                   // the threads' best 32, in every warp
+            __syncthreads();
+        }
+        Best found = {0, __shfl_sync(kAll, list, p.top - 1), 0, p.top, shared.buffers[warp]};
+        if constexpr (WARPS == 1) {
+            for (int e0 = 0; e0 < run.eights; e0 += 32) {
+                float x[8];
+                Eight<T> raw;
+                if (e0 + lane < run.eights) raw.load(run.eight(e0 + lane));
+                else raw.zero();
+                raw.get(x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    found.push(e0 + lane < run.eights ? key_of(x[j], base + run.head + 8 * (e0 + lane) + j) : 0);
+            }
+            found.push(lane < run.head ? key_of(widen(run.from[lane]), base + lane) : 0);
+            const int at = run.rest() + lane;
+            found.push(at < run.n ? key_of(widen(run.from[at]), base + at) : 0);
+        } else {
+            for (int w = warp; w < p.top; w += WARPS) {
+                const Key winner = __shfl_sync(kAll, list, w);
+                if (!winner) break;
+                int of = index_of(winner) - base;           // whose it is
+                of = of < run.head ? of : of >= run.rest() ? of - run.rest() : (of - run.head) / 8 % kThreads;
+                for (int e0 = of; e0 < run.eights; e0 += 32 * kThreads) {
+                    const int at = e0 + lane * kThreads;
+                    float x[8];
+                    Eight<T> raw;
+                    if (at < run.eights) raw.load(run.eight(at));
+                    else raw.zero();
+                    raw.get(x);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) found.push(at < run.eights ? key_of(x[j], base + run.head + 8 * at + j) : 0);
+                }
+                const int at = lane == 0 && of < run.head ? of : lane == 1 && run.rest() + of < run.n ? run.rest() + of : -1;
+                found.push(at >= 0 ? key_of(widen(run.from[at]), base + at) : 0);
+            }
+        }
+        found.flush();
+        list = found.list;
+        if constexpr (WARPS > 1) list = join_lists(list, shared.lists);
+    }
+
+    sums = join_lanes<32>(sums, c);
+    if constexpr (WARPS > 1) {
+        if (lane == 0) shared.sums[warp] = sums;
+        __syncthreads();
+        if (warp == 0) sums = join_lanes<WARPS>(shared.sums[lane % WARPS], c);
+        if (p.split > 1) {
+            cg::cluster_group cluster = cg::this_cluster();
+            if (threadIdx.x == 0) shared.whole = sums;
+            cluster.sync();
+            if (writer) {
+                const int r = lane % kMaxSplit;             // in every eight lanes
+                sums = r < p.split ? *cluster.map_shared_rank(&shared.whole, r) : Sums{neg_inf(), 0.0f, 0.0f};
+                sums = join_lanes<kMaxSplit>(sums, c);
+                if constexpr (TOP)
+                    for (int q = 1; q < p.split; ++q) list = merge_keys(list, *cluster.map_shared_rank(&shared.lists[0][lane], q));
+            }
+            cluster.sync();                                 // their shared memory stays until it is read
+        }
+    }
+    if (!writer) return;
+    const bool nothing = sums.m == neg_inf() && sums.s == 0.0f;      // no logit above -inf
+    const float log_sum = nothing ? 0.0f : logf(sums.s);
+    if (lane == 0) {
+        if (p.logp && target >= 0)
+            p.logp[row] = nothing ? neg_inf() : (widen(logits[target]) - sums.m) * p.scale - log_sum;
+        if (ENTROPY) p.entropy[row] = nothing ? 0.0f : log_sum - kLn2 * __fdiv_rn(sums.a, sums.s);
+        *reinterpret_cast<float2*>(p.stats + 2 * row) = make_float2(sums.m * p.scale, log_sum);
+    }
+    if constexpr (TOP) {
+        if (lane < p.top) {
+            p.top_index[row * p.top + lane] = list ? index_of(list) : -1;
+            p.top_logp[row * p.top + lane] =
+                list ? (value_of(list) - sums.m) * p.scale - log_sum : sums.s == sums.s ? neg_inf() : nan_value();
+        }
+    }
+}
+
+// ---------------------------------------------------------------- backward
+
+// d log p_t / d z_i = [i = t] - p_i and d H / d z_i = -p_i (log p_i + H): a thread's
+// elements of a row take -p (alpha + beta log2 p).
+struct Slope {
+    float scale, top, log_sum2, alpha, beta;
+
+    template <bool ENTROPY>
+    __device__ __forceinline__ float at(float x) const {
+        const float d = fmaf(fmaf(x, scale, -top), kLog2e, -log_sum2);  // log2 p
+        const float y = ENTROPY ? fmaf(beta, fmaxf(d, kFloor), alpha) : alpha;
+        return -exp2_fast(d) * y;
+    }
+};
+
+template <typename T, bool ENTROPY>
+__global__ void __launch_bounds__(kBackThreads) logp_backward_kernel(const __grid_constant__ LogpParams p) {
+    ddpk::dev::pdl_wait();
+    ddpk::dev::pdl_trigger();
+    const long long row = blockIdx.x / p.split;
+    const long long lo = blockIdx.x % p.split * p.segment, hi = min(static_cast<long long>(p.vocab), lo + p.segment);
+    const T* const logits = static_cast<const T*>(p.logits) + row * p.stride;
+    T* const out = static_cast<T*>(p.out) + row * p.out_stride;
+    const int target = target_of(p, row);
+    const float2 stat = *reinterpret_cast<const float2*>(p.stats + 2 * row);
+    const float g = p.grad_logp && target >= 0 ? p.grad_logp[row] : 0.0f;
+    const float h = ENTROPY ? p.grad_entropy[row] : 0.0f;
+    const Slope slope = {p.scale, stat.x, stat.y * kLog2e, p.scale * (ENTROPY ? fmaf(h, p.entropy[row], g) : g), p.scale * h * kLn2};
+    const bool zero = target == -1 || (stat.x == neg_inf() && stat.y == 0.0f);     // (a row of NaN has a NaN sum)
+    const float extra = p.scale * g;
+    const Run<T> run(logits, lo, hi);
+    T* const to = out + lo;
+    const bool vec = ((reinterpret_cast<uintptr_t>(run.from) ^ reinterpret_cast<uintptr_t>(to)) & 15) == 0;
+    const int aim = target - static_cast<int>(lo);
+    const auto single = [&](int i, T x) {
+        float y = zero ? 0.0f : slope.at<ENTROPY>(widen(x));
+        if (i == aim && !zero) y += extra;
+        to[i] = narrow<T>(y);
+    };
+    if (!vec) {                                             // element by element, eight of a thread on their way at once
+        for (int i0 = threadIdx.x; i0 < run.n; i0 += kBackThreads * 8) {
+            T x[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) x[u] = !zero && i0 + u * kBackThreads < run.n ? run.from[i0 + u * kBackThreads] : T(0);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (i0 + u * kBackThreads < run.n) single(i0 + u * kBackThreads, x[u]);
+        }
+        return;
+    }
+    if (threadIdx.x < run.head) single(threadIdx.x, run.from[threadIdx.x]);
+    if (threadIdx.x < run.n - run.rest()) single(run.rest() + threadIdx.x, run.from[run.rest() + threadIdx.x]);
+    for (int i0 = threadIdx.x; i0 < run.eights; i0 += kBackThreads * kBackEights) {
+        Eight<T> raw[kBackEights];
+#pragma unroll
+        for (int u = 0; u < kBackEights; ++u) {
+            const int i = i0 + u * kBackThreads;
+            if (!zero && i < run.eights) raw[u].load_once(run.eight(i));
+        }
+#pragma unroll
+        for (int u = 0; u < kBackEights; ++u) {
+            const int i = i0 + u * kBackThreads;
+            if (i >= run.eights) break;
+            float x[8];
+            if (zero) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = 0.0f;
+            } else {
+                raw[u].get(x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = slope.at<ENTROPY>(x[j]);
+                const unsigned place = static_cast<unsigned>(aim - run.head - 8 * i);
+                if (place < 8) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (place == j) x[j] += extra;
+                }
+            }
+            raw[u].put(x);
+            raw[u].store_once(to + run.head + 8 * i);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+template <typename T, int WARPS>
+cudaError_t forward_as(const LogpParams& p, cudaStream_t stream) {
+    void (*kernel)(LogpParams);
+    if (p.entropy) kernel = p.top ? logp_kernel<T, WARPS, true, true> : logp_kernel<T, WARPS, true, false>;
+    else kernel = p.top ? logp_kernel<T, WARPS, false, true> : logp_kernel<T, WARPS, false, false>;
+    if (WARPS == 1) return launch(kernel, (p.rows + kRowWarps - 1) / kRowWarps, 32 * kRowWarps, 0, stream, p);
+    return launch(kernel, p.rows * p.split, 32 * WARPS, 0, stream, p, p.split);
+}
+
+template <typename T>
+cudaError_t forward(LogpParams& p, cudaStream_t stream) {
+    p.split = 1;
+    p.segment = p.vocab;
+    if (p.vocab <= kWarpVocab) return forward_as<T, 1>(p, stream);
+    // few rows: as many CTAs a row as keep every thread an eight or more
+    while (p.split < kMaxSplit && p.rows * p.split < 2 * kSms && p.vocab / (2 * p.split) >= 8 * 32 * kWarps) p.split *= 2;
+    p.segment = ((p.vocab + p.split - 1) / p.split + 7) / 8 * 8;
+    return forward_as<T, kWarps>(p, stream);
+}
+
+template <typename T>
+cudaError_t backward(LogpParams& p, cudaStream_t stream) {
+    p.segment = 8LL * kBackThreads * kBackEights;
+    p.split = static_cast<int>((p.vocab + p.segment - 1) / p.segment);
+    return launch(p.grad_entropy ? logp_backward_kernel<T, true> : logp_backward_kernel<T, false>, p.rows * p.split, kBackThreads, 0,
+                  stream, p);
+}
+
+bool valid(const ddp_logprobs_args* a) {
+    return a && a->rows >= 0 && a->rows <= INT32_MAX / 8 && a->vocab >= 1 && a->vocab <= 1 << 24 && a->row_stride >= a->vocab &&
+           a->top >= 0 && a->top <= kMaxTop && a->top <= a->vocab && std::isfinite(a->scale) && a->scale > 0.0f &&
+           (a->dtype == DDP_F32 || a->dtype == DDP_BF16) && (a->index_bits == 32 || a->index_bits == 64);
+}
+
+LogpParams params_of(const ddp_logprobs_args* a) {
+    LogpParams p = {};
+    p.rows = a->rows;
+    p.vocab = static_cast<int>(a->vocab);
+    p.stride = a->row_stride;
+    p.top = a->top;
+    p.wide = a->index_bits == 64;
+    p.scale = a->scale;
+    p.scale2 = static_cast<float>(a->scale * 1.4426950408889634);
+    return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ddp_logprobs(const ddp_logprobs_args* a, const void* logits, const void* targets, float* logp, float* entropy, float* stats,
+                 int32_t* top_index, float* top_logp, void* stream) {
+    if (!valid(a)) return DDP_ERR_INVALID_ARG;
+    if (a->rows == 0) return DDP_OK;
+    if (!logits || !stats || !targets != !logp || (a->top > 0 && (!top_index || !top_logp)) ||
+        !aligned(logits, a->dtype == DDP_F32 ? 4 : 2) || !aligned(targets, a->index_bits / 8) || !aligned(logp, 4) ||
+        !aligned(entropy, 4) || !aligned(stats, 8) || !aligned(top_index, 4) || !aligned(top_logp, 4))
+        return DDP_ERR_INVALID_ARG;
+    LogpParams p = params_of(a);
+    p.logits = logits;
+    p.targets = targets;
+    p.logp = logp;
+    p.entropy = entropy;
+    p.stats = stats;
+    p.top_index = top_index;
+    p.top_logp = top_logp;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = a->dtype == DDP_F32 ? forward<float>(p, st) : forward<uint16_t>(p, st);
+    return e == cudaSuccess ? DDP_OK : DDP_ERR_CUDA;
+}
+
+int ddp_logprobs_backward(const ddp_logprobs_args* a, const void* logits, const void* targets, const float* stats,
+                          const float* entropy, const float* grad_logp, const float* grad_entropy, void* grad_logits,
+                          int64_t grad_stride, void* stream) {
+    ddp_logprobs_args without_top = a ? *a : ddp_logprobs_args{};
+    without_top.top = 0;
+    if (!a || !valid(&without_top) || grad_stride < a->vocab) return DDP_ERR_INVALID_ARG;
+    if (a->rows == 0) return DDP_OK;
+    const int size = a->dtype == DDP_F32 ? 4 : 2;
+    if (!logits || !stats || !grad_logits || (grad_logp && !targets) || !entropy != !grad_entropy || (!grad_logp && !grad_entropy) ||
+        !aligned(logits, size) || !aligned(grad_logits, size) || !aligned(targets, a->index_bits / 8) || !aligned(stats, 8) ||
+        !aligned(entropy, 4) || !aligned(grad_logp, 4) || !aligned(grad_entropy, 4))
+        return DDP_ERR_INVALID_ARG;
+    LogpParams p = params_of(a);
+    p.logits = logits;
+    p.targets = targets;
+    p.stats = const_cast<float*>(stats);
+    p.entropy = const_cast<float*>(entropy);
+    p.grad_logp = grad_logp;
+    p.grad_entropy = grad_entropy;
+    p.out = grad_logits;
+    p.out_stride = grad_stride;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = a->dtype == DDP_F32 ? backward<float>(p, st) : backward<uint16_t>(p, st);
+    return e == cudaSuccess ? DDP_OK : DDP_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,140 @@
+// Helpers of the operators that work on rows of activations (embedding, layer
+// norm, dropout, log probabilities): eight neighbouring elements at a time,
+// sums over a warp, launches.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "ddp_device.cuh"
+
+namespace ddpk {
+namespace rows {
+
+constexpr unsigned kAll = 0xffffffffu;
+
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(uint16_t x) { return dev::widen1(x); }
+
+template <typename T> __device__ __forceinline__ T narrow(float x);
+template <> __device__ __forceinline__ float narrow<float>(float x) { return x; }
+template <> __device__ __forceinline__ uint16_t narrow<uint16_t>(float x) {
+    uint16_t h;
+    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(h) : "f"(x));
+    return h;
+}
+
+// Two fp32 numbers rounded to bf16 (to nearest even), the first in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+__device__ __forceinline__ float nan_value() { return __int_as_float(0x7fffffff); }
+
+// 16 bytes that this kernel reads once, past L1; not through the read-only
+// path, so that the same thread may store to them afterwards.
+__device__ __forceinline__ uint4 ld_once(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// Eight neighbouring elements as they lie in memory: one or two accesses of 16
+// bytes, from a 16-byte boundary.
+template <typename T> struct Eight;
+
+template <> struct Eight<uint16_t> {
+    uint4 v;
+    __device__ __forceinline__ void load_once(const uint16_t* p) { v = ld_once(p); }
+    __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&f)[8]) const { dev::Vec<uint16_t>::unpack(v, f); }
+    __device__ __forceinline__ void put(const float (&f)[8]) {
+        v = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+    }
+    __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = v; }
+    __device__ __forceinline__ void store_once(uint16_t* p) const { __stcs(reinterpret_cast<uint4*>(p), v); }
+};
+
+template <> struct Eight<float> {
+    uint4 v[2];
+    __device__ __forceinline__ void load_once(const float* p) { v[0] = ld_once(p); v[1] = ld_once(p + 4); }
+    __device__ __forceinline__ void load(const float* p) {
+        v[0] = reinterpret_cast<const uint4*>(p)[0];
+        v[1] = reinterpret_cast<const uint4*>(p)[1];
+    }
+    __device__ __forceinline__ void zero() { v[0] = v[1] = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            f[4 * i] = __uint_as_float(v[i].x); f[4 * i + 1] = __uint_as_float(v[i].y);
+            f[4 * i + 2] = __uint_as_float(v[i].z); f[4 * i + 3] = __uint_as_float(v[i].w);
+        }
+    }
+    __device__ __forceinline__ void put(const float (&f)[8]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            v[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]),
+                              __float_as_uint(f[4 * i + 3]));
+    }
+    __device__ __forceinline__ void store(float* p) const {
+        reinterpret_cast<uint4*>(p)[0] = v[0];
+        reinterpret_cast<uint4*>(p)[1] = v[1];
+    }
+    __device__ __forceinline__ void store_once(float* p) const {
+        __stcs(reinterpret_cast<uint4*>(p), v[0]);
+        __stcs(reinterpret_cast<uint4*>(p) + 1, v[1]);
+    }
+};
+
+// Over LANES neighbouring lanes (a power of two), the result in all of them.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float x) {
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
+    return x;
+}
+
+// ------------------------------------------------------------------ host
+
+inline bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+inline int power_of_two(long long x) {
+    int p = 1;
+    while (p < x) p *= 2;
+    return p;
+}
+
+// A launch that may begin while the one before it ends; the kernel waits for
+// that one's end (dev::pdl_wait) before it touches memory.
+template <typename P>
+cudaError_t launch(void (*kernel)(P), long long ctas, int threads, size_t shared, cudaStream_t stream, const P& params,
+                   int cluster = 1) {
+    if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = shared;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, params);
+}
+
+// The multiprocessors that grids are sized for, and shares of work counted by:
+// a constant, so that sums are split alike wherever the library runs.
+constexpr int kSms = 152;
+
+}  // namespace rows
+}  // namespace ddpk

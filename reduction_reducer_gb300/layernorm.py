@@ -1,0 +1,142 @@
+"""Layer norm and its gradient (``ddp_layer_norm`` and
+``ddp_layer_norm_backward`` of include/ddp_reducer.h).  Only argument
+marshalling happens here; the arithmetic is the library's kernels'."""
+
+from __future__ import annotations
+
+import struct
+
+from . import _lib, _rows
+from ._rows import _device, _stream
+
+
+def _pack(rows, dim, x_stride, out_stride, eps, code, param_code):
+    try:
+        return _lib.pack_layer_norm(rows, dim, x_stride, out_stride, eps, code, param_code)
+    except (struct.error, OverflowError, TypeError) as e:
+        raise ValueError(f"eps: {e}") from None
+
+
+def _params(dim, device, **tensors):
+    """(their dtype's code, their addresses) of parameter vectors of one dtype."""
+    dtype, at = None, []
+    for name, t in tensors.items():
+        if t is None:
+            at.append(None)
+            continue
+        if dtype is None:
+            dtype = t.dtype
+            if dtype not in _rows.DTYPES:
+                raise ValueError(f"{name}: expected fp32 or bf16 on {_rows.found(device, t)}")
+        at.append(_rows.vector(name, t, (dim,), device, dtype))
+    return _rows.DTYPES.get(dtype, _lib.DDP_F32), at
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stats=None, stream=None,
+               lib_path: str = _lib.LIB_PATH):
+    """(y, stats): y = (x - mean) / sqrt(variance + eps) * weight + bias over
+    the last dimension, and fp32 [*x.shape[:-1], 2], each row's mean and
+    1 / sqrt(variance + eps), which the gradient takes.
+
+    x: fp32 or bf16 (rows may be strided); weight, bias: [dim], fp32 or bf16,
+    or None; out, stats: the results' places (without them they are allocated
+    on `stream`).  All tensors lie on the current device."""
+    torch = _rows.torch or _rows.load_torch()
+    device = _device()
+    rows, dim, x_stride, code = _rows.matrix("x", x, device)
+    param_code, (w, b) = _params(dim, device, weight=weight, bias=bias)
+    if out is None:
+        out = _rows.empty(x.shape, x.dtype, x.device, stream)
+    shape = (*x.shape[:-1], 2)
+    if stats is None:
+        stats = _rows.empty(shape, torch.float32, x.device, stream)
+    _, _, out_stride, _ = _rows.matrix("out", out, device, x.shape, code)
+    st = _lib.load(lib_path).ddp_layer_norm(_pack(rows, dim, x_stride, out_stride, eps, code, param_code), x.data_ptr(), w, b,
+                                            out.data_ptr(), _rows.vector("stats", stats, shape, device, torch.float32),
+                                            _stream(stream))
+    if st:
+        _rows.refused(st, "ddp_layer_norm", rows=rows, dim=dim, eps=eps)
+    return out, stats
+
+
+def layer_norm_backward(grad, x, stats, weight=None, grad_weight=None, grad_bias=None, out=None, input_grad: bool = True,
+                        accumulate: bool = False, workspace=None, stream=None, lib_path: str = _lib.LIB_PATH):
+    """(grad_x, grad_weight, grad_bias) from the gradient of y and the stats
+    that ``layer_norm`` gave.
+
+    grad_weight, grad_bias: [dim] of the parameters' dtype, which are written
+    (or, with accumulate and fp32, added to) where they are given: gradient
+    fields or bucket views; out: the place of grad_x; input_grad: False
+    leaves grad_x out (None); workspace: bytes that no other call uses
+    meanwhile (without one they are allocated on `stream`)."""
+    torch = _rows.torch or _rows.load_torch()
+    device = _device()
+    rows, dim, x_stride, code = _rows.matrix("x", x, device)
+    _, _, grad_stride, _ = _rows.matrix("grad", grad, device, x.shape, code)
+    param_code, (w, gw, gb) = _params(dim, device, weight=weight, grad_weight=grad_weight, grad_bias=grad_bias)
+    out_stride = dim
+    if input_grad:
+        if out is None:
+            out = _rows.empty(x.shape, x.dtype, x.device, stream)
+        _, _, out_stride, _ = _rows.matrix("out", out, device, x.shape, code)
+    else:
+        out = None
+        if gw is None and gb is None:
+            return None, None, None
+    lib = _lib.load(lib_path)
+    args = _pack(rows, dim, x_stride, out_stride, 0.0, code, param_code)
+    size = lib.ddp_layer_norm_workspace(args) if gw is not None or gb is not None else 0
+    st = size
+    if size >= 0:
+        ws = _rows.workspace(workspace, size, x.device, stream) if size else None
+        st = lib.ddp_layer_norm_backward(args, grad.data_ptr(), grad_stride, x.data_ptr(),
+                                         _rows.vector("stats", stats, (*x.shape[:-1], 2), device, torch.float32), w,
+                                         out.data_ptr() if input_grad else None, gw, gb, 1 if accumulate else 0,
+                                         ws.data_ptr() if size else None, _stream(stream))
+    if st:
+        _rows.refused(st, "ddp_layer_norm_backward", rows=rows, dim=dim, accumulate=accumulate)
+    return out, grad_weight, grad_bias
+
+
+_Normed = None     # the autograd function, made on first use
+
+
+def _autograd():
+    global _Normed
+    if _Normed is None:
+        torch = _rows.load_torch()
+
+        class Normed(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x, weight, bias, eps, grad_into):
+                y, stats = layer_norm(x, weight, bias, eps)
+                ctx.save_for_backward(x, stats, weight)
+                ctx.bias_dtype, ctx.into = None if bias is None else bias.dtype, grad_into
+                return y
+
+            @staticmethod
+            @torch.autograd.function.once_differentiable      # a second derivative raises
+            def backward(ctx, grad):
+                x, stats, weight = ctx.saved_tensors
+                need_x, need_w, need_b = ctx.needs_input_grad[:3]
+                if ctx.into is not None:
+                    gw, gb = ctx.into
+                    dx, _, _ = layer_norm_backward(_rows.row_gradient(grad), x, stats, weight, gw, gb, input_grad=need_x,
+                                                   accumulate=True)
+                    return dx, None, None, None, None
+                dim = x.shape[-1:]
+                gw = torch.empty(dim, dtype=weight.dtype, device=x.device) if need_w else None
+                gb = torch.empty(dim, dtype=ctx.bias_dtype, device=x.device) if need_b else None
+                dx, gw, gb = layer_norm_backward(_rows.row_gradient(grad), x, stats, weight, gw, gb, input_grad=need_x)
+                return dx, gw, gb, None, None
+
+        _Normed = Normed
+    return _Normed
+
+
+def layer_normed(x, weight=None, bias=None, eps: float = 1e-5, grad_into=None):
+    """``layer_norm`` under autograd, on the current stream: y.  grad_into:
+    (grad_weight, grad_bias), fp32 gradient fields or bucket views (either may
+    be None) that the parameters' gradients are added to in the backward pass;
+    autograd then gets none for them."""
+    return _autograd().apply(x, weight, bias, eps, grad_into)
