@@ -20,12 +20,18 @@ namespace {
 
 using namespace ddpk::rows;
 
-constexpr int kThreads = 256;          // of a CTA that holds several rows
-constexpr int kMaxWarps = 32;
-constexpr int kRows = 4;               // backward: rows of a group at once
+constexpr int kForwardThreads = 128;   // of a CTA that holds several rows
+constexpr int kBackwardThreads = 256;
+constexpr int kMaxWarps = 16;          // of a CTA that holds a row, in registers
+constexpr int kLongThreads = 1024;     // of one that reads it again and again
+constexpr int kLongWarps = kLongThreads / 32;
+constexpr int kColumns = 256;          // of a CTA of norm_columns_kernel
 constexpr int kJoinLanes = 32;         // join_kernel: threads of a column
-constexpr int kMaxParts = kSms * 5;    // backward: CTAs that sum the weight's gradient over rows of their own
-constexpr int kMinRows = 8;            // and rows of each, at least
+constexpr int kWarpsPerSm = 16;        // resident, at 128 registers
+// Rows of a group on their way, with the one under work (of 512 threads' fp32
+// rows more would not fit); and rounds of rows of the gradient.
+template <typename T> constexpr int kForwardStages = sizeof(T) == 2 ? 4 : 3;
+constexpr int kBackwardStages = 3;
 
 struct NormParams {
     const void* x;
@@ -45,83 +51,97 @@ struct NormParams {
     int nparts;
 };
 
-// Thread t's element j of chunk c in a group of G threads.
+// Thread t's element j of chunk c in a group of G threads: eights next to one
+// another, or (rows that do not lie in vectors) every G-th element.
 template <bool VEC>
 __device__ __forceinline__ int place(int c, int j, int t, int G) {
     return VEC ? (c * G + t) * 8 + j : (c * 8 + j) * G + t;
 }
 
-// A thread's elements of a row; zeros past its end.
-template <int CH, bool VEC, typename T>
-__device__ __forceinline__ void load_row(const T* row, bool on, int t, int G, int dim, float (&x)[CH * 8]) {
-    if constexpr (VEC) {
-        Eight<T> raw[CH];
+__device__ __forceinline__ float param_at(const void* p, int bf16, int at) {
+    return bf16 ? widen(static_cast<const uint16_t*>(p)[at]) : static_cast<const float*>(p)[at];
+}
+
+// A thread's elements of a parameter vector, in pairs; `none` where there is no
+// vector, and past its end.
+template <int CH, bool VEC>
+__device__ __forceinline__ void load_param(const void* p, int bf16, float none, int t, int G, int dim, float2 (&f)[CH * 4]) {
+#pragma unroll
+    for (int i = 0; i < CH * 4; ++i) {
+        f[i] = both(none);
+        if (!p) continue;
+        const int at = place<VEC>(i / 4, 2 * (i % 4), t, G), next = place<VEC>(i / 4, 2 * (i % 4) + 1, t, G);
+        if (at < dim) f[i].x = param_at(p, bf16, at);
+        if (next < dim) f[i].y = param_at(p, bf16, next);
+    }
+}
+
+// A thread's place in shared memory for one row: the 16-byte pieces of all
+// threads next to one another.
+template <typename T, int CH>
+struct Slot {
+    static constexpr int kPieces = CH * static_cast<int>(sizeof(Eight<T>)) / 16;
+    static constexpr int kBytes = 16 * kPieces;              // of a thread
+
+    uint4* at;
+
+    __device__ __forceinline__ void request(const T* row, int t, int G, int dim) const {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+            if (place<true>(c, 0, t, G) < dim)
+#pragma unroll
+                for (int u = 0; u < kPieces / CH; ++u)
+                    copy_async(at + (c * (kPieces / CH) + u) * blockDim.x, reinterpret_cast<const uint4*>(row + place<true>(c, 0, t, G)) + u);
+    }
+    __device__ __forceinline__ void take(int t, int G, int dim, float2 (&x)[CH * 4]) const {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int at = place<true>(c, 0, t, G);
-            if (on && at < dim) raw[c].load_once(row + at);
-            else raw[c].zero();
-        }
+            uint4 raw[kPieces / CH];
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            float f[8];
-            raw[c].get(f);
+            for (int u = 0; u < kPieces / CH; ++u)
+                raw[u] = place<true>(c, 0, t, G) < dim ? at[(c * (kPieces / CH) + u) * blockDim.x] : make_uint4(0, 0, 0, 0);
+            if constexpr (sizeof(T) == 2) {
+                const uint32_t w[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[c * 8 + j] = f[j];
-        }
-    } else {
+                for (int j = 0; j < 4; ++j) x[c * 4 + j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+            } else {
 #pragma unroll
-        for (int i = 0; i < CH * 8; ++i) {
-            const int at = place<false>(i / 8, i % 8, t, G);
-            x[i] = on && at < dim ? widen(row[at]) : 0.0f;
+                for (int u = 0; u < 2; ++u) {
+                    x[c * 4 + 2 * u] = make_float2(__uint_as_float(raw[u].x), __uint_as_float(raw[u].y));
+                    x[c * 4 + 2 * u + 1] = make_float2(__uint_as_float(raw[u].z), __uint_as_float(raw[u].w));
+                }
+            }
         }
+    }
+};
+
+// A thread's elements of a row that does not lie in vectors; zeros past its end.
+template <int CH, typename T>
+__device__ __forceinline__ void load_single(const T* row, bool on, int t, int G, int dim, float2 (&x)[CH * 4]) {
+#pragma unroll
+    for (int i = 0; i < CH * 4; ++i) {
+        const int at = place<false>(i / 4, 2 * (i % 4), t, G), next = place<false>(i / 4, 2 * (i % 4) + 1, t, G);
+        x[i].x = on && at < dim ? widen(row[at]) : 0.0f;
+        x[i].y = on && next < dim ? widen(row[next]) : 0.0f;
     }
 }
 
 template <int CH, bool VEC, typename T>
-__device__ __forceinline__ void store_row(T* row, int t, int G, int dim, const float (&x)[CH * 8]) {
+__device__ __forceinline__ void store_row(T* row, int t, int G, int dim, const float2 (&x)[CH * 4]) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         if constexpr (VEC) {
-            const int at = place<true>(c, 0, t, G);
-            float f[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = x[c * 8 + j];
+            const float f[8] = {x[c * 4].x, x[c * 4].y, x[c * 4 + 1].x, x[c * 4 + 1].y,
+                                x[c * 4 + 2].x, x[c * 4 + 2].y, x[c * 4 + 3].x, x[c * 4 + 3].y};
             Eight<T> raw;
             raw.put(f);
-            if (at < dim) raw.store_once(row + at);
+            if (place<true>(c, 0, t, G) < dim) raw.store_once(row + place<true>(c, 0, t, G));
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int at = place<false>(c, j, t, G);
-                if (at < dim) row[at] = narrow<T>(x[c * 8 + j]);
+                if (at < dim) row[at] = narrow<T>(j & 1 ? x[c * 4 + j / 2].y : x[c * 4 + j / 2].x);
             }
-        }
-    }
-}
-
-// Eight of a parameter vector, from an element of the thread's on.
-template <bool VEC>
-__device__ __forceinline__ void load_param(const void* p, int bf16, int c, int t, int G, int dim, float (&f)[8]) {
-    if constexpr (VEC) {
-        const int at = place<true>(c, 0, t, G);
-        if (at >= dim) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = 0.0f;
-        } else if (bf16) {
-            Eight<uint16_t> raw;
-            raw.load(static_cast<const uint16_t*>(p) + at);
-            raw.get(f);
-        } else {
-            Eight<float> raw;
-            raw.load(static_cast<const float*>(p) + at);
-            raw.get(f);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int at = place<false>(c, j, t, G);
-            f[j] = at >= dim ? 0.0f : bf16 ? widen(static_cast<const uint16_t*>(p)[at]) : static_cast<const float*>(p)[at];
         }
     }
 }
@@ -141,60 +161,75 @@ __device__ __forceinline__ float group_sum(float x, float* shared) {
     }
 }
 
-__device__ __forceinline__ float param_at(const void* p, int bf16, int at) {
-    return bf16 ? widen(static_cast<const uint16_t*>(p)[at]) : static_cast<const float*>(p)[at];
-}
-
 // ---------------------------------------------------------------- forward
 
+// A group takes every so many rows and keeps its columns' weight and bias in
+// registers; rows that lie in vectors are copied to shared memory ahead.
 template <typename T, int LANES, int CH, bool VEC>
-__global__ void __launch_bounds__(LANES ? kThreads : 1024) norm_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(LANES ? kForwardThreads : 32 * kMaxWarps) norm_kernel(const __grid_constant__ NormParams p) {
+    extern __shared__ uint4 ahead[];
     __shared__ float shared[2][kMaxWarps];
+    constexpr int kStages = kForwardStages<T>;
     const int G = LANES ? LANES : blockDim.x, t = threadIdx.x % G;
-    const int groups = LANES ? kThreads / LANES : 1, group = LANES ? threadIdx.x / LANES : 0;
+    const int groups = LANES ? kForwardThreads / LANES : 1, group = LANES ? threadIdx.x / LANES : 0;
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
-    const long long stride = static_cast<long long>(gridDim.x) * groups;
+    const long long stride = static_cast<long long>(gridDim.x) * groups, first = static_cast<long long>(blockIdx.x) * groups + group;
+    const T* const from = static_cast<const T*>(p.x);
+    const auto slot = [&](int stage) { return Slot<T, CH>{ahead + stage * Slot<T, CH>::kPieces * blockDim.x + threadIdx.x}; };
+    const auto request = [&](long long row, int stage) {
+        if (row < p.rows) slot(stage).request(from + row * p.x_stride, t, G, p.dim);
+        copy_commit();
+    };
+    if constexpr (VEC)
+#pragma unroll
+        for (int s = 0; s + 1 < kStages; ++s) request(first + s * stride, s);
+    float2 w[CH * 4], b[CH * 4];
+    load_param<CH, VEC>(p.weight, p.param_bf16, 1.0f, t, G, p.dim, w);
+    load_param<CH, VEC>(p.bias, p.param_bf16, 0.0f, t, G, p.dim, b);
+    int stage = 0;
     // all groups of a warp take as many rounds, for their sums' shuffles
-    for (long long r0 = static_cast<long long>(blockIdx.x) * groups; r0 < p.rows; r0 += stride) {
-        const long long row = r0 + group;
+    for (long long row = first; row - group < p.rows; row += stride) {
         const bool on = row < p.rows;
-        float x[CH * 8];
-        load_row<CH, VEC>(static_cast<const T*>(p.x) + row * p.x_stride, on, t, G, p.dim, x);
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < CH * 8; ++i) sum += x[i];
-        const float mean = __fdiv_rn(group_sum<LANES>(sum, shared[0]), static_cast<float>(p.dim));
-        sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < CH * 8; ++i) {
-            x[i] -= mean;
-            if (place<VEC>(i / 8, i % 8, t, G) < p.dim) sum = fmaf(x[i], x[i], sum);
+        float2 x[CH * 4];
+        if constexpr (VEC) {
+            copy_wait<kStages - 2>();
+            slot(stage).take(t, G, p.dim, x);
+            // into the stage before this one, whose row has been used up
+            request(row + (kStages - 1) * stride, stage ? stage - 1 : kStages - 1);
+            stage = stage + 1 < kStages ? stage + 1 : 0;
+        } else {
+            load_single<CH>(from + row * p.x_stride, on, t, G, p.dim, x);
         }
-        const float variance = __fdiv_rn(group_sum<LANES>(sum, shared[1]), static_cast<float>(p.dim));
+        float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < CH * 4; ++i) sum = add2(sum, x[i]);
+        const float mean = __fdiv_rn(group_sum<LANES>(sum.x + sum.y, shared[0]), static_cast<float>(p.dim));
+        sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < CH * 4; ++i) {
+            x[i] = add2(x[i], both(-mean));
+            // elements past the row's end count for nothing
+            if constexpr (VEC) {
+                if (place<true>(i / 4, 0, t, G) < p.dim) sum = fma2(x[i], x[i], sum);
+            } else {
+                if (place<false>(i / 4, 2 * (i % 4), t, G) < p.dim) sum.x = fmaf(x[i].x, x[i].x, sum.x);
+                if (place<false>(i / 4, 2 * (i % 4) + 1, t, G) < p.dim) sum.y = fmaf(x[i].y, x[i].y, sum.y);
+            }
+        }
+        const float variance = __fdiv_rn(group_sum<LANES>(sum.x + sum.y, shared[1]), static_cast<float>(p.dim));
         const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(variance + p.eps));
         if (on && t == 0) *reinterpret_cast<float2*>(p.stats + 2 * row) = make_float2(mean, rstd);
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            float w[8], b[8];
-            if (p.weight) load_param<VEC>(p.weight, p.param_bf16, c, t, G, p.dim, w);
-            if (p.bias) load_param<VEC>(p.bias, p.param_bf16, c, t, G, p.dim, b);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float y = x[c * 8 + j] * rstd;
-                if (p.weight) y *= w[j];
-                if (p.bias) y += b[j];
-                x[c * 8 + j] = y;
-            }
-        }
+        for (int i = 0; i < CH * 4; ++i) x[i] = fma2(mul2(x[i], both(rstd)), w[i], b[i]);
         if (on) store_row<CH, VEC>(static_cast<T*>(p.out) + row * p.out_stride, t, G, p.dim, x);
     }
 }
 
 // Rows of any length, a CTA each, read three times.
 template <typename T>
-__global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__ NormParams p) {
-    __shared__ float shared[2][kMaxWarps];
+__global__ void __launch_bounds__(kLongThreads) norm_long_kernel(const __grid_constant__ NormParams p) {
+    __shared__ float shared[2][kLongWarps];
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
     for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
@@ -222,13 +257,16 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__
 
 // ---------------------------------------------------------------- backward
 
-// Sums of eight values over a warp, for nine shuffles: each step halves the
-// values that a lane keeps.  The sum of value i is in the lanes whose bits 4, 3
-// and 2 spell i.
-__device__ __forceinline__ float sum_eight(float (&v)[8]) {
+// Sums of N values over a warp: each of the first steps halves the values that a
+// lane keeps (eight take nine shuffles instead of 40).  The sum of value i is in
+// lane_of<N>(i), and in the lanes whose bits above those of the last steps are
+// the same.
+template <int N>
+__device__ __forceinline__ float sum_many(float (&v)[N]) {
     const int lane = threadIdx.x & 31;
+    int o = 16;
 #pragma unroll
-    for (int n = 4, o = 16; n; n /= 2, o /= 2) {
+    for (int n = N / 2; n; n /= 2, o /= 2) {
         const bool upper = lane & o;
 #pragma unroll
         for (int i = 0; i < n; ++i) {
@@ -236,101 +274,136 @@ __device__ __forceinline__ float sum_eight(float (&v)[8]) {
             v[i] = mine + __shfl_xor_sync(kAll, other, o);
         }
     }
-    v[0] += __shfl_xor_sync(kAll, v[0], 2);
-    return v[0] + __shfl_xor_sync(kAll, v[0], 1);
+    float sum = v[0];
+#pragma unroll
+    for (int q = 16 / N; q; q /= 2) sum += __shfl_xor_sync(kAll, sum, q);
+    return sum;
 }
 
-__device__ __forceinline__ int lane_of_eight(int i) { return (i & 4) << 2 | (i & 2) << 2 | (i & 1) << 2; }
+template <int N>
+__device__ __forceinline__ int lane_of(int i) { return i * (32 / N); }
 
 // dx = r (g - mean(g) - xh mean(g xh)), g = dy w, xh = (x - mean) r; dw = sum dy xh
-// and db = sum dy over the CTA's rows, a thread its columns.
-template <typename T, int LANES, int CH, bool VEC>
-__global__ void __launch_bounds__(LANES ? kThreads : 512) norm_backward_kernel(const __grid_constant__ NormParams p) {
-    __shared__ float shared[2][kMaxWarps][8];
-    __shared__ float columns[LANES ? 16 * kThreads : 1];
+// and db = sum dy over the CTA's rows, a thread its columns.  A round is ROWS rows
+// of each group, so that a barrier serves as many.
+template <typename T, int LANES, int CH, int ROWS, bool VEC>
+__global__ void __launch_bounds__(LANES ? kBackwardThreads : 32 * kMaxWarps) norm_backward_kernel(const __grid_constant__ NormParams p) {
+    constexpr int N = 2 * ROWS;
+    extern __shared__ uint4 ahead[];
+    __shared__ float shared[2][kMaxWarps][N];
     const int G = LANES ? LANES : blockDim.x, t = threadIdx.x % G;
-    const int groups = LANES ? kThreads / LANES : 1, group = LANES ? threadIdx.x / LANES : 0;
+    const int groups = LANES ? kBackwardThreads / LANES : 1, group = LANES ? threadIdx.x / LANES : 0;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
-    float dw[CH * 8], db[CH * 8], w[CH * 8];
+    const int tile = groups * ROWS;
+    const long long first = static_cast<long long>(blockIdx.x) * tile, stride = static_cast<long long>(gridDim.x) * tile;
+    const T* const from_x = static_cast<const T*>(p.x);
+    const T* const from_dy = static_cast<const T*>(p.grad);
+    const auto slot = [&](int stage, int r, int which) {
+        return Slot<T, CH>{ahead + ((stage * ROWS + r) * 2 + which) * Slot<T, CH>::kPieces * blockDim.x + threadIdx.x};
+    };
+    const auto request = [&](long long r0, int stage) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        float f[8];
-        if (p.weight) load_param<VEC>(p.weight, p.param_bf16, c, t, G, p.dim, f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            w[c * 8 + j] = p.weight ? f[j] : 1.0f;
-            dw[c * 8 + j] = db[c * 8 + j] = 0.0f;
+        for (int r = 0; r < ROWS; ++r) {
+            const long long row = r0 + r * groups + group;
+            if (row < p.rows) {
+                slot(stage, r, 0).request(from_x + row * p.x_stride, t, G, p.dim);
+                slot(stage, r, 1).request(from_dy + row * p.grad_stride, t, G, p.dim);
+            }
         }
-    }
-    const float over = __fdiv_rn(1.0f, static_cast<float>(p.dim));
-    const int tile = groups * kRows;
-    int phase = 0;
-    for (long long r0 = static_cast<long long>(blockIdx.x) * tile; r0 < p.rows; r0 += static_cast<long long>(gridDim.x) * tile) {
-        float x[kRows][CH * 8], dy[kRows][CH * 8], sums[2 * kRows];
-        float2 stat[kRows];
+        copy_commit();
+    };
+    if constexpr (VEC)
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
+        for (int s = 0; s + 1 < kBackwardStages; ++s) request(first + s * stride, s);
+    float2 dw[CH * 4], db[CH * 4], w[CH * 4];
+    load_param<CH, VEC>(p.weight, p.param_bf16, 1.0f, t, G, p.dim, w);
+#pragma unroll
+    for (int i = 0; i < CH * 4; ++i) dw[i] = db[i] = make_float2(0.0f, 0.0f);
+    const float over = __fdiv_rn(1.0f, static_cast<float>(p.dim));
+    int phase = 0, stage = 0;
+    for (long long r0 = first; r0 < p.rows; r0 += stride) {
+        float2 x[ROWS][CH * 4], dy[ROWS][CH * 4], stat[ROWS];
+        float sums[N];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            const long long row = r0 + r * groups + group;
+            stat[r] = row < p.rows ? *reinterpret_cast<const float2*>(p.stats + 2 * row) : make_float2(0.0f, 0.0f);
+        }
+        if constexpr (VEC) copy_wait<kBackwardStages - 2>();
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
             const long long row = r0 + r * groups + group;
             const bool on = row < p.rows;
-            stat[r] = on ? *reinterpret_cast<const float2*>(p.stats + 2 * row) : make_float2(0.0f, 0.0f);
-            load_row<CH, VEC>(static_cast<const T*>(p.x) + row * p.x_stride, on, t, G, p.dim, x[r]);
-            load_row<CH, VEC>(static_cast<const T*>(p.grad) + row * p.grad_stride, on, t, G, p.dim, dy[r]);
+            if constexpr (VEC) {
+                const int dim = on ? p.dim : 0;                  // (zeros)
+                slot(stage, r, 0).take(t, G, dim, x[r]);
+                slot(stage, r, 1).take(t, G, dim, dy[r]);
+            } else {
+                load_single<CH>(from_x + row * p.x_stride, on, t, G, p.dim, x[r]);
+                load_single<CH>(from_dy + row * p.grad_stride, on, t, G, p.dim, dy[r]);
+            }
+        }
+        if constexpr (VEC) {
+            request(r0 + (kBackwardStages - 1) * stride, stage ? stage - 1 : kBackwardStages - 1);   // used up a round ago
+            stage = stage + 1 < kBackwardStages ? stage + 1 : 0;
         }
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            float a = 0.0f, b = 0.0f;
+        for (int r = 0; r < ROWS; ++r) {
+            float2 a = make_float2(0.0f, 0.0f), b = a;
 #pragma unroll
-            for (int i = 0; i < CH * 8; ++i) {
-                x[r][i] = (x[r][i] - stat[r].x) * stat[r].y;
-                db[i] += dy[r][i];
-                dw[i] = fmaf(dy[r][i], x[r][i], dw[i]);          // zeros past the row's end: dy is zero there
-                dy[r][i] *= w[i];
-                a += dy[r][i];
-                b = fmaf(dy[r][i], x[r][i], b);
+            for (int i = 0; i < CH * 4; ++i) {
+                x[r][i] = mul2(add2(x[r][i], both(-stat[r].x)), both(stat[r].y));
+                db[i] = add2(db[i], dy[r][i]);
+                dw[i] = fma2(dy[r][i], x[r][i], dw[i]);          // nothing past the row's end: dy is zero there
+                dy[r][i] = mul2(dy[r][i], w[i]);
+                a = add2(a, dy[r][i]);
+                b = fma2(dy[r][i], x[r][i], b);
             }
-            sums[2 * r] = a;
-            sums[2 * r + 1] = b;
+            sums[2 * r] = a.x + a.y;
+            sums[2 * r + 1] = b.x + b.y;
         }
         if constexpr (LANES > 0) {
 #pragma unroll
-            for (int i = 0; i < 2 * kRows; ++i) sums[i] = lanes_sum<LANES>(sums[i]);
+            for (int i = 0; i < N; ++i) sums[i] = lanes_sum<LANES>(sums[i]);
         } else {
-            static_assert(kRows == 4, "eight sums");
-            float s = sum_eight(sums);
-            if ((lane & 3) == 0) shared[phase][warp][lane >> 2] = s;     // value lane / 4: its bits are the lane's 4, 3, 2
+            float s = sum_many<N>(sums);
+            if (lane % (32 / N) == 0) shared[phase][warp][lane / (32 / N)] = s;
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sums[i] = lane < warps ? shared[phase][lane][i] : 0.0f;
-            s = sum_eight(sums);
+            for (int i = 0; i < N; ++i) sums[i] = lane < warps ? shared[phase][lane][i] : 0.0f;
+            s = sum_many<N>(sums);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sums[i] = __shfl_sync(kAll, s, lane_of_eight(i));
+            for (int i = 0; i < N; ++i) sums[i] = __shfl_sync(kAll, s, lane_of<N>(i));
             phase ^= 1;                                          // the other half is free: everyone is past this round's barrier
         }
+        if (!p.out) continue;
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
+        for (int r = 0; r < ROWS; ++r) {
             const long long row = r0 + r * groups + group;
-            const float a = sums[2 * r] * over, b = sums[2 * r + 1] * over;
+            const float2 a = both(-sums[2 * r] * over), b = both(-sums[2 * r + 1] * over);
 #pragma unroll
-            for (int i = 0; i < CH * 8; ++i) x[r][i] = stat[r].y * (dy[r][i] - a - x[r][i] * b);
-            if (p.out && row < p.rows) store_row<CH, VEC>(static_cast<T*>(p.out) + row * p.out_stride, t, G, p.dim, x[r]);
+            for (int i = 0; i < CH * 4; ++i) x[r][i] = mul2(both(stat[r].y), fma2(x[r][i], b, add2(dy[r][i], a)));
+            if (row < p.rows) store_row<CH, VEC>(static_cast<T*>(p.out) + row * p.out_stride, t, G, p.dim, x[r]);
         }
     }
     if (!p.parts) return;
     float* const part = p.parts + static_cast<long long>(blockIdx.x) * 2 * p.dim;
     if constexpr (LANES > 0) {
-        // the groups' sums, in order
+        // the groups' sums, in order, through the memory of the rows, which are used up
+        float* const columns = reinterpret_cast<float*>(ahead);
+        __syncthreads();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            columns[(2 * i) * kThreads + threadIdx.x] = dw[i];
-            columns[(2 * i + 1) * kThreads + threadIdx.x] = db[i];
+            columns[(2 * i) * kBackwardThreads + threadIdx.x] = i & 1 ? dw[i / 2].y : dw[i / 2].x;
+            columns[(2 * i + 1) * kBackwardThreads + threadIdx.x] = i & 1 ? db[i / 2].y : db[i / 2].x;
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < 16 * LANES; i += kThreads) {
-            const int which = i / LANES, from = i % LANES, at = place<VEC>(0, which / 2, from, LANES);
+        for (int i = threadIdx.x; i < 16 * LANES; i += kBackwardThreads) {
+            const int which = i / LANES, of = i % LANES, at = place<VEC>(0, which / 2, of, LANES);
             float sum = 0.0f;
-            for (int g = 0; g < groups; ++g) sum += columns[which * kThreads + g * LANES + from];
+            for (int g = 0; g < groups; ++g) sum += columns[which * kBackwardThreads + g * LANES + of];
             if (at < p.dim) part[(which & 1) * p.dim + at] = sum;
         }
     } else {
@@ -338,8 +411,8 @@ __global__ void __launch_bounds__(LANES ? kThreads : 512) norm_backward_kernel(c
         for (int i = 0; i < CH * 8; ++i) {
             const int at = place<VEC>(i / 8, i % 8, t, G);
             if (at < p.dim) {
-                part[at] = dw[i];
-                part[p.dim + at] = db[i];
+                part[at] = i & 1 ? dw[i / 2].y : dw[i / 2].x;
+                part[p.dim + at] = i & 1 ? db[i / 2].y : db[i / 2].x;
             }
         }
     }
@@ -347,8 +420,8 @@ __global__ void __launch_bounds__(LANES ? kThreads : 512) norm_backward_kernel(c
 
 // Rows of any length, a CTA each, read twice: the gradient of x alone.
 template <typename T>
-__global__ void __launch_bounds__(1024) norm_backward_long_kernel(const __grid_constant__ NormParams p) {
-    __shared__ float shared[2][kMaxWarps];
+__global__ void __launch_bounds__(kLongThreads) norm_backward_long_kernel(const __grid_constant__ NormParams p) {
+    __shared__ float shared[2][kLongWarps];
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
     for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
@@ -374,10 +447,10 @@ __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const __grid_c
 
 // And the weight's and the bias's: a thread a column, a CTA 256 of them over every nparts-th row.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) norm_columns_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kColumns) norm_columns_kernel(const __grid_constant__ NormParams p) {
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
-    const int part = blockIdx.x % p.nparts, at = blockIdx.x / p.nparts * kThreads + threadIdx.x;
+    const int part = blockIdx.x % p.nparts, at = blockIdx.x / p.nparts * kColumns + threadIdx.x;
     if (at >= p.dim) return;
     float dw = 0.0f, db = 0.0f;
     for (long long row = part; row < p.rows; row += p.nparts) {
@@ -425,38 +498,51 @@ struct Split {
     int threads;     // of a CTA
 };
 
+// Lanes of a warp while they hold a row in 32 elements each, which needs no
+// barriers; then a CTA of up to 512 threads.
 Split forward_split(int dim) {
     const int eights = (dim + 7) / 8;
-    if (eights <= 8) return {8, 1, kThreads};
-    if (eights <= 32) return {32, 1, kThreads};
-    if (eights <= 64) return {32, 2, kThreads};
-    if (eights <= 128) return {32, 4, kThreads};
-    if (eights <= 4 * 1024) return {0, 4, round_up((eights + 3) / 4, 32)};
-    return {0, 0, 1024};
+    if (eights <= 8) return {8, 1, kForwardThreads};
+    if (eights <= 32) return {32, 1, kForwardThreads};
+    if (eights <= 64) return {32, 2, kForwardThreads};
+    if (eights <= 128) return {32, 4, kForwardThreads};
+    if (eights <= 4 * 32 * kMaxWarps) return {0, 4, round_up((eights + 3) / 4, 32)};
+    return {0, 0, kLongThreads};
 }
 
-Split backward_split(int dim) {
-    const int eights = (dim + 7) / 8;
-    if (eights <= 8) return {8, 1, kThreads};
-    if (eights <= 32) return {32, 1, kThreads};
-    if (eights <= 512) return {0, 1, round_up(eights, 32)};
-    return {0, 0, 1024};
+// The gradient holds 32 values of a round's rows and gradients each in bf16 and
+// 16 in fp32, so that a round takes as many bytes: chunks x rows is 4 or 2.
+Split backward_split(int dim, int size) {
+    const int eights = (dim + 7) / 8, most = 32 * kMaxWarps;
+    if (eights <= 8) return {8, 1, kBackwardThreads};
+    if (eights <= 32) return {32, 1, kBackwardThreads};
+    if (eights <= most) return {0, 1, round_up(eights, 32)};
+    if (eights <= 2 * most) return {0, 2, round_up((eights + 1) / 2, 32)};
+    if (eights <= 4 * most && size == 2) return {0, 4, round_up((eights + 3) / 4, 32)};
+    return {0, 0, kLongThreads};
 }
+
+int resident(int threads) { return kSms * (32 * kWarpsPerSm / threads > 1 ? 32 * kWarpsPerSm / threads : 1); }
 
 // CTAs of the gradient, each with a part of the weight's.
-int backward_parts(int dim, long long rows) {
-    const Split s = backward_split(dim);
-    const long long tile = s.chunks ? (s.lanes ? kThreads / s.lanes : 1) * kRows : kMinRows;
-    const long long most = s.chunks ? kMaxParts : 64, need = (rows + tile - 1) / tile;
+int backward_parts(int dim, int size, long long rows) {
+    const Split s = backward_split(dim, size);
+    const long long tile = s.chunks ? (s.lanes ? kBackwardThreads / s.lanes : 1) * (size == 2 ? 4 : 2) / s.chunks : 8;
+    const long long most = s.chunks ? resident(s.threads) : 64, need = (rows + tile - 1) / tile;
     return static_cast<int>(need < most ? need : most);
 }
 
 template <typename T, int LANES, int CH>
 cudaError_t forward_as(const Split& s, bool vec, const NormParams& p, cudaStream_t stream) {
-    const int groups = LANES ? kThreads / LANES : 1;
-    const long long need = (p.rows + groups - 1) / groups, most = static_cast<long long>(kSms) * 64;
-    return launch(vec ? norm_kernel<T, LANES, CH, true> : norm_kernel<T, LANES, CH, false>, need < most ? need : most,
-                  s.threads, 0, stream, p);
+    static std::atomic<uint64_t> allowed{0};
+    const int groups = LANES ? kForwardThreads / LANES : 1;
+    const long long need = (p.rows + groups - 1) / groups, most = resident(s.threads);
+    const size_t shared = vec ? static_cast<size_t>(kForwardStages<T>) * Slot<T, CH>::kBytes * s.threads : 0;
+    void (*const kernel)(NormParams) = vec ? norm_kernel<T, LANES, CH, true> : norm_kernel<T, LANES, CH, false>;
+    const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), shared, allowed);
+    // (rows that are not copied ahead overlap by having more CTAs wait)
+    const long long most_now = vec ? most : 16 * most;
+    return e != cudaSuccess ? e : launch(kernel, need < most_now ? need : most_now, s.threads, shared, stream, p);
 }
 
 template <typename T>
@@ -470,29 +556,36 @@ cudaError_t forward(bool vec, const NormParams& p, cudaStream_t stream) {
     return forward_as<T, 32, 4>(s, vec, p, stream);
 }
 
-template <typename T, int LANES>
+template <typename T, int LANES, int CH, int ROWS>
 cudaError_t backward_as(const Split& s, bool vec, const NormParams& p, cudaStream_t stream) {
-    return launch(vec ? norm_backward_kernel<T, LANES, 1, true> : norm_backward_kernel<T, LANES, 1, false>, p.nparts,
-                  s.threads, 0, stream, p);
+    static std::atomic<uint64_t> allowed{0};
+    static_assert(kBackwardStages * ROWS * 2 * Slot<T, CH>::kBytes >= 64, "16 columns of a thread");
+    const size_t shared = vec ? static_cast<size_t>(kBackwardStages) * ROWS * 2 * Slot<T, CH>::kBytes * s.threads : LANES ? 64 * s.threads : 0;
+    void (*const kernel)(NormParams) =
+        vec ? norm_backward_kernel<T, LANES, CH, ROWS, true> : norm_backward_kernel<T, LANES, CH, ROWS, false>;
+    const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), shared, allowed);
+    return e != cudaSuccess ? e : launch(kernel, p.nparts, s.threads, shared, stream, p);
 }
 
 template <typename T>
 cudaError_t backward(bool vec, const NormParams& p, cudaStream_t stream) {
-    const Split s = backward_split(p.dim);
-    if (s.chunks) {
-        const cudaError_t e = s.lanes == 8 ? backward_as<T, 8>(s, vec, p, stream)
-                                           : s.lanes ? backward_as<T, 32>(s, vec, p, stream) : backward_as<T, 0>(s, vec, p, stream);
-        if (e != cudaSuccess || !p.parts) return e;
+    constexpr int R = sizeof(T) == 2 ? 4 : 2;                // rows x chunks
+    const Split s = backward_split(p.dim, sizeof(T));
+    cudaError_t e = cudaSuccess;
+    if (s.chunks == 1)
+        e = s.lanes == 8 ? backward_as<T, 8, 1, R>(s, vec, p, stream)
+                         : s.lanes ? backward_as<T, 32, 1, R>(s, vec, p, stream) : backward_as<T, 0, 1, R>(s, vec, p, stream);
+    else if (s.chunks == 2)
+        e = backward_as<T, 0, 2, R / 2>(s, vec, p, stream);
+    else if (s.chunks == 4) {
+        if constexpr (R == 4) e = backward_as<T, 0, 4, 1>(s, vec, p, stream);
     } else {
-        if (p.out) {
-            const cudaError_t e = launch(norm_backward_long_kernel<T>, p.rows < kSms * 2 ? p.rows : kSms * 2, s.threads, 0, stream, p);
-            if (e != cudaSuccess) return e;
-        }
-        if (!p.parts) return cudaSuccess;
-        const cudaError_t e = launch(norm_columns_kernel<T>, static_cast<long long>(p.nparts) * ((p.dim + kThreads - 1) / kThreads),
-                                     kThreads, 0, stream, p);
-        if (e != cudaSuccess) return e;
+        if (p.out) e = launch(norm_backward_long_kernel<T>, p.rows < kSms * 2 ? p.rows : kSms * 2, s.threads, 0, stream, p);
+        if (e == cudaSuccess && p.parts)
+            e = launch(norm_columns_kernel<T>, static_cast<long long>(p.nparts) * ((p.dim + kColumns - 1) / kColumns), kColumns, 0,
+                       stream, p);
     }
+    if (e != cudaSuccess || !p.parts) return e;
     return launch(join_kernel, (2LL * p.dim + 31) / 32, 32 * kJoinLanes, 0, stream, p);
 }
 
@@ -531,7 +624,7 @@ int ddp_layer_norm(const ddp_layer_norm_args* a, const void* x, const void* weig
     p.bias = bias;
     p.out = y;
     p.stats = stats;
-    const bool vec = a->dim % 8 == 0 && aligned(x, 16) && aligned(y, 16) && aligned(weight, 16) && aligned(bias, 16) &&
+    const bool vec = a->dim % 8 == 0 && aligned(x, 16) && aligned(y, 16) &&
                      (a->rows == 1 || (a->x_stride * size % 16 == 0 && a->out_stride * size % 16 == 0));
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = a->dtype == DDP_F32 ? forward<float>(vec, p, st) : forward<uint16_t>(vec, p, st);
@@ -540,7 +633,7 @@ int ddp_layer_norm(const ddp_layer_norm_args* a, const void* x, const void* weig
 
 int64_t ddp_layer_norm_workspace(const ddp_layer_norm_args* a) {
     if (!valid(a)) return DDP_ERR_INVALID_ARG;
-    return a->rows == 0 ? 0 : 8LL * a->dim * backward_parts(static_cast<int>(a->dim), a->rows);
+    return a->rows == 0 ? 0 : 8LL * a->dim * backward_parts(static_cast<int>(a->dim), a->dtype == DDP_F32 ? 4 : 2, a->rows);
 }
 
 int ddp_layer_norm_backward(const ddp_layer_norm_args* a, const void* grad_y, int64_t grad_stride, const void* x,
@@ -571,8 +664,8 @@ int ddp_layer_norm_backward(const ddp_layer_norm_args* a, const void* grad_y, in
     p.grad_bias = grad_bias;
     p.accumulate = accumulate != 0;
     p.parts = params ? static_cast<float*>(workspace) : nullptr;
-    p.nparts = backward_parts(p.dim, p.rows);
-    const bool vec = a->dim % 8 == 0 && aligned(x, 16) && aligned(grad_y, 16) && aligned(grad_x, 16) && aligned(weight, 16) &&
+    p.nparts = backward_parts(p.dim, size, p.rows);
+    const bool vec = a->dim % 8 == 0 && aligned(x, 16) && aligned(grad_y, 16) && aligned(grad_x, 16) &&
                      (a->rows == 1 || (a->x_stride * size % 16 == 0 && a->out_stride * size % 16 == 0 && grad_stride * size % 16 == 0));
     const cudaError_t e = a->dtype == DDP_F32 ? backward<float>(vec, p, st) : backward<uint16_t>(vec, p, st);
     return e == cudaSuccess ? DDP_OK : DDP_ERR_CUDA;
