@@ -27,6 +27,7 @@ constexpr int kLongThreads = 1024;     // of one that reads it again and again
 constexpr int kLongWarps = kLongThreads / 32;
 constexpr int kColumns = 256;          // of a CTA of norm_columns_kernel
 constexpr int kJoinLanes = 32;         // join_kernel: threads of a column
+constexpr int kForwardWaves = 3;       // 65,536 x 1024 in bf16: one 50.1 us, two 46.3, three 44.7, four 45.8, six 52.7
 constexpr int kWarpsPerSm = 16;        // resident, at 128 registers
 // Rows of a group on their way, with the one under work (of 512 threads' fp32
 // rows more would not fit); and rounds of rows of the gradient.
@@ -175,15 +176,19 @@ __global__ void __launch_bounds__(LANES ? kForwardThreads : 32 * kMaxWarps) norm
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
     const long long stride = static_cast<long long>(gridDim.x) * groups, first = static_cast<long long>(blockIdx.x) * groups + group;
-    const T* const from = static_cast<const T*>(p.x);
     const auto slot = [&](int stage) { return Slot<T, CH>{ahead + stage * Slot<T, CH>::kPieces * blockDim.x + threadIdx.x}; };
-    const auto request = [&](long long row, int stage) {
-        if (row < p.rows) slot(stage).request(from + row * p.x_stride, t, G, p.dim);
+    const T* x_next = static_cast<const T*>(p.x) + first * p.x_stride;
+    T* out_next = static_cast<T*>(p.out) + first * p.out_stride;
+    long long asked = first;                                     // the row that is asked for next
+    const auto request = [&](int stage) {
+        if (asked < p.rows) slot(stage).request(x_next, t, G, p.dim);
         copy_commit();
+        asked += stride;
+        x_next += stride * p.x_stride;
     };
     if constexpr (VEC)
 #pragma unroll
-        for (int s = 0; s + 1 < kStages; ++s) request(first + s * stride, s);
+        for (int s = 0; s + 1 < kStages; ++s) request(s);
     float2 w[CH * 4], b[CH * 4];
     load_param<CH, VEC>(p.weight, p.param_bf16, 1.0f, t, G, p.dim, w);
     load_param<CH, VEC>(p.bias, p.param_bf16, 0.0f, t, G, p.dim, b);
@@ -196,10 +201,11 @@ __global__ void __launch_bounds__(LANES ? kForwardThreads : 32 * kMaxWarps) norm
             copy_wait<kStages - 2>();
             slot(stage).take(t, G, p.dim, x);
             // into the stage before this one, whose row has been used up
-            request(row + (kStages - 1) * stride, stage ? stage - 1 : kStages - 1);
+            request(stage ? stage - 1 : kStages - 1);
             stage = stage + 1 < kStages ? stage + 1 : 0;
         } else {
-            load_single<CH>(from + row * p.x_stride, on, t, G, p.dim, x);
+            load_single<CH>(x_next, on, t, G, p.dim, x);
+            x_next += stride * p.x_stride;
         }
         float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -222,7 +228,8 @@ __global__ void __launch_bounds__(LANES ? kForwardThreads : 32 * kMaxWarps) norm
         if (on && t == 0) *reinterpret_cast<float2*>(p.stats + 2 * row) = make_float2(mean, rstd);
 #pragma unroll
         for (int i = 0; i < CH * 4; ++i) x[i] = fma2(mul2(x[i], both(rstd)), w[i], b[i]);
-        if (on) store_row<CH, VEC>(static_cast<T*>(p.out) + row * p.out_stride, t, G, p.dim, x);
+        if (on) store_row<CH, VEC>(out_next, t, G, p.dim, x);
+        out_next += stride * p.out_stride;
     }
 }
 
@@ -286,8 +293,8 @@ __device__ __forceinline__ int lane_of(int i) { return i * (32 / N); }
 // dx = r (g - mean(g) - xh mean(g xh)), g = dy w, xh = (x - mean) r; dw = sum dy xh
 // and db = sum dy over the CTA's rows, a thread its columns.  A round is ROWS rows
 // of each group, so that a barrier serves as many.
-template <typename T, int LANES, int CH, int ROWS, bool VEC>
-__global__ void __launch_bounds__(LANES ? kBackwardThreads : 32 * kMaxWarps) norm_backward_kernel(const __grid_constant__ NormParams p) {
+template <typename T, int LANES, int CH, int ROWS, bool VEC, int MAXT>
+__global__ void __launch_bounds__(MAXT, 32 * kWarpsPerSm / MAXT) norm_backward_kernel(const __grid_constant__ NormParams p) {
     constexpr int N = 2 * ROWS;
     extern __shared__ uint4 ahead[];
     __shared__ float shared[2][kMaxWarps][N];
@@ -298,25 +305,33 @@ __global__ void __launch_bounds__(LANES ? kBackwardThreads : 32 * kMaxWarps) nor
     ddpk::dev::pdl_trigger();
     const int tile = groups * ROWS;
     const long long first = static_cast<long long>(blockIdx.x) * tile, stride = static_cast<long long>(gridDim.x) * tile;
-    const T* const from_x = static_cast<const T*>(p.x);
-    const T* const from_dy = static_cast<const T*>(p.grad);
     const auto slot = [&](int stage, int r, int which) {
         return Slot<T, CH>{ahead + ((stage * ROWS + r) * 2 + which) * Slot<T, CH>::kPieces * blockDim.x + threadIdx.x};
     };
-    const auto request = [&](long long r0, int stage) {
+    // of this thread's first row of a round: how many rows are left from it on, and where it is
+    const auto left_of = [&](long long r0) { return static_cast<int>(min(p.rows - r0 - group, 1LL << 30)); };
+    const long long x_step = groups * p.x_stride, dy_step = groups * p.grad_stride, out_step = groups * p.out_stride;
+    const T* x_next = static_cast<const T*>(p.x) + (first + group) * p.x_stride;
+    const T* dy_next = static_cast<const T*>(p.grad) + (first + group) * p.grad_stride;
+    T* out_next = static_cast<T*>(p.out) + (first + group) * p.out_stride;
+    const float2* stat_next = reinterpret_cast<const float2*>(p.stats) + first + group;
+    long long asked = first;                                     // of the round that is asked for next
+    const auto request = [&](int stage) {
+        const int left = left_of(asked);
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            const long long row = r0 + r * groups + group;
-            if (row < p.rows) {
-                slot(stage, r, 0).request(from_x + row * p.x_stride, t, G, p.dim);
-                slot(stage, r, 1).request(from_dy + row * p.grad_stride, t, G, p.dim);
+        for (int r = 0; r < ROWS; ++r)
+            if (r * groups < left) {
+                slot(stage, r, 0).request(x_next + r * x_step, t, G, p.dim);
+                slot(stage, r, 1).request(dy_next + r * dy_step, t, G, p.dim);
             }
-        }
         copy_commit();
+        asked += stride;
+        x_next += stride * p.x_stride;
+        dy_next += stride * p.grad_stride;
     };
     if constexpr (VEC)
 #pragma unroll
-        for (int s = 0; s + 1 < kBackwardStages; ++s) request(first + s * stride, s);
+        for (int s = 0; s + 1 < kBackwardStages; ++s) request(s);
     float2 dw[CH * 4], db[CH * 4], w[CH * 4];
     load_param<CH, VEC>(p.weight, p.param_bf16, 1.0f, t, G, p.dim, w);
 #pragma unroll
@@ -326,29 +341,32 @@ __global__ void __launch_bounds__(LANES ? kBackwardThreads : 32 * kMaxWarps) nor
     for (long long r0 = first; r0 < p.rows; r0 += stride) {
         float2 x[ROWS][CH * 4], dy[ROWS][CH * 4], stat[ROWS];
         float sums[N];
+        const int left = left_of(r0);
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            const long long row = r0 + r * groups + group;
-            stat[r] = row < p.rows ? *reinterpret_cast<const float2*>(p.stats + 2 * row) : make_float2(0.0f, 0.0f);
-        }
+        for (int r = 0; r < ROWS; ++r) stat[r] = r * groups < left ? stat_next[r * groups] : make_float2(0.0f, 0.0f);
         if constexpr (VEC) copy_wait<kBackwardStages - 2>();
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-            const long long row = r0 + r * groups + group;
-            const bool on = row < p.rows;
+            const bool on = r * groups < left;
             if constexpr (VEC) {
                 const int dim = on ? p.dim : 0;                  // (zeros)
                 slot(stage, r, 0).take(t, G, dim, x[r]);
                 slot(stage, r, 1).take(t, G, dim, dy[r]);
             } else {
-                load_single<CH>(from_x + row * p.x_stride, on, t, G, p.dim, x[r]);
-                load_single<CH>(from_dy + row * p.grad_stride, on, t, G, p.dim, dy[r]);
+                load_single<CH>(x_next + r * x_step, on, t, G, p.dim, x[r]);
+                load_single<CH>(dy_next + r * dy_step, on, t, G, p.dim, dy[r]);
             }
         }
         if constexpr (VEC) {
-            request(r0 + (kBackwardStages - 1) * stride, stage ? stage - 1 : kBackwardStages - 1);   // used up a round ago
+            request(stage ? stage - 1 : kBackwardStages - 1);    // used up a round ago
             stage = stage + 1 < kBackwardStages ? stage + 1 : 0;
+        } else {
+            x_next += stride * p.x_stride;
+            dy_next += stride * p.grad_stride;
         }
+        stat_next += stride;
+        if (t < ROWS && t * groups < left_of(r0 + stride))       // near by the time that they are loaded
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(stat_next + t * groups));
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
             float2 a = make_float2(0.0f, 0.0f), b = a;
@@ -381,12 +399,12 @@ __global__ void __launch_bounds__(LANES ? kBackwardThreads : 32 * kMaxWarps) nor
         if (!p.out) continue;
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-            const long long row = r0 + r * groups + group;
             const float2 a = both(-sums[2 * r] * over), b = both(-sums[2 * r + 1] * over);
 #pragma unroll
             for (int i = 0; i < CH * 4; ++i) x[r][i] = mul2(both(stat[r].y), fma2(x[r][i], b, add2(dy[r][i], a)));
-            if (row < p.rows) store_row<CH, VEC>(static_cast<T*>(p.out) + row * p.out_stride, t, G, p.dim, x[r]);
+            if (r * groups < left) store_row<CH, VEC>(out_next + r * out_step, t, G, p.dim, x[r]);
         }
+        out_next += stride * p.out_stride;
     }
     if (!p.parts) return;
     float* const part = p.parts + static_cast<long long>(blockIdx.x) * 2 * p.dim;
@@ -536,7 +554,7 @@ template <typename T, int LANES, int CH>
 cudaError_t forward_as(const Split& s, bool vec, const NormParams& p, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed{0};
     const int groups = LANES ? kForwardThreads / LANES : 1;
-    const long long need = (p.rows + groups - 1) / groups, most = resident(s.threads);
+    const long long need = (p.rows + groups - 1) / groups, most = kForwardWaves * resident(s.threads);
     const size_t shared = vec ? static_cast<size_t>(kForwardStages<T>) * Slot<T, CH>::kBytes * s.threads : 0;
     void (*const kernel)(NormParams) = vec ? norm_kernel<T, LANES, CH, true> : norm_kernel<T, LANES, CH, false>;
     const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), shared, allowed);
@@ -556,13 +574,13 @@ cudaError_t forward(bool vec, const NormParams& p, cudaStream_t stream) {
     return forward_as<T, 32, 4>(s, vec, p, stream);
 }
 
-template <typename T, int LANES, int CH, int ROWS>
+template <typename T, int LANES, int CH, int ROWS, int MAXT>
 cudaError_t backward_as(const Split& s, bool vec, const NormParams& p, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed{0};
     static_assert(kBackwardStages * ROWS * 2 * Slot<T, CH>::kBytes >= 64, "16 columns of a thread");
     const size_t shared = vec ? static_cast<size_t>(kBackwardStages) * ROWS * 2 * Slot<T, CH>::kBytes * s.threads : LANES ? 64 * s.threads : 0;
     void (*const kernel)(NormParams) =
-        vec ? norm_backward_kernel<T, LANES, CH, ROWS, true> : norm_backward_kernel<T, LANES, CH, ROWS, false>;
+        vec ? norm_backward_kernel<T, LANES, CH, ROWS, true, MAXT> : norm_backward_kernel<T, LANES, CH, ROWS, false, MAXT>;
     const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), shared, allowed);
     return e != cudaSuccess ? e : launch(kernel, p.nparts, s.threads, shared, stream, p);
 }
@@ -573,12 +591,12 @@ cudaError_t backward(bool vec, const NormParams& p, cudaStream_t stream) {
     const Split s = backward_split(p.dim, sizeof(T));
     cudaError_t e = cudaSuccess;
     if (s.chunks == 1)
-        e = s.lanes == 8 ? backward_as<T, 8, 1, R>(s, vec, p, stream)
-                         : s.lanes ? backward_as<T, 32, 1, R>(s, vec, p, stream) : backward_as<T, 0, 1, R>(s, vec, p, stream);
-    else if (s.chunks == 2)
-        e = backward_as<T, 0, 2, R / 2>(s, vec, p, stream);
-    else if (s.chunks == 4) {
-        if constexpr (R == 4) e = backward_as<T, 0, 4, 1>(s, vec, p, stream);
+        e = s.lanes == 8 ? backward_as<T, 8, 1, R, 256>(s, vec, p, stream)
+                         : s.lanes ? backward_as<T, 32, 1, R, 256>(s, vec, p, stream) : s.threads <= 128 ? backward_as<T, 0, 1, R, 128>(s, vec, p, stream) : backward_as<T, 0, 1, R, 512>(s, vec, p, stream);
+    else if (s.chunks == 2) {
+        if constexpr (R >= 2) e = backward_as<T, 0, 2, R / 2, 512>(s, vec, p, stream);
+    } else if (s.chunks == 4) {
+        if constexpr (R == 4) e = backward_as<T, 0, 4, 1, 512>(s, vec, p, stream);
     } else {
         if (p.out) e = launch(norm_backward_long_kernel<T>, p.rows < kSms * 2 ? p.rows : kSms * 2, s.threads, 0, stream, p);
         if (e == cudaSuccess && p.parts)
