@@ -4,8 +4,8 @@
 // The gradient sorts the tokens first (a stable radix sort, so that equal tokens
 // keep their order), and each row of the table then sums its tokens' gradients
 // one after another: equal inputs give equal bits, and a row's sum does not depend
-// on the other tokens'.  Tokens that fall often are summed in parts of kLong (or
-// more) rows by a CTA each, and whoever ends last adds the parts in their order.
+// on the other tokens'.  A word that falls often is summed in parts of kPart
+// tokens, and whoever ends last adds the parts (groups of them) in their order.
 
 #include "ddp_reducer.h"
 
@@ -28,9 +28,12 @@ constexpr int kMaxBins = 1 << kMaxBits;
 constexpr int kItems = 8;              // of a thread in a tile of the sort
 constexpr int kTile = kThreads * kItems;
 constexpr int kMaxSortCtas = 128;
-constexpr int kLong = 64;              // tokens of a part, at least
-constexpr int kMaxParts = 512;         // of one row, at most
+constexpr int kSmall = 8192;           // tokens that are sorted by counting
+constexpr int kRankLanes = 8;
+constexpr int kPart = 64;              // sorted places of a CTA, and tokens that are summed in one go
+constexpr int kGroup = 64;             // parts of a row that are added up in one go
 constexpr int kUnroll = 8;             // rows on their way at once
+constexpr int kFillBytes = 64 * 1024;  // of the rows that a CTA looks at for empty ones
 
 struct EmbedParams {
     const void* table;
@@ -51,7 +54,7 @@ struct SortParams {
     int* places;
     int* counts;             // [ctas][bins]
     int* tickets;            // zeroed by the first pass
-    long long ntickets;
+    long long ntickets;      // a multiple of four
     long long n, vocab, share;     // share: tokens of a CTA, a multiple of kTile
     int wide, ctas, shift, bits;
 };
@@ -63,8 +66,8 @@ struct SumParams {
     void* out;
     float* parts;
     int* tickets;
-    long long n, vocab, grad_stride, out_stride, windows;
-    int dim, long_row, rows, row_threads;      // long_row: tokens of a part; rows: of the table, of a CTA
+    long long n, vocab, grad_stride, out_stride, windows, tickets_each;
+    int dim, rows, row_threads;                // rows: of the table, of a CTA
     int accumulate;
     float scale;
 };
@@ -144,9 +147,9 @@ __global__ void __launch_bounds__(kThreads) sort_count_kernel(const __grid_const
     for (int b = threadIdx.x; b < nbins; b += kThreads) bins[b] = 0;
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
-    for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < p.ntickets;
+    for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < p.ntickets / 4;
          i += static_cast<long long>(gridDim.x) * kThreads)
-        p.tickets[i] = 0;
+        reinterpret_cast<int4*>(p.tickets)[i] = make_int4(0, 0, 0, 0);
     __syncthreads();
     const long long from = blockIdx.x * p.share, to = min(p.n, from + p.share);
 #pragma unroll 4
@@ -233,6 +236,40 @@ __global__ void __launch_bounds__(kThreads) sort_move_kernel(const __grid_consta
     }
 }
 
+// Few tokens: each one's place is the number of smaller ones and of equal ones
+// before it, counted against all of them by kRankLanes lanes, each with every
+// kRankLanes-th four.  4,096 tokens are a million warp instructions, spread over
+// all SMs in one launch.
+__global__ void __launch_bounds__(kThreads) sort_small_kernel(const __grid_constant__ SortParams p) {
+    extern __shared__ int4 all[];
+    const int n = static_cast<int>(p.n), fours = (n + 3) / 4;
+    ddpk::dev::pdl_wait();
+    ddpk::dev::pdl_trigger();
+    for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < p.ntickets / 4;
+         i += static_cast<long long>(gridDim.x) * kThreads)
+        reinterpret_cast<int4*>(p.tickets)[i] = make_int4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int i = threadIdx.x; i < 4 * fours; i += kThreads) reinterpret_cast<int*>(all)[i] = i < n ? key_at(p, i) : INT32_MAX;
+    __syncthreads();
+    const int i = blockIdx.x * (kThreads / kRankLanes) + threadIdx.x / kRankLanes, lane = threadIdx.x % kRankLanes;
+    const int key = i < n ? reinterpret_cast<const int*>(all)[i] : 0, mine = i / 4;
+    int rank = 0;
+#pragma unroll 4
+    for (int c = lane; c < fours; c += kRankLanes) {
+        const int4 x = all[c];
+        const int least = key + (c < mine);                  // equal ones count before this token's four
+        rank += (x.x < least) + (x.y < least) + (x.z < least) + (x.w < least);
+    }
+    if (lane == mine % kRankLanes && i < n)                  // and within it
+        for (int j = 4 * mine; j < i; ++j) rank += reinterpret_cast<const int*>(all)[j] == key;
+#pragma unroll
+    for (int o = kRankLanes / 2; o; o /= 2) rank += __shfl_xor_sync(kAll, rank, o);
+    if (lane == 0 && i < n) {
+        p.keys[rank] = key;
+        p.places[rank] = i;
+    }
+}
+
 // ---------------------------------------------------------------- sums
 
 // How many of the n sorted keys are below `key`, of which those before lo are
@@ -241,7 +278,7 @@ __device__ __forceinline__ long long warp_lower_bound(const int* keys, long long
     const int lane = threadIdx.x & 31;
     while (hi > lo) {
         const long long step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step - 1;
-        const bool below = at < hi && keys[at] < key;
+        const bool below = at < hi && __ldcg(keys + at) < key;
         const int n = __popc(__ballot_sync(kAll, below));       // steps that lie below: the keys are sorted
         lo += n * step;
         hi = min(hi, lo + step - 1);
@@ -253,157 +290,243 @@ __device__ __forceinline__ long long warp_lower_bound(const int* keys, long long
 __device__ __forceinline__ long long lower_bound(const int* keys, long long lo, long long hi, long long key) {
     while (hi > lo) {
         const long long mid = (lo + hi) / 2;
-        if (keys[mid] < key) lo = mid + 1;
+        if (__ldcg(keys + mid) < key) lo = mid + 1;
         else hi = mid;
     }
     return lo;
 }
 
-// The gradients at sorted places [lo, hi), columns from `at` on.
-template <typename T, bool VEC>
-__device__ __forceinline__ void sum_rows(const SumParams& p, long long lo, long long hi, int at, float (&sum)[VEC ? 8 : 1]) {
+// A row of the table's gradient, columns from `at` on.  What is added to is not
+// waited for: one addition for each element, so no order is left open.
+template <typename Tout, bool VEC>
+__device__ __forceinline__ void put_row(const SumParams& p, long long row, int at, const float (&sum)[VEC ? 8 : 1]) {
+    Tout* const to = static_cast<Tout*>(p.out) + row * p.out_stride + at;
+    float f[VEC ? 8 : 1];
+#pragma unroll
+    for (int j = 0; j < (VEC ? 8 : 1); ++j) f[j] = sum[j] * p.scale;
+    if constexpr (sizeof(Tout) == 4) {
+        if (p.accumulate) {
+            if constexpr (VEC) {
+#pragma unroll
+                for (int j = 0; j < 8; j += 4)
+                    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(to + j), "f"(f[j]), "f"(f[j + 1]),
+                                 "f"(f[j + 2]), "f"(f[j + 3]) : "memory");
+            } else {
+                asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(to), "f"(f[0]) : "memory");
+            }
+            return;
+        }
+    }
+    if constexpr (VEC) {
+        Eight<Tout> raw;
+        raw.put(f);
+        raw.store_once(to);
+    } else {
+        *to = narrow<Tout>(f[0]);
+    }
+}
+
+// A part of a row of more than kPart tokens: part m of those that begin at sorted
+// place `start` and end before `end`.  A CTA's window of kPart places holds at most
+// two beginnings of parts, of which one is its row's first.
+struct Parts {
+    long long start, end;
+
+    __device__ __forceinline__ int count() const { return static_cast<int>((end - start + kPart - 1) / kPart); }
+    __device__ __forceinline__ long long slot(int m) const { return (start + static_cast<long long>(m) * kPart) / kPart * 2 + (m == 0); }
+};
+
+// One thread's columns of part m are summed: keeps them, and, where this thread
+// is the last of a group of parts (and its group the row's last), adds up the
+// group's (and the groups') in their order and gives the whole in `sum`.
+template <int N>
+__device__ __forceinline__ bool join_parts(const SumParams& p, const Parts& of, int m, int at, float (&sum)[N]) {
+    const auto put = [&](int part) {
+        float* const to = p.parts + of.slot(part) * p.dim + at;
+#pragma unroll
+        for (int j = 0; j < N; ++j) __stcg(to + j, sum[j]);
+        __threadfence();
+    };
+    const auto add = [&](int from, int to, int step) {
+        __threadfence();
+#pragma unroll
+        for (int j = 0; j < N; ++j) sum[j] = 0.0f;
+#pragma unroll 8
+        for (int q = from; q < to; q += step) {
+            const float* const x = p.parts + of.slot(q) * p.dim + at;
+#pragma unroll
+            for (int j = 0; j < N; ++j) sum[j] += __ldcg(x + j);
+        }
+    };
+    const int count = of.count(), group = m / kGroup * kGroup, end = min(count, group + kGroup);
+    const long long columns = (p.dim + N - 1) / N, column = at / N;
+    put(m);
+    if (atomicAdd(p.tickets + of.slot(group) * columns + column, 1) != end - group - 1) return false;
+    add(group, end, 1);
+    if (count <= kGroup) return true;
+    put(group);
+    if (atomicAdd(p.tickets + p.tickets_each + of.slot(0) * columns + column, 1) != (count + kGroup - 1) / kGroup - 1) return false;
+    add(0, count, kGroup);
+    return true;
+}
+
+// A CTA sums the tokens of a window of kPart sorted places: a run of rows and
+// parts of rows that begin in the window, one after another, with the next ones'
+// gradients on their way.
+template <typename T, typename Tout, bool VEC>
+__global__ void __launch_bounds__(kThreads) embed_sum_kernel(const __grid_constant__ SumParams p) {
     constexpr int N = VEC ? 8 : 1;
+    __shared__ int keys[2 * kPart + 1];            // from the place before the window's first on
+    __shared__ int places[2 * kPart];
+    __shared__ uint32_t begins[2 * kPart / 32];    // bit q: a row, or a part of one, begins at the window's place q
+    __shared__ int valid;                          // places that hold a token of the table
+    __shared__ long long of_first[2], of_last[2];           // the rows at the window's ends, where they are long
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int t = threadIdx.x % p.row_threads, slot = threadIdx.x / p.row_threads, slots = blockDim.x / p.row_threads;
+    ddpk::dev::pdl_wait();
+    ddpk::dev::pdl_trigger();
+    const long long w0 = static_cast<long long>(blockIdx.x) * kPart;
+    for (int i = threadIdx.x; i <= 2 * kPart; i += blockDim.x) {
+        const long long at = w0 - 1 + i;
+        keys[i] = at < 0 ? -1 : at < p.n ? p.keys[at] : INT32_MAX;
+        if (i) places[i - 1] = at < p.n ? p.places[at] : 0;
+    }
+    __syncthreads();
+    const int first = keys[1], last = keys[kPart];
+    if (warp == 0) {
+        const bool goes_on = keys[0] == first, is_long = goes_on || keys[kPart + 1] == first;
+        if (is_long && first < p.vocab) {
+            const long long start = goes_on ? warp_lower_bound(p.keys, 0, w0, first) : w0;
+            const long long end = warp_lower_bound(p.keys, w0, p.n, first + 1LL);
+            if (lane == 0) { of_first[0] = start; of_first[1] = end; }
+            __syncwarp();
+        }
+        const long long start = goes_on && first < p.vocab ? of_first[0] : w0;
+        uint32_t rows[2 * kPart / 32];
+        int count = 0;
+#pragma unroll
+        for (int w = 0; w < 2 * kPart / 32; ++w) {
+            const int q = 32 * w + lane;
+            rows[w] = __ballot_sync(kAll, keys[q + 1] != keys[q]);
+            count += __popc(__ballot_sync(kAll, keys[q + 1] < p.vocab));
+            long long from = start;                      // where this place's row begins
+#pragma unroll
+            for (int v = 0; v <= w; ++v) {
+                const uint32_t up_to = v < w ? rows[v] : rows[v] & (0xffffffffu >> (31 - lane));
+                if (up_to) from = w0 + 32 * v + 31 - __clz(up_to);
+            }
+            const uint32_t b = __ballot_sync(kAll, (w0 + q - from) % kPart == 0);
+            if (lane == 0) begins[w] = b;
+        }
+        if (lane == 0) valid = count;
+    } else if (warp == 1 && last != first && keys[kPart + 1] == last && last < p.vocab) {
+        int from = kPart;                                // of a row that begins in the window and goes on behind it
+        while (keys[from - 1] == last) --from;
+        const long long end = warp_lower_bound(p.keys, w0 + kPart, p.n, last + 1LL);
+        if (lane == 0) { of_last[0] = w0 + from - 1; of_last[1] = end; }
+    }
+    __syncthreads();
+    const int each = kPart / slots, a = slot * each, b = a + each;
+    const auto next_begin = [&](int q) {                 // the first beginning at q or behind it
+        for (int w = q / 32; w < 2 * kPart / 32; ++w) {
+            const uint32_t bits = begins[w] & (w == q / 32 ? 0xffffffffu << (q % 32) : 0xffffffffu);
+            if (bits) return 32 * w + __ffs(bits) - 1;
+        }
+        return 2 * kPart;
+    };
+    const int i0 = next_begin(a), i1 = min(next_begin(b), valid);
+    if (i0 >= min(b, valid)) return;
     const T* const grad = static_cast<const T*>(p.grad);
+    for (int at = t * N; at < p.dim; at += p.row_threads * N) {
+        float sum[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) sum[j] = 0.0f;
-    for (long long i = lo; i < hi; i += kUnroll) {
-        if constexpr (VEC) {
-            Eight<T> raw[kUnroll];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
-                if (i + u < hi) raw[u].load_once(grad + static_cast<long long>(p.places[i + u]) * p.grad_stride + at);
+        for (int j = 0; j < N; ++j) sum[j] = 0.0f;
+        int begin = i0;
+        for (int i = i0; i < i1; i += kUnroll) {
+            Eight<T> raw[VEC ? kUnroll : 1];
+            float single[VEC ? 1 : kUnroll];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                if (i + u < hi) {
+                const T* const from = grad + static_cast<long long>(i + u < i1 ? places[i + u] : 0) * p.grad_stride + at;
+                if constexpr (VEC) {
+                    if (i + u < i1) raw[u].load_once(from);
+                } else {
+                    single[u] = i + u < i1 ? widen(*from) : 0.0f;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int q = i + u + 1;
+                if (q > i1) break;
+                if constexpr (VEC) {
                     float f[8];
                     raw[u].get(f);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) sum[j] += f[j];
+                } else {
+                    sum[0] += single[u];
                 }
+                if (q < i1 && !(begins[q / 32] >> (q % 32) & 1)) continue;
+                // a row ends here, or a part of one that is long
+                const int key = keys[q];
+                bool whole = true;
+                if (keys[q + 1] == key || keys[begin] == key) {
+                    const Parts of = key == first ? Parts{of_first[0], of_first[1]} : Parts{of_last[0], of_last[1]};
+                    whole = join_parts<N>(p, of, static_cast<int>((w0 + begin - of.start) / kPart), at, sum);
+                }
+                if (whole) put_row<Tout, VEC>(p, key, at, sum);
+#pragma unroll
+                for (int j = 0; j < N; ++j) sum[j] = 0.0f;
+                begin = q;
             }
-        } else {
-            float f[kUnroll];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
-                f[u] = i + u < hi ? widen(grad[static_cast<long long>(p.places[i + u]) * p.grad_stride + at]) : 0.0f;
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) sum[0] += f[u];
         }
     }
 }
 
-// A row of the table's gradient, columns from `at` on.
-template <typename Tout, bool VEC>
-__device__ __forceinline__ void put_row(const SumParams& p, long long row, int at, const float (&sum)[VEC ? 8 : 1]) {
-    Tout* const to = static_cast<Tout*>(p.out) + row * p.out_stride + at;
-    if constexpr (VEC) {
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = sum[j] * p.scale;
-        Eight<Tout> raw;
-        if (p.accumulate) {
-            float old[8];
-            raw.load_once(to);
-            raw.get(old);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] += old[j];
-        }
-        raw.put(f);
-        raw.store_once(to);
-    } else {
-        *to = narrow<Tout>(p.accumulate ? widen(*to) + sum[0] * p.scale : sum[0] * p.scale);
-    }
-}
-
-// The first `windows` CTAs look for long rows: each takes the parts that begin in
-// its window of long_row sorted places (at most one that is its row's first, and
-// one that is not: a part's slot is 2 window + (first)).  The others take `rows`
-// rows of the table each, but the long ones.
-template <typename T, typename Tout, bool VEC>
-__global__ void __launch_bounds__(kThreads) embed_sum_kernel(const __grid_constant__ SumParams p) {
-    constexpr int N = VEC ? 8 : 1;
-    __shared__ long long bounds[4];
-    __shared__ long long starts[kThreads + 1];
-    __shared__ int last;
-    const int warp = threadIdx.x >> 5;
-    ddpk::dev::pdl_wait();
-    ddpk::dev::pdl_trigger();
-    if (blockIdx.x < p.windows) {
-        // a long row that begins behind the window's start reaches past its end, so the
-        // rows at both ends are all that can have a part here
-        const long long w0 = static_cast<long long>(blockIdx.x) * p.long_row, w1 = w0 + p.long_row;
-        const int key0 = p.keys[w0], key1 = w1 < p.n ? p.keys[w1] : key0;
-        if (warp < 4) {
-            const long long at = warp < 2 ? w0 : min(w1, p.n - 1), key = warp < 2 ? key0 : key1;
-            const long long x = warp_lower_bound(p.keys, warp & 1 ? at : 0, warp & 1 ? p.n : at, key + (warp & 1));
-            if ((threadIdx.x & 31) == 0) bounds[warp] = x;
-        }
-        __syncthreads();
-        for (int which = 0; which < 2; ++which) {
-            const int key = which ? key1 : key0;
-            if (key >= p.vocab || (which && key1 == key0)) break;
-            const long long start = bounds[2 * which], end = bounds[2 * which + 1], count = end - start;
-            const long long part = start > w0 ? 0 : (w0 - start + p.long_row - 1) / p.long_row, from = start + part * p.long_row;
-            if (count <= p.long_row || from >= min(w1, end)) continue;
-            const long long to = min(end, from + p.long_row), nparts = (count + p.long_row - 1) / p.long_row;
-            float* const mine = p.parts + (2LL * blockIdx.x + (part == 0)) * p.dim;
-            for (int at = threadIdx.x * N; at < p.dim; at += kThreads * N) {
-                float sum[N];
-                sum_rows<T, VEC>(p, from, to, at, sum);
-#pragma unroll
-                for (int j = 0; j < N; ++j) __stcg(mine + at + j, sum[j]);
-            }
-            __threadfence();
-            __syncthreads();
-            if (threadIdx.x == 0) last = atomicAdd(p.tickets + start / p.long_row, 1) == nparts - 1;
-            __syncthreads();
-            if (last) {
-                __threadfence();
-                for (int at = threadIdx.x * N; at < p.dim; at += kThreads * N) {
-                    float sum[N] = {};
-                    for (long long q = 0; q < nparts; ++q) {
-                        const long long window = (start + q * p.long_row) / p.long_row;
-                        const float* const from_part = p.parts + (2 * window + (q == 0)) * p.dim + at;
-#pragma unroll
-                        for (int j = 0; j < N; ++j) sum[j] += __ldcg(from_part + j);
-                    }
-                    put_row<Tout, VEC>(p, key, at, sum);
-                }
-            }
-            __syncthreads();
-        }
-        return;
-    }
-    const long long v0 = static_cast<long long>(blockIdx.x - p.windows) * p.rows, v1 = min(p.vocab, v0 + p.rows);
+// Zeros into the rows of the table that have no token, `rows` of them a CTA.  It
+// needs the sorted keys alone, which were there before the sums' kernel let it
+// start, so it runs beside that one and waits for it only before it ends.
+template <typename Tout>
+__global__ void __launch_bounds__(kThreads) embed_fill_kernel(const __grid_constant__ SumParams p) {
+    __shared__ long long bounds[2];
+    __shared__ int starts[kThreads + 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long v0 = static_cast<long long>(blockIdx.x) * p.rows, v1 = min(p.vocab, v0 + p.rows);
     if (warp < 2) {
         const long long x = warp_lower_bound(p.keys, 0, p.n, warp ? v1 : v0);
-        if ((threadIdx.x & 31) == 0) bounds[warp] = x;
+        if (lane == 0) bounds[warp] = x;
     }
     __syncthreads();
-    for (int r = threadIdx.x; r <= v1 - v0; r += kThreads) starts[r] = lower_bound(p.keys, bounds[0], bounds[1], v0 + r);
+    for (int r = threadIdx.x; r <= v1 - v0; r += kThreads)
+        starts[r] = static_cast<int>(lower_bound(p.keys, bounds[0], bounds[1], v0 + r));
     __syncthreads();
     const int t = threadIdx.x % p.row_threads, slot = threadIdx.x / p.row_threads, slots = kThreads / p.row_threads;
     for (int r = slot; r < v1 - v0; r += slots) {
-        const long long lo = starts[r], hi = starts[r + 1];
-        if (hi - lo > p.long_row || (lo == hi && p.accumulate)) continue;
-        for (int at = t * N; at < p.dim; at += p.row_threads * N) {
-            float sum[N];
-            sum_rows<T, VEC>(p, lo, hi, at, sum);
-            put_row<Tout, VEC>(p, v0 + r, at, sum);
-        }
+        if (starts[r] != starts[r + 1]) continue;
+        Tout* const to = static_cast<Tout*>(p.out) + (v0 + r) * p.out_stride;
+        // a few elements up to a 16-byte boundary, 16 bytes at a time, the rest
+        const int head = min(p.dim, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(to) & 15)) % 16 / sizeof(Tout)));
+        constexpr int kEach = 16 / sizeof(Tout);
+        const int pieces = (p.dim - head) / kEach;
+        for (int i = t; i < pieces; i += p.row_threads) __stcs(reinterpret_cast<uint4*>(to + head) + i, make_uint4(0, 0, 0, 0));
+        for (int i = t; i < p.dim - pieces * kEach; i += p.row_threads)
+            to[i < head ? i : i + pieces * kEach] = narrow<Tout>(0.0f);
     }
+    ddpk::dev::pdl_wait();
+    ddpk::dev::pdl_trigger();
 }
 
 // ---------------------------------------------------------------- host
 
 struct Plan {
-    int sort_ctas, passes, bits, long_row;
+    int sort_ctas, passes, bits;
     long long share, windows;
     int64_t keys, places, counts, parts, tickets, bytes;      // offsets into the workspace; two of the first two
 };
 
 int64_t up(int64_t x) { return (x + 255) / 256 * 256; }
 
+// The same whatever the alignment: tickets for columns one by one.
 Plan plan_of(const ddp_embed_args* a) {
     Plan q = {};
     const int64_t n = a->tokens;
@@ -414,9 +537,7 @@ Plan plan_of(const ddp_embed_args* a) {
     const int64_t tiles = (n + kTile - 1) / kTile, each = (tiles + kMaxSortCtas - 1) / kMaxSortCtas;
     q.share = each * kTile;
     q.sort_ctas = static_cast<int>((n + q.share - 1) / q.share);
-    q.long_row = kLong;
-    while (static_cast<int64_t>(q.long_row) * kMaxParts < n) q.long_row *= 2;
-    q.windows = (n + q.long_row - 1) / q.long_row;
+    q.windows = (n + kPart - 1) / kPart;
     int64_t at = 0;
     q.keys = at;
     at += 2 * up(4 * n);
@@ -425,7 +546,7 @@ Plan plan_of(const ddp_embed_args* a) {
     q.counts = at;
     at += up(4LL * kMaxBins * q.sort_ctas);
     q.tickets = at;
-    at += up(4 * q.windows);
+    at += 2 * up(4 * (2 * q.windows * a->dim + 4));
     q.parts = at;
     at += up(8 * q.windows * a->dim);
     q.bytes = at;
@@ -458,8 +579,8 @@ cudaError_t embed_as(bool vec, long long ctas, const EmbedParams& p, cudaStream_
 }
 
 template <typename T, typename Tout>
-cudaError_t sum_as(bool vec, long long ctas, const SumParams& p, cudaStream_t stream) {
-    return launch(vec ? embed_sum_kernel<T, Tout, true> : embed_sum_kernel<T, Tout, false>, ctas, kThreads, 0, stream, p);
+cudaError_t sum_as(bool vec, int threads, const SumParams& p, cudaStream_t stream) {
+    return launch(vec ? embed_sum_kernel<T, Tout, true> : embed_sum_kernel<T, Tout, false>, p.windows, threads, 0, stream, p);
 }
 
 }  // namespace
@@ -517,6 +638,7 @@ int ddp_embed_backward(const ddp_embed_args* a, const void* grad, const void* to
     uint8_t* const ws = static_cast<uint8_t*>(workspace);
     int* const keys[2] = {reinterpret_cast<int*>(ws + q.keys), reinterpret_cast<int*>(ws + q.keys + up(4 * a->tokens))};
     int* const places[2] = {reinterpret_cast<int*>(ws + q.places), reinterpret_cast<int*>(ws + q.places + up(4 * a->tokens))};
+    const bool vec = vectors(a, grad_table, grad);
     SortParams s = {};
     s.tokens = tokens;
     s.counts = reinterpret_cast<int*>(ws + q.counts);
@@ -527,19 +649,30 @@ int ddp_embed_backward(const ddp_embed_args* a, const void* grad, const void* to
     s.wide = a->index_bits == 64;
     s.ctas = q.sort_ctas;
     s.bits = q.bits;
+    SumParams p = {};
+    p.windows = q.windows;
+    p.tickets_each = (2 * q.windows * (vec ? a->dim / 8 : a->dim) + 3) / 4 * 4;
+    // the second level of them is for rows of more parts than a group's
+    s.ntickets = p.tickets_each * (a->tokens > kPart * kGroup ? 2 : 1);
     cudaError_t e = cudaSuccess;
-    for (int pass = 0; pass < q.passes && e == cudaSuccess; ++pass) {
-        s.shift = pass * q.bits;
-        s.keys_in = pass ? keys[(pass - 1) & 1] : nullptr;
-        s.places_in = pass ? places[(pass - 1) & 1] : nullptr;
-        s.keys = keys[pass & 1];
-        s.places = places[pass & 1];
-        s.ntickets = pass ? 0 : q.windows;
-        e = launch(sort_count_kernel, s.ctas, kThreads, 0, st, s);
-        if (e == cudaSuccess) e = launch(sort_move_kernel, s.ctas, kThreads, 0, st, s);
+    if (a->tokens <= kSmall) {
+        s.keys = keys[0];
+        s.places = places[0];
+        const long long each = kThreads / kRankLanes;
+        e = launch(sort_small_kernel, (a->tokens + each - 1) / each, kThreads, (a->tokens + 3) / 4 * 16, st, s);
+    } else {
+        for (int pass = 0; pass < q.passes && e == cudaSuccess; ++pass) {
+            s.shift = pass * q.bits;
+            s.keys_in = pass ? keys[(pass - 1) & 1] : nullptr;
+            s.places_in = pass ? places[(pass - 1) & 1] : nullptr;
+            s.keys = keys[pass & 1];
+            s.places = places[pass & 1];
+            e = launch(sort_count_kernel, s.ctas, kThreads, 0, st, s);
+            if (e == cudaSuccess) e = launch(sort_move_kernel, s.ctas, kThreads, 0, st, s);
+            s.ntickets = 0;
+        }
     }
     if (e != cudaSuccess) return DDP_ERR_CUDA;
-    SumParams p = {};
     p.grad = grad;
     p.keys = s.keys;
     p.places = s.places;
@@ -551,18 +684,19 @@ int ddp_embed_backward(const ddp_embed_args* a, const void* grad, const void* to
     p.dim = static_cast<int>(a->dim);
     p.grad_stride = a->row_stride;
     p.out_stride = a->table_stride;
-    p.windows = q.windows;
-    p.long_row = q.long_row;
     p.accumulate = accumulate != 0;
     p.scale = a->scale;
-    const bool vec = vectors(a, grad_table, grad);
     p.row_threads = row_threads(a->dim, vec);
-    const int slots = kThreads / p.row_threads;
-    p.rows = slots * 4 < 16 ? 16 : slots * 4 < kThreads ? slots * 4 : kThreads;
-    const long long ctas = p.windows + (p.vocab + p.rows - 1) / p.rows;
+    const int threads = kPart * p.row_threads < kThreads ? kPart * p.row_threads : kThreads;
     const bool in32 = a->dtype == DDP_F32, out32 = a->table_dtype == DDP_F32;
-    e = in32 ? (out32 ? sum_as<float, float>(vec, ctas, p, st) : sum_as<float, uint16_t>(vec, ctas, p, st))
-             : (out32 ? sum_as<uint16_t, float>(vec, ctas, p, st) : sum_as<uint16_t, uint16_t>(vec, ctas, p, st));
+    e = in32 ? (out32 ? sum_as<float, float>(vec, threads, p, st) : sum_as<float, uint16_t>(vec, threads, p, st))
+             : (out32 ? sum_as<uint16_t, float>(vec, threads, p, st) : sum_as<uint16_t, uint16_t>(vec, threads, p, st));
+    if (e == cudaSuccess && !accumulate) {
+        const int64_t row_bytes = a->dim * size_of(a->table_dtype), fit = kFillBytes / row_bytes;
+        p.rows = static_cast<int>(fit < 8 ? 8 : fit < kThreads ? fit : kThreads);
+        p.row_threads = row_bytes / 16 >= kThreads ? kThreads : power_of_two(row_bytes / 16);
+        e = launch(out32 ? embed_fill_kernel<float> : embed_fill_kernel<uint16_t>, (p.vocab + p.rows - 1) / p.rows, kThreads, 0, st, p);
+    }
     return e == cudaSuccess ? DDP_OK : DDP_ERR_CUDA;
 }
 

@@ -195,3 +195,15 @@ def test_streams_graphs_and_workspaces():
         assert torch.equal(outs[1], embed_backward(ins[1], tokens, torch.empty(90, 64, device="cuda")))
         [o.zero_() for o in outs]
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("vocab", [2, 255, 256, 70000])
+@pytest.mark.parametrize("n", [1, 31, 1024, 1025, 8191, 8192, 8193, 20000])
+def test_both_sorts(n, vocab):
+    """Whole numbers around the sizes at which one CTA sorts, and around those of its rounds and digits."""
+    tokens = words(n, vocab, n + vocab)
+    grad = torch.randint(-4, 5, (n, 16), generator=generator(n), device="cuda").float()
+    there = (tokens >= 0) & (tokens < vocab)
+    want = torch.zeros(vocab, 16, device="cuda").index_add_(0, tokens.clamp(0, vocab - 1), grad * there.unsqueeze(1))
+    out = torch.full((vocab, 16), 7.0, device="cuda")
+    assert torch.equal(embed_backward(grad, tokens, out), want)
