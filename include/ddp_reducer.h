@@ -556,7 +556,7 @@ int ddp_embed(const ddp_embed_args* args, const void* table, const void* tokens,
 int64_t ddp_embed_workspace(const ddp_embed_args* args);
 
 /* grad_table[v] = scale * sum of grad[i] over the tokens i that are v, in fp32
- * and in ascending order (rows of more than 64 tokens in parts, and these in
+ * and in ascending order (rows of more than 32 tokens in parts, and these in
  * order); rows without a token get zeros.  With accumulate (fp32 tables only)
  * the sums are added to grad_table, and rows without a token stay as they are.
  * Errors: INVALID_ARG, CUDA. */

@@ -21,18 +21,32 @@ namespace {
 using namespace ddpk::rows;
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kAhead = 4;              // forward: rows of a thread at once
 constexpr int kMaxBits = 8;            // of a digit of the sort
 constexpr int kMaxBins = 1 << kMaxBits;
-constexpr int kItems = 8;              // of a thread in a tile of the sort
-constexpr int kTile = kThreads * kItems;
+constexpr int kSortThreads = 512;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kItems = 4;              // of a thread in a tile of the sort
+constexpr int kTile = kSortThreads * kItems;
 constexpr int kMaxSortCtas = 128;
 constexpr int kSmall = 8192;           // tokens that are sorted by counting
-constexpr int kRankLanes = 8;
-constexpr int kPart = 64;              // sorted places of a CTA, and tokens that are summed in one go
-constexpr int kGroup = 64;             // parts of a row that are added up in one go
-constexpr int kUnroll = 8;             // rows on their way at once
+constexpr int kRankLanes = 16;
+constexpr int kPart = 32;              // sorted places of a window, and tokens that are summed in one go
+constexpr int kGroup = 32;             // parts of a row that are added up in one go
+constexpr int kChunk = 256;            // columns of a warp
+#ifndef MB
+#define MB 5
+#endif
+#ifndef MS
+#define MS 8
+#endif
+#ifndef RG
+#define RG 8
+#endif
+// Rows of a warp on their way, with the one under work.
+template <typename T> constexpr int kRing = sizeof(T) == 2 ? RG : RG / 2;
+constexpr int kMaxSplits = MS;          // shares of a window,
+constexpr int kFewWarps = kSms * 24;   // while there are fewer warps than these
 constexpr int kFillBytes = 64 * 1024;  // of the rows that a CTA looks at for empty ones
 
 struct EmbedParams {
@@ -68,6 +82,8 @@ struct SumParams {
     int* tickets;
     long long n, vocab, grad_stride, out_stride, windows, tickets_each;
     int dim, rows, row_threads;                // rows: of the table, of a CTA
+    int splits, chunks;                        // shares of a window; kChunk columns of a row
+    unsigned sum_ctas;
     int accumulate;
     float scale;
 };
@@ -141,65 +157,77 @@ __device__ __forceinline__ int key_at(const SortParams& p, long long i) {
 }
 
 // How often each digit falls in each CTA's share.
-__global__ void __launch_bounds__(kThreads) sort_count_kernel(const __grid_constant__ SortParams p) {
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const __grid_constant__ SortParams p) {
     __shared__ int bins[kMaxBins];
     const int nbins = 1 << p.bits;
-    for (int b = threadIdx.x; b < nbins; b += kThreads) bins[b] = 0;
+    for (int b = threadIdx.x; b < nbins; b += kSortThreads) bins[b] = 0;
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
-    for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < p.ntickets / 4;
-         i += static_cast<long long>(gridDim.x) * kThreads)
+    for (long long i = static_cast<long long>(blockIdx.x) * kSortThreads + threadIdx.x; i < p.ntickets / 4;
+         i += static_cast<long long>(gridDim.x) * kSortThreads)
         reinterpret_cast<int4*>(p.tickets)[i] = make_int4(0, 0, 0, 0);
     __syncthreads();
     const long long from = blockIdx.x * p.share, to = min(p.n, from + p.share);
 #pragma unroll 4
-    for (long long i = from + threadIdx.x; i < to; i += kThreads) atomicAdd(&bins[key_at(p, i) >> p.shift & (nbins - 1)], 1);
+    for (long long i = from + threadIdx.x; i < to; i += kSortThreads) atomicAdd(&bins[key_at(p, i) >> p.shift & (nbins - 1)], 1);
     __syncthreads();
-    for (int b = threadIdx.x; b < nbins; b += kThreads) p.counts[blockIdx.x * nbins + b] = bins[b];
+    for (int b = threadIdx.x; b < nbins; b += kSortThreads) p.counts[blockIdx.x * nbins + b] = bins[b];
 }
 
 // Each token to its place by the digit, behind the earlier ones of the same.
-__global__ void __launch_bounds__(kThreads) sort_move_kernel(const __grid_constant__ SortParams p) {
+__global__ void __launch_bounds__(kSortThreads) sort_move_kernel(const __grid_constant__ SortParams p) {
+    constexpr int kHalves = kSortThreads / kMaxBins;
     __shared__ int next[kMaxBins];                 // place of the next token of a digit
-    __shared__ int of_warp[kWarps][kMaxBins];      // in a tile, of each warp: how many, and then where they begin
-    __shared__ int totals[kWarps];
-    const int nbins = 1 << p.bits, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    ddpk::dev::pdl_wait();
-    ddpk::dev::pdl_trigger();
-    // a thread a digit: what smaller digits have, and the same in earlier shares
-    const int b = threadIdx.x;
-    int all = 0, earlier = 0;
-    if (b < nbins) {
-#pragma unroll 8
-        for (int c = 0; c < p.ctas; ++c) {
-            const int n = p.counts[c * nbins + b];
-            all += n;
-            if (c < static_cast<int>(blockIdx.x)) earlier += n;
-        }
-    }
-    int before = all;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-        const int x = __shfl_up_sync(kAll, before, o);
-        if (lane >= o) before += x;
-    }
-    if (lane == 31) totals[warp] = before;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) before += totals[w];
-    if (b < nbins) next[b] = before - all + earlier;
-
+    __shared__ int of_warp[kSortWarps][kMaxBins];  // in a tile, of each warp: how many, and then where they begin
+    __shared__ int2 halves[kHalves][kMaxBins];
+    __shared__ int totals[kMaxBins / 32];
+    const int nbins = 1 << p.bits, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = threadIdx.x % kMaxBins;
     const long long from = blockIdx.x * p.share, to = min(p.n, from + p.share);
-    for (long long t0 = from; t0 < to; t0 += kTile) {
-        for (int i = lane; i < nbins; i += 32) of_warp[warp][i] = 0;
-        __syncwarp();
-        int key[kItems], place[kItems], rank[kItems];
-        const long long mine = t0 + warp * (32 * kItems) + lane;
+    int key[kItems], place[kItems], rank[kItems];
+    const auto load = [&](long long t0) {
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
-            const long long at = mine + i * 32;
+            const long long at = t0 + warp * (32 * kItems) + lane + i * 32;
             key[i] = at < to ? key_at(p, at) : -1;
             place[i] = at < to ? (p.keys_in ? p.places_in[at] : static_cast<int>(at)) : 0;
         }
+    };
+    ddpk::dev::pdl_wait();
+    ddpk::dev::pdl_trigger();
+    load(from);
+    // what smaller digits have, and the same in earlier shares: a digit's counts by kHalves threads
+    int2 sum = make_int2(0, 0);
+    if (b < nbins) {
+#pragma unroll 16
+        for (int c = threadIdx.x / kMaxBins; c < p.ctas; c += kHalves) {
+            const int n = p.counts[c * nbins + b];
+            sum.x += n;
+            if (c < static_cast<int>(blockIdx.x)) sum.y += n;
+        }
+    }
+    halves[threadIdx.x / kMaxBins][b] = sum;
+    __syncthreads();
+    int all = 0, before = 0, earlier = 0;
+    if (threadIdx.x < kMaxBins) {
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) { all += halves[h][b].x; earlier += halves[h][b].y; }
+        before = all;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int x = __shfl_up_sync(kAll, before, o);
+            if (lane >= o) before += x;
+        }
+        if (lane == 31) totals[warp] = before;
+    }
+    __syncthreads();
+    if (threadIdx.x < kMaxBins) {
+        for (int w = 0; w < warp; ++w) before += totals[w];
+        next[b] = before - all + earlier;
+    }
+    for (long long t0 = from; t0 < to; t0 += kTile) {
+        if (t0 > from) load(t0);
+        for (int i = lane; i < nbins; i += 32) of_warp[warp][i] = 0;
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < kItems; ++i) {
             const int digit = key[i] < 0 ? nbins : key[i] >> p.shift & (nbins - 1);
@@ -214,10 +242,10 @@ __global__ void __launch_bounds__(kThreads) sort_move_kernel(const __grid_consta
             rank[i] = __shfl_sync(kAll, had, first) + __popc(same & ((1u << lane) - 1));
         }
         __syncthreads();
-        if (b < nbins) {
+        if (threadIdx.x < nbins) {
             int at = next[b];
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
+            for (int w = 0; w < kSortWarps; ++w) {
                 const int n = of_warp[w][b];
                 of_warp[w][b] = at;
                 at += n;
@@ -248,7 +276,7 @@ __global__ void __launch_bounds__(kThreads) sort_small_kernel(const __grid_const
     for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < p.ntickets / 4;
          i += static_cast<long long>(gridDim.x) * kThreads)
         reinterpret_cast<int4*>(p.tickets)[i] = make_int4(0, 0, 0, 0);
-#pragma unroll 4
+#pragma unroll 8
     for (int i = threadIdx.x; i < 4 * fours; i += kThreads) reinterpret_cast<int*>(all)[i] = i < n ? key_at(p, i) : INT32_MAX;
     __syncthreads();
     const int i = blockIdx.x * (kThreads / kRankLanes) + threadIdx.x / kRankLanes, lane = threadIdx.x % kRankLanes;
@@ -296,23 +324,38 @@ __device__ __forceinline__ long long lower_bound(const int* keys, long long lo, 
     return lo;
 }
 
-// A row of the table's gradient, columns from `at` on.  What is added to is not
-// waited for: one addition for each element, so no order is left open.
+// The eight columns of a lane among the kChunk of its warp: next to one another,
+// or (rows that do not lie in vectors) every 32nd.
+template <bool VEC>
+struct Columns {
+    int first, dim;
+
+    __device__ __forceinline__ Columns(int chunk, int dim)
+        : first(chunk * kChunk + (threadIdx.x & 31) * (VEC ? 8 : 1)), dim(dim) {}
+    __device__ __forceinline__ int at(int j) const { return first + j * (VEC ? 1 : 32); }
+    __device__ __forceinline__ bool on(int j) const { return (VEC ? first : at(j)) < dim; }
+};
+
+// A row of the table's gradient.  What is added to is not waited for: one
+// addition for each element, so no order is left open.
 template <typename Tout, bool VEC>
-__device__ __forceinline__ void put_row(const SumParams& p, long long row, int at, const float (&sum)[VEC ? 8 : 1]) {
-    Tout* const to = static_cast<Tout*>(p.out) + row * p.out_stride + at;
-    float f[VEC ? 8 : 1];
+__device__ __forceinline__ void put_row(const SumParams& p, long long row, const Columns<VEC>& c, const float (&sum)[8]) {
+    Tout* const to = static_cast<Tout*>(p.out) + row * p.out_stride;
+    float f[8];
 #pragma unroll
-    for (int j = 0; j < (VEC ? 8 : 1); ++j) f[j] = sum[j] * p.scale;
+    for (int j = 0; j < 8; ++j) f[j] = sum[j] * p.scale;
     if constexpr (sizeof(Tout) == 4) {
         if (p.accumulate) {
             if constexpr (VEC) {
+                if (!c.on(0)) return;
 #pragma unroll
                 for (int j = 0; j < 8; j += 4)
-                    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(to + j), "f"(f[j]), "f"(f[j + 1]),
-                                 "f"(f[j + 2]), "f"(f[j + 3]) : "memory");
+                    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(to + c.first + j), "f"(f[j]),
+                                 "f"(f[j + 1]), "f"(f[j + 2]), "f"(f[j + 3]) : "memory");
             } else {
-                asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(to), "f"(f[0]) : "memory");
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (c.on(j)) asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(to + c.at(j)), "f"(f[j]) : "memory");
             }
             return;
         }
@@ -320,178 +363,200 @@ __device__ __forceinline__ void put_row(const SumParams& p, long long row, int a
     if constexpr (VEC) {
         Eight<Tout> raw;
         raw.put(f);
-        raw.store_once(to);
+        if (c.on(0)) raw.store_once(to + c.first);
     } else {
-        *to = narrow<Tout>(f[0]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c.on(j)) to[c.at(j)] = narrow<Tout>(f[j]);
     }
 }
 
-// A part of a row of more than kPart tokens: part m of those that begin at sorted
-// place `start` and end before `end`.  A CTA's window of kPart places holds at most
-// two beginnings of parts, of which one is its row's first.
-struct Parts {
-    long long start, end;
-
-    __device__ __forceinline__ int count() const { return static_cast<int>((end - start + kPart - 1) / kPart); }
-    __device__ __forceinline__ long long slot(int m) const { return (start + static_cast<long long>(m) * kPart) / kPart * 2 + (m == 0); }
+struct Sum {
+    float v[8];
+    bool whole;              // a row's, not a part's
 };
 
-// One thread's columns of part m are summed: keeps them, and, where this thread
-// is the last of a group of parts (and its group the row's last), adds up the
-// group's (and the groups') in their order and gives the whole in `sum`.
-template <int N>
-__device__ __forceinline__ bool join_parts(const SumParams& p, const Parts& of, int m, int at, float (&sum)[N]) {
+// A warp's columns of part m of a row of more than kPart tokens, whose first is at
+// sorted place `start`, are summed: keeps them, and, where this warp is the last
+// of a group of parts (and its group the row's last), adds up the group's (and
+// the groups') in their order and gives the whole.  A window of kPart places
+// holds at most two beginnings of parts, of which one is its row's first: each
+// has a slot of its own.
+template <bool VEC>
+__device__ __noinline__ Sum join_parts(const SumParams& p, int key, long long start, int m, int chunk, Sum sum) {
+    const Columns<VEC> c(chunk, p.dim);
+    const int lane = threadIdx.x & 31;
+    const long long here = start + static_cast<long long>(m) * kPart;
+    const long long end = warp_lower_bound(p.keys, here, p.n, key + 1LL);
+    const int count = static_cast<int>((end - start + kPart - 1) / kPart), group = m / kGroup * kGroup, last = min(count, group + kGroup);
+    const auto slot = [&](int part) { return (start + static_cast<long long>(part) * kPart) / kPart * 2 + (part == 0); };
     const auto put = [&](int part) {
-        float* const to = p.parts + of.slot(part) * p.dim + at;
+        float* const to = p.parts + slot(part) * p.dim;
+        if constexpr (VEC) {
+            if (c.on(0)) {
+                __stcg(reinterpret_cast<float4*>(to + c.first), make_float4(sum.v[0], sum.v[1], sum.v[2], sum.v[3]));
+                __stcg(reinterpret_cast<float4*>(to + c.first) + 1, make_float4(sum.v[4], sum.v[5], sum.v[6], sum.v[7]));
+            }
+        } else {
 #pragma unroll
-        for (int j = 0; j < N; ++j) __stcg(to + j, sum[j]);
+            for (int j = 0; j < 8; ++j)
+                if (c.on(j)) __stcg(to + c.at(j), sum.v[j]);
+        }
         __threadfence();
+        __syncwarp();
+    };
+    // whether this warp is the last of `all`
+    const auto last_of = [&](int* tickets, int part, int all) {
+        int before = 0;
+        if (lane == 0) before = atomicAdd(tickets + slot(part) * p.chunks + chunk, 1);
+        return __shfl_sync(kAll, before, 0) == all - 1;
     };
     const auto add = [&](int from, int to, int step) {
         __threadfence();
 #pragma unroll
-        for (int j = 0; j < N; ++j) sum[j] = 0.0f;
+        for (int j = 0; j < 8; ++j) sum.v[j] = 0.0f;
 #pragma unroll 8
         for (int q = from; q < to; q += step) {
-            const float* const x = p.parts + of.slot(q) * p.dim + at;
+            const float* const x = p.parts + slot(q) * p.dim;
+            float f[8] = {};
+            if constexpr (VEC) {
+                if (c.on(0)) {
+                    const float4 a = __ldcg(reinterpret_cast<const float4*>(x + c.first)), b = __ldcg(reinterpret_cast<const float4*>(x + c.first) + 1);
+                    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+                }
+            } else {
 #pragma unroll
-            for (int j = 0; j < N; ++j) sum[j] += __ldcg(x + j);
+                for (int j = 0; j < 8; ++j) f[j] = c.on(j) ? __ldcg(x + c.at(j)) : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum.v[j] += f[j];
         }
     };
-    const int count = of.count(), group = m / kGroup * kGroup, end = min(count, group + kGroup);
-    const long long columns = (p.dim + N - 1) / N, column = at / N;
+    sum.whole = false;
     put(m);
-    if (atomicAdd(p.tickets + of.slot(group) * columns + column, 1) != end - group - 1) return false;
-    add(group, end, 1);
-    if (count <= kGroup) return true;
-    put(group);
-    if (atomicAdd(p.tickets + p.tickets_each + of.slot(0) * columns + column, 1) != (count + kGroup - 1) / kGroup - 1) return false;
-    add(0, count, kGroup);
-    return true;
+    if (!last_of(p.tickets, group, last - group)) return sum;
+    add(group, last, 1);
+    if (count > kGroup) {
+        put(group);
+        if (!last_of(p.tickets + p.tickets_each, 0, (count + kGroup - 1) / kGroup)) return sum;
+        add(0, count, kGroup);
+    }
+    sum.whole = true;
+    return sum;
 }
 
-// A CTA sums the tokens of a window of kPart sorted places: a run of rows and
-// parts of rows that begin in the window, one after another, with the next ones'
-// gradients on their way.
+// A warp sums kChunk columns of the rows, and parts of rows, that begin among some
+// of the kPart sorted places of a window (all of them, or, with `splits`, a share),
+// one after another, with the next ones' gradients on their way to shared memory.
+// It needs no other warp: the window's keys and places lie in its lanes.  The
+// loop over rows is short code on purpose: a warp that sums a few rows would wait
+// longer for instructions than for the rows.
 template <typename T, typename Tout, bool VEC>
-__global__ void __launch_bounds__(kThreads) embed_sum_kernel(const __grid_constant__ SumParams p) {
-    constexpr int N = VEC ? 8 : 1;
-    __shared__ int keys[2 * kPart + 1];            // from the place before the window's first on
-    __shared__ int places[2 * kPart];
-    __shared__ uint32_t begins[2 * kPart / 32];    // bit q: a row, or a part of one, begins at the window's place q
-    __shared__ int valid;                          // places that hold a token of the table
-    __shared__ long long of_first[2], of_last[2];           // the rows at the window's ends, where they are long
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int t = threadIdx.x % p.row_threads, slot = threadIdx.x / p.row_threads, slots = blockDim.x / p.row_threads;
-    ddpk::dev::pdl_wait();
-    ddpk::dev::pdl_trigger();
-    const long long w0 = static_cast<long long>(blockIdx.x) * kPart;
-    for (int i = threadIdx.x; i <= 2 * kPart; i += blockDim.x) {
-        const long long at = w0 - 1 + i;
-        keys[i] = at < 0 ? -1 : at < p.n ? p.keys[at] : INT32_MAX;
-        if (i) places[i - 1] = at < p.n ? p.places[at] : 0;
+__device__ __forceinline__ void sum_window(const SumParams& p, long long window, int split, int chunk, uint4* memory) {
+    const int lane = threadIdx.x & 31;
+    const long long w0 = window * kPart, at0 = w0 + lane, at1 = at0 + kPart;
+    // the window's, those behind it that its last rows reach, and those before it
+    const int key0 = at0 < p.n ? p.keys[at0] : INT32_MAX, key1 = at1 < p.n ? p.keys[at1] : INT32_MAX;
+    const int before = at0 >= kPart ? p.keys[at0 - kPart] : -1;
+    const int place0 = at0 < p.n ? p.places[at0] : 0, place1 = at1 < p.n ? p.places[at1] : 0;
+    const int first = __shfl_sync(kAll, key0, 0);
+    const int up0 = __shfl_up_sync(kAll, key0, 1), up1 = __shfl_up_sync(kAll, key1, 1);
+    const int end_before = __shfl_sync(kAll, before, 31), end0 = __shfl_sync(kAll, key0, 31);
+    // bit q: a row begins at the window's place q
+    const uint32_t rows0 = __ballot_sync(kAll, key0 != (lane ? up0 : end_before));
+    const uint32_t rows1 = __ballot_sync(kAll, key1 != (lane ? up1 : end0));
+    const int valid = __popc(__ballot_sync(kAll, key0 < p.vocab)) + __popc(__ballot_sync(kAll, key1 < p.vocab));
+    long long start = w0;                                        // where the window's first row begins
+    if (!(rows0 & 1)) {
+        const uint32_t others = __ballot_sync(kAll, before != first);
+        if (others) start = w0 - __clz(others);
+        else if (first < p.vocab) start = warp_lower_bound(p.keys, 0, w0 - kPart, first);
     }
-    __syncthreads();
-    const int first = keys[1], last = keys[kPart];
-    if (warp == 0) {
-        const bool goes_on = keys[0] == first, is_long = goes_on || keys[kPart + 1] == first;
-        if (is_long && first < p.vocab) {
-            const long long start = goes_on ? warp_lower_bound(p.keys, 0, w0, first) : w0;
-            const long long end = warp_lower_bound(p.keys, w0, p.n, first + 1LL);
-            if (lane == 0) { of_first[0] = start; of_first[1] = end; }
-            __syncwarp();
-        }
-        const long long start = goes_on && first < p.vocab ? of_first[0] : w0;
-        uint32_t rows[2 * kPart / 32];
-        int count = 0;
-#pragma unroll
-        for (int w = 0; w < 2 * kPart / 32; ++w) {
-            const int q = 32 * w + lane;
-            rows[w] = __ballot_sync(kAll, keys[q + 1] != keys[q]);
-            count += __popc(__ballot_sync(kAll, keys[q + 1] < p.vocab));
-            long long from = start;                      // where this place's row begins
-#pragma unroll
-            for (int v = 0; v <= w; ++v) {
-                const uint32_t up_to = v < w ? rows[v] : rows[v] & (0xffffffffu >> (31 - lane));
-                if (up_to) from = w0 + 32 * v + 31 - __clz(up_to);
-            }
-            const uint32_t b = __ballot_sync(kAll, (w0 + q - from) % kPart == 0);
-            if (lane == 0) begins[w] = b;
-        }
-        if (lane == 0) valid = count;
-    } else if (warp == 1 && last != first && keys[kPart + 1] == last && last < p.vocab) {
-        int from = kPart;                                // of a row that begins in the window and goes on behind it
-        while (keys[from - 1] == last) --from;
-        const long long end = warp_lower_bound(p.keys, w0 + kPart, p.n, last + 1LL);
-        if (lane == 0) { of_last[0] = w0 + from - 1; of_last[1] = end; }
-    }
-    __syncthreads();
-    const int each = kPart / slots, a = slot * each, b = a + each;
-    const auto next_begin = [&](int q) {                 // the first beginning at q or behind it
-        for (int w = q / 32; w < 2 * kPart / 32; ++w) {
-            const uint32_t bits = begins[w] & (w == q / 32 ? 0xffffffffu << (q % 32) : 0xffffffffu);
-            if (bits) return 32 * w + __ffs(bits) - 1;
-        }
-        return 2 * kPart;
+    // and bit q: a part of a row does
+    const auto begin_of = [&](uint32_t rows, long long other) {  // of the row that this lane's place is in
+        const uint32_t up_to = rows & (0xffffffffu >> (31 - lane));
+        return up_to ? 31 - __clz(up_to) : other;
+    };
+    const uint32_t parts0 = __ballot_sync(kAll, (lane - begin_of(rows0, start - w0)) % kPart == 0);
+    const long long open = rows0 ? 31 - __clz(rows0) : start - w0;           // where the row that goes on behind begins
+    const uint32_t parts1 = __ballot_sync(kAll, (kPart + lane - (rows1 & (0xffffffffu >> (31 - lane)) ? kPart + begin_of(rows1, 0) : open)) % kPart == 0);
+    const int each = kPart / p.splits, a = split * each, b = a + each;
+    const auto next_begin = [&](int q) {                         // the first beginning at q or behind it
+        const uint32_t bits = q < 32 ? parts0 & (0xffffffffu << q) : 0u;
+        return bits ? __ffs(bits) - 1 : parts1 ? 31 + __ffs(parts1) : 2 * kPart;
     };
     const int i0 = next_begin(a), i1 = min(next_begin(b), valid);
     if (i0 >= min(b, valid)) return;
+    const Columns<VEC> c(chunk, p.dim);
     const T* const grad = static_cast<const T*>(p.grad);
-    for (int at = t * N; at < p.dim; at += p.row_threads * N) {
-        float sum[N];
+    constexpr int kPieces = static_cast<int>(sizeof(Eight<T>)) / 16;
+    uint4* const ring = memory + (threadIdx.x >> 5) * (kRing<T> * kPieces * 32) + lane;
+    const auto row_of = [&](int q) {
+        const int place = __shfl_sync(kAll, q < kPart ? place0 : place1, q & 31);
+        return grad + static_cast<long long>(place) * p.grad_stride;
+    };
+    const auto request = [&](int q) {
+        const T* const from = row_of(q);
+        if (q < i1 && c.on(0))
 #pragma unroll
-        for (int j = 0; j < N; ++j) sum[j] = 0.0f;
-        int begin = i0;
-        for (int i = i0; i < i1; i += kUnroll) {
-            Eight<T> raw[VEC ? kUnroll : 1];
-            float single[VEC ? 1 : kUnroll];
+            for (int u = 0; u < kPieces; ++u)
+                copy_async(ring + (q % kRing<T> * kPieces + u) * 32, reinterpret_cast<const uint4*>(from + c.first) + u);
+        copy_commit();
+    };
+    float next[8] = {};
+    const auto load = [&](int q) {                               // rows that do not lie in vectors
+        const T* const from = row_of(q);
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const T* const from = grad + static_cast<long long>(i + u < i1 ? places[i + u] : 0) * p.grad_stride + at;
-                if constexpr (VEC) {
-                    if (i + u < i1) raw[u].load_once(from);
-                } else {
-                    single[u] = i + u < i1 ? widen(*from) : 0.0f;
-                }
-            }
+        for (int j = 0; j < 8; ++j) next[j] = q < i1 && c.on(j) ? widen(from[c.at(j)]) : 0.0f;
+    };
+    if constexpr (VEC)
+        for (int k = 0; k + 1 < kRing<T>; ++k) request(i0 + k);
+    else
+        load(i0);
+    Sum sum = {};
+    int begin = i0;
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) {
+        if constexpr (VEC) {
+            copy_wait<kRing<T> - 2>();
+            Eight<T> raw;
+            uint4* const words = reinterpret_cast<uint4*>(&raw);
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int q = i + u + 1;
-                if (q > i1) break;
-                if constexpr (VEC) {
-                    float f[8];
-                    raw[u].get(f);
+            for (int u = 0; u < kPieces; ++u) words[u] = ring[(i % kRing<T> * kPieces + u) * 32];
+            float f[8];
+            raw.get(f);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) sum[j] += f[j];
-                } else {
-                    sum[0] += single[u];
-                }
-                if (q < i1 && !(begins[q / 32] >> (q % 32) & 1)) continue;
-                // a row ends here, or a part of one that is long
-                const int key = keys[q];
-                bool whole = true;
-                if (keys[q + 1] == key || keys[begin] == key) {
-                    const Parts of = key == first ? Parts{of_first[0], of_first[1]} : Parts{of_last[0], of_last[1]};
-                    whole = join_parts<N>(p, of, static_cast<int>((w0 + begin - of.start) / kPart), at, sum);
-                }
-                if (whole) put_row<Tout, VEC>(p, key, at, sum);
+            for (int j = 0; j < 8; ++j) sum.v[j] += f[j];
+            request(i + kRing<T> - 1);                           // into the place of the row before, which is used up
+        } else {
 #pragma unroll
-                for (int j = 0; j < N; ++j) sum[j] = 0.0f;
-                begin = q;
-            }
+            for (int j = 0; j < 8; ++j) sum.v[j] += next[j];
+            load(i + 1);
         }
+        const int q = i + 1;
+        if (q < i1 && !((q < kPart ? parts0 >> q : parts1 >> (q - kPart)) & 1)) continue;
+        // a row ends here, or a part of one that is long
+        const int key = __shfl_sync(kAll, q <= kPart ? key0 : key1, i & 31);
+        sum.whole = true;
+        if (!((q < kPart ? rows0 >> q : rows1 >> (q - kPart)) & 1) || !(rows0 >> begin & 1)) {
+            const uint32_t up_to = rows0 & (0xffffffffu >> (31 - begin));
+            const long long row = up_to ? w0 + 31 - __clz(up_to) : start;
+            sum = join_parts<VEC>(p, key, row, static_cast<int>((w0 + begin - row) / kPart), chunk, sum);
+        }
+        if (sum.whole) put_row<Tout, VEC>(p, key, c, sum.v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum.v[j] = 0.0f;
+        begin = q;
     }
 }
 
-// Zeros into the rows of the table that have no token, `rows` of them a CTA.  It
-// needs the sorted keys alone, which were there before the sums' kernel let it
-// start, so it runs beside that one and waits for it only before it ends.
+// Zeros into those of a CTA's `rows` rows of the table that have no token.
 template <typename Tout>
-__global__ void __launch_bounds__(kThreads) embed_fill_kernel(const __grid_constant__ SumParams p) {
+__device__ __forceinline__ void fill_rows(const SumParams& p, long long v0) {
     __shared__ long long bounds[2];
     __shared__ int starts[kThreads + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long v0 = static_cast<long long>(blockIdx.x) * p.rows, v1 = min(p.vocab, v0 + p.rows);
+    const long long v1 = min(p.vocab, v0 + p.rows);
     if (warp < 2) {
         const long long x = warp_lower_bound(p.keys, 0, p.n, warp ? v1 : v0);
         if (lane == 0) bounds[warp] = x;
@@ -512,8 +577,20 @@ __global__ void __launch_bounds__(kThreads) embed_fill_kernel(const __grid_const
         for (int i = t; i < p.dim - pieces * kEach; i += p.row_threads)
             to[i < head ? i : i + pieces * kEach] = narrow<Tout>(0.0f);
     }
+}
+
+// The first sum_ctas CTAs sum, a warp an item of window, split and chunk of
+// columns; the others write the rows without a token, meanwhile.
+template <typename T, typename Tout, bool VEC>
+__global__ void __launch_bounds__(kThreads, MB) embed_sum_kernel(const __grid_constant__ SumParams p) {
+    extern __shared__ uint4 memory[];
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
+    if (blockIdx.x >= p.sum_ctas) return fill_rows<Tout>(p, static_cast<long long>(blockIdx.x - p.sum_ctas) * p.rows);
+    const long long item = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    const int chunk = static_cast<int>(item % p.chunks), split = static_cast<int>(item / p.chunks % p.splits);
+    const long long window = item / p.chunks / p.splits;
+    if (window < p.windows) sum_window<T, Tout, VEC>(p, window, split, chunk, memory);
 }
 
 // ---------------------------------------------------------------- host
@@ -526,7 +603,6 @@ struct Plan {
 
 int64_t up(int64_t x) { return (x + 255) / 256 * 256; }
 
-// The same whatever the alignment: tickets for columns one by one.
 Plan plan_of(const ddp_embed_args* a) {
     Plan q = {};
     const int64_t n = a->tokens;
@@ -546,7 +622,7 @@ Plan plan_of(const ddp_embed_args* a) {
     q.counts = at;
     at += up(4LL * kMaxBins * q.sort_ctas);
     q.tickets = at;
-    at += 2 * up(4 * (2 * q.windows * a->dim + 4));
+    at += 2 * up(4 * (2 * q.windows * ((a->dim + kChunk - 1) / kChunk) + 4));
     q.parts = at;
     at += up(8 * q.windows * a->dim);
     q.bytes = at;
@@ -568,10 +644,7 @@ bool vectors(const ddp_embed_args* a, const void* table, const void* rows) {
            (a->tokens == 1 || a->row_stride * size_of(a->dtype) % 16 == 0);
 }
 
-int row_threads(int64_t dim, bool vec) {
-    const int64_t pieces = vec ? dim / 8 : dim;
-    return pieces >= kThreads ? kThreads : power_of_two(pieces);
-}
+int row_threads(int64_t pieces) { return pieces >= kThreads ? kThreads : power_of_two(pieces); }
 
 template <typename Tin, typename Tout>
 cudaError_t embed_as(bool vec, long long ctas, const EmbedParams& p, cudaStream_t stream) {
@@ -579,8 +652,9 @@ cudaError_t embed_as(bool vec, long long ctas, const EmbedParams& p, cudaStream_
 }
 
 template <typename T, typename Tout>
-cudaError_t sum_as(bool vec, int threads, const SumParams& p, cudaStream_t stream) {
-    return launch(vec ? embed_sum_kernel<T, Tout, true> : embed_sum_kernel<T, Tout, false>, p.windows, threads, 0, stream, p);
+cudaError_t sum_as(bool vec, long long ctas, const SumParams& p, cudaStream_t stream) {
+    return launch(vec ? embed_sum_kernel<T, Tout, true> : embed_sum_kernel<T, Tout, false>, ctas, kThreads,
+                  vec ? kRing<T> * sizeof(Eight<T>) * kThreads : 0, stream, p);
 }
 
 }  // namespace
@@ -605,7 +679,7 @@ int ddp_embed(const ddp_embed_args* a, const void* table, const void* tokens, vo
     p.wide = a->index_bits == 64;
     p.scale = a->scale;
     const bool vec = vectors(a, table, out);
-    p.row_threads = row_threads(a->dim, vec);
+    p.row_threads = row_threads(vec ? a->dim / 8 : a->dim);
     const long long tile = static_cast<long long>(kThreads / p.row_threads) * kAhead;
     const long long ctas = (p.n + tile - 1) / tile;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -651,7 +725,8 @@ int ddp_embed_backward(const ddp_embed_args* a, const void* grad, const void* to
     s.bits = q.bits;
     SumParams p = {};
     p.windows = q.windows;
-    p.tickets_each = (2 * q.windows * (vec ? a->dim / 8 : a->dim) + 3) / 4 * 4;
+    p.chunks = static_cast<int>((a->dim + kChunk - 1) / kChunk);
+    p.tickets_each = (2 * q.windows * p.chunks + 3) / 4 * 4;
     // the second level of them is for rows of more parts than a group's
     s.ntickets = p.tickets_each * (a->tokens > kPart * kGroup ? 2 : 1);
     cudaError_t e = cudaSuccess;
@@ -667,8 +742,8 @@ int ddp_embed_backward(const ddp_embed_args* a, const void* grad, const void* to
             s.places_in = pass ? places[(pass - 1) & 1] : nullptr;
             s.keys = keys[pass & 1];
             s.places = places[pass & 1];
-            e = launch(sort_count_kernel, s.ctas, kThreads, 0, st, s);
-            if (e == cudaSuccess) e = launch(sort_move_kernel, s.ctas, kThreads, 0, st, s);
+            e = launch(sort_count_kernel, s.ctas, kSortThreads, 0, st, s);
+            if (e == cudaSuccess) e = launch(sort_move_kernel, s.ctas, kSortThreads, 0, st, s);
             s.ntickets = 0;
         }
     }
@@ -686,17 +761,19 @@ int ddp_embed_backward(const ddp_embed_args* a, const void* grad, const void* to
     p.out_stride = a->table_stride;
     p.accumulate = accumulate != 0;
     p.scale = a->scale;
-    p.row_threads = row_threads(a->dim, vec);
-    const int threads = kPart * p.row_threads < kThreads ? kPart * p.row_threads : kThreads;
+    p.splits = 1;
+    while (p.splits < kMaxSplits && q.windows * p.chunks * p.splits < kFewWarps) p.splits *= 2;
+    const int64_t warps = q.windows * p.chunks * p.splits, sums = (warps + kThreads / 32 - 1) / (kThreads / 32);
+    if (sums > INT32_MAX) return DDP_ERR_INVALID_ARG;
+    p.sum_ctas = static_cast<unsigned>(sums);
+    const int64_t row_bytes = a->dim * size_of(a->table_dtype), fit = kFillBytes / row_bytes;
+    const int64_t each = (a->vocab + 8 * kSms - 1) / (8 * kSms), rows = fit < each ? fit : each;
+    p.rows = static_cast<int>(rows < 8 ? 8 : rows < kThreads ? rows : kThreads);
+    p.row_threads = row_threads(row_bytes / 16);
+    const long long ctas = sums + (accumulate ? 0 : (p.vocab + p.rows - 1) / p.rows);
     const bool in32 = a->dtype == DDP_F32, out32 = a->table_dtype == DDP_F32;
-    e = in32 ? (out32 ? sum_as<float, float>(vec, threads, p, st) : sum_as<float, uint16_t>(vec, threads, p, st))
-             : (out32 ? sum_as<uint16_t, float>(vec, threads, p, st) : sum_as<uint16_t, uint16_t>(vec, threads, p, st));
-    if (e == cudaSuccess && !accumulate) {
-        const int64_t row_bytes = a->dim * size_of(a->table_dtype), fit = kFillBytes / row_bytes;
-        p.rows = static_cast<int>(fit < 8 ? 8 : fit < kThreads ? fit : kThreads);
-        p.row_threads = row_bytes / 16 >= kThreads ? kThreads : power_of_two(row_bytes / 16);
-        e = launch(out32 ? embed_fill_kernel<float> : embed_fill_kernel<uint16_t>, (p.vocab + p.rows - 1) / p.rows, kThreads, 0, st, p);
-    }
+    e = in32 ? (out32 ? sum_as<float, float>(vec, ctas, p, st) : sum_as<float, uint16_t>(vec, ctas, p, st))
+             : (out32 ? sum_as<uint16_t, float>(vec, ctas, p, st) : sum_as<uint16_t, uint16_t>(vec, ctas, p, st));
     return e == cudaSuccess ? DDP_OK : DDP_ERR_CUDA;
 }
 

@@ -112,10 +112,10 @@ def test_tokens_that_fall_often(n, vocab, few, dim):
     assert bool(((got.double() - want).abs() <= (count + 3).unsqueeze(1) * U * size).all())
 
 
-@pytest.mark.parametrize("edge", [63, 64, 65, 127, 128, 129, 192])
+@pytest.mark.parametrize("edge", [31, 32, 33, 63, 64, 65, 127, 128, 129, 192, 1023, 1024, 1025, 1056, 1057])
 def test_rows_at_the_borders_of_parts(edge):
     """Runs of one token of every length around a part's, after every start."""
-    for before in (0, 1, 62, 63, 64, 65):
+    for before in (0, 1, 30, 31, 32, 33, 62, 63, 64, 65):
         tokens = torch.cat([torch.arange(before) % 3, torch.full((edge,), 5), torch.full((70,), 6), torch.full((3,), -1)]).cuda()
         grad = torch.randint(-8, 9, (len(tokens), 16), generator=generator(edge), device="cuda").float()
         want = torch.zeros(9, 16, device="cuda").index_add_(0, tokens.clamp(min=0), grad * (tokens >= 0).unsqueeze(1))
