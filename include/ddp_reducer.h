@@ -537,7 +537,7 @@ int ddp_route_backward(const ddp_route_args* args, const void* logits, const int
  * Outputs overlap no inputs but where it is said. */
 
 typedef struct ddp_embed_args {
-    int64_t tokens;          /* >= 0, < 2^31 */
+    int64_t tokens;          /* >= 0, < 2^31; of a gradient at most 2^24 */
     int64_t vocab;           /* rows of the table, >= 1, < 2^31 - 1 */
     int64_t dim;             /* elements of a row, 1 .. 2^24 */
     int64_t table_stride;    /* of the table, or of its gradient, >= dim */

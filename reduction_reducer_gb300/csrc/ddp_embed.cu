@@ -34,19 +34,11 @@ constexpr int kRankLanes = 16;
 constexpr int kPart = 32;              // sorted places of a window, and tokens that are summed in one go
 constexpr int kGroup = 32;             // parts of a row that are added up in one go
 constexpr int kChunk = 256;            // columns of a warp
-#ifndef MB
-#define MB 5
-#endif
-#ifndef MS
-#define MS 8
-#endif
-#ifndef RG
-#define RG 8
-#endif
 // Rows of a warp on their way, with the one under work.
-template <typename T> constexpr int kRing = sizeof(T) == 2 ? RG : RG / 2;
-constexpr int kMaxSplits = MS;          // shares of a window,
+template <typename T> constexpr int kRing = sizeof(T) == 2 ? 8 : 4;
+constexpr int kMaxSplits = 32;         // shares of a window,
 constexpr int kFewWarps = kSms * 24;   // while there are fewer warps than these
+constexpr int64_t kMaxTokens = 1 << 24;      // of a gradient: groups of a row's parts are counted in 15 bits
 constexpr int kFillBytes = 64 * 1024;  // of the rows that a CTA looks at for empty ones
 
 struct EmbedParams {
@@ -378,17 +370,16 @@ struct Sum {
 
 // A warp's columns of part m of a row of more than kPart tokens, whose first is at
 // sorted place `start`, are summed: keeps them, and, where this warp is the last
-// of a group of parts (and its group the row's last), adds up the group's (and
-// the groups') in their order and gives the whole.  A window of kPart places
+// of a group of kGroup parts (and its group the row's last), adds up the group's
+// (and the groups') in their order and gives the whole.  A window of kPart places
 // holds at most two beginnings of parts, of which one is its row's first: each
-// has a slot of its own.
+// has a slot of its own.  Tickets count arrivals; that of the row's end, which
+// alone knows how many there are, adds their number above kArrivals.
 template <bool VEC>
-__device__ __noinline__ Sum join_parts(const SumParams& p, int key, long long start, int m, int chunk, Sum sum) {
+__device__ __noinline__ Sum join_parts(const SumParams& p, long long start, int m, bool ends, int chunk, Sum sum) {
+    constexpr int kArrivals = 1 << 16, kMask = kArrivals - 1;
     const Columns<VEC> c(chunk, p.dim);
-    const int lane = threadIdx.x & 31;
-    const long long here = start + static_cast<long long>(m) * kPart;
-    const long long end = warp_lower_bound(p.keys, here, p.n, key + 1LL);
-    const int count = static_cast<int>((end - start + kPart - 1) / kPart), group = m / kGroup * kGroup, last = min(count, group + kGroup);
+    const int lane = threadIdx.x & 31, group = m / kGroup * kGroup;
     const auto slot = [&](int part) { return (start + static_cast<long long>(part) * kPart) / kPart * 2 + (part == 0); };
     const auto put = [&](int part) {
         float* const to = p.parts + slot(part) * p.dim;
@@ -405,11 +396,13 @@ __device__ __noinline__ Sum join_parts(const SumParams& p, int key, long long st
         __threadfence();
         __syncwarp();
     };
-    // whether this warp is the last of `all`
-    const auto last_of = [&](int* tickets, int part, int all) {
-        int before = 0;
-        if (lane == 0) before = atomicAdd(tickets + slot(part) * p.chunks + chunk, 1);
-        return __shfl_sync(kAll, before, 0) == all - 1;
+    const auto arrive = [&](int* tickets, int part, int count) {
+        int now = 0;
+        if (lane == 0) {
+            const int add = 1 + count * kArrivals;
+            now = atomicAdd(tickets + slot(part) * p.chunks + chunk, add) + add;
+        }
+        return __shfl_sync(kAll, now, 0);
     };
     const auto add = [&](int from, int to, int step) {
         __threadfence();
@@ -434,12 +427,14 @@ __device__ __noinline__ Sum join_parts(const SumParams& p, int key, long long st
     };
     sum.whole = false;
     put(m);
-    if (!last_of(p.tickets, group, last - group)) return sum;
-    add(group, last, 1);
-    if (count > kGroup) {
+    const int here = arrive(p.tickets, group, ends ? m - group + 1 : 0), arrived = here & kMask, due = here / kArrivals;
+    if (arrived != (due ? due : kGroup)) return sum;
+    add(group, group + arrived, 1);
+    if (group || !due) {                                         // (else the row's only group)
         put(group);
-        if (!last_of(p.tickets + p.tickets_each, 0, (count + kGroup - 1) / kGroup)) return sum;
-        add(0, count, kGroup);
+        const int all = arrive(p.tickets + p.tickets_each, 0, due ? group / kGroup + 1 : 0);
+        if ((all & kMask) != all / kArrivals) return sum;
+        add(0, all / kArrivals * kGroup, kGroup);
     }
     sum.whole = true;
     return sum;
@@ -459,6 +454,9 @@ __device__ __forceinline__ void sum_window(const SumParams& p, long long window,
     const int key0 = at0 < p.n ? p.keys[at0] : INT32_MAX, key1 = at1 < p.n ? p.keys[at1] : INT32_MAX;
     const int before = at0 >= kPart ? p.keys[at0 - kPart] : -1;
     const int place0 = at0 < p.n ? p.places[at0] : 0, place1 = at1 < p.n ? p.places[at1] : 0;
+    // the first ones of the 32 windows before it, for a row that began there
+    const long long back = w0 - (lane + 1) * kPart;
+    const int far = back >= 0 ? p.keys[back] : -1;
     const int first = __shfl_sync(kAll, key0, 0);
     const int up0 = __shfl_up_sync(kAll, key0, 1), up1 = __shfl_up_sync(kAll, key1, 1);
     const int end_before = __shfl_sync(kAll, before, 31), end0 = __shfl_sync(kAll, key0, 31);
@@ -470,7 +468,16 @@ __device__ __forceinline__ void sum_window(const SumParams& p, long long window,
     if (!(rows0 & 1)) {
         const uint32_t others = __ballot_sync(kAll, before != first);
         if (others) start = w0 - __clz(others);
-        else if (first < p.vocab) start = warp_lower_bound(p.keys, 0, w0 - kPart, first);
+        else if (first < p.vocab) {
+            const int same = __popc(__ballot_sync(kAll, far == first));      // the nearest of them: the keys are sorted
+            start = w0 - static_cast<long long>(same) * kPart;
+            if (same == 32) {
+                start = warp_lower_bound(p.keys, 0, start, first);
+            } else {
+                const long long at = start - kPart + lane;
+                start -= __clz(__ballot_sync(kAll, (at >= 0 ? p.keys[at] : -1) != first));
+            }
+        }
     }
     // and bit q: a part of a row does
     const auto begin_of = [&](uint32_t rows, long long other) {  // of the row that this lane's place is in
@@ -538,10 +545,11 @@ __device__ __forceinline__ void sum_window(const SumParams& p, long long window,
         // a row ends here, or a part of one that is long
         const int key = __shfl_sync(kAll, q <= kPart ? key0 : key1, i & 31);
         sum.whole = true;
-        if (!((q < kPart ? rows0 >> q : rows1 >> (q - kPart)) & 1) || !(rows0 >> begin & 1)) {
+        const bool ends = (q < kPart ? rows0 >> q : rows1 >> (q - kPart)) & 1;
+        if (!ends || !(rows0 >> begin & 1)) {
             const uint32_t up_to = rows0 & (0xffffffffu >> (31 - begin));
             const long long row = up_to ? w0 + 31 - __clz(up_to) : start;
-            sum = join_parts<VEC>(p, key, row, static_cast<int>((w0 + begin - row) / kPart), chunk, sum);
+            sum = join_parts<VEC>(p, row, static_cast<int>((w0 + begin - row) / kPart), ends, chunk, sum);
         }
         if (sum.whole) put_row<Tout, VEC>(p, key, c, sum.v);
 #pragma unroll
@@ -582,7 +590,7 @@ __device__ __forceinline__ void fill_rows(const SumParams& p, long long v0) {
 // The first sum_ctas CTAs sum, a warp an item of window, split and chunk of
 // columns; the others write the rows without a token, meanwhile.
 template <typename T, typename Tout, bool VEC>
-__global__ void __launch_bounds__(kThreads, MB) embed_sum_kernel(const __grid_constant__ SumParams p) {
+__global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const __grid_constant__ SumParams p) {
     extern __shared__ uint4 memory[];
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
@@ -690,13 +698,13 @@ int ddp_embed(const ddp_embed_args* a, const void* table, const void* tokens, vo
 }
 
 int64_t ddp_embed_workspace(const ddp_embed_args* a) {
-    if (!valid(a)) return DDP_ERR_INVALID_ARG;
+    if (!valid(a) || a->tokens > kMaxTokens) return DDP_ERR_INVALID_ARG;
     return a->tokens ? plan_of(a).bytes : 0;
 }
 
 int ddp_embed_backward(const ddp_embed_args* a, const void* grad, const void* tokens, void* grad_table, int32_t accumulate,
                        void* workspace, void* stream) {
-    if (!valid(a) || (accumulate && a->table_dtype != DDP_F32)) return DDP_ERR_INVALID_ARG;
+    if (!valid(a) || a->tokens > kMaxTokens || (accumulate && a->table_dtype != DDP_F32)) return DDP_ERR_INVALID_ARG;
     if (!grad_table || !aligned(grad_table, size_of(a->table_dtype))) return DDP_ERR_INVALID_ARG;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (a->tokens == 0) {

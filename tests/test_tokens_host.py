@@ -62,6 +62,8 @@ def test_embed_pointer_refusals(lib):
     half = C.byref(embed_args(table_dtype=1))
     assert lib.ddp_embed_backward(half, 64, 64, 64, 1, 64, None) == -1          # sums are not kept in bf16
     assert lib.ddp_embed_workspace(a) > 0
+    many = C.byref(embed_args(tokens=2 ** 24 + 1))                            # of a gradient
+    assert lib.ddp_embed_backward(many, 64, 64, 64, 0, 64, None) == -1 and lib.ddp_embed_workspace(many) == -1
     none = C.byref(embed_args(tokens=0))
     assert lib.ddp_embed(none, None, None, None, None) == 0 and lib.ddp_embed_workspace(none) == 0
     assert lib.ddp_embed_backward(none, None, None, 64, 1, None, None) == 0
