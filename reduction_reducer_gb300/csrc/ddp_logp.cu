@@ -28,10 +28,10 @@ namespace {
 using namespace ddpk::rows;
 namespace cg = cooperative_groups;
 
-constexpr int kWarps = 16;             // of a CTA with a row to itself
-constexpr int kRowWarps = 8;           // of a CTA with a row a warp
+constexpr int kWarps = 8;              // of a CTA: with a row to itself, or a row a warp
 constexpr int kWarpVocab = 2048;       // up to which a row is a warp's
-constexpr int kBatch = 4;              // eights of a thread at once
+constexpr int kStages = 4;             // pieces of a thread on their way, with the one under work
+constexpr int kPiece = 32;             // bytes of one
 constexpr int kMaxTop = 32;
 constexpr int kMaxSplit = 8;           // CTAs of a row
 constexpr int kBackThreads = 256;
@@ -92,12 +92,12 @@ __device__ __forceinline__ Sums join_lanes(Sums x, float c) {
     return x;
 }
 
-// N more elements.  Whether the largest grew.
+// 2 N more elements.  Whether the largest grew.
 template <int N, bool ENTROPY>
-__device__ __forceinline__ bool take(const float (&x)[N], float c, Sums& t) {
-    float top = x[0];
+__device__ __forceinline__ bool take(const float2 (&x)[N], float c, Sums& t) {
+    float top = fmaxf(x[0].x, x[0].y);
 #pragma unroll
-    for (int i = 1; i < N; ++i) top = fmaxf(top, x[i]);
+    for (int i = 1; i < N; ++i) top = fmaxf(top, fmaxf(x[i].x, x[i].y));
     const bool grew = top > t.m;
     if (grew) {
         const float d = fmaxf((t.m - top) * c, kFloor), f = exp2_fast(d);
@@ -106,16 +106,22 @@ __device__ __forceinline__ bool take(const float (&x)[N], float c, Sums& t) {
         t.m = top;
     }
     const float m = t.m == neg_inf() ? 0.0f : t.m;
-    float s = 0.0f, a = 0.0f;
+    float2 s = make_float2(0.0f, 0.0f), a = s;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float d = (x[i] - m) * c, e = exp2_fast(d);
-        s += e;
-        if constexpr (ENTROPY) a = fmaf(e, fmaxf(d, kFloor), a);
+        const float2 d = mul2(add2(x[i], both(-m)), both(c)), e = make_float2(exp2_fast(d.x), exp2_fast(d.y));
+        s = add2(s, e);
+        if constexpr (ENTROPY) a = fma2(e, make_float2(fmaxf(d.x, kFloor), fmaxf(d.y, kFloor)), a);
     }
-    t.s += s;
-    if constexpr (ENTROPY) t.a += a;
+    t.s += s.x + s.y;
+    if constexpr (ENTROPY) t.a += a.x + a.y;
     return grew;
+}
+
+template <bool ENTROPY>
+__device__ __forceinline__ bool take_one(float x, float c, Sums& t) {
+    const float2 pair[1] = {make_float2(x, neg_inf())};
+    return take<1, ENTROPY>(pair, c, t);
 }
 
 // A run of n elements of a row: `head` elements, `eights` eights from a 16-byte
@@ -213,12 +219,12 @@ struct Best {
 
 // ---------------------------------------------------------------- forward
 
-template <int WARPS>
+template <bool TOP>
 struct Shared {
-    Sums sums[WARPS];
+    Sums sums[kWarps];
     Sums whole;                    // of this CTA's part of the row
-    Key lists[WARPS][32];
-    Key buffers[WARPS][64];
+    Key lists[TOP ? kWarps : 1][32];
+    Key buffers[TOP ? kWarps : 1][64];
 };
 
 // The lists of all warps of a CTA as one, in the first warp's lanes.
@@ -237,15 +243,16 @@ __device__ __forceinline__ Key join_lists(Key mine, Key (*lists)[32]) {
 }
 
 template <typename T, int WARPS, bool ENTROPY, bool TOP>
-__global__ void __launch_bounds__(32 * (WARPS == 1 ? kRowWarps : WARPS), WARPS == 1 ? 1 : 2)
-logp_kernel(const __grid_constant__ LogpParams p) {
+__global__ void __launch_bounds__(32 * kWarps, TOP ? 4 : 5) logp_kernel(const __grid_constant__ LogpParams p) {
     constexpr int kThreads = 32 * WARPS;                    // of a row, in this CTA
-    __shared__ Shared<WARPS == 1 ? kRowWarps : WARPS> shared;
+    constexpr int kEights = kPiece / static_cast<int>(sizeof(Eight<T>));
+    __shared__ uint4 ahead[kStages][kPiece / 16][32 * kWarps];
+    __shared__ Shared<TOP> shared;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t = WARPS == 1 ? lane : threadIdx.x;
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
-    const long long row = WARPS == 1 ? static_cast<long long>(blockIdx.x) * kRowWarps + warp : blockIdx.x / p.split;
+    const long long row = WARPS == 1 ? static_cast<long long>(blockIdx.x) * kWarps + warp : blockIdx.x / p.split;
     const int part = WARPS == 1 ? 0 : blockIdx.x % p.split;
     if (WARPS == 1 && row >= p.rows) return;
     const bool writer = part == 0 && (WARPS == 1 || warp == 0);     // this warp writes what the row gives
@@ -269,37 +276,42 @@ logp_kernel(const __grid_constant__ LogpParams p) {
     const Run<T> run(logits, lo, hi);
     const float c = p.scale2;
     Sums sums = {neg_inf(), 0.0f, 0.0f};
-    int best = -1;                                          // where this thread's largest lies: its batch's first eight; -2: head, -3: rest
-    if (t < run.head) {
-        const float x[1] = {widen(run.from[t])};
-        if (take<1, ENTROPY>(x, c, sums)) best = -2;
-    }
-    int i = t;
-    for (; i + (kBatch - 1) * kThreads < run.eights; i += kBatch * kThreads) {
-        Eight<T> raw[kBatch];
+    // where this thread's largest lies: in the eights of a piece from this one on; -2: head, -3: rest
+    int best = -1;
+    const auto request = [&](int piece) {
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) raw[u].load(run.eight(i + u * kThreads));
-        float x[8 * kBatch];
+        for (int e = 0; e < kEights; ++e) {
+            const int i = t + (piece * kEights + e) * kThreads;
+            if (i < run.eights)
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            float f[8];
-            raw[u].get(f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[8 * u + j] = f[j];
+                for (int u = 0; u < kPiece / 16 / kEights; ++u)
+                    copy_async(&ahead[piece % kStages][e * (kPiece / 16 / kEights) + u][threadIdx.x],
+                               reinterpret_cast<const uint4*>(run.eight(i)) + u);
         }
-        if (take<8 * kBatch, ENTROPY>(x, c, sums)) best = i;
+        copy_commit();
+    };
+#pragma unroll
+    for (int s = 0; s + 1 < kStages; ++s) request(s);
+    if (t < run.head && take_one<ENTROPY>(widen(run.from[t]), c, sums)) best = -2;
+    for (int piece = 0; t + piece * kEights * kThreads < run.eights; ++piece) {
+        copy_wait<kStages - 2>();
+        float2 x[4 * kEights];
+#pragma unroll
+        for (int e = 0; e < kEights; ++e) {
+            Eight<T> raw;
+            uint4* const words = reinterpret_cast<uint4*>(&raw);
+#pragma unroll
+            for (int u = 0; u < kPiece / 16 / kEights; ++u) words[u] = ahead[piece % kStages][e * (kPiece / 16 / kEights) + u][threadIdx.x];
+            float f[8];
+            raw.get(f);
+            const bool on = e == 0 || t + (piece * kEights + e) * kThreads < run.eights;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[4 * e + j] = on ? make_float2(f[2 * j], f[2 * j + 1]) : both(neg_inf());
+        }
+        request(piece + kStages - 1);                       // into the place of the piece before, which is used up
+        if (take<4 * kEights, ENTROPY>(x, c, sums)) best = t + piece * kEights * kThreads;
     }
-    for (; i < run.eights; i += kThreads) {
-        Eight<T> raw;
-        raw.load(run.eight(i));
-        float x[8];
-        raw.get(x);
-        if (take<8, ENTROPY>(x, c, sums)) best = i;
-    }
-    if (t < run.n - run.rest()) {
-        const float x[1] = {widen(run.from[run.rest() + t])};
-        if (take<1, ENTROPY>(x, c, sums)) best = -3;
-    }
+    if (t < run.n - run.rest() && take_one<ENTROPY>(widen(run.from[run.rest() + t]), c, sums)) best = -3;
 
     Key list = 0;
     if constexpr (TOP) {
@@ -309,7 +321,7 @@ logp_kernel(const __grid_constant__ LogpParams p) {
         if (best == -2) mine = key_of(sums.m, base + t);
         if (best == -3) mine = key_of(sums.m, base + run.rest() + t);
         if (best >= 0) {
-            for (int u = 0; u < kBatch && !mine; ++u) {
+            for (int u = 0; u < kEights && !mine; ++u) {
                 const int at = best + u * kThreads;
                 if (at >= run.eights) break;
                 Eight<T> raw;
@@ -407,85 +419,120 @@ logp_kernel(const __grid_constant__ LogpParams p) {
 
 // ---------------------------------------------------------------- backward
 
+template <int N> struct Constant { static constexpr int value = N; };
+
 // d log p_t / d z_i = [i = t] - p_i and d H / d z_i = -p_i (log p_i + H): a thread's
-// elements of a row take -p (alpha + beta log2 p).
+// elements of a row take p (alpha + beta log2 p).
 struct Slope {
     float scale, top, log_sum2, alpha, beta;
 
     template <bool ENTROPY>
-    __device__ __forceinline__ float at(float x) const {
-        const float d = fmaf(fmaf(x, scale, -top), kLog2e, -log_sum2);  // log2 p
-        const float y = ENTROPY ? fmaf(beta, fmaxf(d, kFloor), alpha) : alpha;
-        return -exp2_fast(d) * y;
+    __device__ __forceinline__ float2 at(float2 x) const {
+        const float2 d = fma2(fma2(x, both(scale), both(-top)), both(kLog2e), both(-log_sum2));      // log2 p
+        float2 y = both(alpha);
+        if constexpr (ENTROPY) y = fma2(both(beta), make_float2(fmaxf(d.x, kFloor), fmaxf(d.y, kFloor)), y);
+        return mul2(make_float2(exp2_fast(d.x), exp2_fast(d.y)), y);
     }
 };
 
+// Eight elements from an address `shift` bytes behind a 16-byte boundary, whole
+// elements: of the 16-byte words that they touch, none of which lies past them.
+template <typename T>
+struct Shifted {
+    static constexpr int kWords = static_cast<int>(sizeof(Eight<T>)) / 4;
+    uint4 v[kWords / 4 + 1];
+
+    __device__ __forceinline__ void load(const T* p, int shift) {
+        const uint4* const from = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p) - shift);
+#pragma unroll
+        for (int i = 0; i < kWords / 4 + 1; ++i)
+            if (i < kWords / 4 || shift) v[i] = from[i];
+    }
+    __device__ __forceinline__ Eight<T> get(int shift) const {
+        uint32_t w[kWords + 4], out[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords / 4 + 1; ++i) { w[4 * i] = v[i].x; w[4 * i + 1] = v[i].y; w[4 * i + 2] = v[i].z; w[4 * i + 3] = v[i].w; }
+        const int bits = shift % 4 * 8;
+        // the shift is the row's: one of four constant selections
+        const auto select = [&](auto first) {
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) {
+                constexpr int from = decltype(first)::value;
+                out[k] = sizeof(T) == 4 ? w[from + k] : __funnelshift_r(w[from + k], w[from + k + 1], bits);
+            }
+        };
+        switch (shift / 4) {
+            case 0: select(Constant<0>()); break;
+            case 1: select(Constant<1>()); break;
+            case 2: select(Constant<2>()); break;
+            default: select(Constant<3>()); break;
+        }
+        Eight<T> x;
+        uint4* const to = reinterpret_cast<uint4*>(&x);
+#pragma unroll
+        for (int i = 0; i < kWords / 4; ++i) to[i] = make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+        return x;
+    }
+};
+
+// Eights that start on 16 bytes of the gradient; the logits' eights lie `shift`
+// bytes off, the same all along a row.
 template <typename T, bool ENTROPY>
 __global__ void __launch_bounds__(kBackThreads) logp_backward_kernel(const __grid_constant__ LogpParams p) {
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
     const long long row = blockIdx.x / p.split;
     const long long lo = blockIdx.x % p.split * p.segment, hi = min(static_cast<long long>(p.vocab), lo + p.segment);
-    const T* const logits = static_cast<const T*>(p.logits) + row * p.stride;
-    T* const out = static_cast<T*>(p.out) + row * p.out_stride;
+    const T* const from = static_cast<const T*>(p.logits) + row * p.stride + lo;
+    const Run<T> run(static_cast<const T*>(p.out) + row * p.out_stride, lo, hi);
+    T* const to = static_cast<T*>(p.out) + row * p.out_stride + lo;
     const int target = target_of(p, row);
     const float2 stat = *reinterpret_cast<const float2*>(p.stats + 2 * row);
+    const bool zero = target == -1 || (stat.x == neg_inf() && stat.y == 0.0f);     // (a row of NaN has a NaN sum)
+    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(from + run.head) & 15);
+    Shifted<T> raw[kBackEights];
+#pragma unroll
+    for (int u = 0; u < kBackEights; ++u) {
+        const int i = threadIdx.x + u * kBackThreads;
+        if (!zero && i < run.eights) raw[u].load(from + run.head + 8 * i, shift);
+    }
     const float g = p.grad_logp && target >= 0 ? p.grad_logp[row] : 0.0f;
     const float h = ENTROPY ? p.grad_entropy[row] : 0.0f;
-    const Slope slope = {p.scale, stat.x, stat.y * kLog2e, p.scale * (ENTROPY ? fmaf(h, p.entropy[row], g) : g), p.scale * h * kLn2};
-    const bool zero = target == -1 || (stat.x == neg_inf() && stat.y == 0.0f);     // (a row of NaN has a NaN sum)
+    const Slope slope = {p.scale, stat.x, stat.y * kLog2e, -p.scale * (ENTROPY ? fmaf(h, p.entropy[row], g) : g), -p.scale * h * kLn2};
     const float extra = p.scale * g;
-    const Run<T> run(logits, lo, hi);
-    T* const to = out + lo;
-    const bool vec = ((reinterpret_cast<uintptr_t>(run.from) ^ reinterpret_cast<uintptr_t>(to)) & 15) == 0;
     const int aim = target - static_cast<int>(lo);
-    const auto single = [&](int i, T x) {
-        float y = zero ? 0.0f : slope.at<ENTROPY>(widen(x));
+    // the ends, at most seven elements each
+    const int ends = run.n - 8 * run.eights;
+    if (threadIdx.x < ends) {
+        const int i = threadIdx.x < run.head ? threadIdx.x : threadIdx.x + 8 * run.eights;
+        float y = zero ? 0.0f : slope.at<ENTROPY>(both(widen(from[i]))).x;
         if (i == aim && !zero) y += extra;
         to[i] = narrow<T>(y);
-    };
-    if (!vec) {                                             // element by element, eight of a thread on their way at once
-        for (int i0 = threadIdx.x; i0 < run.n; i0 += kBackThreads * 8) {
-            T x[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u) x[u] = !zero && i0 + u * kBackThreads < run.n ? run.from[i0 + u * kBackThreads] : T(0);
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (i0 + u * kBackThreads < run.n) single(i0 + u * kBackThreads, x[u]);
-        }
-        return;
     }
-    if (threadIdx.x < run.head) single(threadIdx.x, run.from[threadIdx.x]);
-    if (threadIdx.x < run.n - run.rest()) single(run.rest() + threadIdx.x, run.from[run.rest() + threadIdx.x]);
-    for (int i0 = threadIdx.x; i0 < run.eights; i0 += kBackThreads * kBackEights) {
-        Eight<T> raw[kBackEights];
 #pragma unroll
-        for (int u = 0; u < kBackEights; ++u) {
-            const int i = i0 + u * kBackThreads;
-            if (!zero && i < run.eights) raw[u].load_once(run.eight(i));
-        }
-#pragma unroll
-        for (int u = 0; u < kBackEights; ++u) {
-            const int i = i0 + u * kBackThreads;
-            if (i >= run.eights) break;
+    for (int u = 0; u < kBackEights; ++u) {
+        const int i = threadIdx.x + u * kBackThreads;
+        if (i >= run.eights) break;
+        Eight<T> out;
+        out.zero();
+        if (!zero) {
             float x[8];
-            if (zero) {
+            raw[u].get(shift).get(x);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = 0.0f;
-            } else {
-                raw[u].get(x);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = slope.at<ENTROPY>(x[j]);
-                const unsigned place = static_cast<unsigned>(aim - run.head - 8 * i);
-                if (place < 8) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (place == j) x[j] += extra;
-                }
+            for (int j = 0; j < 8; j += 2) {
+                const float2 y = slope.at<ENTROPY>(make_float2(x[j], x[j + 1]));
+                x[j] = y.x;
+                x[j + 1] = y.y;
             }
-            raw[u].put(x);
-            raw[u].store_once(to + run.head + 8 * i);
+            const unsigned place = static_cast<unsigned>(aim - run.head - 8 * i);
+            if (place < 8) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (place == j) x[j] += extra;
+            }
+            out.put(x);
         }
+        out.store_once(to + run.head + 8 * i);
     }
 }
 
@@ -496,8 +543,8 @@ cudaError_t forward_as(const LogpParams& p, cudaStream_t stream) {
     void (*kernel)(LogpParams);
     if (p.entropy) kernel = p.top ? logp_kernel<T, WARPS, true, true> : logp_kernel<T, WARPS, true, false>;
     else kernel = p.top ? logp_kernel<T, WARPS, false, true> : logp_kernel<T, WARPS, false, false>;
-    if (WARPS == 1) return launch(kernel, (p.rows + kRowWarps - 1) / kRowWarps, 32 * kRowWarps, 0, stream, p);
-    return launch(kernel, p.rows * p.split, 32 * WARPS, 0, stream, p, p.split);
+    if (WARPS == 1) return launch(kernel, (p.rows + kWarps - 1) / kWarps, 32 * kWarps, 0, stream, p);
+    return launch(kernel, p.rows * p.split, 32 * kWarps, 0, stream, p, p.split);
 }
 
 template <typename T>
