@@ -619,7 +619,7 @@ typedef struct ddp_logprobs_args {
     int64_t row_stride;      /* of the logits, >= vocab */
     int32_t top;             /* alternatives, 0 .. 32, <= vocab */
     int32_t index_bits;      /* of a target: 32 or 64 (signed) */
-    float scale;             /* finite, > 0: of the logits (1 / temperature) */
+    float scale;             /* 2^-64 .. 2^64: of the logits (1 / temperature) */
     ddp_dtype dtype;         /* of the logits and of their gradient */
 } ddp_logprobs_args;
 

@@ -530,10 +530,7 @@ __device__ __forceinline__ void sum_window(const SumParams& p, long long window,
             uint4* const words = reinterpret_cast<uint4*>(&raw);
 #pragma unroll
             for (int u = 0; u < kPieces; ++u) words[u] = ring[(i % kRing<T> * kPieces + u) * 32];
-            float f[8];
-            raw.get(f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum.v[j] += f[j];
+            raw.add_to(sum.v);
             request(i + kRing<T> - 1);                           // into the place of the row before, which is used up
         } else {
 #pragma unroll

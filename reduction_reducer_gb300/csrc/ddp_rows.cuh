@@ -35,6 +35,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 __device__ __forceinline__ float nan_value() { return __int_as_float(0x7fffffff); }
 
+// A pair of bf16 as they lie in memory plus fp32 numbers, without widening them first.
+__device__ __forceinline__ float2 add_pair(uint32_t x, float2 y) {
+    float2 d;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.f32.bf16 %0, l, %3;\n\tadd.f32.bf16 %1, h, %4;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "r"(x), "f"(y.x), "f"(y.y));
+    return d;
+}
+
 // 16 bytes that this kernel reads once, past L1; not through the read-only
 // path, so that the same thread may store to them afterwards.
 __device__ __forceinline__ uint4 ld_once(const void* p) {
@@ -55,6 +63,15 @@ template <> struct Eight<uint16_t> {
     __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void get(float (&f)[8]) const { dev::Vec<uint16_t>::unpack(v, f); }
+    __device__ __forceinline__ void add_to(float (&f)[8]) const {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 d = add_pair(w[i], make_float2(f[2 * i], f[2 * i + 1]));
+            f[2 * i] = d.x;
+            f[2 * i + 1] = d.y;
+        }
+    }
     __device__ __forceinline__ void put(const float (&f)[8]) {
         v = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
     }
@@ -76,6 +93,12 @@ template <> struct Eight<float> {
             f[4 * i] = __uint_as_float(v[i].x); f[4 * i + 1] = __uint_as_float(v[i].y);
             f[4 * i + 2] = __uint_as_float(v[i].z); f[4 * i + 3] = __uint_as_float(v[i].w);
         }
+    }
+    __device__ __forceinline__ void add_to(float (&f)[8]) const {
+        float x[8];
+        get(x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] += x[i];
     }
     __device__ __forceinline__ void put(const float (&f)[8]) {
 #pragma unroll

@@ -36,7 +36,8 @@ def logprobs(logits, targets=None, top: int = 0, scale: float = 1.0, entropy: bo
     int32 or int64, contiguous, or None; a row whose target lies outside [0,
     vocab), as padding's does, is left out (zeros, alternatives -1); top: 0 ..
     32 alternatives, the largest logits in descending order, ties to the
-    lowest index; scale: 1 / temperature; entropy: whether to give it.
+    lowest index; scale: 1 / temperature, 2^-64 .. 2^64; entropy: whether to
+    give it.
     All tensors lie on the current device."""
     torch = _rows.torch or _rows.load_torch()
     device = _device()

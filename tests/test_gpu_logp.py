@@ -275,3 +275,15 @@ def test_autograd_and_graphs():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((*eager, d), (*again, e)))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [2.0 ** -64, 1e-9, 30.0, 2.0 ** 64])
+def test_extreme_scales(scale, kind):
+    """Scales at which nothing differs, and at which only the largest is left; masked logits stay out of both."""
+    x = draw(4, 3000, kind, 1)
+    x[0, ::3] = -INF
+    x[1, 1::2] = torch.finfo(KINDS[kind]).min
+    x[2] = torch.arange(3000, device="cuda") % 7
+    got = logprobs(x, None, 4, scale, entropy=True)
+    check(x, None, 4, scale, got)

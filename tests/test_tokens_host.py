@@ -115,7 +115,8 @@ def test_drop_pointer_refusals(lib):
 
 @pytest.mark.parametrize("bad", [dict(rows=-1), dict(vocab=0), dict(vocab=2 ** 24 + 1, row_stride=2 ** 25), dict(row_stride=7),
                                  dict(top=-1), dict(top=9), dict(top=33, vocab=64, row_stride=64), dict(scale=0.0),
-                                 dict(scale=-1.0), dict(scale=NAN), dict(scale=INF), dict(dtype=2), dict(index_bits=8)])
+                                 dict(scale=-1.0), dict(scale=NAN), dict(scale=INF), dict(scale=2.0 ** -65), dict(scale=2.0 ** 65), dict(dtype=2),
+                                 dict(index_bits=8)])
 def test_logprobs_refusals(lib, bad):
     a = C.byref(logp_args(**bad))
     assert lib.ddp_logprobs(a, 64, 64, 64, 64, 64, 64, 64, None) == -1
