@@ -29,15 +29,19 @@ def matrix(name, t, device, shape=None, dtype=None):
     """(rows, columns, row stride, dtype's code) of a tensor of at least one
     dimension, whose last are the columns; its shape and dtype checked where
     they are given."""
-    code = DTYPES.get(t.dtype)
-    if code is None or t.dim() == 0 or t.get_device() != device or (dtype is not None and code != dtype) or (
-            shape is not None and t.shape != shape):
+    code, size = DTYPES.get(t.dtype), t.shape
+    if code is None or not size or t.get_device() != device or (dtype is not None and code != dtype) or (
+            shape is not None and size != shape):
         what = "fp32 or bf16" if dtype is None else str(CODES.get(dtype, "fp32 or bf16"))
         raise ValueError(f"{name}: expected {'rows' if shape is None else list(shape)} of {what} on {found(device, t)}")
-    cols = t.shape[-1]
+    cols = size[-1]
     rows = t.numel() // cols if cols else 0
     if t.is_contiguous() or rows == 0:
         return rows, cols, cols, code
+    return rows, cols, _stride(name, t, rows, cols), code
+
+
+def _stride(name, t, rows, cols):
     if t.dim() != 2:
         try:
             t = t.view(-1, cols)
@@ -50,14 +54,14 @@ def matrix(name, t, device, shape=None, dtype=None):
         stride = cols
     if stride < cols:
         raise ValueError(f"{name}: expected rows that do not overlap")
-    return rows, cols, stride, code
+    return stride
 
 
 def vector(name, t, shape, device, dtype):
     """Address of a contiguous tensor, None for None."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: expected {list(shape)} contiguous {dtype} on {found(device, t)}")
     return t.data_ptr()
 

@@ -31,9 +31,11 @@ def drop(x, p: float, seed, offset: int = 0, residual=None, out=None, stream=Non
     if residual is not None:
         _, _, residual_stride, _ = _rows.matrix("residual", residual, device, x.shape, code)
         r = residual.data_ptr()
+    out_stride = cols
     if out is None:
         out = _rows.empty(x.shape, x.dtype, x.device, stream)
-    _, _, out_stride, _ = _rows.matrix("out", out, device, x.shape, code)
+    else:
+        out_stride = _rows.matrix("out", out, device, x.shape, code)[2]
     value, address = seed, 0
     if not isinstance(seed, int):
         value, address = 0, _rows.vector("seed", seed, seed.shape, device, _rows.torch.int64)

@@ -30,10 +30,12 @@ def embed(table, tokens, scale: float = 1.0, dtype=None, out=None, stream=None, 
     device = _device()
     vocab, dim, table_stride, table_code = _rows.matrix("table", table, device)
     address, bits = _rows.indices("tokens", tokens, None, device)
-    shape = (*tokens.shape, dim)
-    if out is None:
+    shape, row_stride = (*tokens.shape, dim), dim
+    code = table_code if dtype is None else _rows.DTYPES.get(dtype, -1)
+    if out is None and code >= 0:
         out = _rows.empty(shape, dtype or table.dtype, table.device, stream)
-    _, _, row_stride, code = _rows.matrix("out", out, device, shape, None if dtype is None else _rows.DTYPES.get(dtype, -1))
+    else:
+        _, _, row_stride, code = _rows.matrix("out", table if out is None else out, device, shape, None if dtype is None else code)
     n = tokens.numel()
     st = _lib.load(lib_path).ddp_embed(_pack(n, vocab, dim, table_stride, row_stride, scale, table_code, code, bits),
                                        table.data_ptr(), address, out.data_ptr(), _stream(stream))

@@ -17,19 +17,14 @@ def _pack(rows, dim, x_stride, out_stride, eps, code, param_code):
         raise ValueError(f"eps: {e}") from None
 
 
-def _params(dim, device, **tensors):
-    """(their dtype's code, their addresses) of parameter vectors of one dtype."""
-    dtype, at = None, []
-    for name, t in tensors.items():
-        if t is None:
-            at.append(None)
-            continue
-        if dtype is None:
-            dtype = t.dtype
-            if dtype not in _rows.DTYPES:
-                raise ValueError(f"{name}: expected fp32 or bf16 on {_rows.found(device, t)}")
-        at.append(_rows.vector(name, t, (dim,), device, dtype))
-    return _rows.DTYPES.get(dtype, _lib.DDP_F32), at
+def _dtype(dim, device, *named):
+    """The dtype of the parameter vectors, given as (name, tensor or None): that of the first."""
+    for name, t in named:
+        if t is not None:
+            if t.dtype not in _rows.DTYPES:
+                raise ValueError(f"{name}: expected [{dim}] contiguous fp32 or bf16 on {_rows.found(device, t)}")
+            return t.dtype
+    return _rows.torch.float32
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stats=None, stream=None,
@@ -44,16 +39,21 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stats=Non
     torch = _rows.torch or _rows.load_torch()
     device = _device()
     rows, dim, x_stride, code = _rows.matrix("x", x, device)
-    param_code, (w, b) = _params(dim, device, weight=weight, bias=bias)
+    kind, each = _dtype(dim, device, ("weight", weight), ("bias", bias)), (dim,)
+    out_stride = dim
     if out is None:
         out = _rows.empty(x.shape, x.dtype, x.device, stream)
-    shape = (*x.shape[:-1], 2)
+    else:
+        out_stride = _rows.matrix("out", out, device, x.shape, code)[2]
     if stats is None:
-        stats = _rows.empty(shape, torch.float32, x.device, stream)
-    _, _, out_stride, _ = _rows.matrix("out", out, device, x.shape, code)
-    st = _lib.load(lib_path).ddp_layer_norm(_pack(rows, dim, x_stride, out_stride, eps, code, param_code), x.data_ptr(), w, b,
-                                            out.data_ptr(), _rows.vector("stats", stats, shape, device, torch.float32),
-                                            _stream(stream))
+        stats = _rows.empty((rows, 2) if x.dim() == 2 else (*x.shape[:-1], 2), torch.float32, x.device, stream)
+        at = stats.data_ptr()
+    else:
+        at = _rows.vector("stats", stats, (*x.shape[:-1], 2), device, torch.float32)
+    st = _lib.load(lib_path).ddp_layer_norm(
+        _pack(rows, dim, x_stride, out_stride, eps, code, _rows.DTYPES[kind]), x.data_ptr(),
+        _rows.vector("weight", weight, each, device, kind), _rows.vector("bias", bias, each, device, kind), out.data_ptr(), at,
+        _stream(stream))
     if st:
         _rows.refused(st, "ddp_layer_norm", rows=rows, dim=dim, eps=eps)
     return out, stats
@@ -73,18 +73,21 @@ def layer_norm_backward(grad, x, stats, weight=None, grad_weight=None, grad_bias
     device = _device()
     rows, dim, x_stride, code = _rows.matrix("x", x, device)
     _, _, grad_stride, _ = _rows.matrix("grad", grad, device, x.shape, code)
-    param_code, (w, gw, gb) = _params(dim, device, weight=weight, grad_weight=grad_weight, grad_bias=grad_bias)
+    kind, each = _dtype(dim, device, ("weight", weight), ("grad_weight", grad_weight), ("grad_bias", grad_bias)), (dim,)
+    w = _rows.vector("weight", weight, each, device, kind)
+    gw = _rows.vector("grad_weight", grad_weight, each, device, kind)
+    gb = _rows.vector("grad_bias", grad_bias, each, device, kind)
     out_stride = dim
-    if input_grad:
-        if out is None:
-            out = _rows.empty(x.shape, x.dtype, x.device, stream)
-        _, _, out_stride, _ = _rows.matrix("out", out, device, x.shape, code)
-    else:
+    if not input_grad:
         out = None
         if gw is None and gb is None:
             return None, None, None
+    elif out is None:
+        out = _rows.empty(x.shape, x.dtype, x.device, stream)
+    else:
+        out_stride = _rows.matrix("out", out, device, x.shape, code)[2]
     lib = _lib.load(lib_path)
-    args = _pack(rows, dim, x_stride, out_stride, 0.0, code, param_code)
+    args = _pack(rows, dim, x_stride, out_stride, 0.0, code, _rows.DTYPES[kind])
     size = lib.ddp_layer_norm_workspace(args) if gw is not None or gb is not None else 0
     st = size
     if size >= 0:

@@ -45,18 +45,23 @@ def logprobs(logits, targets=None, top: int = 0, scale: float = 1.0, entropy: bo
     lead = logits.shape[:-1]
     at, bits = (None, 64) if targets is None else _rows.indices("targets", targets, lead, device)
     args = _pack(rows, vocab, stride, top, bits, scale, code)
-
-    def place(dtype, *more):
-        return _rows.empty((*lead, *more), dtype, logits.device, stream)
-
-    f32 = torch.float32
-    got = LogProbs(None if targets is None else place(f32), place(f32) if entropy else None, place(f32, 2),
-                   place(torch.int32, top) if top > 0 else None, place(f32, top) if top > 0 else None)
-    st = _lib.load(lib_path).ddp_logprobs(args, logits.data_ptr(), at, *(None if t is None else t.data_ptr() for t in got),
+    f32, dev, empty = torch.float32, logits.device, _rows.empty
+    logp = h = index = best = logp_at = h_at = index_at = best_at = None
+    stats = empty((*lead, 2), f32, dev, stream)
+    if targets is not None:
+        logp = empty(lead, f32, dev, stream)
+        logp_at = logp.data_ptr()
+    if entropy:
+        h = empty(lead, f32, dev, stream)
+        h_at = h.data_ptr()
+    if top > 0:
+        index, best = empty((*lead, top), torch.int32, dev, stream), empty((*lead, top), f32, dev, stream)
+        index_at, best_at = index.data_ptr(), best.data_ptr()
+    st = _lib.load(lib_path).ddp_logprobs(args, logits.data_ptr(), at, logp_at, h_at, stats.data_ptr(), index_at, best_at,
                                           _stream(stream))
     if st:
         _rows.refused(st, "ddp_logprobs", rows=rows, vocab=vocab, top=top, scale=scale)
-    return got
+    return LogProbs(logp, h, stats, index, best)
 
 
 def logprobs_backward(grad_logp, logits, targets, stats, scale: float = 1.0, entropy=None, grad_entropy=None, out=None,
@@ -73,9 +78,11 @@ def logprobs_backward(grad_logp, logits, targets, stats, scale: float = 1.0, ent
     at, bits = (None, 64) if targets is None else _rows.indices("targets", targets, lead, device)
     if grad_entropy is None:
         entropy = None
+    out_stride = vocab
     if out is None:
         out = _rows.empty(logits.shape, logits.dtype, logits.device, stream)
-    _, _, out_stride, _ = _rows.matrix("out", out, device, logits.shape, code)
+    else:
+        out_stride = _rows.matrix("out", out, device, logits.shape, code)[2]
     st = _lib.load(lib_path).ddp_logprobs_backward(
         _pack(rows, vocab, stride, 0, bits, scale, code), logits.data_ptr(), at,
         _rows.vector("stats", stats, (*lead, 2), device, f32), _rows.vector("entropy", entropy, lead, device, f32),
