@@ -36,8 +36,11 @@ constexpr int kGroup = 32;             // parts of a row that are added up in on
 constexpr int kChunk = 256;            // columns of a warp
 // Rows of a warp on their way, with the one under work.
 template <typename T> constexpr int kRing = sizeof(T) == 2 ? 8 : 4;
-constexpr int kMaxSplits = 32;         // shares of a window,
-constexpr int kFewWarps = kSms * 24;   // while there are fewer warps than these
+// Shares of a window, while there are fewer warps: one place each where the GPU
+// would not be full (111 tokens of 14 columns: four shares 9.2 us, eight 7.3, 32 6.1), and up
+// to eight where warps would not be many (65,536 tokens of 1,024: one 76.7, two 73.7, four 76.1).
+constexpr int kMaxSplits = 32, kFewWarps = kSms * 24;
+constexpr int kMoreSplits = 8, kMoreWarps = kSms * 96;
 constexpr int64_t kMaxTokens = 1 << 24;      // of a gradient: groups of a row's parts are counted in 15 bits
 constexpr int kFillBytes = 64 * 1024;  // of the rows that a CTA looks at for empty ones
 
@@ -58,7 +61,9 @@ struct SortParams {
     const int* places_in;
     int* keys;
     int* places;
-    int* counts;             // [ctas][bins]
+    int* counts;             // [ctas][bins] of this pass
+    int* next_counts;        // and of the next one, zeros before (NULL: there is none)
+    long long nzeros;        // first pass: counts to be zeroed, a multiple of four
     int* tickets;            // zeroed by the first pass
     long long ntickets;      // a multiple of four
     long long n, vocab, share;     // share: tokens of a CTA, a multiple of kTile
@@ -148,7 +153,7 @@ __device__ __forceinline__ int key_at(const SortParams& p, long long i) {
     return static_cast<int>(t < 0 ? p.vocab : t);
 }
 
-// How often each digit falls in each CTA's share.
+// How often each value of the first digit falls in each CTA's share.
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const __grid_constant__ SortParams p) {
     __shared__ int bins[kMaxBins];
     const int nbins = 1 << p.bits;
@@ -158,6 +163,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const __grid_c
     for (long long i = static_cast<long long>(blockIdx.x) * kSortThreads + threadIdx.x; i < p.ntickets / 4;
          i += static_cast<long long>(gridDim.x) * kSortThreads)
         reinterpret_cast<int4*>(p.tickets)[i] = make_int4(0, 0, 0, 0);
+    for (long long i = static_cast<long long>(blockIdx.x) * kSortThreads + threadIdx.x; i < p.nzeros / 4;
+         i += static_cast<long long>(gridDim.x) * kSortThreads)
+        reinterpret_cast<int4*>(p.next_counts)[i] = make_int4(0, 0, 0, 0);
     __syncthreads();
     const long long from = blockIdx.x * p.share, to = min(p.n, from + p.share);
 #pragma unroll 4
@@ -166,7 +174,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const __grid_c
     for (int b = threadIdx.x; b < nbins; b += kSortThreads) p.counts[blockIdx.x * nbins + b] = bins[b];
 }
 
-// Each token to its place by the digit, behind the earlier ones of the same.
+// Each token to its place by the digit, behind the earlier ones of the same; and
+// how often the next digit falls in each share that tokens are moved to.
 __global__ void __launch_bounds__(kSortThreads) sort_move_kernel(const __grid_constant__ SortParams p) {
     constexpr int kHalves = kSortThreads / kMaxBins;
     __shared__ int next[kMaxBins];                 // place of the next token of a digit
@@ -251,6 +260,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_move_kernel(const __grid_co
             const int at = of_warp[warp][key[i] >> p.shift & (nbins - 1)] + rank[i];
             p.keys[at] = key[i];
             p.places[at] = place[i];
+            if (p.next_counts)
+                atomicAdd(p.next_counts + static_cast<unsigned>(at) / static_cast<unsigned>(p.share) * nbins +
+                              (key[i] >> p.shift >> p.bits & (nbins - 1)), 1);
         }
         __syncwarp();                              // a warp's own counts alone are cleared next
     }
@@ -615,6 +627,7 @@ Plan plan_of(const ddp_embed_args* a) {
     while (a->vocab >> bits) ++bits;                            // keys reach vocab itself
     q.passes = (bits + kMaxBits - 1) / kMaxBits;
     q.bits = (bits + q.passes - 1) / q.passes;
+    if (q.bits < 2) q.bits = 2;                                 // a pass's counts fill 16 bytes
     const int64_t tiles = (n + kTile - 1) / kTile, each = (tiles + kMaxSortCtas - 1) / kMaxSortCtas;
     q.share = each * kTile;
     q.sort_ctas = static_cast<int>((n + q.share - 1) / q.share);
@@ -625,7 +638,7 @@ Plan plan_of(const ddp_embed_args* a) {
     q.places = at;
     at += 2 * up(4 * n);
     q.counts = at;
-    at += up(4LL * kMaxBins * q.sort_ctas);
+    at += up(4LL * kMaxBins * q.sort_ctas * q.passes);
     q.tickets = at;
     at += 2 * up(4 * (2 * q.windows * ((a->dim + kChunk - 1) / kChunk) + 4));
     q.parts = at;
@@ -720,7 +733,7 @@ int ddp_embed_backward(const ddp_embed_args* a, const void* grad, const void* to
     const bool vec = vectors(a, grad_table, grad);
     SortParams s = {};
     s.tokens = tokens;
-    s.counts = reinterpret_cast<int*>(ws + q.counts);
+    int* const counts = reinterpret_cast<int*>(ws + q.counts);
     s.tickets = reinterpret_cast<int*>(ws + q.tickets);
     s.n = a->tokens;
     s.vocab = a->vocab;
@@ -741,15 +754,20 @@ int ddp_embed_backward(const ddp_embed_args* a, const void* grad, const void* to
         const long long each = kThreads / kRankLanes;
         e = launch(sort_small_kernel, (a->tokens + each - 1) / each, kThreads, (a->tokens + 3) / 4 * 16, st, s);
     } else {
+        const int64_t each = static_cast<int64_t>(s.ctas) << q.bits;         // counts of a pass
         for (int pass = 0; pass < q.passes && e == cudaSuccess; ++pass) {
             s.shift = pass * q.bits;
             s.keys_in = pass ? keys[(pass - 1) & 1] : nullptr;
             s.places_in = pass ? places[(pass - 1) & 1] : nullptr;
             s.keys = keys[pass & 1];
             s.places = places[pass & 1];
-            e = launch(sort_count_kernel, s.ctas, kSortThreads, 0, st, s);
+            s.counts = counts + pass * each;
+            s.next_counts = pass + 1 < q.passes ? s.counts + each : nullptr;
+            if (pass == 0) {
+                s.nzeros = each * (q.passes - 1);
+                e = launch(sort_count_kernel, s.ctas, kSortThreads, 0, st, s);
+            }
             if (e == cudaSuccess) e = launch(sort_move_kernel, s.ctas, kSortThreads, 0, st, s);
-            s.ntickets = 0;
         }
     }
     if (e != cudaSuccess) return DDP_ERR_CUDA;
@@ -768,6 +786,7 @@ int ddp_embed_backward(const ddp_embed_args* a, const void* grad, const void* to
     p.scale = a->scale;
     p.splits = 1;
     while (p.splits < kMaxSplits && q.windows * p.chunks * p.splits < kFewWarps) p.splits *= 2;
+    while (p.splits < kMoreSplits && q.windows * p.chunks * p.splits < kMoreWarps) p.splits *= 2;
     const int64_t warps = q.windows * p.chunks * p.splits, sums = (warps + kThreads / 32 - 1) / (kThreads / 32);
     if (sums > INT32_MAX) return DDP_ERR_INVALID_ARG;
     p.sum_ctas = static_cast<unsigned>(sums);
