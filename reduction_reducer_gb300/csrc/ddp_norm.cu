@@ -52,11 +52,12 @@ struct NormParams {
     int nparts;
 };
 
-// Thread t's element j of chunk c in a group of G threads: eights next to one
-// another, or (rows that do not lie in vectors) every G-th element.
-template <bool VEC>
-__device__ __forceinline__ int place(int c, int j, int t, int G) {
-    return VEC ? (c * G + t) * 8 + j : (c * 8 + j) * G + t;
+// Thread t's i-th element of a row in a group of G threads: 16 bytes next to one
+// another at a time, or (rows that do not lie in vectors) every G-th element.
+template <typename T, bool VEC>
+__device__ __forceinline__ int place(int i, int t, int G) {
+    constexpr int kUnit = 16 / static_cast<int>(sizeof(T));
+    return VEC ? (i / kUnit * G + t) * kUnit + i % kUnit : i * G + t;
 }
 
 __device__ __forceinline__ float param_at(const void* p, int bf16, int at) {
@@ -65,85 +66,103 @@ __device__ __forceinline__ float param_at(const void* p, int bf16, int at) {
 
 // A thread's elements of a parameter vector, in pairs; `none` where there is no
 // vector, and past its end.
-template <int CH, bool VEC>
+template <typename T, int CH, bool VEC>
 __device__ __forceinline__ void load_param(const void* p, int bf16, float none, int t, int G, int dim, float2 (&f)[CH * 4]) {
 #pragma unroll
     for (int i = 0; i < CH * 4; ++i) {
         f[i] = both(none);
         if (!p) continue;
-        const int at = place<VEC>(i / 4, 2 * (i % 4), t, G), next = place<VEC>(i / 4, 2 * (i % 4) + 1, t, G);
+        const int at = place<T, VEC>(2 * i, t, G), next = place<T, VEC>(2 * i + 1, t, G);
         if (at < dim) f[i].x = param_at(p, bf16, at);
         if (next < dim) f[i].y = param_at(p, bf16, next);
     }
 }
 
-// A thread's place in shared memory for one row: the 16-byte pieces of all
-// threads next to one another.
-template <typename T, int CH>
-struct Slot {
-    static constexpr int kPieces = CH * static_cast<int>(sizeof(Eight<T>)) / 16;
-    static constexpr int kBytes = 16 * kPieces;              // of a thread
+// Rows on their way to the shared memory of a CTA.  Rows that lie in vectors: each
+// thread copies, and reads, 16-byte pieces of its own.  Others: the group copies
+// the 16-byte words that its row touches (none without an element of it), and all
+// of the group read from them.
+template <typename T, int CH, bool VEC>
+struct Lines {
+    static constexpr int kUnit = 16 / static_cast<int>(sizeof(T)), kPieces = CH * 8 / kUnit;
 
     uint4* at;
 
+    // words of one row of each group
+    static __device__ __host__ __forceinline__ int size(int threads, int groups) { return kPieces * threads + (VEC ? 0 : groups); }
+
+    __device__ __forceinline__ Lines(uint4* row, int group, int G) : at(row + (VEC ? threadIdx.x : group * (kPieces * G + 1))) {}
+
     __device__ __forceinline__ void request(const T* row, int t, int G, int dim) const {
+        if constexpr (VEC) {
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
-            if (place<true>(c, 0, t, G) < dim)
-#pragma unroll
-                for (int u = 0; u < kPieces / CH; ++u)
-                    copy_async(at + (c * (kPieces / CH) + u) * blockDim.x, reinterpret_cast<const uint4*>(row + place<true>(c, 0, t, G)) + u);
+            for (int k = 0; k < kPieces; ++k)
+                if ((k * G + t) * kUnit < dim) copy_async(at + k * blockDim.x, row + (k * G + t) * kUnit);
+        } else {
+            const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15);
+            const uint4* const words = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(row) - shift);
+            const int count = (shift + dim * static_cast<int>(sizeof(T)) + 15) / 16;
+            for (int k = t; k < count; k += G) copy_async(at + k, words + k);
+        }
     }
-    __device__ __forceinline__ void take(int t, int G, int dim, float2 (&x)[CH * 4]) const {
+    // zeros past the row's end
+    __device__ __forceinline__ void take(const T* row, int t, int G, int dim, float2 (&x)[CH * 4]) const {
+        if constexpr (!VEC) {
+            const T* const from = reinterpret_cast<const T*>(reinterpret_cast<const char*>(at) + (reinterpret_cast<uintptr_t>(row) & 15));
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            uint4 raw[kPieces / CH];
+            for (int i = 0; i < CH * 4; ++i) {
+                const int a = place<T, false>(2 * i, t, G), b = place<T, false>(2 * i + 1, t, G);
+                x[i].x = a < dim ? widen(from[a]) : 0.0f;
+                x[i].y = b < dim ? widen(from[b]) : 0.0f;
+            }
+        } else {
 #pragma unroll
-            for (int u = 0; u < kPieces / CH; ++u)
-                raw[u] = place<true>(c, 0, t, G) < dim ? at[(c * (kPieces / CH) + u) * blockDim.x] : make_uint4(0, 0, 0, 0);
-            if constexpr (sizeof(T) == 2) {
-                const uint32_t w[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
+            for (int k = 0; k < kPieces; ++k) {
+                const uint4 raw = (k * G + t) * kUnit < dim ? at[k * blockDim.x] : make_uint4(0, 0, 0, 0);
+                const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+                if constexpr (sizeof(T) == 2) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[c * 4 + j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
-            } else {
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    x[c * 4 + 2 * u] = make_float2(__uint_as_float(raw[u].x), __uint_as_float(raw[u].y));
-                    x[c * 4 + 2 * u + 1] = make_float2(__uint_as_float(raw[u].z), __uint_as_float(raw[u].w));
+                    for (int j = 0; j < 4; ++j) x[k * 4 + j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+                } else {
+                    x[k * 2] = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+                    x[k * 2 + 1] = make_float2(__uint_as_float(w[2]), __uint_as_float(w[3]));
                 }
             }
         }
     }
 };
 
-// A thread's elements of a row that does not lie in vectors; zeros past its end.
-template <int CH, typename T>
-__device__ __forceinline__ void load_single(const T* row, bool on, int t, int G, int dim, float2 (&x)[CH * 4]) {
+template <int CH, bool VEC, typename T>
+__device__ __forceinline__ void store_row(T* row, int t, int G, int dim, const float2 (&x)[CH * 4]) {
+    if constexpr (VEC) {
+        using L = Lines<T, CH, true>;
 #pragma unroll
-    for (int i = 0; i < CH * 4; ++i) {
-        const int at = place<false>(i / 4, 2 * (i % 4), t, G), next = place<false>(i / 4, 2 * (i % 4) + 1, t, G);
-        x[i].x = on && at < dim ? widen(row[at]) : 0.0f;
-        x[i].y = on && next < dim ? widen(row[next]) : 0.0f;
+        for (int k = 0; k < L::kPieces; ++k) {
+            uint4 w;
+            if constexpr (sizeof(T) == 2)
+                w = make_uint4(pack_bf16(x[k * 4].x, x[k * 4].y), pack_bf16(x[k * 4 + 1].x, x[k * 4 + 1].y),
+                               pack_bf16(x[k * 4 + 2].x, x[k * 4 + 2].y), pack_bf16(x[k * 4 + 3].x, x[k * 4 + 3].y));
+            else
+                w = make_uint4(__float_as_uint(x[k * 2].x), __float_as_uint(x[k * 2].y), __float_as_uint(x[k * 2 + 1].x),
+                               __float_as_uint(x[k * 2 + 1].y));
+            if ((k * G + t) * L::kUnit < dim) __stcs(reinterpret_cast<uint4*>(row + (k * G + t) * L::kUnit), w);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < CH * 8; ++i) {
+            const int at = place<T, false>(i, t, G);
+            if (at < dim) row[at] = narrow<T>(i & 1 ? x[i / 2].y : x[i / 2].x);
+        }
     }
 }
 
-template <int CH, bool VEC, typename T>
-__device__ __forceinline__ void store_row(T* row, int t, int G, int dim, const float2 (&x)[CH * 4]) {
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        if constexpr (VEC) {
-            const float f[8] = {x[c * 4].x, x[c * 4].y, x[c * 4 + 1].x, x[c * 4 + 1].y,
-                                x[c * 4 + 2].x, x[c * 4 + 2].y, x[c * 4 + 3].x, x[c * 4 + 3].y};
-            Eight<T> raw;
-            raw.put(f);
-            if (place<true>(c, 0, t, G) < dim) raw.store_once(row + place<true>(c, 0, t, G));
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int at = place<false>(c, j, t, G);
-                if (at < dim) row[at] = narrow<T>(j & 1 ? x[c * 4 + j / 2].y : x[c * 4 + j / 2].x);
-            }
-        }
+// Until the copies of a round have landed, for all of those who read them.
+template <int LANES, bool VEC, int LEFT>
+__device__ __forceinline__ void landed() {
+    copy_wait<LEFT>();
+    if constexpr (!VEC) {
+        if constexpr (LANES > 0) __syncwarp();
+        else __syncthreads();
     }
 }
 
@@ -164,49 +183,46 @@ __device__ __forceinline__ float group_sum(float x, float* shared) {
 
 // ---------------------------------------------------------------- forward
 
-// A group takes every so many rows and keeps its columns' weight and bias in
-// registers; rows that lie in vectors are copied to shared memory ahead.
+// A group takes every so many rows, which are copied to shared memory ahead, and
+// keeps its columns' weight and bias in registers.
 template <typename T, int LANES, int CH, bool VEC>
 __global__ void __launch_bounds__(LANES ? kForwardThreads : 32 * kMaxWarps) norm_kernel(const __grid_constant__ NormParams p) {
     extern __shared__ uint4 ahead[];
     __shared__ float shared[2][kMaxWarps];
     constexpr int kStages = kForwardStages<T>;
+    using L = Lines<T, CH, VEC>;
     const int G = LANES ? LANES : blockDim.x, t = threadIdx.x % G;
     const int groups = LANES ? kForwardThreads / LANES : 1, group = LANES ? threadIdx.x / LANES : 0;
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
     const long long stride = static_cast<long long>(gridDim.x) * groups, first = static_cast<long long>(blockIdx.x) * groups + group;
-    const auto slot = [&](int stage) { return Slot<T, CH>{ahead + stage * Slot<T, CH>::kPieces * blockDim.x + threadIdx.x}; };
+    const auto lines = [&](int stage) { return L(ahead + stage * L::size(blockDim.x, groups), group, G); };
     const T* x_next = static_cast<const T*>(p.x) + first * p.x_stride;
+    const T* x_now = x_next;
     T* out_next = static_cast<T*>(p.out) + first * p.out_stride;
     long long asked = first;                                     // the row that is asked for next
     const auto request = [&](int stage) {
-        if (asked < p.rows) slot(stage).request(x_next, t, G, p.dim);
+        if (asked < p.rows) lines(stage).request(x_next, t, G, p.dim);
         copy_commit();
         asked += stride;
         x_next += stride * p.x_stride;
     };
-    if constexpr (VEC)
 #pragma unroll
-        for (int s = 0; s + 1 < kStages; ++s) request(s);
+    for (int s = 0; s + 1 < kStages; ++s) request(s);
     float2 w[CH * 4], b[CH * 4];
-    load_param<CH, VEC>(p.weight, p.param_bf16, 1.0f, t, G, p.dim, w);
-    load_param<CH, VEC>(p.bias, p.param_bf16, 0.0f, t, G, p.dim, b);
+    load_param<T, CH, VEC>(p.weight, p.param_bf16, 1.0f, t, G, p.dim, w);
+    load_param<T, CH, VEC>(p.bias, p.param_bf16, 0.0f, t, G, p.dim, b);
     int stage = 0;
     // all groups of a warp take as many rounds, for their sums' shuffles
     for (long long row = first; row - group < p.rows; row += stride) {
         const bool on = row < p.rows;
         float2 x[CH * 4];
-        if constexpr (VEC) {
-            copy_wait<kStages - 2>();
-            slot(stage).take(t, G, p.dim, x);
-            // into the stage before this one, whose row has been used up
-            request(stage ? stage - 1 : kStages - 1);
-            stage = stage + 1 < kStages ? stage + 1 : 0;
-        } else {
-            load_single<CH>(x_next, on, t, G, p.dim, x);
-            x_next += stride * p.x_stride;
-        }
+        landed<LANES, VEC, kStages - 2>();
+        lines(stage).take(x_now, t, G, p.dim, x);
+        x_now += stride * p.x_stride;
+        // into the stage before this one, whose row everyone has taken
+        request(stage ? stage - 1 : kStages - 1);
+        stage = stage + 1 < kStages ? stage + 1 : 0;
         float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < CH * 4; ++i) sum = add2(sum, x[i]);
@@ -217,10 +233,10 @@ __global__ void __launch_bounds__(LANES ? kForwardThreads : 32 * kMaxWarps) norm
             x[i] = add2(x[i], both(-mean));
             // elements past the row's end count for nothing
             if constexpr (VEC) {
-                if (place<true>(i / 4, 0, t, G) < p.dim) sum = fma2(x[i], x[i], sum);
+                if (place<T, true>(2 * i, t, G) < p.dim) sum = fma2(x[i], x[i], sum);
             } else {
-                if (place<false>(i / 4, 2 * (i % 4), t, G) < p.dim) sum.x = fmaf(x[i].x, x[i].x, sum.x);
-                if (place<false>(i / 4, 2 * (i % 4) + 1, t, G) < p.dim) sum.y = fmaf(x[i].y, x[i].y, sum.y);
+                if (place<T, false>(2 * i, t, G) < p.dim) sum.x = fmaf(x[i].x, x[i].x, sum.x);
+                if (place<T, false>(2 * i + 1, t, G) < p.dim) sum.y = fmaf(x[i].y, x[i].y, sum.y);
             }
         }
         const float variance = __fdiv_rn(group_sum<LANES>(sum.x + sum.y, shared[1]), static_cast<float>(p.dim));
@@ -303,16 +319,19 @@ __global__ void __launch_bounds__(MAXT, 32 * kWarpsPerSm / MAXT) norm_backward_k
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
+    using L = Lines<T, CH, VEC>;
     const int tile = groups * ROWS;
     const long long first = static_cast<long long>(blockIdx.x) * tile, stride = static_cast<long long>(gridDim.x) * tile;
-    const auto slot = [&](int stage, int r, int which) {
-        return Slot<T, CH>{ahead + ((stage * ROWS + r) * 2 + which) * Slot<T, CH>::kPieces * blockDim.x + threadIdx.x};
+    const auto lines = [&](int stage, int r, int which) {
+        return L(ahead + ((stage * ROWS + r) * 2 + which) * L::size(blockDim.x, groups), group, G);
     };
     // of this thread's first row of a round: how many rows are left from it on, and where it is
     const auto left_of = [&](long long r0) { return static_cast<int>(min(p.rows - r0 - group, 1LL << 30)); };
     const long long x_step = groups * p.x_stride, dy_step = groups * p.grad_stride, out_step = groups * p.out_stride;
     const T* x_next = static_cast<const T*>(p.x) + (first + group) * p.x_stride;
     const T* dy_next = static_cast<const T*>(p.grad) + (first + group) * p.grad_stride;
+    const T* x_now = x_next;                                     // (for their places among 16 bytes)
+    const T* dy_now = dy_next;
     T* out_next = static_cast<T*>(p.out) + (first + group) * p.out_stride;
     const float2* stat_next = reinterpret_cast<const float2*>(p.stats) + first + group;
     long long asked = first;                                     // of the round that is asked for next
@@ -321,19 +340,18 @@ __global__ void __launch_bounds__(MAXT, 32 * kWarpsPerSm / MAXT) norm_backward_k
 #pragma unroll
         for (int r = 0; r < ROWS; ++r)
             if (r * groups < left) {
-                slot(stage, r, 0).request(x_next + r * x_step, t, G, p.dim);
-                slot(stage, r, 1).request(dy_next + r * dy_step, t, G, p.dim);
+                lines(stage, r, 0).request(x_next + r * x_step, t, G, p.dim);
+                lines(stage, r, 1).request(dy_next + r * dy_step, t, G, p.dim);
             }
         copy_commit();
         asked += stride;
         x_next += stride * p.x_stride;
         dy_next += stride * p.grad_stride;
     };
-    if constexpr (VEC)
 #pragma unroll
-        for (int s = 0; s + 1 < kBackwardStages; ++s) request(s);
+    for (int s = 0; s + 1 < kBackwardStages; ++s) request(s);
     float2 dw[CH * 4], db[CH * 4], w[CH * 4];
-    load_param<CH, VEC>(p.weight, p.param_bf16, 1.0f, t, G, p.dim, w);
+    load_param<T, CH, VEC>(p.weight, p.param_bf16, 1.0f, t, G, p.dim, w);
 #pragma unroll
     for (int i = 0; i < CH * 4; ++i) dw[i] = db[i] = make_float2(0.0f, 0.0f);
     const float over = __fdiv_rn(1.0f, static_cast<float>(p.dim));
@@ -344,26 +362,17 @@ __global__ void __launch_bounds__(MAXT, 32 * kWarpsPerSm / MAXT) norm_backward_k
         const int left = left_of(r0);
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) stat[r] = r * groups < left ? stat_next[r * groups] : make_float2(0.0f, 0.0f);
-        if constexpr (VEC) copy_wait<kBackwardStages - 2>();
+        landed<LANES, VEC, kBackwardStages - 2>();
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-            const bool on = r * groups < left;
-            if constexpr (VEC) {
-                const int dim = on ? p.dim : 0;                  // (zeros)
-                slot(stage, r, 0).take(t, G, dim, x[r]);
-                slot(stage, r, 1).take(t, G, dim, dy[r]);
-            } else {
-                load_single<CH>(x_next + r * x_step, on, t, G, p.dim, x[r]);
-                load_single<CH>(dy_next + r * dy_step, on, t, G, p.dim, dy[r]);
-            }
+            const int dim = r * groups < left ? p.dim : 0;       // (zeros)
+            lines(stage, r, 0).take(x_now + r * x_step, t, G, dim, x[r]);
+            lines(stage, r, 1).take(dy_now + r * dy_step, t, G, dim, dy[r]);
         }
-        if constexpr (VEC) {
-            request(stage ? stage - 1 : kBackwardStages - 1);    // used up a round ago
-            stage = stage + 1 < kBackwardStages ? stage + 1 : 0;
-        } else {
-            x_next += stride * p.x_stride;
-            dy_next += stride * p.grad_stride;
-        }
+        x_now += stride * p.x_stride;
+        dy_now += stride * p.grad_stride;
+        request(stage ? stage - 1 : kBackwardStages - 1);        // used up a round ago
+        stage = stage + 1 < kBackwardStages ? stage + 1 : 0;
         stat_next += stride;
         if (t < ROWS && t * groups < left_of(r0 + stride))       // near by the time that they are loaded
             asm volatile("prefetch.global.L1 [%0];" ::"l"(stat_next + t * groups));
@@ -419,7 +428,7 @@ __global__ void __launch_bounds__(MAXT, 32 * kWarpsPerSm / MAXT) norm_backward_k
         }
         __syncthreads();
         for (int i = threadIdx.x; i < 16 * LANES; i += kBackwardThreads) {
-            const int which = i / LANES, of = i % LANES, at = place<VEC>(0, which / 2, of, LANES);
+            const int which = i / LANES, of = i % LANES, at = place<T, VEC>(which / 2, of, LANES);
             float sum = 0.0f;
             for (int g = 0; g < groups; ++g) sum += columns[which * kBackwardThreads + g * LANES + of];
             if (at < p.dim) part[(which & 1) * p.dim + at] = sum;
@@ -427,7 +436,7 @@ __global__ void __launch_bounds__(MAXT, 32 * kWarpsPerSm / MAXT) norm_backward_k
     } else {
 #pragma unroll
         for (int i = 0; i < CH * 8; ++i) {
-            const int at = place<VEC>(i / 8, i % 8, t, G);
+            const int at = place<T, VEC>(i, t, G);
             if (at < p.dim) {
                 part[at] = i & 1 ? dw[i / 2].y : dw[i / 2].x;
                 part[p.dim + at] = i & 1 ? db[i / 2].y : db[i / 2].x;
@@ -521,6 +530,7 @@ struct Split {
 Split forward_split(int dim) {
     const int eights = (dim + 7) / 8;
     if (eights <= 8) return {8, 1, kForwardThreads};
+    if (eights <= 16) return {16, 1, kForwardThreads};
     if (eights <= 32) return {32, 1, kForwardThreads};
     if (eights <= 64) return {32, 2, kForwardThreads};
     if (eights <= 128) return {32, 4, kForwardThreads};
@@ -533,6 +543,7 @@ Split forward_split(int dim) {
 Split backward_split(int dim, int size) {
     const int eights = (dim + 7) / 8, most = 32 * kMaxWarps;
     if (eights <= 8) return {8, 1, kBackwardThreads};
+    if (eights <= 16) return {16, 1, kBackwardThreads};
     if (eights <= 32) return {32, 1, kBackwardThreads};
     if (eights <= most) return {0, 1, round_up(eights, 32)};
     if (eights <= 2 * most) return {0, 2, round_up((eights + 1) / 2, 32)};
@@ -552,15 +563,14 @@ int backward_parts(int dim, int size, long long rows) {
 
 template <typename T, int LANES, int CH>
 cudaError_t forward_as(const Split& s, bool vec, const NormParams& p, cudaStream_t stream) {
-    static std::atomic<uint64_t> allowed{0};
+    static std::atomic<uint64_t> allowed[2];                     // of the kernel for vectors, and of the other
     const int groups = LANES ? kForwardThreads / LANES : 1;
     const long long need = (p.rows + groups - 1) / groups, most = kForwardWaves * resident(s.threads);
-    const size_t shared = vec ? static_cast<size_t>(kForwardStages<T>) * Slot<T, CH>::kBytes * s.threads : 0;
+    const size_t shared = 16ull * kForwardStages<T> *
+                          (vec ? Lines<T, CH, true>::size(s.threads, groups) : Lines<T, CH, false>::size(s.threads, groups));
     void (*const kernel)(NormParams) = vec ? norm_kernel<T, LANES, CH, true> : norm_kernel<T, LANES, CH, false>;
-    const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), shared, allowed);
-    // (rows that are not copied ahead overlap by having more CTAs wait)
-    const long long most_now = vec ? most : 16 * most;
-    return e != cudaSuccess ? e : launch(kernel, need < most_now ? need : most_now, s.threads, shared, stream, p);
+    const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), shared, allowed[vec]);
+    return e != cudaSuccess ? e : launch(kernel, need < most ? need : most, s.threads, shared, stream, p);
 }
 
 template <typename T>
@@ -568,6 +578,7 @@ cudaError_t forward(bool vec, const NormParams& p, cudaStream_t stream) {
     const Split s = forward_split(p.dim);
     if (!s.chunks) return launch(norm_long_kernel<T>, p.rows < kSms * 2 ? p.rows : kSms * 2, s.threads, 0, stream, p);
     if (s.lanes == 8) return forward_as<T, 8, 1>(s, vec, p, stream);
+    if (s.lanes == 16) return forward_as<T, 16, 1>(s, vec, p, stream);
     if (s.lanes == 0) return forward_as<T, 0, 4>(s, vec, p, stream);
     if (s.chunks == 1) return forward_as<T, 32, 1>(s, vec, p, stream);
     if (s.chunks == 2) return forward_as<T, 32, 2>(s, vec, p, stream);
@@ -576,12 +587,14 @@ cudaError_t forward(bool vec, const NormParams& p, cudaStream_t stream) {
 
 template <typename T, int LANES, int CH, int ROWS, int MAXT>
 cudaError_t backward_as(const Split& s, bool vec, const NormParams& p, cudaStream_t stream) {
-    static std::atomic<uint64_t> allowed{0};
-    static_assert(kBackwardStages * ROWS * 2 * Slot<T, CH>::kBytes >= 64, "16 columns of a thread");
-    const size_t shared = vec ? static_cast<size_t>(kBackwardStages) * ROWS * 2 * Slot<T, CH>::kBytes * s.threads : LANES ? 64 * s.threads : 0;
+    static std::atomic<uint64_t> allowed[2];                     // of the kernel for vectors, and of the other
+    static_assert(kBackwardStages * ROWS * 2 * Lines<T, CH, true>::kPieces >= 4, "16 columns of a thread");
+    const int groups = LANES ? kBackwardThreads / LANES : 1;
+    const size_t shared = 16ull * kBackwardStages * ROWS * 2 *
+                          (vec ? Lines<T, CH, true>::size(s.threads, groups) : Lines<T, CH, false>::size(s.threads, groups));
     void (*const kernel)(NormParams) =
         vec ? norm_backward_kernel<T, LANES, CH, ROWS, true, MAXT> : norm_backward_kernel<T, LANES, CH, ROWS, false, MAXT>;
-    const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), shared, allowed);
+    const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), shared, allowed[vec]);
     return e != cudaSuccess ? e : launch(kernel, p.nparts, s.threads, shared, stream, p);
 }
 
@@ -591,10 +604,12 @@ cudaError_t backward(bool vec, const NormParams& p, cudaStream_t stream) {
     const Split s = backward_split(p.dim, sizeof(T));
     cudaError_t e = cudaSuccess;
     if (s.chunks == 1)
-        e = s.lanes == 8 ? backward_as<T, 8, 1, R, 256>(s, vec, p, stream)
-                         : s.lanes ? backward_as<T, 32, 1, R, 256>(s, vec, p, stream) : s.threads <= 128 ? backward_as<T, 0, 1, R, 128>(s, vec, p, stream) : backward_as<T, 0, 1, R, 512>(s, vec, p, stream);
+        e = s.lanes == 8    ? backward_as<T, 8, 1, R, 256>(s, vec, p, stream)
+            : s.lanes == 16 ? backward_as<T, 16, 1, R, 256>(s, vec, p, stream)
+            : s.lanes == 32 ? backward_as<T, 32, 1, R, 256>(s, vec, p, stream)
+            : s.threads <= 128 ? backward_as<T, 0, 1, R, 128>(s, vec, p, stream) : backward_as<T, 0, 1, R, 512>(s, vec, p, stream);
     else if (s.chunks == 2) {
-        if constexpr (R >= 2) e = backward_as<T, 0, 2, R / 2, 512>(s, vec, p, stream);
+        e = backward_as<T, 0, 2, R / 2, 512>(s, vec, p, stream);
     } else if (s.chunks == 4) {
         if constexpr (R == 4) e = backward_as<T, 0, 4, 1, 512>(s, vec, p, stream);
     } else {
@@ -642,7 +657,7 @@ int ddp_layer_norm(const ddp_layer_norm_args* a, const void* x, const void* weig
     p.bias = bias;
     p.out = y;
     p.stats = stats;
-    const bool vec = a->dim % 8 == 0 && aligned(x, 16) && aligned(y, 16) &&
+    const bool vec = a->dim * size % 16 == 0 && aligned(x, 16) && aligned(y, 16) &&
                      (a->rows == 1 || (a->x_stride * size % 16 == 0 && a->out_stride * size % 16 == 0));
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = a->dtype == DDP_F32 ? forward<float>(vec, p, st) : forward<uint16_t>(vec, p, st);
@@ -683,7 +698,7 @@ int ddp_layer_norm_backward(const ddp_layer_norm_args* a, const void* grad_y, in
     p.accumulate = accumulate != 0;
     p.parts = params ? static_cast<float*>(workspace) : nullptr;
     p.nparts = backward_parts(p.dim, size, p.rows);
-    const bool vec = a->dim % 8 == 0 && aligned(x, 16) && aligned(grad_y, 16) && aligned(grad_x, 16) &&
+    const bool vec = a->dim * size % 16 == 0 && aligned(x, 16) && aligned(grad_y, 16) && aligned(grad_x, 16) &&
                      (a->rows == 1 || (a->x_stride * size % 16 == 0 && a->out_stride * size % 16 == 0 && grad_stride * size % 16 == 0));
     const cudaError_t e = a->dtype == DDP_F32 ? backward<float>(vec, p, st) : backward<uint16_t>(vec, p, st);
     return e == cudaSuccess ? DDP_OK : DDP_ERR_CUDA;

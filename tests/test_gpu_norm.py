@@ -21,7 +21,7 @@ pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
 KINDS = {"f32": torch.float32, "bf16": torch.bfloat16}
 HALF = {"f32": U, "bf16": 2.0 ** -8}
-DIMS = [1, 3, 8, 64, 72, 100, 256, 264, 512, 769, 1000, 1024, 1032, 2048, 2500, 4096, 4104, 8200, 33000]
+DIMS = [1, 3, 4, 8, 60, 64, 72, 100, 128, 129, 136, 256, 264, 512, 769, 1000, 1004, 1023, 1024, 1032, 2048, 2500, 4096, 4104, 8200, 11101, 16384, 33000]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -70,7 +70,7 @@ def check_forward(x, w, b, eps, got, kind):
 @pytest.mark.parametrize("kind,param_kind", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16"), ("f32", "bf16")])
 @pytest.mark.parametrize("dim", DIMS)
 def test_forward(dim, kind, param_kind):
-    for n, extra, shift in ((1, 0, 0), (5, 8, 0), (37, 0, 0), (6, 3, 1)):
+    for n, extra, shift in ((1, 0, 0), (5, 8, 0), (37, 0, 0), (6, 3, 1), (3, 4, 2), (140, 1, 0)):
         x = rows(n, dim, kind, dim, extra, shift)
         w, b = params(dim, param_kind, 7, shift)
         for weight, bias in ((w, b), (w, None), (None, None)):
@@ -101,7 +101,7 @@ def check_backward(x, g, stats, w, kind, param_kind, **how):
 @pytest.mark.parametrize("kind,param_kind", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16"), ("f32", "bf16")])
 @pytest.mark.parametrize("dim", DIMS)
 def test_backward(dim, kind, param_kind):
-    for n, extra, shift in ((1, 0, 0), (5, 8, 0), (131, 0, 0), (6, 3, 1)):
+    for n, extra, shift in ((1, 0, 0), (5, 8, 0), (131, 0, 0), (6, 3, 1), (3, 4, 2), (140, 1, 0)):
         x, g = rows(n, dim, kind, dim, extra, shift), rows(n, dim, kind, dim + 1, extra, shift, 0.1)
         w, _ = params(dim, param_kind, 7, shift)
         stats = layer_norm(x, w)[1]
