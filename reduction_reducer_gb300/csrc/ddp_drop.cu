@@ -77,7 +77,7 @@ __device__ __forceinline__ uint32_t staying(const DropParams& p, long long group
     return p.none ? 0u : mask;
 }
 
-// Whole: one run of n elements from 16-byte boundaries.  Rows: rows of a multiple
+// Whole: one run of n elements from boundaries of eight.  Rows: rows of a multiple
 // of eight elements, each from one.  Single: anything else, element by element.
 enum Layout { kWhole, kRows, kSingle };
 
@@ -122,8 +122,8 @@ __global__ void __launch_bounds__(kThreads) drop_kernel(const __grid_constant__ 
                 at[i] = row * p.out_stride + col;
             }
             if (count[i] == 8) {
-                a[i].load_once(x + rx);
-                if constexpr (RESIDUAL) r[i].load_once(residual + rr);
+                a[i].load_wide(x + rx);
+                if constexpr (RESIDUAL) r[i].load_wide(residual + rr);
             }
         }
 #pragma unroll
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads) drop_kernel(const __grid_constant__ 
                     if constexpr (RESIDUAL) y[j] += z[j];
                 }
                 a[i].put(y);
-                a[i].store_once(out + at[i]);
+                a[i].store_wide(out + at[i]);
             } else {
                 for (int j = 0; j < count[i]; ++j) {          // the last few of a whole run
                     float y = mask >> j & 1 ? widen(x[at[i] + j]) * p.scale : 0.0f;
@@ -192,8 +192,9 @@ extern "C" int ddp_drop(const ddp_drop_args* a, const void* x, const void* resid
     p.none = least >> 32 != 0;
     p.least = static_cast<uint32_t>(least);
     p.scale = p.none ? 0.0f : static_cast<float>(1.0 / (1.0 - a->p));
-    const bool vectors = aligned(x, 16) && aligned(residual, 16) && aligned(out, 16);
-    const auto strided = [&](int64_t stride) { return stride * size % 16 != 0; };
+    const int eight = 8 * size;                             // bytes, and where eights have to start
+    const bool vectors = aligned(x, eight) && aligned(residual, eight) && aligned(out, eight);
+    const auto strided = [&](int64_t stride) { return stride % 8 != 0; };
     Layout layout = kSingle;
     if (a->rows == 1 || (p.x_stride == p.cols && p.residual_stride == p.cols && p.out_stride == p.cols)) {
         p.cols = p.n;                                       // one run

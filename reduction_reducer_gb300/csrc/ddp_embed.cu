@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__
                     }
                     Eight<Tout> y;
                     y.put(f);
-                    if (r0 + u * slots < p.n) y.store_once(out + (r0 + u * slots) * p.out_stride + at);
+                    if (r0 + u * slots < p.n) y.store_wide(out + (r0 + u * slots) * p.out_stride + at);
                 }
             } else {
                 float f[kAhead];
@@ -367,7 +367,7 @@ __device__ __forceinline__ void put_row(const SumParams& p, long long row, const
     if constexpr (VEC) {
         Eight<Tout> raw;
         raw.put(f);
-        if (c.on(0)) raw.store_once(to + c.first);
+        if (c.on(0)) raw.store_wide(to + c.first);
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -657,9 +657,8 @@ bool valid(const ddp_embed_args* a) {
 int size_of(int dtype) { return dtype == DDP_F32 ? 4 : 2; }
 
 bool vectors(const ddp_embed_args* a, const void* table, const void* rows) {
-    return a->dim % 8 == 0 && aligned(table, 16) && aligned(rows, 16) &&
-           (a->vocab == 1 || a->table_stride * size_of(a->table_dtype) % 16 == 0) &&
-           (a->tokens == 1 || a->row_stride * size_of(a->dtype) % 16 == 0);
+    return a->dim % 8 == 0 && aligned(table, 8 * size_of(a->table_dtype)) && aligned(rows, 8 * size_of(a->dtype)) &&
+           (a->vocab == 1 || a->table_stride % 8 == 0) && (a->tokens == 1 || a->row_stride % 8 == 0);
 }
 
 int row_threads(int64_t pieces) { return pieces >= kThreads ? kThreads : power_of_two(pieces); }

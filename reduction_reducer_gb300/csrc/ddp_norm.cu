@@ -11,6 +11,7 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -25,6 +26,7 @@ constexpr int kBackwardThreads = 256;
 constexpr int kMaxWarps = 16;          // of a CTA that holds a row, in registers
 constexpr int kLongThreads = 1024;     // of one that reads it again and again
 constexpr int kLongWarps = kLongThreads / 32;
+constexpr int kLongParts = 64;         // of rows of any length, over which the columns are summed
 constexpr int kColumns = 256;          // of a CTA of norm_columns_kernel
 constexpr int kJoinLanes = 32;         // join_kernel: threads of a column
 constexpr int kForwardWaves = 3;       // 65,536 x 1024 in bf16: one 50.1 us, two 46.3, three 44.7, four 45.8, six 52.7
@@ -456,17 +458,27 @@ __global__ void __launch_bounds__(kLongThreads) norm_backward_long_kernel(const 
         const T* const dy = static_cast<const T*>(p.grad) + row * p.grad_stride;
         T* const dx = static_cast<T*>(p.out) + row * p.out_stride;
         const float2 stat = *reinterpret_cast<const float2*>(p.stats + 2 * row);
+        const auto weight = [&](int i) { return p.weight ? param_at(p.weight, p.param_bf16, i) : 1.0f; };
         float a = 0.0f, b = 0.0f;
-        for (int i = threadIdx.x; i < p.dim; i += blockDim.x) {
-            const float g = widen(dy[i]) * (p.weight ? param_at(p.weight, p.param_bf16, i) : 1.0f);
+#pragma unroll 4
+        for (int i = threadIdx.x; i < p.dim; i += kLongThreads) {
+            const float g = widen(dy[i]) * weight(i);
             a += g;
             b = fmaf(g, (widen(x[i]) - stat.x) * stat.y, b);
         }
         a = __fdiv_rn(group_sum<0>(a, shared[0]), static_cast<float>(p.dim));
         b = __fdiv_rn(group_sum<0>(b, shared[1]), static_cast<float>(p.dim));
-        for (int i = threadIdx.x; i < p.dim; i += blockDim.x) {
-            const float g = widen(dy[i]) * (p.weight ? param_at(p.weight, p.param_bf16, i) : 1.0f);
-            dx[i] = narrow<T>(stat.y * (g - a - (widen(x[i]) - stat.x) * stat.y * b));
+        for (int i0 = threadIdx.x; i0 < p.dim; i0 += 4 * kLongThreads) {
+            float g[4], xh[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + u * kLongThreads;
+                g[u] = i < p.dim ? widen(dy[i]) * weight(i) : 0.0f;
+                xh[u] = i < p.dim ? (widen(x[i]) - stat.x) * stat.y : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (i0 + u * kLongThreads < p.dim) dx[i0 + u * kLongThreads] = narrow<T>(stat.y * (g[u] - a - xh[u] * b));
         }
         __syncthreads();                   // shared is written again by the next row
     }
@@ -480,6 +492,7 @@ __global__ void __launch_bounds__(kColumns) norm_columns_kernel(const __grid_con
     const int part = blockIdx.x % p.nparts, at = blockIdx.x / p.nparts * kColumns + threadIdx.x;
     if (at >= p.dim) return;
     float dw = 0.0f, db = 0.0f;
+#pragma unroll 8
     for (long long row = part; row < p.rows; row += p.nparts) {
         const float2 stat = *reinterpret_cast<const float2*>(p.stats + 2 * row);
         const float g = widen(static_cast<const T*>(p.grad)[row * p.grad_stride + at]);
@@ -539,25 +552,28 @@ Split forward_split(int dim) {
 }
 
 // The gradient holds 32 values of a round's rows and gradients each in bf16 and
-// 16 in fp32, so that a round takes as many bytes: chunks x rows is 4 or 2.
-Split backward_split(int dim, int size) {
+// 16 in fp32, so that a round takes as many bytes: chunks x rows is 4 or 2.  32
+// columns of a thread do not fit its registers with their sums, but read in
+// vectors they are still faster than the rows of any length (4,089 bf16 rows of
+// 16,384: 152 us and 269; of 11,101, one by one: 536 and 310).
+Split backward_split(int dim, int size, bool vec) {
     const int eights = (dim + 7) / 8, most = 32 * kMaxWarps;
     if (eights <= 8) return {8, 1, kBackwardThreads};
     if (eights <= 16) return {16, 1, kBackwardThreads};
     if (eights <= 32) return {32, 1, kBackwardThreads};
     if (eights <= most) return {0, 1, round_up(eights, 32)};
     if (eights <= 2 * most) return {0, 2, round_up((eights + 1) / 2, 32)};
-    if (eights <= 4 * most && size == 2) return {0, 4, round_up((eights + 3) / 4, 32)};
+    if (eights <= 4 * most && size == 2 && vec) return {0, 4, round_up((eights + 3) / 4, 32)};
     return {0, 0, kLongThreads};
 }
 
 int resident(int threads) { return kSms * (32 * kWarpsPerSm / threads > 1 ? 32 * kWarpsPerSm / threads : 1); }
 
 // CTAs of the gradient, each with a part of the weight's.
-int backward_parts(int dim, int size, long long rows) {
-    const Split s = backward_split(dim, size);
+int backward_parts(int dim, int size, bool vec, long long rows) {
+    const Split s = backward_split(dim, size, vec);
     const long long tile = s.chunks ? (s.lanes ? kBackwardThreads / s.lanes : 1) * (size == 2 ? 4 : 2) / s.chunks : 8;
-    const long long most = s.chunks ? resident(s.threads) : 64, need = (rows + tile - 1) / tile;
+    const long long most = s.chunks ? resident(s.threads) : kLongParts, need = (rows + tile - 1) / tile;
     return static_cast<int>(need < most ? need : most);
 }
 
@@ -592,8 +608,9 @@ cudaError_t backward_as(const Split& s, bool vec, const NormParams& p, cudaStrea
     const int groups = LANES ? kBackwardThreads / LANES : 1;
     const size_t shared = 16ull * kBackwardStages * ROWS * 2 *
                           (vec ? Lines<T, CH, true>::size(s.threads, groups) : Lines<T, CH, false>::size(s.threads, groups));
-    void (*const kernel)(NormParams) =
-        vec ? norm_backward_kernel<T, LANES, CH, ROWS, true, MAXT> : norm_backward_kernel<T, LANES, CH, ROWS, false, MAXT>;
+    void (*kernel)(NormParams) = norm_backward_kernel<T, LANES, CH, ROWS, true, MAXT>;
+    if constexpr (CH < 4)
+        if (!vec) kernel = norm_backward_kernel<T, LANES, CH, ROWS, false, MAXT>;
     const cudaError_t e = allow_shared(reinterpret_cast<const void*>(kernel), shared, allowed[vec]);
     return e != cudaSuccess ? e : launch(kernel, p.nparts, s.threads, shared, stream, p);
 }
@@ -601,7 +618,7 @@ cudaError_t backward_as(const Split& s, bool vec, const NormParams& p, cudaStrea
 template <typename T>
 cudaError_t backward(bool vec, const NormParams& p, cudaStream_t stream) {
     constexpr int R = sizeof(T) == 2 ? 4 : 2;                // rows x chunks
-    const Split s = backward_split(p.dim, sizeof(T));
+    const Split s = backward_split(p.dim, sizeof(T), vec);
     cudaError_t e = cudaSuccess;
     if (s.chunks == 1)
         e = s.lanes == 8    ? backward_as<T, 8, 1, R, 256>(s, vec, p, stream)
@@ -666,7 +683,9 @@ int ddp_layer_norm(const ddp_layer_norm_args* a, const void* x, const void* weig
 
 int64_t ddp_layer_norm_workspace(const ddp_layer_norm_args* a) {
     if (!valid(a)) return DDP_ERR_INVALID_ARG;
-    return a->rows == 0 ? 0 : 8LL * a->dim * backward_parts(static_cast<int>(a->dim), a->dtype == DDP_F32 ? 4 : 2, a->rows);
+    if (a->rows == 0) return 0;
+    const int dim = static_cast<int>(a->dim), size = a->dtype == DDP_F32 ? 4 : 2;
+    return 8LL * dim * std::max(backward_parts(dim, size, false, a->rows), backward_parts(dim, size, true, a->rows));
 }
 
 int ddp_layer_norm_backward(const ddp_layer_norm_args* a, const void* grad_y, int64_t grad_stride, const void* x,
@@ -697,9 +716,9 @@ int ddp_layer_norm_backward(const ddp_layer_norm_args* a, const void* grad_y, in
     p.grad_bias = grad_bias;
     p.accumulate = accumulate != 0;
     p.parts = params ? static_cast<float*>(workspace) : nullptr;
-    p.nparts = backward_parts(p.dim, size, p.rows);
     const bool vec = a->dim * size % 16 == 0 && aligned(x, 16) && aligned(grad_y, 16) && aligned(grad_x, 16) &&
                      (a->rows == 1 || (a->x_stride * size % 16 == 0 && a->out_stride * size % 16 == 0 && grad_stride * size % 16 == 0));
+    p.nparts = backward_parts(p.dim, size, vec, p.rows);
     const cudaError_t e = a->dtype == DDP_F32 ? backward<float>(vec, p, st) : backward<uint16_t>(vec, p, st);
     return e == cudaSuccess ? DDP_OK : DDP_ERR_CUDA;
 }

@@ -54,7 +54,7 @@ __device__ __forceinline__ uint4 ld_once(const void* p) {
 }
 
 // Eight neighbouring elements as they lie in memory: one or two accesses of 16
-// bytes, from a 16-byte boundary.
+// bytes, from a 16-byte boundary, or (wide) one, from a boundary of their size.
 template <typename T> struct Eight;
 
 template <> struct Eight<uint16_t> {
@@ -75,7 +75,8 @@ template <> struct Eight<uint16_t> {
     __device__ __forceinline__ void put(const float (&f)[8]) {
         v = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
     }
-    __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = v; }
+    __device__ __forceinline__ void load_wide(const uint16_t* p) { v = ld_once(p); }
+    __device__ __forceinline__ void store_wide(uint16_t* p) const { __stcs(reinterpret_cast<uint4*>(p), v); }
     __device__ __forceinline__ void store_once(uint16_t* p) const { __stcs(reinterpret_cast<uint4*>(p), v); }
 };
 
@@ -106,9 +107,16 @@ template <> struct Eight<float> {
             v[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]),
                               __float_as_uint(f[4 * i + 3]));
     }
-    __device__ __forceinline__ void store(float* p) const {
-        reinterpret_cast<uint4*>(p)[0] = v[0];
-        reinterpret_cast<uint4*>(p)[1] = v[1];
+    // whole sectors at once, from a 32-byte boundary: halves of one that two
+    // accesses past L1 ask for are fetched twice
+    __device__ __forceinline__ void load_wide(const float* p) {
+        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x), "=r"(v[1].y), "=r"(v[1].z), "=r"(v[1].w)
+                     : "l"(p));
+    }
+    __device__ __forceinline__ void store_wide(float* p) const {
+        asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0].x), "r"(v[0].y), "r"(v[0].z),
+                     "r"(v[0].w), "r"(v[1].x), "r"(v[1].y), "r"(v[1].z), "r"(v[1].w) : "memory");
     }
     __device__ __forceinline__ void store_once(float* p) const {
         __stcs(reinterpret_cast<uint4*>(p), v[0]);
