@@ -34,7 +34,7 @@ struct DropParams {
     uint64_t seed;
     uint32_t offset_lo, offset_hi;
     uint32_t least;          // an element stays where its bits are no less
-    int none;                // nothing stays
+    int none;                // nothing stays (and least is 2^32 - 1)
     float scale;
 };
 
@@ -52,17 +52,17 @@ __device__ __forceinline__ Words philox(uint32_t c0, uint32_t c1, uint32_t c2, u
     return Words{{c0, c1, c2, c3}};
 }
 
-// Which of the eight elements of a group stay: bit j for element j.
-__device__ __forceinline__ uint32_t staying(const DropParams& p, long long group, uint32_t k0, uint32_t k1) {
+// Which of the eight elements of a group stay.
+__device__ __forceinline__ void staying(const DropParams& p, long long group, uint32_t k0, uint32_t k1, bool (&stays)[8]) {
     const uint32_t lo = static_cast<uint32_t>(group), hi = static_cast<uint32_t>(group >> 32);
     const Words u = philox(lo, hi, p.offset_lo, p.offset_hi, k0, k1);
     const uint32_t border = p.least & 0xffff0000u;
-    uint32_t mask = 0, closest = 0xffffffffu;
+    uint32_t closest = 0xffffffffu;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         // the 16 bits at the top, and something below them that does not matter
         const uint32_t bits = j & 1 ? u.w[j / 2] : u.w[j / 2] << 16;
-        mask |= bits >= border ? 1u << j : 0u;
+        stays[j] = bits >= border;
         closest = min(closest, bits - border);
     }
     if (closest < 0x10000u && (p.least & 0xffffu)) {      // some have the border's upper half: the lower decides
@@ -71,21 +71,20 @@ __device__ __forceinline__ uint32_t staying(const DropParams& p, long long group
         for (int j = 0; j < 8; ++j) {
             const uint32_t upper = j & 1 ? u.w[j / 2] & 0xffff0000u : u.w[j / 2] << 16;
             const uint32_t lower = j & 1 ? v.w[j / 2] >> 16 : v.w[j / 2] & 0xffffu;
-            if (upper == border && lower < (p.least & 0xffffu)) mask &= ~(1u << j);
+            if (upper == border && (lower < (p.least & 0xffffu) || p.none)) stays[j] = false;
         }
     }
-    return p.none ? 0u : mask;
 }
 
 // Whole: one run of n elements from boundaries of eight.  Rows: rows of a multiple
 // of eight elements, each from one.  Single: anything else, element by element.
 enum Layout { kWhole, kRows, kSingle };
 
-template <typename T, bool RESIDUAL, Layout LAYOUT>
+template <typename T, bool RESIDUAL, Layout LAYOUT, bool SEED>
 __global__ void __launch_bounds__(kThreads) drop_kernel(const __grid_constant__ DropParams p) {
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
-    const uint64_t seed = p.device_seed ? *p.device_seed : p.seed;
+    const uint64_t seed = SEED ? *p.device_seed : p.seed;
     const uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
     const T* const x = static_cast<const T*>(p.x);
     const T* const residual = static_cast<const T*>(p.residual);
@@ -95,10 +94,13 @@ __global__ void __launch_bounds__(kThreads) drop_kernel(const __grid_constant__ 
         for (int i = 0; i < kGroups; ++i) {
             const long long group = first + i * kThreads, from = group * 8;
             if (from >= p.n) return;
-            const uint32_t mask = staying(p, group, k0, k1);
+            bool stays[8];
+            staying(p, group, k0, k1, stays);
             long long row = from / p.cols, col = from % p.cols;
-            for (int j = 0; j < 8 && from + j < p.n; ++j) {
-                float y = mask >> j & 1 ? widen(x[row * p.x_stride + col]) * p.scale : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (from + j >= p.n) break;
+                float y = stays[j] ? widen(x[row * p.x_stride + col]) * p.scale : 0.0f;
                 if constexpr (RESIDUAL) y += widen(residual[row * p.residual_stride + col]);
                 out[row * p.out_stride + col] = narrow<T>(y);
                 if (++col == p.cols) { col = 0; ++row; }
@@ -128,21 +130,24 @@ __global__ void __launch_bounds__(kThreads) drop_kernel(const __grid_constant__ 
         }
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
-            const uint32_t mask = staying(p, first + i * kThreads, k0, k1);
+            bool stays[8];
+            staying(p, first + i * kThreads, k0, k1, stays);
             if (count[i] == 8) {
                 float y[8], z[8];
                 a[i].get(y);
                 if constexpr (RESIDUAL) r[i].get(z);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    y[j] = mask >> j & 1 ? y[j] * p.scale : 0.0f;
+                    y[j] = stays[j] ? y[j] * p.scale : 0.0f;
                     if constexpr (RESIDUAL) y[j] += z[j];
                 }
                 a[i].put(y);
                 a[i].store_wide(out + at[i]);
             } else {
-                for (int j = 0; j < count[i]; ++j) {          // the last few of a whole run
-                    float y = mask >> j & 1 ? widen(x[at[i] + j]) * p.scale : 0.0f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {                 // the last few of a whole run
+                    if (j >= count[i]) break;
+                    float y = stays[j] ? widen(x[at[i] + j]) * p.scale : 0.0f;
                     if constexpr (RESIDUAL) y += widen(residual[at[i] + j]);
                     out[at[i] + j] = narrow<T>(y);
                 }
@@ -151,15 +156,16 @@ __global__ void __launch_bounds__(kThreads) drop_kernel(const __grid_constant__ 
     }
 }
 
+template <typename T, bool RESIDUAL, bool SEED>
+void (*kernel_of(Layout layout))(DropParams) {
+    return layout == kWhole ? drop_kernel<T, RESIDUAL, kWhole, SEED>
+                            : layout == kRows ? drop_kernel<T, RESIDUAL, kRows, SEED> : drop_kernel<T, RESIDUAL, kSingle, SEED>;
+}
+
 template <typename T>
 cudaError_t launch_drop(Layout layout, long long ctas, const DropParams& p, cudaStream_t stream) {
-    void (*kernel)(DropParams);
-    if (p.residual)
-        kernel = layout == kWhole ? drop_kernel<T, true, kWhole>
-                                  : layout == kRows ? drop_kernel<T, true, kRows> : drop_kernel<T, true, kSingle>;
-    else
-        kernel = layout == kWhole ? drop_kernel<T, false, kWhole>
-                                  : layout == kRows ? drop_kernel<T, false, kRows> : drop_kernel<T, false, kSingle>;
+    void (*const kernel)(DropParams) = p.residual ? (p.device_seed ? kernel_of<T, true, true>(layout) : kernel_of<T, true, false>(layout))
+                                                  : (p.device_seed ? kernel_of<T, false, true>(layout) : kernel_of<T, false, false>(layout));
     return launch(kernel, ctas, kThreads, 0, stream, p);
 }
 
@@ -190,7 +196,7 @@ extern "C" int ddp_drop(const ddp_drop_args* a, const void* x, const void* resid
     p.offset_hi = static_cast<uint32_t>(a->offset >> 32);
     const long long least = std::llrint(a->p * 4294967296.0);
     p.none = least >> 32 != 0;
-    p.least = static_cast<uint32_t>(least);
+    p.least = p.none ? 0xffffffffu : static_cast<uint32_t>(least);
     p.scale = p.none ? 0.0f : static_cast<float>(1.0 / (1.0 - a->p));
     const int eight = 8 * size;                             // bytes, and where eights have to start
     const bool vectors = aligned(x, eight) && aligned(residual, eight) && aligned(out, eight);
