@@ -31,8 +31,9 @@ namespace cg = cooperative_groups;
 
 constexpr int kWarps = 8;              // of a CTA: with a row to itself, or a row a warp
 constexpr int kWarpVocab = 2048;       // up to which a row is a warp's
+constexpr int kManyVocab = 8192, kManyTopVocab = 5120;      // and up to which it is, of many rows, without and with alternatives
 constexpr int kStages = 4;             // pieces of a thread on their way, with the one under work
-constexpr int kPiece = 32;             // bytes of one
+constexpr int kUnits = 2;              // of 16 bytes, of a piece
 constexpr int kMaxTop = 32;
 constexpr int kMaxSplit = 8;           // CTAs of a row
 constexpr int kBackThreads = 128;
@@ -156,22 +157,29 @@ __device__ __forceinline__ bool take_one(float x, float c, Sums& t) {
     return take<1, ENTROPY>(pair, c, t);
 }
 
-// A run of n elements of a row: `head` elements, `eights` eights from a 16-byte
+// A run of n elements of a row: `head` elements, `units` of N each from a 16-byte
 // boundary on, and a rest.
-template <typename T>
+template <typename T, int N>
 struct Run {
     const T* from;
-    int n, head, eights;
+    int n, head, units;
 
     __device__ __forceinline__ Run(const T* row, long long lo, long long hi) {
         from = row + lo;
         n = hi > lo ? static_cast<int>(hi - lo) : 0;
         head = min(n, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(from) & 15)) % 16 / sizeof(T)));
-        eights = (n - head) / 8;
+        units = (n - head) / N;
     }
-    __device__ __forceinline__ const T* eight(int i) const { return from + head + 8 * i; }
-    __device__ __forceinline__ int rest() const { return head + 8 * eights; }
+    __device__ __forceinline__ const T* unit(int i) const { return from + head + N * i; }
+    __device__ __forceinline__ int rest() const { return head + N * units; }
 };
+
+// 16 bytes as fp32 numbers.
+__device__ __forceinline__ void numbers(const uint16_t* p, float (&f)[8]) { ddpk::dev::Vec<uint16_t>::unpack(*reinterpret_cast<const uint4*>(p), f); }
+__device__ __forceinline__ void numbers(const float* p, float (&f)[4]) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+}
 
 // ---------------------------------------------------------------- the best alternatives
 
@@ -277,8 +285,8 @@ __device__ __forceinline__ Key join_lists(Key mine, Key (*lists)[32]) {
 template <typename T, int WARPS, bool ENTROPY, bool TOP>
 __global__ void __launch_bounds__(32 * kWarps, TOP ? 4 : 5) logp_kernel(const __grid_constant__ LogpParams p) {
     constexpr int kThreads = 32 * WARPS;                    // of a row, in this CTA
-    constexpr int kEights = kPiece / static_cast<int>(sizeof(Eight<T>));
-    __shared__ uint4 ahead[kStages][kPiece / 16][32 * kWarps];
+    constexpr int N = 16 / static_cast<int>(sizeof(T));     // of 16 bytes
+    __shared__ uint4 ahead[kStages][kUnits][32 * kWarps];
     __shared__ Shared<TOP> shared;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t = WARPS == 1 ? lane : threadIdx.x;
@@ -305,53 +313,42 @@ __global__ void __launch_bounds__(32 * kWarps, TOP ? 4 : 5) logp_kernel(const __
     }
     const T* const logits = static_cast<const T*>(p.logits) + row * p.stride;
     const long long lo = part * p.segment, hi = min(static_cast<long long>(p.vocab), lo + p.segment);
-    const Run<T> run(logits, lo, hi);
+    const Run<T, N> run(logits, lo, hi);
     const float c = p.scale2;
     Sums sums = {neg_inf(), 0.0f, 0.0f};
-    // where this thread's largest lies: in the eights of a piece from this one on; -2: head, -3: rest
+    // where this thread's largest lies: in the units of a piece from this one on; -2: head, -3: rest
     int best = -1;
     const auto request = [&](int piece) {
 #pragma unroll
-        for (int e = 0; e < kEights; ++e) {
-            const int i = t + (piece * kEights + e) * kThreads;
-            if (i < run.eights)
-#pragma unroll
-                for (int u = 0; u < kPiece / 16 / kEights; ++u)
-                    copy_async(&ahead[piece % kStages][e * (kPiece / 16 / kEights) + u][threadIdx.x],
-                               reinterpret_cast<const uint4*>(run.eight(i)) + u);
+        for (int u = 0; u < kUnits; ++u) {
+            const int i = t + (piece * kUnits + u) * kThreads;
+            if (i < run.units) copy_async(&ahead[piece % kStages][u][threadIdx.x], run.unit(i));
         }
         copy_commit();
     };
 #pragma unroll
     for (int s = 0; s + 1 < kStages; ++s) request(s);
     if (t < run.head && take_one<ENTROPY>(widen(run.from[t]), c, sums)) best = -2;
-    for (int piece = 0; t + piece * kEights * kThreads < run.eights; ++piece) {
+    for (int piece = 0; t + piece * kUnits * kThreads < run.units; ++piece) {
         copy_wait<kStages - 2>();
-        constexpr int kEach = kPiece / 16 / kEights;         // 16-byte words of an eight
         using Pair = typename std::conditional<sizeof(T) == 2, uint32_t, float2>::type;
-        Pair x[4 * kEights];
+        Pair x[N / 2 * kUnits];
 #pragma unroll
-        for (int e = 0; e < kEights; ++e) {
-            const bool on = e == 0 || t + (piece * kEights + e) * kThreads < run.eights;
-            uint4 w[kEach];
+        for (int u = 0; u < kUnits; ++u) {
+            const bool on = u == 0 || t + (piece * kUnits + u) * kThreads < run.units;
+            const uint4 v = ahead[piece % kStages][u][threadIdx.x];
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int u = 0; u < kEach; ++u) w[u] = ahead[piece % kStages][e * kEach + u][threadIdx.x];
-            if constexpr (sizeof(T) == 2) {
-                x[4 * e] = w[0].x; x[4 * e + 1] = w[0].y; x[4 * e + 2] = w[0].z; x[4 * e + 3] = w[0].w;
+            for (int j = 0; j < 4; ++j)
+                if (!on) w[j] = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;      // -inf
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (!on) x[4 * e + j] = 0xff80ff80u;     // -inf
-            } else {
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    x[4 * e + 2 * u] = make_float2(__uint_as_float(w[u].x), __uint_as_float(w[u].y));
-                    x[4 * e + 2 * u + 1] = make_float2(__uint_as_float(w[u].z), __uint_as_float(w[u].w));
-                }
+            for (int j = 0; j < N / 2; ++j) {
+                if constexpr (sizeof(T) == 2) x[u * (N / 2) + j] = w[j];
+                else x[u * (N / 2) + j] = make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
             }
         }
-        static_assert(sizeof(T) == 2 || kEights == 1, "no fp32 eight past the run's end");
         request(piece + kStages - 1);                       // into the place of the piece before, which is used up
-        if (take<4 * kEights, ENTROPY>(x, c, sums)) best = t + piece * kEights * kThreads;
+        if (take<N / 2 * kUnits, ENTROPY>(x, c, sums)) best = t + piece * kUnits * kThreads;
     }
     if (t < run.n - run.rest() && take_one<ENTROPY>(widen(run.from[run.rest() + t]), c, sums)) best = -3;
 
@@ -363,16 +360,14 @@ __global__ void __launch_bounds__(32 * kWarps, TOP ? 4 : 5) logp_kernel(const __
         if (best == -2) mine = key_of(sums.m, base + t);
         if (best == -3) mine = key_of(sums.m, base + run.rest() + t);
         if (best >= 0) {
-            for (int u = 0; u < kEights && !mine; ++u) {
+            for (int u = 0; u < kUnits && !mine; ++u) {
                 const int at = best + u * kThreads;
-                if (at >= run.eights) break;
-                Eight<T> raw;
-                raw.load(run.eight(at));
-                float x[8];
-                raw.get(x);
+                if (at >= run.units) break;
+                float x[N];
+                numbers(run.unit(at), x);
 #pragma unroll
-                for (int j = 7; j >= 0; --j)
-                    if (x[j] == sums.m) mine = key_of(x[j], base + run.head + 8 * at + j);
+                for (int j = N - 1; j >= 0; --j)
+                    if (x[j] == sums.m) mine = key_of(x[j], base + run.head + N * at + j);
             }
         }
         list = sort_keys(mine);
@@ -384,15 +379,12 @@ __global__ void __launch_bounds__(32 * kWarps, TOP ? 4 : 5) logp_kernel(const __
         }
         Best found = {0, __shfl_sync(kAll, list, p.top - 1), 0, p.top, shared.buffers[warp]};
         if constexpr (WARPS == 1) {
-            for (int e0 = 0; e0 < run.eights; e0 += 32) {
-                float x[8];
-                Eight<T> raw;
-                if (e0 + lane < run.eights) raw.load(run.eight(e0 + lane));
-                else raw.zero();
-                raw.get(x);
+            for (int i0 = 0; i0 < run.units; i0 += 32) {
+                const int at = i0 + lane;
+                float x[N] = {};
+                if (at < run.units) numbers(run.unit(at), x);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    found.push(e0 + lane < run.eights ? key_of(x[j], base + run.head + 8 * (e0 + lane) + j) : 0);
+                for (int j = 0; j < N; ++j) found.push(at < run.units ? key_of(x[j], base + run.head + N * at + j) : 0);
             }
             found.push(lane < run.head ? key_of(widen(run.from[lane]), base + lane) : 0);
             const int at = run.rest() + lane;
@@ -402,16 +394,13 @@ __global__ void __launch_bounds__(32 * kWarps, TOP ? 4 : 5) logp_kernel(const __
                 const Key winner = __shfl_sync(kAll, list, w);
                 if (!winner) break;
                 int of = index_of(winner) - base;           // whose it is
-                of = of < run.head ? of : of >= run.rest() ? of - run.rest() : (of - run.head) / 8 % kThreads;
-                for (int e0 = of; e0 < run.eights; e0 += 32 * kThreads) {
-                    const int at = e0 + lane * kThreads;
-                    float x[8];
-                    Eight<T> raw;
-                    if (at < run.eights) raw.load(run.eight(at));
-                    else raw.zero();
-                    raw.get(x);
+                of = of < run.head ? of : of >= run.rest() ? of - run.rest() : (of - run.head) / N % kThreads;
+                for (int i0 = of; i0 < run.units; i0 += 32 * kThreads) {
+                    const int at = i0 + lane * kThreads;
+                    float x[N] = {};
+                    if (at < run.units) numbers(run.unit(at), x);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) found.push(at < run.eights ? key_of(x[j], base + run.head + 8 * at + j) : 0);
+                    for (int j = 0; j < N; ++j) found.push(at < run.units ? key_of(x[j], base + run.head + N * at + j) : 0);
                 }
                 const int at = lane == 0 && of < run.head ? of : lane == 1 && run.rest() + of < run.n ? run.rest() + of : -1;
                 found.push(at >= 0 ? key_of(widen(run.from[at]), base + at) : 0);
@@ -521,7 +510,7 @@ __global__ void __launch_bounds__(kBackThreads, kBackCtas) logp_backward_kernel(
     const long long row = blockIdx.x / p.split;
     const long long lo = blockIdx.x % p.split * p.segment, hi = min(static_cast<long long>(p.vocab), lo + p.segment);
     const T* const from = static_cast<const T*>(p.logits) + row * p.stride + lo;
-    const Run<T> run(static_cast<const T*>(p.out) + row * p.out_stride, lo, hi);
+    const Run<T, 8> run(static_cast<const T*>(p.out) + row * p.out_stride, lo, hi);
     T* const to = static_cast<T*>(p.out) + row * p.out_stride + lo;
     const int target = target_of(p, row);
     const float2 stat = *reinterpret_cast<const float2*>(p.stats + 2 * row);
@@ -534,10 +523,10 @@ __global__ void __launch_bounds__(kBackThreads, kBackCtas) logp_backward_kernel(
 #pragma unroll
     for (int u = 0; u < kEights; ++u) {
         const int i = first + u * 32;
-        if (!zero && i < run.eights) raw[u].load(words + 8 * i);
-        else if (!zero && i == run.eights && shift) *reinterpret_cast<uint4*>(&raw[u]) = *reinterpret_cast<const uint4*>(words + 8 * i);
+        if (!zero && i < run.units) raw[u].load(words + 8 * i);
+        else if (!zero && i == run.units && shift) *reinterpret_cast<uint4*>(&raw[u]) = *reinterpret_cast<const uint4*>(words + 8 * i);
     }
-    if (!zero && shift && lane == 0 && first + 32 * kEights <= run.eights)
+    if (!zero && shift && lane == 0 && first + 32 * kEights <= run.units)
         last = *reinterpret_cast<const uint4*>(words + 8 * (first + 32 * kEights));
     const float g = p.grad_logp && target >= 0 ? p.grad_logp[row] : 0.0f;
     const float h = ENTROPY ? p.grad_entropy[row] : 0.0f;
@@ -545,9 +534,9 @@ __global__ void __launch_bounds__(kBackThreads, kBackCtas) logp_backward_kernel(
     const float extra = p.scale * g;
     const int aim = target - static_cast<int>(lo);
     // the ends, at most seven elements each
-    const int ends = run.n - 8 * run.eights;
+    const int ends = run.n - 8 * run.units;
     if (threadIdx.x < ends) {
-        const int i = threadIdx.x < run.head ? threadIdx.x : threadIdx.x + 8 * run.eights;
+        const int i = threadIdx.x < run.head ? threadIdx.x : threadIdx.x + 8 * run.units;
         float y = zero ? 0.0f : slope.at<ENTROPY>(both(widen(from[i]))).x;
         if (i == aim && !zero) y += extra;
         to[i] = narrow<T>(y);
@@ -555,7 +544,7 @@ __global__ void __launch_bounds__(kBackThreads, kBackCtas) logp_backward_kernel(
 #pragma unroll
     for (int u = 0; u < kEights; ++u) {
         const int i = first + u * 32;
-        if (i - lane >= run.eights) break;                  // the whole warp's
+        if (i - lane >= run.units) break;                  // the whole warp's
         if (shift && !zero) {
             const uint4 mine = *reinterpret_cast<const uint4*>(&raw[u]);
             const uint4 ahead = u + 1 < kEights ? *reinterpret_cast<const uint4*>(&raw[u + 1 < kEights ? u + 1 : 0]) : last;
@@ -565,7 +554,7 @@ __global__ void __launch_bounds__(kBackThreads, kBackCtas) logp_backward_kernel(
                                             __shfl_sync(kAll, give.z, next), __shfl_sync(kAll, give.w, next));
             raw[u] = shifted(raw[u], behind, shift);
         }
-        if (i >= run.eights) continue;
+        if (i >= run.units) continue;
         Eight<T> out;
         out.zero();
         if (!zero) {
@@ -604,8 +593,14 @@ template <typename T>
 cudaError_t forward(LogpParams& p, cudaStream_t stream) {
     p.split = 1;
     p.segment = p.vocab;
-    if (p.vocab <= kWarpVocab) return forward_as<T, 1>(p, stream);
-    // few rows: as many CTAs a row as keep every thread an eight or more
+    // Many rows of a middling length: what a CTA does at a row's ends (its warps'
+    // sums and lists joined) costs more than a warp's longer row.  8,192 rows, us
+    // with a CTA / a warp each: 2,500 bf16 32 / 12, with 5 of the best 102 / 38;
+    // 8,192 bf16 37 / 28, with 5 109 / 92, fp32 49 / 49, with 5 107 / 137; 16,384
+    // bf16 50 / 50, fp32 79 / 86.  1,024 rows of 5,003 with 5: 17 / 19.
+    const bool many = p.top ? p.rows >= 16 * kSms && p.vocab <= kManyTopVocab : p.rows >= 8 * kSms && p.vocab <= kManyVocab;
+    if (p.vocab <= kWarpVocab || many) return forward_as<T, 1>(p, stream);
+    // few rows: as many CTAs a row as keep every thread eight elements or more
     while (p.split < kMaxSplit && p.rows * p.split < 2 * kSms && p.vocab / (2 * p.split) >= 8 * 32 * kWarps) p.split *= 2;
     p.segment = ((p.vocab + p.split - 1) / p.split + 7) / 8 * 8;
     return forward_as<T, kWarps>(p, stream);
