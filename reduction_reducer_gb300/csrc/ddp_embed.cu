@@ -22,6 +22,9 @@ using namespace ddpk::rows;
 
 constexpr int kThreads = 256;
 constexpr int kAhead = 4;              // forward: rows of a thread at once
+constexpr int kColumns = 4;            // and, where they do not lie in vectors, columns of each,
+constexpr int kScalarThreads = 128;    // which is then at most this many threads' (26,800 of 2,500 fp32: 256 with one column
+                                       // 91 us, with four 87, 128 with four 77, 32 94)
 constexpr int kMaxBits = 8;            // of a digit of the sort
 constexpr int kMaxBins = 1 << kMaxBits;
 constexpr int kSortThreads = 512;
@@ -36,11 +39,14 @@ constexpr int kGroup = 32;             // parts of a row that are added up in on
 constexpr int kChunk = 256;            // columns of a warp
 // Rows of a warp on their way, with the one under work.
 template <typename T> constexpr int kRing = sizeof(T) == 2 ? 8 : 4;
+// Words of one.
+template <typename T, bool VEC> constexpr int slot_of = kChunk * static_cast<int>(sizeof(T)) / 16 + (VEC ? 0 : 1);
 // Shares of a window, while there are fewer warps: one place each where the GPU
-// would not be full (111 tokens of 14 columns: four shares 9.2 us, eight 7.3, 32 6.1), and up
-// to eight where warps would not be many (65,536 tokens of 1,024: one 76.7, two 73.7, four 76.1).
+// would not be full (111 tokens of 14 columns: four shares 9.2 us, eight 7.3, 32 6.1), and two
+// where warps would not be many (65,536 tokens onto 50,257 rows of 1,024: one 76.7, two 73.7, four
+// 76.1; of 64: one 41.4, two 41.3, four 45.1, eight 50.4).
 constexpr int kMaxSplits = 32, kFewWarps = kSms * 24;
-constexpr int kMoreSplits = 8, kMoreWarps = kSms * 96;
+constexpr int kMoreSplits = 2, kMoreWarps = kSms * 96;
 constexpr int64_t kMaxTokens = 1 << 24;      // of a gradient: groups of a row's parts are counted in 15 bits
 constexpr int kFillBytes = 64 * 1024;  // of the rows that a CTA looks at for empty ones
 
@@ -109,7 +115,7 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__
             const long long r = r0 + u * slots;
             from[u] = r < p.n ? token_at(p.tokens, p.wide, r, p.vocab) : -1;
         }
-        for (int at = t * N; at < p.dim; at += p.row_threads * N) {
+        for (int at = t * N; at < p.dim; at += p.row_threads * (VEC ? N : kColumns)) {
             if constexpr (VEC) {
                 Eight<Tin> raw[kAhead];
 #pragma unroll
@@ -132,13 +138,22 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__
                     if (r0 + u * slots < p.n) y.store_wide(out + (r0 + u * slots) * p.out_stride + at);
                 }
             } else {
-                float f[kAhead];
+                float f[kAhead][kColumns];
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u)
-                    f[u] = from[u] >= 0 ? widen(table[from[u] * p.table_stride + at]) * p.scale : 0.0f;
+#pragma unroll
+                    for (int k = 0; k < kColumns; ++k) {
+                        const int col = at + k * p.row_threads;
+                        f[u][k] = from[u] >= 0 && col < p.dim ? widen(table[from[u] * p.table_stride + col]) : 0.0f;
+                    }
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u)
-                    if (r0 + u * slots < p.n) out[(r0 + u * slots) * p.out_stride + at] = narrow<Tout>(f[u]);
+#pragma unroll
+                    for (int k = 0; k < kColumns; ++k) {
+                        const int col = at + k * p.row_threads;
+                        if (r0 + u * slots < p.n && col < p.dim)
+                            out[(r0 + u * slots) * p.out_stride + col] = narrow<Tout>(from[u] >= 0 ? f[u][k] * p.scale : 0.0f);
+                    }
             }
         }
     }
@@ -508,47 +523,54 @@ __device__ __forceinline__ void sum_window(const SumParams& p, long long window,
     if (i0 >= min(b, valid)) return;
     const Columns<VEC> c(chunk, p.dim);
     const T* const grad = static_cast<const T*>(p.grad);
-    constexpr int kPieces = static_cast<int>(sizeof(Eight<T>)) / 16;
-    uint4* const ring = memory + (threadIdx.x >> 5) * (kRing<T> * kPieces * 32) + lane;
+    // A row's columns of this chunk on their way to shared memory: a lane's own
+    // eight, or, where rows do not lie in vectors, the 16-byte words that the
+    // chunk touches, of which a lane reads every 32nd element.
+    constexpr int kSlot = slot_of<T, VEC>, kEach = 16 / static_cast<int>(sizeof(T)), kPieces = 8 / kEach;
+    uint4* const ring = memory + (threadIdx.x >> 5) * (kRing<T> * kSlot);
+    const int columns = min(kChunk, p.dim - chunk * kChunk);
     const auto row_of = [&](int q) {
         const int place = __shfl_sync(kAll, q < kPart ? place0 : place1, q & 31);
-        return grad + static_cast<long long>(place) * p.grad_stride;
+        return grad + static_cast<long long>(place) * p.grad_stride + chunk * kChunk;
     };
+    const auto head_of = [&](const T* from) { return static_cast<int>((reinterpret_cast<uintptr_t>(from) & 15) / sizeof(T)); };
     const auto request = [&](int q) {
         const T* const from = row_of(q);
-        if (q < i1 && c.on(0))
+        uint4* const to = ring + q % kRing<T> * kSlot + lane;
+        if constexpr (VEC) {
+            if (q < i1 && c.on(0))
 #pragma unroll
-            for (int u = 0; u < kPieces; ++u)
-                copy_async(ring + (q % kRing<T> * kPieces + u) * 32, reinterpret_cast<const uint4*>(from + c.first) + u);
+                for (int u = 0; u < kPieces; ++u) copy_async(to + 32 * u, reinterpret_cast<const uint4*>(from + 8 * lane) + u);
+        } else if (q < i1) {
+            const int words = (head_of(from) + columns + kEach - 1) / kEach;
+            const uint4* const first_word = reinterpret_cast<const uint4*>(from - head_of(from)) + lane;
+#pragma unroll
+            for (int u = 0; u <= kPieces; ++u)
+                if (lane + 32 * u < words) copy_async(to + 32 * u, first_word + 32 * u);
+        }
         copy_commit();
     };
-    float next[8] = {};
-    const auto load = [&](int q) {                               // rows that do not lie in vectors
-        const T* const from = row_of(q);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) next[j] = q < i1 && c.on(j) ? widen(from[c.at(j)]) : 0.0f;
-    };
-    if constexpr (VEC)
-        for (int k = 0; k + 1 < kRing<T>; ++k) request(i0 + k);
-    else
-        load(i0);
+    for (int k = 0; k + 1 < kRing<T>; ++k) request(i0 + k);
     Sum sum = {};
     int begin = i0;
 #pragma unroll 1
     for (int i = i0; i < i1; ++i) {
+        copy_wait<kRing<T> - 2>();
+        const uint4* const row = ring + i % kRing<T> * kSlot;
         if constexpr (VEC) {
-            copy_wait<kRing<T> - 2>();
             Eight<T> raw;
             uint4* const words = reinterpret_cast<uint4*>(&raw);
 #pragma unroll
-            for (int u = 0; u < kPieces; ++u) words[u] = ring[(i % kRing<T> * kPieces + u) * 32];
+            for (int u = 0; u < kPieces; ++u) words[u] = row[lane + 32 * u];
             raw.add_to(sum.v);
-            request(i + kRing<T> - 1);                           // into the place of the row before, which is used up
         } else {
+            __syncwarp();
+            const T* const x = reinterpret_cast<const T*>(row) + head_of(row_of(i)) + lane;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum.v[j] += next[j];
-            load(i + 1);
+            for (int j = 0; j < 8; ++j)
+                if (c.on(j)) sum.v[j] += widen(x[32 * j]);
         }
+        request(i + kRing<T> - 1);                               // into the place of the row before, which is used up
         const int q = i + 1;
         if (q < i1 && !((q < kPart ? parts0 >> q : parts1 >> (q - kPart)) & 1)) continue;
         // a row ends here, or a part of one that is long
@@ -671,7 +693,7 @@ cudaError_t embed_as(bool vec, long long ctas, const EmbedParams& p, cudaStream_
 template <typename T, typename Tout>
 cudaError_t sum_as(bool vec, long long ctas, const SumParams& p, cudaStream_t stream) {
     return launch(vec ? embed_sum_kernel<T, Tout, true> : embed_sum_kernel<T, Tout, false>, ctas, kThreads,
-                  vec ? kRing<T> * sizeof(Eight<T>) * kThreads : 0, stream, p);
+                  kThreads / 32 * kRing<T> * (vec ? slot_of<T, true> : slot_of<T, false>) * sizeof(uint4), stream, p);
 }
 
 }  // namespace
@@ -696,7 +718,8 @@ int ddp_embed(const ddp_embed_args* a, const void* table, const void* tokens, vo
     p.wide = a->index_bits == 64;
     p.scale = a->scale;
     const bool vec = vectors(a, table, out);
-    p.row_threads = row_threads(vec ? a->dim / 8 : a->dim);
+    p.row_threads = row_threads(vec ? a->dim / 8 : (a->dim + kColumns - 1) / kColumns);
+    if (!vec && p.row_threads > kScalarThreads) p.row_threads = kScalarThreads;
     const long long tile = static_cast<long long>(kThreads / p.row_threads) * kAhead;
     const long long ctas = (p.n + tile - 1) / tile;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
