@@ -524,12 +524,15 @@ int ddp_route_backward(const ddp_route_args* args, const void* logits, const int
  * the forward pass and back: the embedding, layer norm, dropout on a residual
  * branch, and the log probabilities that a loss is made of.  The gradients of
  * the embedding's table and of a norm's weight and bias are sums over all
- * tokens, in an order that depends on the sizes alone (equal inputs give equal
- * bits), and are written, or with accumulate added, straight into the gradient
+ * tokens, in an order that depends on the sizes and the addresses' alignment
+ * alone (equal inputs give equal bits), and are written, or with accumulate added, straight into the gradient
  * fields that ddp_bind and ddp_adamw_bind take.
  * Rows are elements next to one another; strides count elements between two
- * rows.  Any element alignment is correct; rows that start on 16 bytes and
- * whose length is a multiple of eight are read and written in vectors.
+ * rows.  Any element alignment is correct.  Rows that start on 16 bytes (fp32
+ * ones of the embedding and of dropout on 32) and whose length is a multiple of
+ * eight are read and written in vectors; the norms and the log probabilities
+ * read any others in whole words of 16 bytes too, and so does the embedding's
+ * gradient, whose words may hold neighbours' elements, which are not looked at.
  * Arithmetic is fp32; bf16 results are rounded once, to nearest even.
  * Every call is asynchronous on `stream`, runs on the current device and keeps
  * nothing; a workspace is the caller's, device memory aligned to 16 bytes, one

@@ -106,4 +106,6 @@ def embedded(table, tokens, scale: float = 1.0, dtype=None, grad_into=None):
     """``embed`` under autograd, on the current stream.  grad_into: fp32
     [vocab, dim], a gradient field or bucket view that the table's gradient is
     added to in the backward pass; autograd then gets none for the table."""
+    if grad_into is not None and (grad_into.dtype is not _rows.load_torch().float32 or grad_into.shape != table.shape):
+        raise ValueError(f"grad_into: expected fp32 {list(table.shape)}; found {list(grad_into.shape)} of {grad_into.dtype}")
     return _autograd().apply(table, tokens, scale, dtype, grad_into)

@@ -34,8 +34,8 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stats=Non
     1 / sqrt(variance + eps), which the gradient takes.
 
     x: fp32 or bf16 (rows may be strided); weight, bias: [dim], fp32 or bf16,
-    or None; out, stats: the results' places (without them they are allocated
-    on `stream`).  All tensors lie on the current device."""
+    or None, both of one dtype; out, stats: the results' places, which do not
+    overlap x (without them they are allocated on `stream`).  All tensors lie on the current device."""
     torch = _rows.torch or _rows.load_torch()
     device = _device()
     rows, dim, x_stride, code = _rows.matrix("x", x, device)
@@ -66,7 +66,8 @@ def layer_norm_backward(grad, x, stats, weight=None, grad_weight=None, grad_bias
 
     grad_weight, grad_bias: [dim] of the parameters' dtype, which are written
     (or, with accumulate and fp32, added to) where they are given: gradient
-    fields or bucket views; out: the place of grad_x; input_grad: False
+    fields or bucket views; out: the place of grad_x, which overlaps neither
+    grad nor x; input_grad: False
     leaves grad_x out (None); workspace: bytes that no other call uses
     meanwhile (without one they are allocated on `stream`)."""
     torch = _rows.torch or _rows.load_torch()
@@ -140,6 +141,11 @@ def _autograd():
 def layer_normed(x, weight=None, bias=None, eps: float = 1e-5, grad_into=None):
     """``layer_norm`` under autograd, on the current stream: y.  grad_into:
     (grad_weight, grad_bias), fp32 gradient fields or bucket views (either may
-    be None) that the parameters' gradients are added to in the backward pass;
-    autograd then gets none for them."""
+    be None) that the gradients of parameters in fp32 are added to in the
+    backward pass; autograd then gets none for them."""
+    if grad_into is not None:
+        _rows.load_torch()
+        for t in (weight, bias, *grad_into):
+            if t is not None and (t.dtype is not _rows.torch.float32 or t.shape != x.shape[-1:]):
+                raise ValueError(f"grad_into: expected fp32 [{x.shape[-1]}] for parameters in fp32; found {list(t.shape)} of {t.dtype}")
     return _autograd().apply(x, weight, bias, eps, grad_into)
