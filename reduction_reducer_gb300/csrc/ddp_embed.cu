@@ -100,7 +100,7 @@ __device__ __forceinline__ long long token_at(const void* tokens, int wide, long
 // ---------------------------------------------------------------- forward
 
 template <typename Tin, typename Tout, bool VEC>
-__global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__ EmbedParams p) {
+__global__ void __launch_bounds__(kThreads, VEC && sizeof(Tin) == 2 ? 5 : 4) embed_kernel(const __grid_constant__ EmbedParams p) {
     ddpk::dev::pdl_wait();
     ddpk::dev::pdl_trigger();
     constexpr int N = VEC ? 8 : 1;
@@ -127,11 +127,12 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__
                 for (int u = 0; u < kAhead; ++u) {
                     float f[8];
                     raw[u].get(f);
+                    const float2 s = both(from[u] >= 0 ? p.scale : 0.0f);      // (no -0 where there is no row)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] *= p.scale;
-                    if (from[u] < 0) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) f[j] = 0.0f;       // (and not -0)
+                    for (int j = 0; j < 8; j += 2) {
+                        const float2 d = mul2(make_float2(f[j], f[j + 1]), s);
+                        f[j] = d.x;
+                        f[j + 1] = d.y;
                     }
                     Eight<Tout> y;
                     y.put(f);
