@@ -31,7 +31,8 @@ namespace cg = cooperative_groups;
 
 constexpr int kWarps = 8;              // of a CTA: with a row to itself, or a row a warp
 constexpr int kWarpVocab = 2048;       // up to which a row is a warp's
-constexpr int kManyVocab = 8192, kManyTopVocab = 5120;      // and up to which it is, of many rows, without and with alternatives
+// Bytes of a row up to which it is a warp's, of some rows and of many.
+constexpr int64_t kSomeRows = 6 * kSms, kSomeBytes = 16 << 10, kManyRows = 16 * kSms, kManyBytes = 32 << 10;
 constexpr int kStages = 4;             // pieces of a thread on their way, with the one under work
 constexpr int kUnits = 2;              // of 16 bytes, of a piece
 constexpr int kMaxTop = 32;
@@ -174,11 +175,20 @@ struct Run {
     __device__ __forceinline__ int rest() const { return head + N * units; }
 };
 
-// 16 bytes as fp32 numbers.
-__device__ __forceinline__ void numbers(const uint16_t* p, float (&f)[8]) { ddpk::dev::Vec<uint16_t>::unpack(*reinterpret_cast<const uint4*>(p), f); }
-__device__ __forceinline__ void numbers(const float* p, float (&f)[4]) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+// A 16-byte unit as fp32 numbers.
+__device__ __forceinline__ void numbers(uint4 v, float (&f)[8]) { ddpk::dev::Vec<uint16_t>::unpack(v, f); }
+__device__ __forceinline__ void numbers(uint4 v, float (&f)[4]) {
+    f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y); f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+}
+
+// The largest of one, NaN aside.
+template <typename T>
+__device__ __forceinline__ float largest(uint4 v) {
+    if constexpr (sizeof(T) == 4)
+        return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+    uint32_t x = v.x;
+    asm("max.bf16x2 %0, %0, %1;\n\tmax.bf16x2 %0, %0, %2;\n\tmax.bf16x2 %0, %0, %3;" : "+r"(x) : "r"(v.y), "r"(v.z), "r"(v.w));
+    return fmaxf(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
 }
 
 // ---------------------------------------------------------------- the best alternatives
@@ -226,34 +236,65 @@ __device__ __forceinline__ Key merge_keys(Key x, Key y) {
 }
 
 // The largest keys that a warp was given, up to 32: in order in its lanes, and
-// up to 31 more that wait in `buffer` [64].
+// more that wait in its part of the memory of the pieces, which are used up: kRow
+// keys of each of the rows.
 struct Best {
+    static constexpr int kRow = 64, kStride = 64 * kWarps;
     Key list, least;       // least: what a key has to reach
     int waiting, k;
     Key* buffer;
 
+    __device__ __forceinline__ Key& place(int i) const { return buffer[i / kRow * kStride + i % kRow]; }
+
+    // the last 32 that wait into the list
     __device__ __forceinline__ void flush() {
-        const int lane = threadIdx.x & 31;
-        list = merge_keys(list, sort_keys(lane < waiting ? buffer[lane] : 0));
+        const int lane = threadIdx.x & 31, n = min(waiting, 32);
+        waiting -= n;
+        list = merge_keys(list, sort_keys(lane < n ? place(waiting + lane) : 0));
         const Key kth = __shfl_sync(kAll, list, k - 1);
         if (kth > least) least = kth;
-        __syncwarp();
-        if (waiting > 32 && lane < waiting - 32) {
-            const Key x = buffer[32 + lane];
-            buffer[lane] = x;                       // (other places than those read)
-        }
-        waiting = max(waiting - 32, 0);
-        __syncwarp();
     }
-    // by the whole warp
+    // by the whole warp; a unit's elements, at most, before the next settle
     __device__ __forceinline__ void push(Key x) {
         const bool on = x >= least && x != 0;
         const unsigned b = __ballot_sync(kAll, on);
-        if (!b) return;
-        if (on) buffer[waiting + __popc(b & ((1u << (threadIdx.x & 31)) - 1))] = x;
+        if (on) place(waiting + __popc(b & ((1u << (threadIdx.x & 31)) - 1))) = x;
         waiting += __popc(b);
+    }
+    __device__ __forceinline__ void settle(int left) {
         __syncwarp();
-        if (waiting >= 32) flush();
+#pragma unroll 1
+        while (waiting > left) flush();
+        __syncwarp();
+    }
+    // The run's units first, first + step, ..., a lane each, by the whole warp, with
+    // three on their way.  Units without an element that reaches the bound are
+    // passed over.  The code is short on purpose, since it runs few times for its
+    // instructions' way: with every element pushed by itself 8,192 rows of 2,500 in
+    // bf16 with five of the best took 38 us instead of 30, units passed over but four
+    // at a time unrolled 47.
+    template <typename T, int N>
+    __device__ __forceinline__ void scan(const Run<T, N>& run, int first, int step, int base) {
+        static_assert(31 + 32 * N <= kStages * kUnits * kRow, "a unit of every lane has to fit behind 31 keys");
+        const auto load = [&](int at) { return at < run.units ? *reinterpret_cast<const uint4*>(run.unit(at)) : make_uint4(0, 0, 0, 0); };
+        const int hop = 32 * step;
+        int at = first + static_cast<int>(threadIdx.x & 31) * step;
+        uint4 next[3] = {load(at), load(at + hop), load(at + 2 * hop)};
+#pragma unroll 1
+        for (int i = first; i < run.units; i += hop, at += hop) {
+            const uint4 raw = next[0];
+            next[0] = next[1];
+            next[1] = next[2];
+            next[2] = load(at + 3 * hop);
+            const float bound = least ? value_of(least) : neg_inf(), top = at < run.units ? largest<T>(raw) : neg_inf();
+            const bool on = top >= bound && top > neg_inf();
+            if (!__ballot_sync(kAll, on)) continue;
+            float x[N];
+            numbers(raw, x);
+#pragma unroll
+            for (int j = 0; j < N; ++j) push(on ? key_of(x[j], base + run.head + N * at + j) : 0);
+            settle(31);
+        }
     }
 };
 
@@ -264,7 +305,6 @@ struct Shared {
     Sums sums[kWarps];
     Sums whole;                    // of this CTA's part of the row
     Key lists[TOP ? kWarps : 1][32];
-    Key buffers[TOP ? kWarps : 1][64];
 };
 
 // The lists of all warps of a CTA as one, in the first warp's lanes.
@@ -371,12 +411,13 @@ __global__ void __launch_bounds__(32 * kWarps, TOP ? 4 : 5) logp_kernel(const __
                 const int at = best + u * kThreads;
                 if (at >= run.units) break;
                 float x[N];
-                numbers(run.unit(at), x);
+                numbers(*reinterpret_cast<const uint4*>(run.unit(at)), x);
 #pragma unroll
                 for (int j = N - 1; j >= 0; --j)
                     if (x[j] == sums.m) mine = key_of(x[j], base + run.head + N * at + j);
             }
         }
+        __syncwarp();                                       // the pieces' memory is free from here on
         list = sort_keys(mine);
         if constexpr (WARPS > 1) {
             list = join_lists(list, shared.lists);
@@ -384,15 +425,9 @@ __global__ void __launch_bounds__(32 * kWarps, TOP ? 4 : 5) logp_kernel(const __
             list = shared.lists[0][lane];                   // the threads' best 32, in every warp
             __syncthreads();
         }
-        Best found = {0, __shfl_sync(kAll, list, p.top - 1), 0, p.top, shared.buffers[warp]};
+        Best found = {0, __shfl_sync(kAll, list, p.top - 1), 0, p.top, reinterpret_cast<Key*>(ahead) + warp * Best::kRow};
         if constexpr (WARPS == 1) {
-            for (int i0 = 0; i0 < run.units; i0 += 32) {
-                const int at = i0 + lane;
-                float x[N] = {};
-                if (at < run.units) numbers(run.unit(at), x);
-#pragma unroll
-                for (int j = 0; j < N; ++j) found.push(at < run.units ? key_of(x[j], base + run.head + N * at + j) : 0);
-            }
+            found.scan(run, 0, 1, base);
             found.push(lane < run.head ? key_of(widen(run.from[lane]), base + lane) : 0);
             const int at = run.rest() + lane;
             found.push(at < run.n ? key_of(widen(run.from[at]), base + at) : 0);
@@ -402,18 +437,13 @@ __global__ void __launch_bounds__(32 * kWarps, TOP ? 4 : 5) logp_kernel(const __
                 if (!winner) break;
                 int of = index_of(winner) - base;           // whose it is
                 of = of < run.head ? of : of >= run.rest() ? of - run.rest() : (of - run.head) / N % kThreads;
-                for (int i0 = of; i0 < run.units; i0 += 32 * kThreads) {
-                    const int at = i0 + lane * kThreads;
-                    float x[N] = {};
-                    if (at < run.units) numbers(run.unit(at), x);
-#pragma unroll
-                    for (int j = 0; j < N; ++j) found.push(at < run.units ? key_of(x[j], base + run.head + N * at + j) : 0);
-                }
+                found.scan(run, of, kThreads, base);
                 const int at = lane == 0 && of < run.head ? of : lane == 1 && run.rest() + of < run.n ? run.rest() + of : -1;
                 found.push(at >= 0 ? key_of(widen(run.from[at]), base + at) : 0);
+                found.settle(31);
             }
         }
-        found.flush();
+        found.settle(0);
         list = found.list;
         if constexpr (WARPS > 1) list = join_lists(list, shared.lists);
     }
@@ -603,12 +633,15 @@ template <typename T>
 cudaError_t forward(LogpParams& p, cudaStream_t stream) {
     p.split = 1;
     p.segment = p.vocab;
-    // Many rows of a middling length: what a CTA does at a row's ends (its warps'
-    // sums and lists joined) costs more than a warp's longer row.  8,192 rows, us
-    // with a CTA / a warp each: 2,500 bf16 32 / 12, with 5 of the best 102 / 38;
-    // 8,192 bf16 37 / 28, with 5 109 / 92, fp32 49 / 49, with 5 107 / 137; 16,384
-    // bf16 50 / 50, fp32 79 / 86.  1,024 rows of 5,003 with 5: 17 / 19.
-    const bool many = p.top ? p.rows >= 16 * kSms && p.vocab <= kManyTopVocab : p.rows >= 8 * kSms && p.vocab <= kManyVocab;
+    // Rows of a middling length, where there are many: what a CTA does at a row's
+    // ends (its warps' sums and lists joined, few CTAs at a time) costs more than a
+    // warp's longer row.  us with a CTA / a warp each, 8,192 rows: 2,500 bf16 32 /
+    // 12, with 5 of the best 104 / 30; 8,192 bf16 37 / 28, with 5 111 / 53, fp32 49 /
+    // 49, with 5 111 / 110; 16,384 bf16 50 / 50, with 5 127 / 116, fp32 79 / 86, with
+    // 5 136 / 213.  1,024 rows: 8,192 bf16 6.0 / 4.4, with 5 16.0 / 15.0; 12,000 bf16
+    // with 5 17.4 / 19.5.
+    const int64_t bytes = p.vocab * static_cast<int64_t>(sizeof(T));
+    const bool many = (p.rows >= kSomeRows && bytes <= kSomeBytes) || (p.rows >= kManyRows && bytes <= kManyBytes);
     if (p.vocab <= kWarpVocab || many) return forward_as<T, 1>(p, stream);
     // few rows: as many CTAs a row as keep every thread eight elements or more
     while (p.split < kMaxSplit && p.rows * p.split < 2 * kSms && p.vocab / (2 * p.split) >= 8 * 32 * kWarps) p.split *= 2;

@@ -146,7 +146,8 @@ def test_rows_that_start_anywhere(shift, extra, kind):
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("n,vocab,top", [(1215, 8192, 0), (1216, 8192, 0), (1217, 8193, 0), (2431, 5120, 6), (2432, 5120, 32),
-                                         (2433, 5121, 1), (2433, 2049, 7)])
+                                         (2433, 5121, 1), (2433, 2049, 7), (911, 8192, 3), (912, 8192, 3),
+                                         (2432, 16384, 20), (2431, 16384, 20)])
 def test_many_rows_of_middling_vocabularies(n, vocab, top, kind):
     """Against single rows, which have eight warps each; sums of fewer than 2^13 terms that are at most 1, of the largest
     being 1: their order and the exponentials' errors come to less than 2^9 u (for sums by lanes of 2^13 / 32 terms)."""
