@@ -59,7 +59,6 @@ template <typename T> struct Eight;
 
 template <> struct Eight<uint16_t> {
     uint4 v;
-    __device__ __forceinline__ void load_once(const uint16_t* p) { v = ld_once(p); }
     __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void get(float (&f)[8]) const { dev::Vec<uint16_t>::unpack(v, f); }
@@ -82,7 +81,6 @@ template <> struct Eight<uint16_t> {
 
 template <> struct Eight<float> {
     uint4 v[2];
-    __device__ __forceinline__ void load_once(const float* p) { v[0] = ld_once(p); v[1] = ld_once(p + 4); }
     __device__ __forceinline__ void load(const float* p) {
         v[0] = reinterpret_cast<const uint4*>(p)[0];
         v[1] = reinterpret_cast<const uint4*>(p)[1];
