@@ -530,9 +530,9 @@ int ddp_route_backward(const ddp_route_args* args, const void* logits, const int
  * Rows are elements next to one another; strides count elements between two
  * rows.  Any element alignment is correct.  Rows that start on 16 bytes (fp32
  * ones of the embedding and of dropout on 32) and whose length is a multiple of
- * eight are read and written in vectors; the norms and the log probabilities
- * read any others in whole words of 16 bytes too, and so does the embedding's
- * gradient, whose words may hold neighbours' elements, which are not looked at.
+ * eight are read and written in vectors; others are mostly read in whole words
+ * of 16 bytes too, each with an element of theirs; what else is in these is not
+ * looked at.
  * Arithmetic is fp32; bf16 results are rounded once, to nearest even.
  * Every call is asynchronous on `stream`, runs on the current device and keeps
  * nothing; a workspace is the caller's, device memory aligned to 16 bytes, one

@@ -25,8 +25,7 @@ using namespace ddpk::rows;
 constexpr int kThreads = 256;
 constexpr int kAhead = 4;              // forward: rows of a thread at once
 constexpr int kColumns = 4;            // and, where they do not lie in vectors, columns of each,
-constexpr int kScalarThreads = 128;    // which is then at most this many threads' (26,800 of 2,500 fp32: 256 with one column
-                                       // 91 us, with four 87, 128 with four 77, 32 94)
+constexpr int kShiftColumns = 96;      // while these are fewer (65,536 rows of 45 bf16: by columns 7.2 us, shifted 16.9; 133: 22.0, 16.9)
 constexpr int kMaxBits = 8;            // of a digit of the sort
 constexpr int kMaxBins = 1 << kMaxBits;
 constexpr int kSortThreads = 512;
@@ -107,8 +106,8 @@ __device__ __forceinline__ long long token_at(const void* tokens, int wide, long
 // bounds it is the way from L2: the rows of common words are read from there again
 // and again, 268 MB with 134 MB written, 10.5 TB/s.  Occupancy is what it lives
 // on: three CTAs an SM 45.2 us, four 38.9; of bf16 tables, which leave more
-// registers, four 35.0 and five 31.2.  Rows that do not lie in vectors go element
-// by element (1,023: 81 us).
+// registers, four 35.0 and five 31.2.  Rows that do not lie in vectors and are short
+// go element by element.
 template <typename Tin, typename Tout, bool VEC>
 __global__ void __launch_bounds__(kThreads, VEC && sizeof(Tin) == 2 ? 5 : 4) embed_kernel(const __grid_constant__ EmbedParams p) {
     ddpk::dev::pdl_wait();
@@ -166,6 +165,73 @@ __global__ void __launch_bounds__(kThreads, VEC && sizeof(Tin) == 2 ? 5 : 4) emb
                             out[(r0 + u * slots) * p.out_stride + col] = narrow<Tout>(from[u] >= 0 ? f[u][k] * p.scale : 0.0f);
                     }
             }
+        }
+    }
+}
+
+// Rows that do not lie in vectors, a warp each: eights that start on 16 bytes of the
+// result, shifted out of the aligned words that the table's row lies in; a lane
+// loads those that its eights begin in, and has the next lane's for their ends.  No
+// word is loaded that does not hold an element of the row.  65,493 rows of 1,023
+// from fp32 to bf16 54 us, from bf16 37 (floor 29 and 25; 92 and 110 by columns).
+template <typename Tin, typename Tout>
+__global__ void __launch_bounds__(kThreads, 4) embed_shift_kernel(const __grid_constant__ EmbedParams p) {
+    constexpr int kEights = sizeof(Tin) == 2 ? 4 : 2;
+    ddpk::dev::pdl_wait();
+    ddpk::dev::pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const long long r = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    if (r >= p.n) return;
+    const long long token = token_at(p.tokens, p.wide, r, p.vocab);
+    const bool zero = token < 0;
+    Tout* const out = static_cast<Tout*>(p.out) + r * p.out_stride;
+    const int head = min(p.dim, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(out) & 15)) % 16 / sizeof(Tout)));
+    const int units = (p.dim - head) / 8, ends = p.dim - 8 * units;
+    const Tin* const from = static_cast<const Tin*>(p.table) + (zero ? 0 : token) * p.table_stride;
+    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(from + head) & 15);
+    const Tin* const words = reinterpret_cast<const Tin*>(reinterpret_cast<const char*>(from + head) - shift);
+    if (lane < ends) {                                     // at most seven elements of each end
+        const int i = lane < head ? lane : lane + 8 * units;
+        out[i] = narrow<Tout>(zero ? 0.0f : widen(from[i]) * p.scale);
+    }
+    for (int i0 = 0; i0 < units; i0 += 32 * kEights) {
+        Eight<Tin> raw[kEights];
+        uint4 last = make_uint4(0, 0, 0, 0);                // lane 0: what follows the warp's eights
+#pragma unroll
+        for (int u = 0; u < kEights; ++u) {
+            const int i = i0 + u * 32 + lane;
+            raw[u].zero();
+            if (!zero && i < units) raw[u].load(words + 8 * i);
+            else if (!zero && i == units && shift) *reinterpret_cast<uint4*>(&raw[u]) = *reinterpret_cast<const uint4*>(words + 8 * i);
+        }
+        if (!zero && shift && lane == 0 && i0 + 32 * kEights <= units)
+            last = *reinterpret_cast<const uint4*>(words + 8 * (i0 + 32 * kEights));
+#pragma unroll
+        for (int u = 0; u < kEights; ++u) {
+            const int i = i0 + u * 32 + lane;
+            if (i - lane >= units) break;                  // the whole warp's
+            if (shift && !zero) {
+                const uint4 mine = *reinterpret_cast<const uint4*>(&raw[u]);
+                const uint4 ahead = u + 1 < kEights ? *reinterpret_cast<const uint4*>(&raw[u + 1 < kEights ? u + 1 : 0]) : last;
+                const uint4 give = lane == 0 ? ahead : mine;        // lane 0 to lane 31
+                const int next = (lane + 1) & 31;
+                const uint4 behind = make_uint4(__shfl_sync(kAll, give.x, next), __shfl_sync(kAll, give.y, next),
+                                                __shfl_sync(kAll, give.z, next), __shfl_sync(kAll, give.w, next));
+                raw[u] = shifted(raw[u], behind, shift);
+            }
+            if (i >= units) continue;
+            float f[8];
+            raw[u].get(f);
+            const float2 s = both(zero ? 0.0f : p.scale);
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const float2 d = mul2(make_float2(f[j], f[j + 1]), s);
+                f[j] = d.x;
+                f[j + 1] = d.y;
+            }
+            Eight<Tout> y;
+            y.put(f);
+            y.store_once(out + head + 8 * i);
         }
     }
 }
@@ -706,8 +772,12 @@ bool vectors(const ddp_embed_args* a, const void* table, const void* rows) {
 int row_threads(int64_t pieces) { return pieces >= kThreads ? kThreads : power_of_two(pieces); }
 
 template <typename Tin, typename Tout>
-cudaError_t embed_as(bool vec, long long ctas, const EmbedParams& p, cudaStream_t stream) {
-    return launch(vec ? embed_kernel<Tin, Tout, true> : embed_kernel<Tin, Tout, false>, ctas, kThreads, 0, stream, p);
+cudaError_t embed_as(bool vec, EmbedParams& p, cudaStream_t stream) {
+    if (!vec && p.dim >= kShiftColumns)
+        return launch(embed_shift_kernel<Tin, Tout>, (p.n + kThreads / 32 - 1) / (kThreads / 32), kThreads, 0, stream, p);
+    p.row_threads = row_threads(vec ? p.dim / 8 : (p.dim + kColumns - 1) / kColumns);
+    const long long tile = static_cast<long long>(kThreads / p.row_threads) * kAhead;
+    return launch(vec ? embed_kernel<Tin, Tout, true> : embed_kernel<Tin, Tout, false>, (p.n + tile - 1) / tile, kThreads, 0, stream, p);
 }
 
 template <typename T, typename Tout>
@@ -738,14 +808,10 @@ int ddp_embed(const ddp_embed_args* a, const void* table, const void* tokens, vo
     p.wide = a->index_bits == 64;
     p.scale = a->scale;
     const bool vec = vectors(a, table, out);
-    p.row_threads = row_threads(vec ? a->dim / 8 : (a->dim + kColumns - 1) / kColumns);
-    if (!vec && p.row_threads > kScalarThreads) p.row_threads = kScalarThreads;
-    const long long tile = static_cast<long long>(kThreads / p.row_threads) * kAhead;
-    const long long ctas = (p.n + tile - 1) / tile;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool in32 = a->table_dtype == DDP_F32, out32 = a->dtype == DDP_F32;
-    const cudaError_t e = in32 ? (out32 ? embed_as<float, float>(vec, ctas, p, st) : embed_as<float, uint16_t>(vec, ctas, p, st))
-                               : (out32 ? embed_as<uint16_t, float>(vec, ctas, p, st) : embed_as<uint16_t, uint16_t>(vec, ctas, p, st));
+    const cudaError_t e = in32 ? (out32 ? embed_as<float, float>(vec, p, st) : embed_as<float, uint16_t>(vec, p, st))
+                               : (out32 ? embed_as<uint16_t, float>(vec, p, st) : embed_as<uint16_t, uint16_t>(vec, p, st));
     return e == cudaSuccess ? DDP_OK : DDP_ERR_CUDA;
 }
 

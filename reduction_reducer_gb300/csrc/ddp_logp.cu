@@ -487,8 +487,6 @@ __global__ void __launch_bounds__(32 * kWarps, TOP ? 4 : 5) logp_kernel(const __
 
 // ---------------------------------------------------------------- backward
 
-template <int N> struct Constant { static constexpr int value = N; };
-
 // d log p_t / d z_i = [i = t] - p_i and d H / d z_i = -p_i (log p_i + H): a thread's
 // elements of a row take p (alpha + beta log2 p).
 struct Slope {
@@ -502,38 +500,6 @@ struct Slope {
         return mul2(make_float2(exp2_fast(d.x), exp2_fast(d.y)), y);
     }
 };
-
-// Eight elements that begin `shift` bytes, whole elements, behind the start of
-// 16-byte words: of those words and of the one behind them.
-template <typename T>
-__device__ __forceinline__ Eight<T> shifted(const Eight<T>& here, uint4 behind, int shift) {
-    constexpr int kWords = static_cast<int>(sizeof(Eight<T>)) / 4;
-    uint32_t w[kWords + 4], out[kWords];
-    const uint4* const words = reinterpret_cast<const uint4*>(&here);
-#pragma unroll
-    for (int i = 0; i < kWords / 4; ++i) { w[4 * i] = words[i].x; w[4 * i + 1] = words[i].y; w[4 * i + 2] = words[i].z; w[4 * i + 3] = words[i].w; }
-    w[kWords] = behind.x; w[kWords + 1] = behind.y; w[kWords + 2] = behind.z; w[kWords + 3] = behind.w;
-    const int bits = shift % 4 * 8;
-    // the shift is the row's: one of four constant selections
-    const auto select = [&](auto first) {
-#pragma unroll
-        for (int k = 0; k < kWords; ++k) {
-            constexpr int from = decltype(first)::value;
-            out[k] = sizeof(T) == 4 ? w[from + k] : __funnelshift_r(w[from + k], w[from + k + 1], bits);
-        }
-    };
-    switch (shift / 4) {
-        case 0: select(Constant<0>()); break;
-        case 1: select(Constant<1>()); break;
-        case 2: select(Constant<2>()); break;
-        default: select(Constant<3>()); break;
-    }
-    Eight<T> x;
-    uint4* const to = reinterpret_cast<uint4*>(&x);
-#pragma unroll
-    for (int i = 0; i < kWords / 4; ++i) to[i] = make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
-    return x;
-}
 
 // Eights that start on 16 bytes of the gradient; the logits' eights lie `shift`
 // bytes off, the same all along a row.  A lane loads the aligned words that its
