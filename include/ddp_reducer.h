@@ -627,7 +627,11 @@ typedef struct ddp_logprobs_args {
 } ddp_logprobs_args;
 
 /* For every row, z = scale * logits and m its largest:
- *   stats      fp32 [rows * 2]: m, and log S of S = sum of e^(z - m)
+ *   stats      fp32 [rows * 2]: m, and log S of S = sum of e^(z - m), for the
+ *              gradient, which finds the largest logit itself in them: where
+ *              |m| is above 64 and rounded, fp32 rows have its last bit as that
+ *              of log S; a row whose m is past the fp32 range has the largest
+ *              logit and -log S (-0 for 0)
  *   logp       fp32 [rows]: z_target - m - log S
  *   entropy    fp32 [rows] or NULL: log S - (sum of e^(z - m) (z - m)) / S
  *   top_index, top_logp  int32 and fp32 [rows * top]: the largest logits, in

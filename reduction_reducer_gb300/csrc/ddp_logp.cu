@@ -42,6 +42,7 @@ constexpr int kBackCtas = 12;          // on an SM: loads on their way (8,192 x 
 template <typename T> constexpr int kBackEights = sizeof(T) == 2 ? 4 : 2;      // of a thread
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kFloor = -1000.0f;     // 2^-1000 is zero; stands in for -inf where it meets a zero
+constexpr float kFar = 64.0f;          // from where on the rounding of m scale (half a step: 1.9e-6) is more than log S's
 
 struct LogpParams {
     const void* logits;
@@ -58,6 +59,7 @@ struct LogpParams {
     long long segment;             // elements of a CTA of a row
     int vocab, top, wide, split;
     float scale, scale2;           // scale2: scale log2(e)
+    int rounds;                    // m scale is rounded: scale is no power of two
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -298,6 +300,64 @@ struct Best {
     }
 };
 
+// ---------------------------------------------------------------- statistics
+
+// What a row's statistics keep of its largest logit m is m scale, and the gradient
+// is formed from (x - m) scale as the log probabilities are: with m scale in its
+// stead the rounding of m scale would be an error of log p, 3e-4 at 10,000 and 57 in
+// a row that is masked with -1e9.  So m has to follow from m scale and log S.
+// Two fp32 numbers at most, neighbours, have the same product with scale (their
+// products lie more than half a step apart): from kFar on the last bit of log S,
+// a step of its own, is m's.  A product past the fp32 range says nothing of m:
+// there the statistics are m itself and -log S (-0 for 0), which they are in no
+// other row.
+template <typename T>
+__device__ __forceinline__ float2 stats_of(const LogpParams& p, float m, float log_sum) {
+    const float z = __fmul_rn(m, p.scale);
+    if (isinf(z) && !isinf(m)) return make_float2(m, -log_sum);
+    if (sizeof(T) == 4 && p.rounds && fabsf(z) > kFar)
+        log_sum = __int_as_float((__float_as_int(log_sum) & ~1) | (__float_as_int(m) & 1));
+    return make_float2(z, log_sum);
+}
+
+// log p = (x times + plus) unit - log S, in base two: (x - m) scale, or, where the
+// product's rounding is none or does not matter, x scale - m scale.
+struct Origin {
+    float times, plus, unit, log_sum;
+};
+
+template <typename T>
+__device__ __noinline__ Origin far_origin_of(float2 stat, float scale, float scale2, int rounds) {
+    float m = stat.x;
+    bool known = __float_as_int(stat.y) < 0 && isinf(__fmul_rn(m, scale));
+    if (known) {
+        stat.y = -stat.y;
+    } else if (rounds) {
+        const float near = __fdiv_rn(stat.x, scale);          // within a step of m
+        if constexpr (sizeof(T) == 2) {
+            m = widen(narrow<T>(near));
+            known = __fmul_rn(m, scale) == stat.x;
+        } else {
+#pragma unroll
+            for (int i = -1; i <= 1; ++i) {
+                const float c = __int_as_float(__float_as_int(near) + i);
+                if (__fmul_rn(c, scale) == stat.x && ((__float_as_int(c) ^ __float_as_int(stat.y)) & 1) == 0) {
+                    m = c;
+                    known = true;
+                }
+            }
+        }
+    }
+    if (known) return Origin{1.0f, -m, scale2, stat.y};
+    return Origin{scale, -stat.x, kLog2e, stat.y};
+}
+
+template <typename T>
+__device__ __forceinline__ Origin origin_of(const LogpParams& p, float2 stat) {
+    if (fabsf(stat.x) > kFar) return far_origin_of<T>(stat, p.scale, p.scale2, p.rounds);
+    return Origin{p.scale, -stat.x, kLog2e, stat.y};
+}
+
 // ---------------------------------------------------------------- forward
 
 template <bool TOP>
@@ -474,7 +534,7 @@ __global__ void __launch_bounds__(32 * kWarps, TOP ? 4 : 5) logp_kernel(const __
         if (p.logp && target >= 0)
             p.logp[row] = nothing ? neg_inf() : (widen(logits[target]) - sums.m) * p.scale - log_sum;
         if (ENTROPY) p.entropy[row] = nothing ? 0.0f : log_sum - kLn2 * __fdiv_rn(sums.a, sums.s);
-        *reinterpret_cast<float2*>(p.stats + 2 * row) = make_float2(sums.m * p.scale, log_sum);
+        *reinterpret_cast<float2*>(p.stats + 2 * row) = stats_of<T>(p, sums.m, log_sum);
     }
     if constexpr (TOP) {
         if (lane < p.top) {
@@ -490,11 +550,11 @@ __global__ void __launch_bounds__(32 * kWarps, TOP ? 4 : 5) logp_kernel(const __
 // d log p_t / d z_i = [i = t] - p_i and d H / d z_i = -p_i (log p_i + H): a thread's
 // elements of a row take p (alpha + beta log2 p).
 struct Slope {
-    float scale, top, log_sum2, alpha, beta;
+    float times, plus, unit, log_sum2, alpha, beta;
 
     template <bool ENTROPY>
     __device__ __forceinline__ float2 at(float2 x) const {
-        const float2 d = fma2(fma2(x, both(scale), both(-top)), both(kLog2e), both(-log_sum2));      // log2 p
+        const float2 d = fma2(fma2(x, both(times), both(plus)), both(unit), both(-log_sum2));      // log2 p
         float2 y = both(alpha);
         if constexpr (ENTROPY) y = fma2(both(beta), make_float2(fmaxf(d.x, kFloor), fmaxf(d.y, kFloor)), y);
         return mul2(make_float2(exp2_fast(d.x), exp2_fast(d.y)), y);
@@ -536,7 +596,9 @@ __global__ void __launch_bounds__(kBackThreads, kBackCtas) logp_backward_kernel(
         last = *reinterpret_cast<const uint4*>(words + 8 * (first + 32 * kEights));
     const float g = p.grad_logp && target >= 0 ? p.grad_logp[row] : 0.0f;
     const float h = ENTROPY ? p.grad_entropy[row] : 0.0f;
-    const Slope slope = {p.scale, stat.x, stat.y * kLog2e, -p.scale * (ENTROPY ? fmaf(h, p.entropy[row], g) : g), -p.scale * h * kLn2};
+    const Origin origin = origin_of<T>(p, stat);
+    const Slope slope = {origin.times, origin.plus, origin.unit, origin.log_sum * kLog2e,
+                         -p.scale * (ENTROPY ? fmaf(h, p.entropy[row], g) : g), -p.scale * h * kLn2};
     const float extra = p.scale * g;
     const int aim = target - static_cast<int>(lo);
     // the ends, at most seven elements each
@@ -638,6 +700,8 @@ LogpParams params_of(const ddp_logprobs_args* a) {
     p.wide = a->index_bits == 64;
     p.scale = a->scale;
     p.scale2 = static_cast<float>(a->scale * 1.4426950408889634);
+    int exponent;
+    p.rounds = std::frexp(a->scale, &exponent) != 0.5f;
     return p;
 }
 

@@ -16,7 +16,9 @@ class LogProbs(NamedTuple):
     """What ``logprobs`` gives; None for what was not asked for."""
     logp: object          # fp32 [...]: of the targets
     entropy: object       # fp32 [...]
-    stats: object         # fp32 [..., 2]: the largest logit (times scale), and the log of the sum of e^(z - largest)
+    # fp32 [..., 2]: the largest logit (times scale), and the log of the sum of e^(z - largest); the largest logit
+    # itself, and minus that log, where the product is past the fp32 range
+    stats: object
     top_index: object     # int32 [..., top]
     top_logp: object      # fp32 [..., top]
 
