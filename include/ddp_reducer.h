@@ -561,7 +561,8 @@ int64_t ddp_embed_workspace(const ddp_embed_args* args);
 /* grad_table[v] = scale * sum of grad[i] over the tokens i that are v, in fp32
  * and in ascending order (rows of more than 32 tokens in parts, and these in
  * order); rows without a token get zeros.  With accumulate (fp32 tables only)
- * the sums are added to grad_table, and rows without a token stay as they are.
+ * the sums are added to grad_table, numbers below 2^-126 included, and rows
+ * without a token stay as they are.
  * Errors: INVALID_ARG, CUDA. */
 int ddp_embed_backward(const ddp_embed_args* args, const void* grad, const void* tokens, void* grad_table,
                        int32_t accumulate, void* workspace, void* stream);
