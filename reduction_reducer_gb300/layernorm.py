@@ -115,7 +115,7 @@ def _autograd():
             def forward(ctx, x, weight, bias, eps, grad_into):
                 y, stats = layer_norm(x, weight, bias, eps)
                 ctx.save_for_backward(x, stats, weight)
-                ctx.bias_dtype, ctx.into = None if bias is None else bias.dtype, grad_into
+                ctx.dtypes, ctx.into = [None if t is None else t.dtype for t in (weight, bias)], grad_into
                 return y
 
             @staticmethod
@@ -123,16 +123,20 @@ def _autograd():
             def backward(ctx, grad):
                 x, stats, weight = ctx.saved_tensors
                 need_x, need_w, need_b = ctx.needs_input_grad[:3]
-                if ctx.into is not None:
-                    gw, gb = ctx.into
-                    dx, _, _ = layer_norm_backward(_rows.row_gradient(grad), x, stats, weight, gw, gb, input_grad=need_x,
-                                                   accumulate=True)
-                    return dx, None, None, None, None
-                dim = x.shape[-1:]
-                gw = torch.empty(dim, dtype=weight.dtype, device=x.device) if need_w else None
-                gb = torch.empty(dim, dtype=ctx.bias_dtype, device=x.device) if need_b else None
-                dx, gw, gb = layer_norm_backward(_rows.row_gradient(grad), x, stats, weight, gw, gb, input_grad=need_x)
-                return dx, gw, gb, None, None
+                field_w, field_b = ctx.into or (None, None)
+                added = (need_w and field_w is not None) or (need_b and field_b is not None)
+
+                def place(need, field, dtype):      # a call adds to both: what autograd gets then begins with zeros
+                    if not need:
+                        return None
+                    if field is not None:
+                        return field
+                    return (torch.zeros if added else torch.empty)(x.shape[-1:], dtype=dtype, device=x.device)
+
+                gw, gb = place(need_w, field_w, ctx.dtypes[0]), place(need_b, field_b, ctx.dtypes[1])
+                dx, gw, gb = layer_norm_backward(_rows.row_gradient(grad), x, stats, weight, gw, gb, input_grad=need_x,
+                                                 accumulate=added)
+                return dx, gw if field_w is None else None, gb if field_b is None else None, None, None
 
         _Normed = Normed
     return _Normed
@@ -140,9 +144,10 @@ def _autograd():
 
 def layer_normed(x, weight=None, bias=None, eps: float = 1e-5, grad_into=None):
     """``layer_norm`` under autograd, on the current stream: y.  grad_into:
-    (grad_weight, grad_bias), fp32 gradient fields or bucket views (either may
-    be None) that the gradients of parameters in fp32 are added to in the
-    backward pass; autograd then gets none for them."""
+    (grad_weight, grad_bias), fp32 gradient fields or bucket views that the
+    gradients of parameters in fp32 are added to in the backward pass; autograd
+    then gets none for them.  Where one is None, autograd gets that gradient;
+    the field of a parameter that takes no gradient stays as it is."""
     if grad_into is not None:
         _rows.load_torch()
         for t in (weight, bias, *grad_into):
