@@ -62,13 +62,22 @@ def _autograd():
         class Dropped(torch.autograd.Function):
             @staticmethod
             def forward(ctx, x, residual, p, seed, offset):
+                y = drop(x, p, seed, offset, residual)
                 ctx.how = p, seed, offset
-                return drop(x, p, seed, offset, residual)
+                if not isinstance(seed, int):          # that it changed is then an error of the backward pass
+                    ctx.save_for_backward(seed)
+                    ctx.how = p, None, offset
+                return y
 
             @staticmethod
             @torch.autograd.function.once_differentiable      # a second derivative raises
             def backward(ctx, grad):
-                dx = drop(_rows.row_gradient(grad), *ctx.how) if ctx.needs_input_grad[0] else None
+                dx = None
+                if ctx.needs_input_grad[0]:
+                    p, seed, offset = ctx.how
+                    if seed is None:
+                        seed, = ctx.saved_tensors
+                    dx = drop(_rows.row_gradient(grad), p, seed, offset)
                 return dx, grad if ctx.needs_input_grad[1] else None, None, None, None
 
         _Dropped = Dropped
@@ -77,5 +86,6 @@ def _autograd():
 
 def dropped(x, p: float, seed, offset: int = 0, residual=None):
     """``drop`` under autograd, on the current stream; nothing is kept for the
-    backward pass."""
+    backward pass but a seed on the device, which raises there if torch has
+    changed it meanwhile (a replayed graph is not looked at)."""
     return _autograd().apply(x, residual, p, seed, offset)
