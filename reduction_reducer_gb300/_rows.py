@@ -66,12 +66,21 @@ def vector(name, t, shape, device, dtype):
     return t.data_ptr()
 
 
-def indices(name, t, shape, device):
-    """(address, bits) of a contiguous tensor of integers."""
+def indices(name, t, shape, device, stream):
+    """(tensor, address, bits) of integers.  A slice of a batch, as a next-token
+    loss has them, is copied on the call's stream."""
     bits = INDEX.get(t.dtype)
-    if bits is None or (shape is not None and t.shape != shape) or not t.is_contiguous() or t.get_device() != device:
-        raise ValueError(f"{name}: expected {'' if shape is None else list(shape)} contiguous int32 or int64 on {found(device, t)}")
-    return t.data_ptr(), bits
+    if bits is None or (shape is not None and t.shape != shape) or t.get_device() != device:
+        raise ValueError(f"{name}: expected {'' if shape is None else list(shape)} int32 or int64 on {found(device, t)}")
+    if not t.is_contiguous():
+        with on_stream(stream):
+            t = t.contiguous()
+    return t, t.data_ptr(), bits
+
+
+def on_stream(stream):
+    """torch's current stream: the given one (None: as it is)."""
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
 def empty(shape, dtype, device, stream):
@@ -79,7 +88,7 @@ def empty(shape, dtype, device, stream):
     torch's current stream may still be in use there."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+    with on_stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 

@@ -21,15 +21,15 @@ def embed(table, tokens, scale: float = 1.0, dtype=None, out=None, stream=None, 
     """scale * table[tokens]: [*tokens.shape, dim].
 
     table: [vocab, dim] fp32 or bf16 (rows may be strided); tokens: int32 or
-    int64, contiguous, of any shape; those outside [0, vocab), as padding is,
-    give rows of zeros; dtype: of the result (torch.float32 or
+    int64 of any shape (a slice is copied first); those outside [0, vocab), as
+    padding is, give rows of zeros; dtype: of the result (torch.float32 or
     torch.bfloat16; the table's); out: the result's place (its rows may be
     strided).  All tensors lie on the current device."""
     if _rows.torch is None:
         _rows.load_torch()
     device = _device()
     vocab, dim, table_stride, table_code = _rows.matrix("table", table, device)
-    address, bits = _rows.indices("tokens", tokens, None, device)
+    tokens, address, bits = _rows.indices("tokens", tokens, None, device, stream)
     shape, row_stride = (*tokens.shape, dim), dim
     code = table_code if dtype is None else _rows.DTYPES.get(dtype, -1)
     if out is None and code >= 0:
@@ -58,7 +58,7 @@ def embed_backward(grad, tokens, out, scale: float = 1.0, accumulate: bool = Fal
         _rows.load_torch()
     device = _device()
     vocab, dim, table_stride, table_code = _rows.matrix("out", out, device)
-    address, bits = _rows.indices("tokens", tokens, None, device)
+    tokens, address, bits = _rows.indices("tokens", tokens, None, device, stream)
     _, _, row_stride, code = _rows.matrix("grad", grad, device, (*tokens.shape, dim))
     n, lib = tokens.numel(), _lib.load(lib_path)
     args = _pack(n, vocab, dim, table_stride, row_stride, scale, table_code, code, bits)

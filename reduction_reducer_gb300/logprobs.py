@@ -34,18 +34,21 @@ def logprobs(logits, targets=None, top: int = 0, scale: float = 1.0, entropy: bo
              lib_path: str = _lib.LIB_PATH):
     """``LogProbs`` of softmax(scale * logits) over the last dimension.
 
-    logits: [..., vocab] fp32 or bf16 (rows may be strided); targets: [...]
-    int32 or int64, contiguous, or None; a row whose target lies outside [0,
-    vocab), as padding's does, is left out (zeros, alternatives -1); top: 0 ..
-    32 alternatives, the largest logits in descending order, ties to the
-    lowest index; scale: 1 / temperature, 2^-64 .. 2^64; entropy: whether to
-    give it.
+    logits: [..., vocab] fp32 or bf16, rows at one distance from each other;
+    targets: [...] int32 or int64 (a slice is copied first), or None; a row
+    whose target lies outside [0, vocab), as padding's does, is left out (zeros,
+    alternatives -1), and so are the places of a batch that have no next token,
+    without a copy of the others' logits; top: 0 .. 32 alternatives, the largest
+    logits in descending order, ties to the lowest index; scale: 1 /
+    temperature, 2^-64 .. 2^64; entropy: whether to give it.
     All tensors lie on the current device."""
     torch = _rows.torch or _rows.load_torch()
     device = _device()
     rows, vocab, stride, code = _rows.matrix("logits", logits, device)
     lead = logits.shape[:-1]
-    at, bits = (None, 64) if targets is None else _rows.indices("targets", targets, lead, device)
+    at, bits = None, 64
+    if targets is not None:
+        targets, at, bits = _rows.indices("targets", targets, lead, device, stream)
     args = _pack(rows, vocab, stride, top, bits, scale, code)
     f32, dev, empty = torch.float32, logits.device, _rows.empty
     logp = h = index = best = logp_at = h_at = index_at = best_at = None
@@ -77,7 +80,9 @@ def logprobs_backward(grad_logp, logits, targets, stats, scale: float = 1.0, ent
     device = _device()
     rows, vocab, stride, code = _rows.matrix("logits", logits, device)
     lead, f32 = logits.shape[:-1], torch.float32
-    at, bits = (None, 64) if targets is None else _rows.indices("targets", targets, lead, device)
+    at, bits = None, 64
+    if targets is not None:
+        targets, at, bits = _rows.indices("targets", targets, lead, device, stream)
     if grad_entropy is None:
         entropy = None
     out_stride = vocab
