@@ -320,6 +320,12 @@ __device__ __forceinline__ float2 stats_of(const LogpParams& p, float m, float l
     return make_float2(z, log_sum);
 }
 
+// (x - m) scale, also where the difference alone is past the fp32 range.
+__device__ __forceinline__ float below(float x, float m, float scale) {
+    const float d = x - m;
+    return isinf(d) && !isinf(x) && !isinf(m) ? x * scale - m * scale : d * scale;
+}
+
 // log p = (x times + plus) unit - log S, in base two: (x - m) scale, or, where the
 // product's rounding is none or does not matter, x scale - m scale.
 struct Origin {
@@ -532,7 +538,7 @@ __global__ void __launch_bounds__(32 * kWarps, TOP ? 4 : 5) logp_kernel(const __
     const float log_sum = nothing ? 0.0f : logf(sums.s);
     if (lane == 0) {
         if (p.logp && target >= 0)
-            p.logp[row] = nothing ? neg_inf() : (widen(logits[target]) - sums.m) * p.scale - log_sum;
+            p.logp[row] = nothing ? neg_inf() : below(widen(logits[target]), sums.m, p.scale) - log_sum;
         if (ENTROPY) p.entropy[row] = nothing ? 0.0f : log_sum - kLn2 * __fdiv_rn(sums.a, sums.s);
         *reinterpret_cast<float2*>(p.stats + 2 * row) = stats_of<T>(p, sums.m, log_sum);
     }
@@ -540,7 +546,7 @@ __global__ void __launch_bounds__(32 * kWarps, TOP ? 4 : 5) logp_kernel(const __
         if (lane < p.top) {
             p.top_index[row * p.top + lane] = list ? index_of(list) : -1;
             p.top_logp[row * p.top + lane] =
-                list ? (value_of(list) - sums.m) * p.scale - log_sum : sums.s == sums.s ? neg_inf() : nan_value();
+                list ? below(value_of(list), sums.m, p.scale) - log_sum : sums.s == sums.s ? neg_inf() : nan_value();
         }
     }
 }

@@ -104,6 +104,25 @@ def test_gradient(scale, vocab, kind):
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab", [6, 3000, 20000])
+@pytest.mark.parametrize("scale", [0.5, 0.3, 2.0 ** -64, 2.0 ** -40 * 1.7])
+def test_differences_past_the_largest_number(scale, vocab, kind):
+    """The type's largest and lowest in one row: their difference is no fp32 number, and its product with scale is.  It errs
+    by 2 u (two products of different signs, added: 1 u each) and log S, which nothing else in the row adds to, is log 3."""
+    low = torch.finfo(KINDS[kind]).min
+    x = torch.full((2, vocab), -INF, dtype=KINDS[kind], device="cuda")
+    x[:, :3], x[:, 3] = -low, low
+    t = torch.tensor([3, 1], device="cuda")
+    got = logprobs(x, t, 5, scale, entropy=True)
+    log3 = torch.tensor(3.0, dtype=torch.float64).log().item()
+    far = 2 * low * f32(scale)
+    for value, want in ((got.logp[0], far), (got.top_logp[0, 3], far), (got.top_logp[1, 3], far), (got.logp[1], -log3),
+                        (got.top_logp[0, 0], -log3), (got.entropy[0], log3)):
+        assert abs(float(value) - want) <= 4 * U * abs(want) + 20 * U, (float(value), want)
+    assert got.top_index[0].tolist() == [0, 1, 2, 3, -1] and float(got.top_logp[0, 4]) == -INF
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
 def test_many_largest_logits(kind):
     """Every m of a binade and its neighbours, two of which may have the same product with scale."""
     gen = torch.Generator("cuda").manual_seed(3)
