@@ -537,6 +537,8 @@ int ddp_route_backward(const ddp_route_args* args, const void* logits, const int
  * Every call is asynchronous on `stream`, runs on the current device and keeps
  * nothing; a workspace is the caller's, device memory aligned to 16 bytes, one
  * for each call that may run at the same time, and of no value afterwards.
+ * Calls that may run at the same time have outputs of their own, fields that
+ * they add to among these.
  * Outputs overlap no inputs but where it is said. */
 
 typedef struct ddp_embed_args {

@@ -78,13 +78,16 @@ __device__ __forceinline__ void staying(const DropParams& p, long long group, ui
 
 // The kernel reads 16 bf16 or fp32 elements a thread and has their bits computed
 // while these are on their way.  65,536 x 1,024 in bf16 onto a residual: 61 us (403
-// MB, 6.6 TB/s, the copy's rate); without a residual 55 for 268 MB, since a block of
-// four words is 20 wide products and as many exclusive-ors and every element two
-// comparisons: 48 M warp instructions, 71 % of the integer pipe.  A mask of eight
-// bits instead of eight flags took 57 and 64.
+// MB, 6.6 TB/s, the copy's rate); without a residual 55 for 268 MB (floor 40): 48.7 M
+// warp instructions, 71 % of the integer pipe.  These are 185 for eight elements of a
+// lane, of which a block's wide products and exclusive-ors are 40; the others are
+// comparisons, the closest to the border, the products with the scale, widening,
+// packing and addresses.  A mask of eight bits instead of eight flags took 57 and 64.
 
 // Whole: one run of n elements from boundaries of eight.  Rows: rows of a multiple
-// of eight elements, each from one.  Single: anything else, element by element.
+// of eight elements, each from one.  Single: anything else, element by element.  us
+// for 65,536 rows, without a residual / with one: 1,024 bf16 in one run 56 / 61, in
+// rows of 1,032 67 / 74, in rows of 1,028 176 / 181; fp32 78 / 113, 78 / 114, 257 / 273.
 enum Layout { kWhole, kRows, kSingle };
 
 template <typename T, bool RESIDUAL, Layout LAYOUT, bool SEED>

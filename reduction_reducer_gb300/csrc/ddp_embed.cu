@@ -103,9 +103,10 @@ __device__ __forceinline__ long long token_at(const void* tokens, int wide, long
 // out[i] = scale table[tokens[i]].  A thread has kAhead rows' eight columns on their
 // way at once; a row is as many threads as it has eights.  65,536 rows of 1,024
 // from fp32 to bf16: 38.3 us, 189 MB from and to HBM (4.9 TB/s, floor 28 us).  What
-// bounds it is the way from L2: the rows of common words are read from there again
-// and again, 268 MB with 134 MB written, 10.5 TB/s.  Occupancy is what it lives
-// on: three CTAs an SM 45.2 us, four 38.9; of bf16 tables, which leave more
+// bounds it is latency: a CTA has one tile, and waits for its tokens and then for
+// their rows; HBM is at 44 % of its rate and L2, from which common words' rows come
+// again and again, at 39 %, with 41 % of the warps resident.  So occupancy is what
+// it lives on: three CTAs an SM 45.2 us, four 38.9; of bf16 tables, which leave more
 // registers, four 35.0 and five 31.2.  Rows that do not lie in vectors and are short
 // go element by element.
 template <typename Tin, typename Tout, bool VEC>
@@ -592,7 +593,9 @@ __device__ __noinline__ Sum join_parts(const SumParams& p, long long start, int 
 // longer for instructions than for the rows.
 // 65,536 rows of 1,024 in bf16, added to fp32 rows: 134 MB read, and 130 MB of the
 // table's rows read and written, in 57 us cold (74 with the sort, floor 39); without
-// the copies ahead 114 with the sort.  62 % of the issue slots are busy, most with
+// the copies ahead 114 with the sort.  2.43 instructions a cycle while an SM has warps
+// (62 % of what a scheduler can issue), 1.86 over all: 2,048 CTAs are 3.4 waves, whose
+// warps have one to many rows, and SMs run dry at the end.  Most instructions are
 // what a row costs whatever its length: its place from another lane, its address,
 // whether it ends here.  4,093 rows onto 30,522, 125 MB of zeros beside them: 33 us.
 template <typename T, typename Tout, bool VEC>

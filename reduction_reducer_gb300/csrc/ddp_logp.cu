@@ -332,6 +332,8 @@ struct Origin {
     float times, plus, unit, log_sum;
 };
 
+// Of a row whose m scale is far from zero: a call, as few rows take it (inlined the
+// gradient of the others took 235.2 us instead of 234.6).
 template <typename T>
 __device__ __noinline__ Origin far_origin_of(float2 stat, float scale, float scale2, int rounds) {
     float m = stat.x;
@@ -339,7 +341,7 @@ __device__ __noinline__ Origin far_origin_of(float2 stat, float scale, float sca
     if (known) {
         stat.y = -stat.y;
     } else if (rounds) {
-        const float near = __fdiv_rn(stat.x, scale);          // within a step of m
+        const float near = __fdiv_rn(stat.x, scale);               // within a step of m
         if constexpr (sizeof(T) == 2) {
             m = widen(narrow<T>(near));
             known = __fmul_rn(m, scale) == stat.x;
@@ -355,7 +357,7 @@ __device__ __noinline__ Origin far_origin_of(float2 stat, float scale, float sca
         }
     }
     if (known) return Origin{1.0f, -m, scale2, stat.y};
-    return Origin{scale, -stat.x, kLog2e, stat.y};
+    return Origin{scale, -stat.x, kLog2e, stat.y};             // exact as it is, or not this library's statistics
 }
 
 template <typename T>
@@ -392,7 +394,7 @@ __device__ __forceinline__ Key join_lists(Key mine, Key (*lists)[32]) {
 // fp32 logits two units a lane took 1.55 times as long, for sectors fetched twice),
 // kStages - 1 pieces of them on their way to shared memory while it adds up another.
 // 8,192 rows of 50,257 in bf16, a tenth of them left out, with the entropy: 119 us,
-// 6.2 TB/s (floor 111); 81 % of the issue slots are busy (10 warp instructions
+// 6.2 TB/s (floor 111); a warp issues in 78 % of the cycles (10 warp instructions
 // for 32 elements).  Loaded when they were due, and added up one by one, 172.  Four rows with eight alternatives:
 // 9.6 us, most of it the alternatives' second pass and the two waits for the cluster.
 template <typename T, int WARPS, bool ENTROPY, bool TOP>
@@ -572,8 +574,9 @@ struct Slope {
 // eights begin in, and has the next lane's for their ends; none is loaded that
 // does not hold a logit of the row.  A CTA takes 4,096 (fp32: 2,048) elements and
 // has nothing to wait for but its loads, and twelve are resident.  8,192 rows of
-// 50,257 in bf16, entropy too: 234 us, 6.7 TB/s, the copy's rate (floor 233); logits
-// element by element 415, shifted out of two loads each 271.
+// 50,257 in bf16, entropy too: 234.6 us, 6.7 TB/s, the copy's rate (floor 233); logits
+// element by element 415, shifted out of two loads each 271.  4,096 rows in fp32 231,
+// and 3 % more where m is far from zero and is looked for.
 template <typename T, bool ENTROPY>
 __global__ void __launch_bounds__(kBackThreads, kBackCtas) logp_backward_kernel(const __grid_constant__ LogpParams p) {
     constexpr int kEights = kBackEights<T>;

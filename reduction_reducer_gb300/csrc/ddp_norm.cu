@@ -30,7 +30,7 @@ constexpr int kLongParts = 64;         // of rows of any length, over which the 
 constexpr int kColumns = 256;          // of a CTA of norm_columns_kernel
 constexpr int kJoinLanes = 32;         // join_kernel: threads of a column
 constexpr int kForwardWaves = 3;       // 65,536 x 1024 in bf16: one 50.1 us, two 46.3, three 44.7, four 45.8, six 52.7
-constexpr int kWarpsPerSm = 16;        // resident, at 128 registers
+constexpr int kWarpsPerSm = 16;        // resident, at 128 registers (odd bf16 rows of 32 columns a lane take 155: 12)
 // Rows of a group on their way, with the one under work (of 512 threads' fp32
 // rows more would not fit); and rounds of rows of the gradient.
 template <typename T> constexpr int kForwardStages = sizeof(T) == 2 ? 4 : 3;

@@ -50,7 +50,7 @@ def embed_backward(grad, tokens, out, scale: float = 1.0, accumulate: bool = Fal
 
     grad: [*tokens.shape, dim] fp32 or bf16 (rows may be strided); out:
     [vocab, dim], fp32 or, without accumulate, bf16: a gradient field or a
-    bucket view (rows may be strided).  Rows without a token get zeros, and
+    bucket view (rows may be strided) that no other call writes meanwhile.  Rows without a token get zeros, and
     stay as they are with accumulate.  Sums are fp32, in the tokens' order.
     workspace: bytes that no other call uses meanwhile (without one they are
     allocated on `stream`)."""
